@@ -18,6 +18,9 @@ Two levels:
     tensors, allocate outputs with torch when none are given, call the C entry
     point on the current stream and raise ``AttnError`` on a non-zero status.
   * ``fwd_host``: the same for host (CPU) tensors through ``attn_fwd_host``.
+
+The operators around the cache (include/attn_kv.h: rotary positions, page plans, cache appends, page
+sketches, page-sparse attention) are in ``kv``, both levels, and re-exported here.
 """
 import ctypes
 import math
@@ -105,6 +108,7 @@ def lib():
             L.attn_device_status.argtypes = [vp]
             L.attn_status_string.restype = ctypes.c_char_p
             L.attn_status_string.argtypes = [i]
+            kv._declare(L)
             _lib = L
         return _lib
 
@@ -496,3 +500,10 @@ def bwd(q, k, v, o, lse, dout, causal=False, scale=None, dq=None, dk=None, dv=No
 def device_status(stream=None):
     """Synchronise and raise AttnError if a kernel flagged a timeout or bad device data."""
     _raise(attn_device_status(_stream(stream)), "attn_device_status")
+
+
+from . import kv  # noqa: E402  (uses the names above)
+from .kv import (  # noqa: E402,F401
+    attn_page_select, attn_page_select_workspace_size, attn_page_sketch, attn_paged_append, attn_paged_plan,
+    attn_paged_sparse_fwd, attn_paged_sparse_fwd_workspace_size, attn_rope, attn_rope_inv_freq, page_select,
+    page_sketch, paged_append, paged_plan, paged_sparse_fwd, rope, rope_inv_freq)

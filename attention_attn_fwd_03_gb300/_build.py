@@ -16,7 +16,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB_NAME = "libattn_gb300.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
-SOURCES = ["api.cu", "prefill.cu", "prefill_sp.cu", "decode.cu", "paged.cu", "backward.cu", "selftest.cu"]
+SOURCES = ["api.cu", "prefill.cu", "prefill_sp.cu", "decode.cu", "paged.cu", "backward.cu", "rope.cu", "pages.cu",
+           "select.cu", "selftest.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -44,7 +45,7 @@ def build(force=False, verbose=False, extra_flags=()):
     os.makedirs(BUILD, exist_ok=True)
     nvcc = nvcc_path()
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    headers.append(os.path.join(INCLUDE, "attn.h"))
+    headers += [os.path.join(INCLUDE, f) for f in ("attn.h", "attn_kv.h")]
     objs, jobs = [], []
     for src in SOURCES:
         s = os.path.join(CSRC, src)

@@ -1,4 +1,5 @@
-// api.cu -- the extern "C" entry points declared in include/attn.h.
+// api.cu -- the extern "C" entry points declared in include/attn.h, and the
+// page selection and page-sparse attention of include/attn_kv.h.
 //
 // Host-side only: argument validation (nothing is enqueued on a bad
 // argument), TMA tensor-map encoding, per-device cached state (the device
@@ -10,6 +11,7 @@
 #include <mutex>
 
 #include "attn.h"
+#include "attn_kv.h"
 #include "kernels.h"
 
 namespace attn {
@@ -73,6 +75,8 @@ attn_status_t device_state(DeviceState** out) {
     *out = &s;
     return ATTN_OK;
 }
+
+size_t round_up256(size_t x) { return (x + 255) / 256 * 256; }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -283,6 +287,94 @@ attn_status_t ragged_prefill(DeviceState* ds, const void* q, const void* k, cons
     return from_cuda(launch_ragged_prefill(d, sp, p, grid, stream));
 }
 
+// ---- page selection and page-sparse attention.
+
+attn_status_t select_sizes_ok(int B, int total_q, int H, int H_kv, int d, int page_size, int max_pages, int budget,
+                              int first, int last) {
+    if (B < 1 || total_q < 1 || H < 1 || H_kv < 1 || max_pages < 1 || budget < 1 || first < 0 || last < 1)
+        return ATTN_ERR_INVALID_ARG;
+    if (H % H_kv != 0 || (long long)first + last > budget) return ATTN_ERR_INVALID_ARG;
+    if (H / H_kv > 128 || (d != 64 && d != 128) || !pow2_in(page_size, 8, 1024)) return ATTN_ERR_UNSUPPORTED;
+    const long long rows = (long long)total_q * H_kv, wide = max_pages > budget ? max_pages : budget;
+    if ((long long)max_pages * page_size > 0x7fffffffLL || (long long)budget * page_size > 0x7fffffffLL ||
+        (long long)B * max_pages > 0x7fffffffLL || (long long)total_q * H > 0x7fffffffLL ||
+        rows > 0x7fffffffLL || wide > 0x7fffffffLL / rows)
+        return ATTN_ERR_INVALID_ARG;
+    return ATTN_OK;
+}
+
+// Splits of a token's chosen keys: with one unit per (token, KV head) too few
+// to occupy the SMs, the keys are cut into runs of whole 128-key blocks until
+// about three units per SM exist.
+struct SparsePlan {
+    int n_splits, split_blocks;
+    size_t tables, lens, cu, list, part_o, part_ml, bytes;  // byte offsets; list: the 256-byte header, then the entries
+};
+constexpr long long kSparseUnits = 456;
+constexpr long long kSparseMinBlocks = 2;
+
+SparsePlan sparse_plan(int total_q, int H, int H_kv, int d, int page_size, int max_pages, int budget) {
+    SparsePlan pl;
+    const long long rows = (long long)total_q * H_kv;
+    const long long keys = (long long)(budget < max_pages ? budget : max_pages) * page_size;
+    const long long blocks = (keys + 127) / 128;
+    const long long want = (kSparseUnits + rows - 1) / rows;
+    long long sb = (blocks + want - 1) / want;
+    if (sb < kSparseMinBlocks) sb = kSparseMinBlocks;
+    if (sb > blocks) sb = blocks;
+    pl.split_blocks = (int)sb;
+    pl.n_splits = (int)((blocks + sb - 1) / sb);
+    size_t at = select_keys_bytes(total_q, H_kv, max_pages, budget);
+    auto take = [&](size_t n) {
+        const size_t here = at;
+        at += round_up256(n);
+        return here;
+    };
+    pl.tables = take((size_t)rows * budget * sizeof(int32_t));
+    pl.lens = take((size_t)total_q * sizeof(int32_t));
+    pl.cu = take(((size_t)total_q + 1) * sizeof(int32_t));
+    pl.list = take(256 + (size_t)rows * pl.n_splits * sizeof(int4));
+    const size_t recs = pl.n_splits > 1 ? (size_t)total_q * H * pl.n_splits : 0;
+    pl.part_o = take(recs * d * sizeof(float));
+    pl.part_ml = take(recs * 2 * sizeof(float));
+    pl.bytes = at;
+    return pl;
+}
+
+void fill_select(SelectParams& s, DeviceState* ds, const void* q, const int8_t* sketch, const float* amp,
+                          const int32_t* block_table, const int32_t* cu_q, const int32_t* seq_lens, int B, int total_q,
+                          int H, int H_kv, int page_size, int max_pages, int num_pages, int budget, int first,
+                          int last) {
+    std::memset(&s, 0, sizeof s);
+    s.q = static_cast<const uint16_t*>(q);
+    s.sketch = sketch;
+    s.amp = amp;
+    s.table = block_table;
+    s.cu = cu_q;
+    s.seq_lens = seq_lens;
+    s.status = ds->status;
+    s.B = B;
+    s.total_q = total_q;
+    s.H = H;
+    s.H_kv = H_kv;
+    s.G = H / H_kv;
+    while ((1 << s.page_shift) < page_size) ++s.page_shift;
+    s.max_pages = max_pages;
+    s.num_pages = num_pages;
+    s.budget = budget;
+    s.first = first;
+    s.last = last;
+    s.n_splits = 1;
+}
+
+// Pointers that a selection reads: 16-byte aligned tensors, 4-byte aligned indices.
+bool select_pointers_ok(const void* q, const int8_t* sketch, const float* amp, const int32_t* block_table,
+                        const int32_t* cu_q, const int32_t* seq_lens, const int32_t* tables, const int32_t* sel_lens) {
+    auto a4 = [](const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 3u) == 0; };
+    return q && sketch && amp && block_table && seq_lens && aligned16(q) && aligned16(sketch) && aligned16(amp) &&
+           a4(block_table) && a4(cu_q) && a4(seq_lens) && a4(tables) && a4(sel_lens);
+}
+
 // ---- host-staged prefill: copy in, compute, copy out, chunk by chunk.
 //
 // The (b, h) range is cut into chunks.  Chunk c uses workspace slot
@@ -304,8 +396,6 @@ struct HostStage {
 
 std::mutex g_host_mu;
 HostStage g_host[kMaxDevices];
-
-size_t round_up256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Byte sizes of the buffers in one slot (each rounded up to 256 bytes).
 struct SlotLayout {
@@ -548,6 +638,7 @@ attn_status_t attn_paged_fwd(const void* q, const void* k_cache, const void* v_c
     p.c_scale = scale * 1.4426950408889634f;
     const int grid = pl.n_units < ds->sm_count ? (int)pl.n_units : ds->sm_count;  // persistent: one CTA per SM
     p.n_ctas = grid;
+    p.table_heads = 1;
     return from_cuda(launch_paged(d, p, grid, static_cast<cudaStream_t>(stream)));
 }
 
@@ -632,7 +723,132 @@ attn_status_t attn_varlen_fwd(const void* q, const void* k, const void* v, const
     p.c_scale = scale * 1.4426950408889634f;
     const int grid = pl.n_units < ds->sm_count ? (int)pl.n_units : ds->sm_count;  // persistent: one CTA per SM
     p.n_ctas = grid;
+    p.table_heads = 1;
     return from_cuda(launch_paged(d, p, grid, static_cast<cudaStream_t>(stream)));
+}
+
+size_t attn_page_select_workspace_size(int total_q, int H_kv, int max_pages, int budget) {
+    // the head dim, group and page size do not enter: any that are allowed will do
+    if (select_sizes_ok(1, total_q, H_kv, H_kv, 128, 8, max_pages, budget, 0, 1) != ATTN_OK) return 0;
+    return select_keys_bytes(total_q, H_kv, max_pages, budget);
+}
+
+attn_status_t attn_page_select(const void* q, const int8_t* sketch, const float* amp, const int32_t* block_table,
+                               const int32_t* cu_seqlens_q, const int32_t* seq_lens, int B, int total_q, int H,
+                               int H_kv, int d, int page_size, int max_pages, int num_pages, int budget, int first,
+                               int last, int32_t* tables, int32_t* sel_lens, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+    if (!select_pointers_ok(q, sketch, amp, block_table, cu_seqlens_q, seq_lens, tables, sel_lens) || !tables ||
+        !sel_lens)
+        return ATTN_ERR_INVALID_ARG;
+    if (!cu_seqlens_q && total_q != B) return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = select_sizes_ok(B, total_q, H, H_kv, d, page_size, max_pages, budget, first, last);
+    if (st != ATTN_OK) return st;
+    if (num_pages < 1 || (long long)num_pages * page_size > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+    if (!workspace || !aligned16(workspace) ||
+        workspace_bytes < select_keys_bytes(total_q, H_kv, max_pages, budget))
+        return ATTN_ERR_WORKSPACE;
+    DeviceState* ds = nullptr;
+    st = device_state(&ds);
+    if (st != ATTN_OK) return st;
+    SelectParams s;
+    fill_select(s, ds, q, sketch, amp, block_table, cu_seqlens_q, seq_lens, B, total_q, H, H_kv, page_size, max_pages,
+                num_pages, budget, first, last);
+    s.keys = static_cast<uint32_t*>(workspace);
+    s.tables = tables;
+    s.sel_lens = sel_lens;
+    return from_cuda(launch_select(d, s, static_cast<cudaStream_t>(stream)));
+}
+
+size_t attn_paged_sparse_fwd_workspace_size(int total_q, int H, int H_kv, int d, int page_size, int max_pages,
+                                            int budget) {
+    if (select_sizes_ok(1, total_q, H, H_kv, d, page_size, max_pages, budget, 0, 1) != ATTN_OK) return 0;
+    return sparse_plan(total_q, H, H_kv, d, page_size, max_pages, budget).bytes;
+}
+
+attn_status_t attn_paged_sparse_fwd(const void* q, const void* k_cache, const void* v_cache,
+                                    const int32_t* block_table, const int32_t* cu_seqlens_q,
+                                    const int32_t* seq_lens, const int8_t* sketch, const float* amp, int B,
+                                    int total_q, int H, int H_kv, int d, int page_size, int max_pages,
+                                    int num_pages, int budget, int first, int last, float scale, void* o,
+                                    float* lse, int32_t* tables, int32_t* sel_lens, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+    if (!k_cache || !v_cache || !o || (tables == nullptr) != (sel_lens == nullptr)) return ATTN_ERR_INVALID_ARG;
+    if (!select_pointers_ok(q, sketch, amp, block_table, cu_seqlens_q, seq_lens, tables, sel_lens))
+        return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) || (reinterpret_cast<uintptr_t>(lse) & 3u))
+        return ATTN_ERR_INVALID_ARG;
+    if (!cu_seqlens_q && total_q != B) return ATTN_ERR_INVALID_ARG;
+    if (!(std::isfinite(scale) && scale > 0.f)) return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = select_sizes_ok(B, total_q, H, H_kv, d, page_size, max_pages, budget, first, last);
+    if (st != ATTN_OK) return st;
+    if (num_pages < 1 || (long long)num_pages * page_size > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+    const SparsePlan pl = sparse_plan(total_q, H, H_kv, d, page_size, max_pages, budget);
+    const long long units = (long long)total_q * H_kv * pl.n_splits;
+    if (units > 0x3fffffffLL) return ATTN_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < pl.bytes || !aligned16(workspace)) return ATTN_ERR_WORKSPACE;
+    DeviceState* ds = nullptr;
+    st = device_state(&ds);
+    if (st != ATTN_OK) return st;
+
+    // the paged kernel with a request per token and a table row per token and KV head
+    char* ws = static_cast<char*>(workspace);
+    PagedParams p;
+    std::memset(&p, 0, sizeof p);
+    const long long slots = (long long)num_pages * page_size;
+    const int R = page_size < 128 ? page_size : 128;
+    const int G = H / H_kv;
+    if (!make_paged_map(&p.tm_q, q, d, H, total_q, G, 1) || !make_paged_map(&p.tm_k, k_cache, d, H_kv, slots, 1, R) ||
+        !make_paged_map(&p.tm_v, v_cache, d, H_kv, slots, 1, R))
+        return ATTN_ERR_CUDA;
+    SelectParams s;
+    fill_select(s, ds, q, sketch, amp, block_table, cu_seqlens_q, seq_lens, B, total_q, H, H_kv, page_size, max_pages,
+                num_pages, budget, first, last);
+    s.keys = reinterpret_cast<uint32_t*>(ws);
+    s.tables = tables ? tables : reinterpret_cast<int32_t*>(ws + pl.tables);
+    s.sel_lens = sel_lens ? sel_lens : reinterpret_cast<int32_t*>(ws + pl.lens);
+    s.cu_out = reinterpret_cast<int32_t*>(ws + pl.cu);
+    s.sched = reinterpret_cast<int*>(ws + pl.list);
+    s.sched_list = reinterpret_cast<int4*>(ws + pl.list + 256);
+    s.n_splits = pl.n_splits;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    st = from_cuda(launch_select(d, s, cs));
+    if (st != ATTN_OK) return st;
+    p.block_table = s.tables;
+    p.table_heads = H_kv;
+    p.cu_q = s.cu_out;
+    p.seq_lens = s.sel_lens;
+    p.o = static_cast<uint16_t*>(o);
+    p.lse = lse;
+    p.sched = s.sched;
+    p.sched_list = s.sched_list;
+    p.listed = 1;
+    if (pl.n_splits > 1) {
+        p.part_o = reinterpret_cast<float*>(ws + pl.part_o);
+        p.part_ml = reinterpret_cast<float*>(ws + pl.part_ml);
+    }
+    p.status = ds->status;
+    p.B = total_q;
+    p.H = H;
+    p.H_kv = H_kv;
+    p.G = G;
+    p.T = 1;
+    p.total_q = total_q;
+    p.max_q_len = 1;
+    p.n_qt = 1;
+    p.page_size = page_size;
+    p.max_pages = budget;
+    p.num_pages = num_pages;
+    p.rows_per_box = R;
+    p.kv_rows = (int)slots;
+    p.n_splits = pl.n_splits;
+    p.split_blocks = pl.split_blocks;
+    p.n_units = (int)units;
+    p.q_tile_bytes = (uint32_t)(d / 64) * (uint32_t)G * 128u;
+    p.c_scale = scale * 1.4426950408889634f;
+    const int grid = units < ds->sm_count ? (int)units : ds->sm_count;
+    p.n_ctas = grid;
+    return from_cuda(launch_paged(d, p, grid, cs));
 }
 
 size_t attn_bwd_workspace_size(int B, int H, int Nq, int d) {

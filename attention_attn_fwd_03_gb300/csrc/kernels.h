@@ -125,6 +125,8 @@ struct PagedParams {
     uint32_t q_tile_bytes;       // bytes one Q tile load delivers
     float c_scale;               // scale * log2(e)
     int n_ctas;                  // CTAs of the paged kernel (its persistent grid)
+    int table_heads;             // 1: a block table row per request; H_kv: one per request and KV head
+    int listed;                  // 1: an earlier kernel has written the work list (no schedule pass)
 };
 
 constexpr int kPagedThreads = 192;  // TMA warp + MMA warp + one softmax warpgroup
@@ -143,6 +145,30 @@ PagedPlan paged_plan(int total_q, int max_q_len, int B, int H, int H_kv, int d, 
 
 int paged_smem_bytes(int d);
 cudaError_t launch_paged(int d, const PagedParams& p, int grid, cudaStream_t stream);
+
+// Page selection (select.cu): sketch scores, then the budget's best pages per
+// (token, KV head); for page-sparse attention also that launch's work list.
+struct SelectParams {
+    const uint16_t* q;         // bf16 [total_q, H, d]
+    const int8_t* sketch;      // [num_pages, H_kv, 2 d]
+    const float* amp;          // [num_pages, H_kv]
+    const int32_t* table;      // [B, max_pages]
+    const int32_t* cu;         // [B + 1] or nullptr: one token per request
+    const int32_t* seq_lens;   // [B]
+    uint32_t* keys;            // [total_q, H_kv, max_pages] ordered scores
+    int32_t* tables;           // out: [total_q, H_kv, budget]
+    int32_t* sel_lens;         // out: [total_q]
+    int32_t* cu_out;           // out: [total_q + 1] the owned tokens as requests of one token, or nullptr
+    int* sched;                // out: the paged kernel's list header and list, or nullptr
+    int4* sched_list;
+    unsigned* status;
+    int B, total_q, H, H_kv, G, page_shift, max_pages, num_pages;
+    int budget, first, last;
+    int n_splits;              // splits per (token, KV head) in the list
+    int n_chunks;              // page chunks per (token, KV head) of the score kernel
+};
+size_t select_keys_bytes(int total_q, int H_kv, int max_pages, int budget);
+cudaError_t launch_select(int d, SelectParams p, cudaStream_t stream);
 
 // Failure-handling test: a bounded wait that nothing completes (selftest.cu).
 cudaError_t launch_selftest_timeout(unsigned* status, cudaStream_t stream);

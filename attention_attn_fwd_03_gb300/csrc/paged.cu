@@ -324,7 +324,8 @@ __device__ void producer_role(const PagedParams& p, uint8_t* smem, const PBars& 
                             row = kst + (int)key;
                         } else {
                             const int pg = (int)(key / p.page_size);
-                            const int id = __ldg(p.block_table + (size_t)g.r * p.max_pages + pg);
+                            const size_t trow = (size_t)g.r * p.table_heads + (p.table_heads > 1 ? g.kvh : 0);
+                            const int id = __ldg(p.block_table + trow * p.max_pages + pg);
                             if (id >= 0 && id < p.num_pages)
                                 row = id * p.page_size + (int)(key % p.page_size);
                             else
@@ -953,11 +954,13 @@ cudaError_t launch_d(const PagedParams& p, int grid, cudaStream_t stream) {
     cudaError_t e =
         cudaFuncSetAttribute(paged_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    paged_schedule_kernel<<<1, 1024, 0, stream>>>(p);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    if (!p.listed) {
+        paged_schedule_kernel<<<1, 1024, 0, stream>>>(p);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
     // programmatic dependent launches: the paged kernel's prologue overlaps
-    // the schedule pass and its producer waits for the pass (griddepcontrol.wait)
+    // the schedule pass (or the selection that wrote the list) and its producer waits for it (griddepcontrol.wait)
     // before reading the list; the merge kernel is scheduled early and waits
     // for the paged kernel to complete
     cudaLaunchAttribute attr[1];

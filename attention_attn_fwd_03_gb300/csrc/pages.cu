@@ -1,0 +1,447 @@
+// pages.cu -- the bookkeeping of a paged cache on the GPU: page plans (table
+// rows, slots and positions from request lengths) and page sketches (8-bit
+// channel extremes of each page's keys, which page selection scores).
+#include <cooperative_groups.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "attn_kv.h"
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace attn {
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+// ---------------------------------------------------------------- page plan
+//
+// Two prefix sums over the requests, new tokens and new pages, place
+// everything: token t belongs to the last request r with cu[r] <= t, and the
+// i-th new page of request r is the (before[r] + i)-th taken from the stack.
+//
+// One cluster does the call.  Every CTA computes both sums for itself into
+// shared memory (a few words per request, read through L2), then the tokens
+// are dealt to the cluster's threads, each finding its request by bisection in
+// shared memory.  The barrier between the two lets outputs replace inputs:
+// every CTA has read the lengths and the free count before CTA 0 writes
+// seq_lens and free_left.  A token that starts a page enters it in the table,
+// so table writes are as balanced as the tokens.  Latency-bound: the largest
+// calls write 8 bytes per token, the smallest a few hundred bytes.
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanMaxB = 16384;
+constexpr int kPlanMaxCluster = 8;
+
+struct PlanParams {
+    const int32_t* ctx;
+    const int32_t* fresh;  // new tokens per request, or nullptr: one each
+    int32_t* table;
+    const int32_t* free_pages;
+    const int32_t* free_count;
+    int32_t *cu, *seq_lens, *positions, *slots, *free_left;
+    unsigned* status;
+    int B, total_q, page_size, max_pages, num_pages, n_free;
+};
+
+__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_constant__ PlanParams p) {
+    extern __shared__ int s_plan[];
+    int* s_cu = s_plan;              // [B + 1], clamped to INT_MAX
+    int* s_ctx = s_cu + p.B + 1;     // [B]
+    int* s_before = s_ctx + p.B;     // [B]
+    __shared__ long long s_tok[32], s_pg[32];
+    __shared__ int s_count;
+    __shared__ long long s_demand;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = (int)cluster.block_rank(), n_ctas = (int)cluster.num_blocks();
+    const int ps = p.page_size;
+    const long long cap = (long long)p.max_pages * ps;
+    bool bad = false;
+
+    if (tid == 0) {
+        const int c = *p.free_count;
+        s_count = c < 0 ? 0 : c > p.n_free ? p.n_free : c;
+        bad = s_count != c;
+    }
+    // each thread sums a run of consecutive requests
+    const int run = (p.B + kPlanThreads - 1) / kPlanThreads;
+    const int r0 = tid * run, r1 = min(p.B, r0 + run);
+    auto lengths = [&](int r, long long& ctx, long long& len) {
+        ctx = p.ctx[r];
+        long long add = p.fresh != nullptr ? p.fresh[r] : 1;
+        if (ctx < 0 || ctx > cap) {
+            bad = true;
+            ctx = ctx < 0 ? 0 : cap;
+        }
+        if (add < 0 || ctx + add > cap) {
+            bad = true;
+            add = add < 0 ? 0 : cap - ctx;
+        }
+        len = ctx + add;
+    };
+    auto pages = [&](long long n) { return (n + ps - 1) / ps; };
+    long long tok = 0, pg = 0;
+    for (int r = r0; r < r1; ++r) {
+        long long ctx, len;
+        lengths(r, ctx, len);
+        tok += len - ctx;
+        pg += pages(len) - pages(ctx);
+    }
+    long long it = tok, ip = pg;  // inclusive sums over the warp, then over the warps
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long a = __shfl_up_sync(0xffffffffu, it, o), b = __shfl_up_sync(0xffffffffu, ip, o);
+        if (lane >= o) {
+            it += a;
+            ip += b;
+        }
+    }
+    if (lane == 31) {
+        s_tok[warp] = it;
+        s_pg[warp] = ip;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        long long a = s_tok[lane], b = s_pg[lane];
+        const long long a0 = a, b0 = b;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
+            if (lane >= o) {
+                a += x;
+                b += y;
+            }
+        }
+        s_tok[lane] = a - a0;
+        s_pg[lane] = b - b0;
+        if (lane == 31) s_demand = b;
+    }
+    __syncthreads();
+    tok = s_tok[warp] + it - tok;
+    pg = s_pg[warp] + ip - pg;
+    auto clip = [](long long x) { return (int)(x < 0x7fffffffLL ? x : 0x7fffffffLL); };
+    for (int r = r0; r < r1; ++r) {
+        long long ctx, len;
+        lengths(r, ctx, len);
+        s_cu[r] = clip(tok);
+        s_ctx[r] = (int)ctx;
+        s_before[r] = clip(pg);
+        tok += len - ctx;
+        pg += pages(len) - pages(ctx);
+        if (r == p.B - 1) {
+            s_cu[p.B] = clip(tok);
+            bad |= tok > p.total_q;
+        }
+    }
+    // all inputs that an output may replace have been read, by every CTA
+    cluster.sync();
+    const int count = s_count;
+    const int owned = s_cu[p.B];
+    if (rank == 0) {
+        for (int r = tid; r < p.B; r += kPlanThreads) p.seq_lens[r] = s_ctx[r] + (s_cu[r + 1] - s_cu[r]);
+        for (int r = tid; r <= p.B; r += kPlanThreads) p.cu[r] = s_cu[r];
+        if (tid == 0) *p.free_left = s_demand < count ? count - (int)s_demand : 0;
+    }
+    for (long long t64 = rank * kPlanThreads + tid; t64 < p.total_q; t64 += n_ctas * kPlanThreads) {
+        const int t = (int)t64;
+        int pos = 0, slot = -1;
+        if (t < owned) {
+            int lo = 0, hi = p.B - 1;  // the last request that starts at or before t
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (s_cu[mid] <= t)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            const int ctx = s_ctx[lo];
+            pos = ctx + (t - s_cu[lo]);
+            const int pi = pos / ps, at = pos - pi * ps;
+            const int held = (int)pages(ctx);
+            int32_t* entry = p.table + (long long)lo * p.max_pages + pi;
+            int id = -1;
+            if (pi < held) {
+                id = *entry;
+            } else {
+                const long long top = (long long)count - 1 - s_before[lo] - (pi - held);  // its place in the stack
+                if (top >= 0) id = p.free_pages[top];
+                if (id >= p.num_pages) id = -1;
+                if (at == 0) *entry = id < 0 ? -1 : id;
+            }
+            if (id >= 0 && id < p.num_pages)
+                slot = id * ps + at;
+            else
+                bad = true;
+        }
+        p.positions[t] = pos;
+        p.slots[t] = slot;
+    }
+    if (bad) atomicOr(p.status, 1u << kStatusDeviceData);
+}
+
+// ---------------------------------------------------------------- page sketch
+//
+// Per page and KV head the channel extremes over the valid rows, scaled by
+// their largest magnitude to 8 bits.  Extremes are exact in bf16 and do not
+// depend on the order of the rows, and the codes are two fp32 roundings
+// (divide, multiply) and one to an integer, so a page's sketch is a function
+// of its keys alone.
+//
+// Bound by reading the keys once.  A CTA takes one page (up to 1024 channels
+// of it): a thread owns 8 channels and every RG-th row, so that a row of the
+// page is read whole, 16 bytes per thread with eight rows in flight; row
+// groups combine through shared memory.
+
+constexpr int kSketchThreads = 256;
+constexpr int kSketchLanes = 128;  // threads across a row at most: 1024 channels
+
+struct SketchParams {
+    const uint16_t* k;
+    const int32_t* table;
+    const int32_t* cu;
+    const int32_t* seq_lens;
+    int8_t* sketch;
+    float* amp;
+    unsigned* status;
+    int B, max_q_len, H_kv, d, page_size, max_pages, num_pages;
+    int per_req, col_blocks;  // pages per request and channel blocks that the grid covers
+};
+
+// Largest / smallest of two packed bf16 pairs; a NaN in either operand stays.
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t code4(uint32_t a, uint32_t b, float amp) {
+    uint32_t r = 0;
+    const float x[4] = {bf16lo_to_f32(a), bf16hi_to_f32(a), bf16lo_to_f32(b), bf16hi_to_f32(b)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        r |= ((uint32_t)__float2int_rn(__fmul_rn(__fdiv_rn(x[i], amp), 127.f)) & 0xffu) << (8 * i);
+    return r;
+}
+
+__global__ void __launch_bounds__(kSketchThreads) page_sketch_kernel(const __grid_constant__ SketchParams p) {
+    __shared__ uint4 s_hi[kSketchThreads], s_lo[kSketchThreads];
+    const int cols = p.H_kv * p.d / 8;  // 16-byte pieces of a row
+    const int L = cols < kSketchLanes ? cols : kSketchLanes;
+    const int RG = kSketchThreads / L;
+    long long u = blockIdx.x;
+    const int cb = (int)(u % p.col_blocks);
+    u /= p.col_blocks;
+    const int nth = (int)(u % p.per_req);
+    const int r = (int)(u / p.per_req);
+
+    const long long cap = (long long)p.max_pages * p.page_size;
+    long long len = __ldg(p.seq_lens + r);
+    long long fresh = p.max_q_len;
+    bool bad = len < 0 || len > cap;
+    len = len < 0 ? 0 : len > cap ? cap : len;
+    if (p.cu != nullptr) {
+        fresh = (long long)__ldg(p.cu + r + 1) - __ldg(p.cu + r);
+        if (fresh < 0 || fresh > p.max_q_len || fresh > len) {
+            bad = true;
+            fresh = fresh < 0 ? 0 : fresh > p.max_q_len ? p.max_q_len : fresh;
+        }
+    }
+    if (fresh > len) fresh = len;
+    if (bad && threadIdx.x == 0 && nth == 0 && cb == 0) atomicOr(p.status, 1u << kStatusDeviceData);
+    if (fresh <= 0) return;
+    const long long page = (len - fresh) / p.page_size + nth;
+    if (page * p.page_size >= len) return;
+    const int rows = (int)min((long long)p.page_size, len - page * p.page_size);
+    const int id = __ldg(p.table + (long long)r * p.max_pages + page);
+    if (id < 0 || id >= p.num_pages) {
+        if (threadIdx.x == 0) atomicOr(p.status, 1u << kStatusDeviceData);
+        return;
+    }
+
+    const int lane = threadIdx.x % L, rg = threadIdx.x / L;
+    const int col = cb * kSketchLanes + lane;
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        hi[i] = 0xff80ff80u;  // -inf
+        lo[i] = 0x7f807f80u;  // +inf
+    }
+    if (rg < RG && col < cols) {
+        const uint4* src = reinterpret_cast<const uint4*>(p.k) + (long long)id * p.page_size * cols + col;
+        constexpr int U = 8;
+        for (int row0 = rg; row0 < rows; row0 += RG * U) {
+            uint4 x[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                // past the last row the first one is read again: extremes do not change
+                const int row = row0 + i * RG < rows ? row0 + i * RG : row0;
+                x[i] = src[(long long)row * cols];
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                hi[0] = max2(hi[0], x[i].x); lo[0] = min2(lo[0], x[i].x);
+                hi[1] = max2(hi[1], x[i].y); lo[1] = min2(lo[1], x[i].y);
+                hi[2] = max2(hi[2], x[i].z); lo[2] = min2(lo[2], x[i].z);
+                hi[3] = max2(hi[3], x[i].w); lo[3] = min2(lo[3], x[i].w);
+            }
+        }
+    }
+    s_hi[threadIdx.x] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    s_lo[threadIdx.x] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    __syncthreads();
+    if (rg == 0) {
+        const int groups = RG < rows ? RG : rows;  // groups that read a row
+        for (int g = 1; g < groups; ++g) {
+            const uint4 a = s_hi[g * L + lane], b = s_lo[g * L + lane];
+            hi[0] = max2(hi[0], a.x); hi[1] = max2(hi[1], a.y); hi[2] = max2(hi[2], a.z); hi[3] = max2(hi[3], a.w);
+            lo[0] = min2(lo[0], b.x); lo[1] = min2(lo[1], b.y); lo[2] = min2(lo[2], b.z); lo[3] = min2(lo[3], b.w);
+        }
+    }
+    // largest magnitude over the head's channels, as bf16 bits without the sign: the order of
+    // the integers is that of the magnitudes, infinities and NaN above every number
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t a = hi[i] & 0x7fff7fffu, b = lo[i] & 0x7fff7fffu;
+        top = max(top, max(max(a & 0xffffu, a >> 16), max(b & 0xffffu, b >> 16)));
+    }
+    const int lanes_per_head = p.d / 8;  // 8 or 16 neighbouring lanes of a warp, whole heads of L
+    for (int o = 1; o < lanes_per_head; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (rg != 0 || col >= cols) return;
+    const bool finite = top < 0x7f80u;
+    const float amp = finite ? __uint_as_float(top << 16) : INFINITY;
+    uint2 ch = make_uint2(0u, 0u), cl = make_uint2(0u, 0u);
+    if (finite && top != 0u) {
+        ch = make_uint2(code4(hi[0], hi[1], amp), code4(hi[2], hi[3], amp));
+        cl = make_uint2(code4(lo[0], lo[1], amp), code4(lo[2], lo[3], amp));
+    }
+    const int head = col / lanes_per_head, c0 = (col % lanes_per_head) * 8;
+    const long long rec = (long long)id * p.H_kv + head;
+    *reinterpret_cast<uint2*>(p.sketch + rec * (2 * p.d) + c0) = ch;
+    *reinterpret_cast<uint2*>(p.sketch + rec * (2 * p.d) + p.d + c0) = cl;
+    if (c0 == 0) p.amp[rec] = amp;
+}
+
+bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+}  // namespace
+
+}  // namespace attn
+
+using namespace attn;
+
+extern "C" {
+
+attn_status_t attn_paged_plan(const int32_t* ctx_lens, const int32_t* new_lens, int32_t* block_table,
+                              const int32_t* free_pages, const int32_t* free_count, int B, int total_q,
+                              int page_size, int max_pages, int num_pages, int n_free, int32_t* cu_seqlens_q,
+                              int32_t* seq_lens, int32_t* positions, int32_t* slots, int32_t* free_left,
+                              void* stream) {
+    if (!ctx_lens || !block_table || !free_pages || !free_count || !cu_seqlens_q || !seq_lens || !positions ||
+        !slots || !free_left)
+        return ATTN_ERR_INVALID_ARG;
+    if (B < 1 || total_q < 1 || page_size < 1 || max_pages < 1 || num_pages < 1 || n_free < 1)
+        return ATTN_ERR_INVALID_ARG;
+    for (const void* ptr : {static_cast<const void*>(ctx_lens), static_cast<const void*>(new_lens),
+                            static_cast<const void*>(block_table), static_cast<const void*>(free_pages),
+                            static_cast<const void*>(free_count), static_cast<const void*>(cu_seqlens_q),
+                            static_cast<const void*>(seq_lens), static_cast<const void*>(positions),
+                            static_cast<const void*>(slots), static_cast<const void*>(free_left)})
+        if (!aligned(ptr, 4)) return ATTN_ERR_INVALID_ARG;
+    if (B > kPlanMaxB || page_size < 8 || page_size > 1024 || page_size % 8 != 0) return ATTN_ERR_UNSUPPORTED;
+    if ((long long)max_pages * page_size > 0x7fffffffLL || (long long)num_pages * page_size > 0x7fffffffLL)
+        return ATTN_ERR_INVALID_ARG;
+
+    PlanParams p;
+    std::memset(&p, 0, sizeof p);
+    attn_status_t st = status_word_address(&p.status);
+    if (st != ATTN_OK) return st;
+    p.ctx = ctx_lens;
+    p.fresh = new_lens;
+    p.table = block_table;
+    p.free_pages = free_pages;
+    p.free_count = free_count;
+    p.cu = cu_seqlens_q;
+    p.seq_lens = seq_lens;
+    p.positions = positions;
+    p.slots = slots;
+    p.free_left = free_left;
+    p.B = B;
+    p.total_q = total_q;
+    p.page_size = page_size;
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    p.n_free = n_free;
+    const int smem = (3 * B + 1) * (int)sizeof(int);
+    if (cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (3 * kPlanMaxB + 1) * (int)sizeof(int)) != cudaSuccess)
+        return ATTN_ERR_CUDA;
+    int ctas = (total_q + kPlanThreads - 1) / kPlanThreads;
+    ctas = ctas >= kPlanMaxCluster ? kPlanMaxCluster : ctas > 2 ? 4 : ctas;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_plan_kernel, p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+attn_status_t attn_page_sketch(const void* k_cache, const int32_t* block_table, const int32_t* cu_seqlens_q,
+                               const int32_t* seq_lens, int B, int max_q_len, int H_kv, int d, int page_size,
+                               int max_pages, int num_pages, int8_t* sketch, float* amp, void* stream) {
+    if (!k_cache || !block_table || !seq_lens || !sketch || !amp) return ATTN_ERR_INVALID_ARG;
+    if (B < 1 || max_q_len < 1 || H_kv < 1 || H_kv > 65535 || page_size < 1 || max_pages < 1 || num_pages < 1)
+        return ATTN_ERR_INVALID_ARG;
+    if (!aligned(k_cache, 16) || !aligned(sketch, 16) || !aligned(amp, 16) || !aligned(block_table, 4) ||
+        !aligned(cu_seqlens_q, 4) || !aligned(seq_lens, 4))
+        return ATTN_ERR_INVALID_ARG;
+    if ((d != 64 && d != 128) || page_size < 8 || page_size > 1024 || (page_size & (page_size - 1)) != 0)
+        return ATTN_ERR_UNSUPPORTED;
+    if ((long long)max_pages * page_size > 0x7fffffffLL || (long long)num_pages * page_size > 0x7fffffffLL)
+        return ATTN_ERR_INVALID_ARG;
+
+    SketchParams p;
+    std::memset(&p, 0, sizeof p);
+    // max_q_len tokens touch at most this many pages, wherever they start
+    long long per_req = ((long long)max_q_len - 1 + page_size - 1) / page_size + 1;
+    if (per_req > max_pages) per_req = max_pages;
+    p.per_req = (int)per_req;
+    const int cols = H_kv * d / 8;
+    p.col_blocks = (cols + kSketchLanes - 1) / kSketchLanes;
+    const long long blocks = (long long)B * per_req * p.col_blocks;
+    if (blocks > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = status_word_address(&p.status);
+    if (st != ATTN_OK) return st;
+    p.k = static_cast<const uint16_t*>(k_cache);
+    p.table = block_table;
+    p.cu = cu_seqlens_q;
+    p.seq_lens = seq_lens;
+    p.sketch = sketch;
+    p.amp = amp;
+    p.B = B;
+    p.max_q_len = max_q_len;
+    p.H_kv = H_kv;
+    p.d = d;
+    p.page_size = page_size;
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    page_sketch_kernel<<<(unsigned)blocks, kSketchThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // extern "C"
