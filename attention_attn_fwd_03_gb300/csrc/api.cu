@@ -303,9 +303,11 @@ attn_status_t select_sizes_ok(int B, int total_q, int H, int H_kv, int d, int pa
     return ATTN_OK;
 }
 
-// Splits of a token's chosen keys: with one unit per (token, KV head) too few
-// to occupy the SMs, the keys are cut into runs of whole 128-key blocks until
-// about three units per SM exist.
+// Workspace of the page-sparse call.  The fused kernel (sparse_fused_ok) needs
+// none; 256 bytes stand for it.  Otherwise the selection kernels and the paged
+// kernel run: with one unit per (token, KV head) too few to occupy the SMs, a
+// token's keys are cut into runs of whole 128-key blocks until about three
+// units per SM exist, with a work list and partials of the runs.
 struct SparsePlan {
     int n_splits, split_blocks;
     size_t tables, lens, cu, list, part_o, part_ml, bytes;  // byte offsets; list: the 256-byte header, then the entries
@@ -315,7 +317,19 @@ constexpr long long kSparseMinBlocks = 2;
 
 SparsePlan sparse_plan(int total_q, int H, int H_kv, int d, int page_size, int max_pages, int budget) {
     SparsePlan pl;
+    std::memset(&pl, 0, sizeof pl);
+    pl.n_splits = 1;
+    if (sparse_fused_ok(d, H / H_kv, max_pages, budget)) {
+        pl.bytes = 256;
+        return pl;
+    }
     const long long rows = (long long)total_q * H_kv;
+    size_t at = select_keys_bytes(total_q, H_kv, max_pages, budget);
+    auto take = [&](size_t n) {
+        const size_t here = at;
+        at += round_up256(n);
+        return here;
+    };
     const long long keys = (long long)(budget < max_pages ? budget : max_pages) * page_size;
     const long long blocks = (keys + 127) / 128;
     const long long want = (kSparseUnits + rows - 1) / rows;
@@ -324,12 +338,6 @@ SparsePlan sparse_plan(int total_q, int H, int H_kv, int d, int page_size, int m
     if (sb > blocks) sb = blocks;
     pl.split_blocks = (int)sb;
     pl.n_splits = (int)((blocks + sb - 1) / sb);
-    size_t at = select_keys_bytes(total_q, H_kv, max_pages, budget);
-    auto take = [&](size_t n) {
-        const size_t here = at;
-        at += round_up256(n);
-        return here;
-    };
     pl.tables = take((size_t)rows * budget * sizeof(int32_t));
     pl.lens = take((size_t)total_q * sizeof(int32_t));
     pl.cu = take(((size_t)total_q + 1) * sizeof(int32_t));
@@ -784,34 +792,52 @@ attn_status_t attn_paged_sparse_fwd(const void* q, const void* k_cache, const vo
     if (st != ATTN_OK) return st;
     if (num_pages < 1 || (long long)num_pages * page_size > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
     const SparsePlan pl = sparse_plan(total_q, H, H_kv, d, page_size, max_pages, budget);
-    const long long units = (long long)total_q * H_kv * pl.n_splits;
-    if (units > 0x3fffffffLL) return ATTN_ERR_INVALID_ARG;
+    if ((long long)total_q * H_kv * pl.n_splits > 0x3fffffffLL) return ATTN_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < pl.bytes || !aligned16(workspace)) return ATTN_ERR_WORKSPACE;
     DeviceState* ds = nullptr;
     st = device_state(&ds);
     if (st != ATTN_OK) return st;
 
-    // the paged kernel with a request per token and a table row per token and KV head
-    char* ws = static_cast<char*>(workspace);
-    PagedParams p;
-    std::memset(&p, 0, sizeof p);
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const long long slots = (long long)num_pages * page_size;
-    const int R = page_size < 128 ? page_size : 128;
     const int G = H / H_kv;
-    if (!make_paged_map(&p.tm_q, q, d, H, total_q, G, 1) || !make_paged_map(&p.tm_k, k_cache, d, H_kv, slots, 1, R) ||
-        !make_paged_map(&p.tm_v, v_cache, d, H_kv, slots, 1, R))
-        return ATTN_ERR_CUDA;
+    const float c_scale = scale * 1.4426950408889634f;
     SelectParams s;
     fill_select(s, ds, q, sketch, amp, block_table, cu_seqlens_q, seq_lens, B, total_q, H, H_kv, page_size, max_pages,
                 num_pages, budget, first, last);
+    s.tables = tables;
+    s.sel_lens = sel_lens;
+    if (sparse_fused_ok(d, G, max_pages, budget)) {
+        SparseParams p;
+        std::memset(&p, 0, sizeof p);
+        const int R = page_size < 16 ? page_size : 16;
+        if (!make_paged_map(&p.tm_k, k_cache, d, H_kv, slots, 1, R) || !make_paged_map(&p.tm_v, v_cache, d, H_kv, slots, 1, R))
+            return ATTN_ERR_CUDA;
+        p.sel = s;
+        p.o = static_cast<uint16_t*>(o);
+        p.lse = lse;
+        p.kv_rows = (int)slots;
+        p.c_scale = c_scale;
+        return from_cuda(launch_sparse(d, p, cs));
+    }
+    char* ws = static_cast<char*>(workspace);
     s.keys = reinterpret_cast<uint32_t*>(ws);
-    s.tables = tables ? tables : reinterpret_cast<int32_t*>(ws + pl.tables);
-    s.sel_lens = sel_lens ? sel_lens : reinterpret_cast<int32_t*>(ws + pl.lens);
+    if (!tables) {
+        s.tables = reinterpret_cast<int32_t*>(ws + pl.tables);
+        s.sel_lens = reinterpret_cast<int32_t*>(ws + pl.lens);
+    }
+
+    // the selection kernels, then the paged kernel with a request per token and a table row per token and KV head
+    PagedParams p;
+    std::memset(&p, 0, sizeof p);
+    const int R = page_size < 128 ? page_size : 128;
+    if (!make_paged_map(&p.tm_q, q, d, H, total_q, G, 1) || !make_paged_map(&p.tm_k, k_cache, d, H_kv, slots, 1, R) ||
+        !make_paged_map(&p.tm_v, v_cache, d, H_kv, slots, 1, R))
+        return ATTN_ERR_CUDA;
     s.cu_out = reinterpret_cast<int32_t*>(ws + pl.cu);
     s.sched = reinterpret_cast<int*>(ws + pl.list);
     s.sched_list = reinterpret_cast<int4*>(ws + pl.list + 256);
     s.n_splits = pl.n_splits;
-    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     st = from_cuda(launch_select(d, s, cs));
     if (st != ATTN_OK) return st;
     p.block_table = s.tables;
@@ -843,12 +869,11 @@ attn_status_t attn_paged_sparse_fwd(const void* q, const void* k_cache, const vo
     p.kv_rows = (int)slots;
     p.n_splits = pl.n_splits;
     p.split_blocks = pl.split_blocks;
-    p.n_units = (int)units;
+    p.n_units = (int)((long long)total_q * H_kv * pl.n_splits);
     p.q_tile_bytes = (uint32_t)(d / 64) * (uint32_t)G * 128u;
-    p.c_scale = scale * 1.4426950408889634f;
-    const int grid = units < ds->sm_count ? (int)units : ds->sm_count;
-    p.n_ctas = grid;
-    return from_cuda(launch_paged(d, p, grid, cs));
+    p.c_scale = c_scale;
+    p.n_ctas = p.n_units < ds->sm_count ? p.n_units : ds->sm_count;
+    return from_cuda(launch_paged(d, p, p.n_ctas, cs));
 }
 
 size_t attn_bwd_workspace_size(int B, int H, int Nq, int d) {

@@ -88,6 +88,13 @@ CASES = [
     ([40, 20], [40, 20], 4, 4, 64, 8, 2, 0, 1),                  # whole prompts: tokens that see one page and more
     ([3000, 2000], None, 128, 1, 128, 32, 20, 0, 1),             # G = 128
     ([2, 5], [4, 5], 2, 1, 64, 8, 1, 0, 1),                      # more tokens than keys: some see none
+    ([900, 60], None, 40, 2, 128, 16, 9, 1, 1),                  # G = 20: three column tiles, the last half empty
+    ([500, 1], None, 32, 1, 64, 8, 33, 1, 1),                    # G = 32
+    ([3000, 20, 1], [2, 1, 1], 12, 1, 128, 8, 50, 2, 1),         # G = 12, two boxes per chunk
+    ([700, 2000], None, 33, 1, 64, 32, 12, 1, 1),                # G = 33: the tiles of 128 rows
+    ([2500, 300], None, 10, 2, 128, 128, 3, 0, 1),               # pages of several chunks
+    ([9000], None, 8, 8, 64, 1024, 4, 1, 1),                     # G = 1, large pages
+    ([9000, 100], None, 4, 2, 64, 8, 1030, 3, 5),                # a budget beyond the fused kernel's list
     ([20000], None, 2, 1, 64, 8, 700, 3, 5),                     # 2500 pages: several selection runs per thread
 ]
 
@@ -134,7 +141,7 @@ def test_many_scored_pages_and_unsplit_units():
 
 
 def test_more_pages_than_a_selection_caches():
-    """20000 pages: the selection reads its scores through L2."""
+    """20000 pages: the selection reads its scores through L2, and the page-sparse call is not fused."""
     lens, page = [160000], 8
     c = _case(5, [800], None, 2, 1, 64, page)
     g = torch.Generator().manual_seed(11)

@@ -213,7 +213,8 @@ def _sparse(**kw):
 @pytest.mark.parametrize("kw,code", SELECTION + [
     (dict(k_cache=None), BAD), (dict(v_cache=FAKE + 8), BAD), (dict(o=None), BAD), (dict(o=FAKE + 4), BAD),
     (dict(lse=FAKE + 2), BAD), (dict(tables=FAKE), BAD), (dict(sel_lens=FAKE), BAD), (dict(scale=0.0), BAD),
-    (dict(scale=float("nan")), BAD), (dict(workspace=None), WS), (dict(workspace_bytes=1000), WS)])
+    (dict(scale=float("nan")), BAD), (dict(workspace=None), WS), (dict(workspace_bytes=255), WS),
+    (dict(H=80, workspace_bytes=4000), WS)])
 def test_sparse_refusals(kw, code):
     assert _sparse(**kw) == code
 
@@ -224,7 +225,11 @@ def test_workspace_sizes():
     assert size(4, 2, 8, 8) == 256  # nothing is scored
     assert size(0, 2, 64, 8) == 0 and size(4, 2, 64, 0) == 0 and size(1 << 16, 1 << 10, 64, 8) == 0
     size = attn.attn_paged_sparse_fwd_workspace_size
-    assert size(4, 8, 2, 128, 64, 64, 8) > attn.attn_page_select_workspace_size(4, 2, 64, 8)
+    assert size(4, 8, 2, 128, 64, 64, 8) == 256  # one kernel, nothing in device memory
+    # groups of more than 32 heads, budgets of more than 1024 pages, tables of more pages than shared memory
+    # holds scores for: scores, selection and work list
+    for H, max_pages, budget in ((80, 64, 8), (8, 2000, 1025), (8, 30000, 8)):
+        assert size(4, H, 2, 128, 64, max_pages, budget) > attn.attn_page_select_workspace_size(4, 2, max_pages, budget)
     assert size(4, 9, 2, 128, 64, 64, 8) == 0 and size(4, 8, 2, 96, 64, 64, 8) == 0 and size(4, 8, 2, 128, 48, 64, 8) == 0
 
 
