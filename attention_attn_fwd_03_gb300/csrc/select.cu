@@ -3,8 +3,7 @@
 //
 // The score kernel is bound by reading 2 d + 4 bytes per page and KV head,
 // 1/64 of a 64-row page's keys: four lanes take a page, up to sixteen 16-byte
-// loads in flight per lane, and the four-byte integer dot products of all G
-// query heads run from registers against codes in shared memory.
+// loads in flight per lane, and go to the matrix units from registers.
 //
 // The selection kernel takes one (token, KV head) per CTA, works from shared
 // memory (or through L2 above kCached pages) and is latency-bound.
@@ -22,14 +21,14 @@ namespace {
 
 constexpr int kScoreWarps = 4;
 constexpr int kSelectThreads = 512;
-constexpr int kCached = 11264;  // scores a selection keeps in shared memory (44 KB: no opt-in size)
+constexpr int kCached = 10240;  // scores a selection keeps in shared memory (40 KB: no opt-in size)
 
 // 8 STEPS pages per warp.
 template <int D, int STEPS>
 __global__ void __launch_bounds__(kScoreWarps * 32) page_score_kernel(const __grid_constant__ SelectParams p) {
     constexpr int PAGES = kScoreWarps * STEPS * 8;
-    extern __shared__ uint4 s_codes[];  // [G][pieces], then |q_h|max [G]
-    float* s_qmax = reinterpret_cast<float*>(s_codes + p.G * kPieces<D>);
+    extern __shared__ uint4 s_codes[];  // [G][pieces], then the heads' scalars [G]
+    float2* s_heads = reinterpret_cast<float2*>(s_codes + p.G * kPieces<D>);
     griddep_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     long long u = blockIdx.x;
@@ -45,11 +44,12 @@ __global__ void __launch_bounds__(kScoreWarps * 32) page_score_kernel(const __gr
     // the sketches are on their way while the codes are made
     const int first = chunk * PAGES + warp * STEPS * 8;
     SketchLoads<D, STEPS> loads;
-    loads.fetch(p, p.table + (long long)k.r * p.max_pages, kvh, first, n_vis, lane, bad);
-    make_codes<D>(p.q + ((long long)t * p.H + kvh * p.G) * D, p.G, s_codes, s_qmax, warp, kScoreWarps, lane);
+    loads.look_up(p.table + (long long)k.r * p.max_pages, first, n_vis, lane);
+    loads.fetch(p, kvh, first, n_vis, lane, bad);
+    make_codes<D>(p.q + ((long long)t * p.H + kvh * p.G) * D, p.G, s_codes, s_heads, warp, kScoreWarps, lane);
     __syncthreads();
     uint32_t key[STEPS];
-    loads.keys(s_codes, s_qmax, p.G, lane, key);
+    loads.template keys<2>(s_codes, s_heads, p.G, lane, key);
     uint32_t* keys = p.keys + ((long long)t * p.H_kv + kvh) * p.max_pages;
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
@@ -62,6 +62,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) page_score_kernel(const __gr
 __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(const __grid_constant__ SelectParams p) {
     extern __shared__ uint32_t s_keys[];  // [kCached] or less
     __shared__ SelectScratch<kSelectThreads> scratch;
+    __shared__ int s_bins[kBins];
     griddep_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31;
     const int kvh = (int)(blockIdx.x % p.H_kv);
@@ -115,26 +116,26 @@ __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(const __gri
         for (int i = tid; i < n; i += kSelectThreads) s_keys[i] = keys[i];
         keys = s_keys;
     }
-    select_best<kSelectThreads>(keys, n, need, scratch,
+    select_best<kSelectThreads>(keys, n, need, s_bins, scratch,
                                 [&](int place, int i) { out[p.first + place] = __ldg(table + p.first + i); });
 }
 
-// Below this many CTAs of 128 pages the score kernel takes 32 pages per CTA.
+// Below this many CTAs of 128 pages the score kernel takes 64 pages per CTA.
 constexpr long long kFewChunks = 608;  // four per SM
 
 template <int D>
 cudaError_t launch_d(SelectParams& p, cudaStream_t stream) {
     const long long rows = (long long)p.total_q * p.H_kv;
-    const int smem = p.G * (2 * D + 4);
+    const int smem = p.G * (2 * D + 8);
     if (p.max_pages > p.budget) {
-        const int wide = kScoreWarps * 32, narrow = kScoreWarps * 8;
+        const int wide = kScoreWarps * 32, narrow = kScoreWarps * 16;
         const long long chunks = (p.max_pages + wide - 1) / wide;
         if (rows * chunks >= kFewChunks) {
             p.n_chunks = (int)chunks;
             page_score_kernel<D, 4><<<(unsigned)(rows * chunks), kScoreWarps * 32, smem, stream>>>(p);
         } else {
             p.n_chunks = (p.max_pages + narrow - 1) / narrow;
-            page_score_kernel<D, 1><<<(unsigned)(rows * p.n_chunks), kScoreWarps * 32, smem, stream>>>(p);
+            page_score_kernel<D, 2><<<(unsigned)(rows * p.n_chunks), kScoreWarps * 32, smem, stream>>>(p);
         }
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;

@@ -7,18 +7,19 @@
 // flight on every SM and little else; for few tokens it is bound by the chain
 // length -> table -> sketches -> selection -> keys, which one launch keeps
 // short.  A cluster of CTAs takes a (token, KV head):
-//   1. its warps score the pages, 32 at a time (select.cuh), and put each
-//      score into the shared memory of every CTA of the cluster;
+//   1. its warps score the pages, 16 at a time (select.cuh), and put each score
+//      into the shared memory of every CTA of the cluster (eight warps per CTA:
+//      the sketches are small and their loads latency-bound);
 //   2. every CTA selects for itself from the whole list (the scores are the
 //      same bits everywhere, so are the choices);
-//   3. the chosen keys are cut into chunks of 16 and dealt to the cluster's
-//      warps.  Each warp is its own pipeline, with no barrier between warps: one
+//   3. the chosen keys are cut into chunks of 16 and dealt to four warps of each
+//      CTA.  Each warp is its own pipeline, with no barrier between warps: one
 //      lane keeps STAGES chunks in flight into the warp's own shared-memory ring
 //      (TMA boxes of up to 16 rows, two boxes where pages hold 8), and the warp
 //      runs the online softmax on the chunk that has landed;
 //   4. the warps' partials (O, m, l) meet in shared memory, across the cluster
 //      through distributed shared memory, in one merge.
-// So a token occupies up to 32 warps without scores, tables or partials in
+// So a token occupies up to eight SMs without scores, tables or partials in
 // device memory, and a CTA is small enough that two share an SM and cover each
 // other's phases.
 //
@@ -49,12 +50,14 @@ namespace cg = cooperative_groups;
 
 constexpr float kTau = 8.0f;  // log2 units
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr int kWarps = 4;
+constexpr int kWarps = 4;       // warps that attend
+constexpr int kAllWarps = 8;    // and all of a CTA's: scores, selection and merge
+constexpr int kThreads = kAllWarps * 32;
 constexpr int kKeys = 16;     // keys per chunk
 constexpr int kMaxCluster = 8;
 constexpr int kMaxG = 32;       // query heads per KV head: four column tiles
 constexpr int kMaxBudget = 1024;  // pages in a CTA's list
-constexpr long long kSparseCtas = 304;  // two per SM
+constexpr long long kSms = 152;
 
 template <int D>
 struct SCfg {
@@ -67,16 +70,18 @@ struct SCfg {
     static constexpr int O_ROW = D + 4;               // floats per head of a warp's partial O: no bank conflicts
     // before the first load the rings hold the query codes and the scores
     static constexpr int OFF_CODES = 0;
-    static constexpr int OFF_QMAX = OFF_CODES + kMaxG * 2 * D;
-    static constexpr int OFF_KEYS = OFF_QMAX + kMaxG * 4;
+    static constexpr int OFF_HEADS = OFF_CODES + kMaxG * 2 * D;
+    static constexpr int OFF_KEYS = OFF_HEADS + kMaxG * 8;
+    static constexpr int AHEAD = D == 128 ? 2 : 4;                   // groups of 16 sketches in a warp's registers
     static constexpr int MAX_PAGES = (kWarps * RING_BYTES - OFF_KEYS) / 4;
     static constexpr int OFF_LIST = kWarps * RING_BYTES;             // the chosen pages [kMaxBudget]
     static constexpr int OFF_ML = OFF_LIST + kMaxBudget * 4;         // (m, l) [kWarps][kMaxG]
     static constexpr int OFF_W = OFF_ML + kWarps * kMaxG * 8;        // merge weights [kMaxG][kMaxCluster * kWarps]
     static constexpr int OFF_BAR = OFF_W + kMaxG * kMaxCluster * kWarps * 4;
     static constexpr int OFF_SCRATCH = OFF_BAR + kWarps * STAGES * 8;
-    static constexpr int OFF_MISC = OFF_SCRATCH + (int)sizeof(SelectScratch<kWarps * 32>);
+    static constexpr int OFF_MISC = OFF_SCRATCH + (int)sizeof(SelectScratch<kThreads>);
     static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;  // + alignment of the ring to 1024
+    static_assert(kBins * 4 <= kMaxG * 2 * D, "the selection's bins take the codes' place");
     static_assert(kMaxG * O_ROW * 4 <= RING_BYTES, "a warp's partial O overlays its ring");
     static_assert(2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs per SM");
 };
@@ -108,7 +113,7 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
 
 // NT column tiles of 8 query heads.
 template <int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32) sparse_kernel(const __grid_constant__ SparseParams p) {
+__global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1) sparse_kernel(const __grid_constant__ SparseParams p) {
     using C = SCfg<D>;
     extern __shared__ uint8_t smem_raw[];
     cg::cluster_group cluster = cg::this_cluster();
@@ -117,12 +122,13 @@ __global__ void __launch_bounds__(kWarps * 32) sparse_kernel(const __grid_consta
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int row = (int)(blockIdx.x / n_ctas);  // (token, KV head)
     const int t = row / sp.H_kv, kvh = row % sp.H_kv;
-    const int W = n_ctas * kWarps, gw = rank * kWarps + warp;  // warps of the cluster, and this one
+    const int W = n_ctas * kWarps, gw = rank * kWarps + warp;  // attending warps of the cluster, and this one
+    const int SW = n_ctas * kAllWarps, gs = rank * kAllWarps + warp;  // the same of all warps
     // the ring starts on 1024 bytes of the shared window, in every CTA alike: a peer's address is this CTA's
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
-    const uint32_t ring = base + warp * C::RING_BYTES;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * C::STAGES;
+    const uint32_t ring = base + (warp % kWarps) * C::RING_BYTES;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + (warp % kWarps) * C::STAGES;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC);
     volatile int* s_skip = abort_flag + 1;  // an earlier launch gave up
     float2* s_ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
@@ -134,7 +140,7 @@ __global__ void __launch_bounds__(kWarps * 32) sparse_kernel(const __grid_consta
             __syncthreads();
     };
 
-    if (lane == 0) {
+    if (lane == 0 && warp < kWarps) {
         for (int s = 0; s < C::STAGES; ++s) bar_init(&bars[s], 1);
         bar_init_fence();
         if (warp == 0) {
@@ -155,71 +161,100 @@ __global__ void __launch_bounds__(kWarps * 32) sparse_kernel(const __grid_consta
     const int32_t* table = sp.table + (long long)tok.r * sp.max_pages;
     const uint16_t* q_group = sp.q + ((long long)t * sp.H + kvh * sp.G) * D;
 
+    // Q^T as the second operand: head lane / 4 of each column tile, dims 16 kk + 2 (lane % 4) and + 8;
+    // loaded ahead of the selection where the registers allow it
+    uint32_t qf[NT][D / 16][2];
+    auto load_q = [&]() {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int h = n * 8 + (lane >> 2);
+            const uint32_t* q = reinterpret_cast<const uint32_t*>(q_group + (long long)(h < sp.G ? h : 0) * D) + (lane & 3);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t a = __ldg(q + kk * 8), b = __ldg(q + kk * 8 + 4);
+                qf[n][kk][0] = h < sp.G ? a : 0u;
+                qf[n][kk][1] = h < sp.G ? b : 0u;
+            }
+        }
+    };
+    if (NT <= 2) load_q();
+
     // ---- 1, 2: the page list (every CTA of the cluster takes the same branches: they depend on the token alone)
     if (n_vis <= sp.budget) {
-        for (int i = tid; i < n_vis; i += kWarps * 32) s_list[i] = __ldg(table + i);
+        for (int i = tid; i < n_vis; i += kThreads) s_list[i] = __ldg(table + i);
     } else {
         const int need = sp.budget - sp.first - sp.last;
         const int n = n_vis - sp.first - sp.last;
-        for (int i = tid; i < sp.first; i += kWarps * 32) s_list[i] = __ldg(table + i);
-        for (int i = tid; i < sp.last; i += kWarps * 32)
+        for (int i = tid; i < sp.first; i += kThreads) s_list[i] = __ldg(table + i);
+        for (int i = tid; i < sp.last; i += kThreads)
             s_list[sp.budget - sp.last + i] = __ldg(table + n_vis - sp.last + i);
         if (need > 0) {
             uint4* s_codes = reinterpret_cast<uint4*>(smem + C::OFF_CODES);
-            float* s_qmax = reinterpret_cast<float*>(smem + C::OFF_QMAX);
+            float2* s_heads = reinterpret_cast<float2*>(smem + C::OFF_HEADS);
             uint32_t* s_keys = reinterpret_cast<uint32_t*>(smem + C::OFF_KEYS);
-            SketchLoads<D, 4> loads;
-            int c0 = gw * 32;  // candidate c is page first + c
-            if (c0 < n) loads.fetch(sp, table + sp.first, kvh, c0, n, lane, bad);
-            make_codes<D>(q_group, sp.G, s_codes, s_qmax, warp, kWarps, lane);
-            sync_all();  // the codes are there, and every CTA of the cluster runs
-            while (c0 < n) {
-                uint32_t key[4];
-                loads.keys(s_codes, s_qmax, sp.G, lane, key);
-                const int round = lane & 3, c = c0 + round * 8 + (lane >> 2);
-                const uint32_t mine = round == 0 ? key[0] : round == 1 ? key[1] : round == 2 ? key[2] : key[3];
-                c0 += W * 32;
-                if (c0 < n) loads.fetch(sp, table + sp.first, kvh, c0, n, lane, bad);
-                if (c < n) {
-                    if (n_ctas > 1)
-                        for (int r = 0; r < n_ctas; ++r) *cluster.map_shared_rank(s_keys + c, r) = mine;
-                    else
-                        s_keys[c] = mine;
-                }
+            // a warp's candidates come in groups of 16, the sketches of kAhead groups on their way to registers
+            const int32_t* from = table + sp.first;  // candidate c is page first + c
+            const int groups = (n + 15) / 16;
+            // the warp's page ids first, all at once, to where their scores will be
+            for (int g = gs + (lane >> 4) * SW; g < groups; g += 2 * SW) {
+                const int c = g * 16 + (lane & 15);
+                if (c < n) s_keys[c] = (uint32_t)__ldg(from + c);
             }
+            __syncwarp();
+            constexpr int kAhead = C::AHEAD;
+            SketchLoads<D, 2> loads[kAhead];
+            auto fetch = [&](SketchLoads<D, 2>& to, int g) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const int c = g * 16 + s * 8 + (lane >> 2);
+                    to.id[s] = c < n ? (int)s_keys[c] : -1;
+                }
+                to.fetch(sp, kvh, g * 16, n, lane, bad);
+            };
+#pragma unroll
+            for (int x = 0; x < kAhead; ++x)
+                if (gs + x * SW < groups) fetch(loads[x], gs + x * SW);
+            make_codes<D>(q_group, sp.G, s_codes, s_heads, warp, kAllWarps, lane);
+            sync_all();  // the codes are there, and every CTA of the cluster runs
+            for (int g0 = gs; g0 < groups; g0 += kAhead * SW)
+#pragma unroll
+                for (int x = 0; x < kAhead; ++x) {
+                    const int g = g0 + x * SW;
+                    if (g >= groups) break;
+                    uint32_t key[2];
+                    loads[x].template keys<NT>(s_codes, s_heads, sp.G, lane, key);
+                    if (g + kAhead * SW < groups) fetch(loads[x], g + kAhead * SW);
+                    const int s = lane & 1, c = g * 16 + s * 8 + (lane >> 2);
+                    if ((lane & 2) == 0 && c < n) {
+                        const uint32_t mine = s ? key[1] : key[0];
+                        if (n_ctas > 1)
+                            for (int r = 0; r < n_ctas; ++r) *cluster.map_shared_rank(s_keys + c, r) = mine;
+                        else
+                            s_keys[c] = mine;
+                    }
+                }
             sync_all();
-            select_best<kWarps * 32>(s_keys, n, need, *reinterpret_cast<SelectScratch<kWarps * 32>*>(smem + C::OFF_SCRATCH),
+            select_best<kThreads>(s_keys, n, need, reinterpret_cast<int*>(smem + C::OFF_CODES),
+                                     *reinterpret_cast<SelectScratch<kThreads>*>(smem + C::OFF_SCRATCH),
                                      [&](int place, int i) { s_list[sp.first + place] = __ldg(table + sp.first + i); });
         }
     }
     if (bad) atomicOr(sp.status, 1u << kStatusDeviceData);
 
-    // Q^T as the second operand: head lane / 4 of each column tile, dims 16 kk + 2 (lane % 4) and + 8
-    uint32_t qf[NT][D / 16][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int h = n * 8 + (lane >> 2);
-        const uint32_t* q = reinterpret_cast<const uint32_t*>(q_group + (long long)(h < sp.G ? h : 0) * D) + (lane & 3);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t a = __ldg(q + kk * 8), b = __ldg(q + kk * 8 + 4);
-            qf[n][kk][0] = h < sp.G ? a : 0u;
-            qf[n][kk][1] = h < sp.G ? b : 0u;
-        }
-    }
+    if (NT > 2) load_q();
     fence_async_smem();  // what the rings held gives way to TMA writes
     __syncthreads();
     const bool skip = *s_skip != 0;
     const int n_keys = skip ? 0 : sel_len;
     if (sp.tables != nullptr && rank == 0) {
         int32_t* out = sp.tables + (long long)row * sp.budget;
-        for (int i = tid; i < sp.budget; i += kWarps * 32) out[i] = i < n_sel ? s_list[i] : -1;
+        for (int i = tid; i < sp.budget; i += kThreads) out[i] = i < n_sel ? s_list[i] : -1;
         if (tid == 0 && kvh == 0) sp.sel_lens[t] = sel_len;
     }
 
     // ---- 3: this warp's chunks: gw, gw + W, gw + 2 W, ..
     const int chunks = (n_keys + kKeys - 1) / kKeys;
-    const int mine = chunks > gw ? (chunks - gw + W - 1) / W : 0;
+    const int mine = warp < kWarps && chunks > gw ? (chunks - gw + W - 1) / W : 0;
     const int boxes = ps < kKeys ? kKeys / ps : 1;  // boxes per panel of a chunk
 
     // cache row of box x of the warp's chunk i: a box past the last page, or of a page that does not exist,
@@ -353,7 +388,7 @@ __global__ void __launch_bounds__(kWarps * 32) sparse_kernel(const __grid_consta
     __syncwarp();
 
     // ---- 4: this warp's partial: O over its ring, (m, l) beside
-    float* po = reinterpret_cast<float*>(smem + warp * C::RING_BYTES);
+    float* po = reinterpret_cast<float*>(smem + (warp % kWarps) * C::RING_BYTES);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -363,8 +398,8 @@ __global__ void __launch_bounds__(kWarps * 32) sparse_kernel(const __grid_consta
             sum += __shfl_xor_sync(0xffffffffu, sum, 8);
             sum += __shfl_xor_sync(0xffffffffu, sum, 16);
             const int h = n * 8 + (lane & 3) * 2 + e;
-            if (lane < 4) s_ml[warp * kMaxG + h] = make_float2(m[n][e], sum);
-            if (h < sp.G) {
+            if (warp < kWarps && lane < 4) s_ml[warp * kMaxG + h] = make_float2(m[n][e], sum);
+            if (warp < kWarps && h < sp.G) {
                 float* to = po + h * C::O_ROW + (lane >> 2);
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x) {
@@ -384,7 +419,7 @@ __global__ void __launch_bounds__(kWarps * 32) sparse_kernel(const __grid_consta
     float* s_w = reinterpret_cast<float*>(smem + C::OFF_W);
     const bool write = !skip && tok.owned && e0 < e1;
     if (write) {
-        for (int h = e0 / PIECES + warp; h <= (e1 - 1) / PIECES; h += kWarps) {
+        for (int h = e0 / PIECES + warp; h <= (e1 - 1) / PIECES; h += kAllWarps) {
             float mj = -INFINITY, lj = 0.f;
             if (lane < W) {
                 const float2* src = s_ml + (lane % kWarps) * kMaxG + h;
@@ -408,8 +443,8 @@ __global__ void __launch_bounds__(kWarps * 32) sparse_kernel(const __grid_consta
     __syncthreads();
     if (write) {
         int ways = 1;
-        while (ways * 2 <= W && (e1 - e0) * ways * 2 <= kWarps * 32) ways *= 2;
-        const int per = kWarps * 32 / ways;  // pieces at a time
+        while (ways * 2 <= W && (e1 - e0) * ways * 2 <= kThreads) ways *= 2;
+        const int per = kThreads / ways;  // pieces at a time
         for (int e = e0 + tid / ways; e < e1 + per; e += per) {  // whole warps, for the shuffles
             if (e - tid / ways >= e1) break;
             const bool in = e < e1;
@@ -452,7 +487,7 @@ cudaError_t launch_t(const SparseParams& p, int cluster, cudaStream_t stream) {
     attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((long long)p.sel.total_q * p.sel.H_kv * cluster));
-    cfg.blockDim = dim3(kWarps * 32);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = C::SMEM_BYTES;
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -478,14 +513,16 @@ bool sparse_fused_ok(int d, int G, int max_pages, int budget) {
 }
 
 cudaError_t launch_sparse(int d, const SparseParams& p, cudaStream_t stream) {
-    // CTAs per (token, KV head): as many as let the whole launch reside on the GPU at once, two CTAs to
-    // an SM, and no more than there is work for (two chunks per warp)
+    // CTAs per (token, KV head): as many as let the whole launch reside on the GPU at once (two CTAs to
+    // an SM, one where a group takes more registers), and no more than there is work for (two chunks
+    // per warp)
     const SelectParams& s = p.sel;
     const long long rows = (long long)s.total_q * s.H_kv;
     const long long keys = (long long)(s.budget < s.max_pages ? s.budget : s.max_pages) << s.page_shift;
     const long long chunks = (keys + kKeys - 1) / kKeys;
+    const long long resident = kSms * ((s.G + 7) / 8 * d <= 128 ? 2 : 1);
     int cluster = 1;
-    while (cluster < kMaxCluster && rows * cluster * 2 <= kSparseCtas && chunks >= (long long)cluster * 4 * kWarps)
+    while (cluster < kMaxCluster && rows * cluster * 2 <= resident && chunks >= (long long)cluster * 4 * kWarps)
         cluster *= 2;
     if (d == 128) return launch_d<128>(p, cluster, stream);
     if (d == 64) return launch_d<64>(p, cluster, stream);

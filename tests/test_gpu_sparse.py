@@ -171,6 +171,25 @@ def test_ties_go_to_the_earlier_page():
     assert torch.equal(tables[0, 0].cpu(), torch.cat([c["table"][0, :6], c["table"][0, 79:80]]))
 
 
+@pytest.mark.parametrize("d,H", [(128, 1), (64, 20)])
+def test_scores_at_the_ends_of_their_range(d, H):
+    """Codes of +-127 throughout: the integer sums reach 2 d 127^2, and pages that differ by one unit in
+    one channel differ in their scores."""
+    c = _case(2, [320], None, H, 1, d, 8)
+    c["q"][:] = torch.where(torch.arange(d) % 3 == 0, -1.0, 1.0)
+    full = np.where(np.arange(d) % 3 == 0, -127, 127).astype(np.int8)
+    ids = c["table"][0, :40].numpy()
+    for p in range(40):
+        c["sk"][ids[p], 0] = np.concatenate([full, full])
+        c["sk"][ids[p], 0, (p * 7) % (2 * d)] //= 1 + p % 4
+        c["sk"][ids[p], 0, 1] = 127 - (p * 11) % 17
+    c["amp"][:] = 1.0
+    for budget in (2, 9, 30):
+        tables, sel = _select(c, _gpu(c), budget, 0, 1)
+        want, want_sel = _want(c, budget, 0, 1)
+        assert np.array_equal(tables.cpu().numpy(), want) and np.array_equal(sel.cpu().numpy(), want_sel)
+
+
 def test_non_finite_queries_and_sketches():
     c = _case(8, [400, 400, 400, 400], None, 4, 1, 64, 8)
     c["q"][1, 2, 5] = float("inf")
