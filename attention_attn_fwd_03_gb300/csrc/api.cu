@@ -480,6 +480,17 @@ attn_status_t host_stage_state(HostStage** out) {
 
 }  // namespace
 
+cudaError_t opt_in_smem(const void* kernel, int bytes, std::atomic<unsigned long long>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (done.load(std::memory_order_acquire) >> dev & 1) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(1ull << dev, std::memory_order_release);
+    return e;
+}
+
 // Device address of the calling device's status word (set-up on first use).
 attn_status_t status_word_address(unsigned** out) {
     DeviceState* ds = nullptr;
@@ -753,9 +764,8 @@ attn_status_t attn_page_select(const void* q, const int8_t* sketch, const float*
     attn_status_t st = select_sizes_ok(B, total_q, H, H_kv, d, page_size, max_pages, budget, first, last);
     if (st != ATTN_OK) return st;
     if (num_pages < 1 || (long long)num_pages * page_size > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
-    if (!workspace || !aligned16(workspace) ||
-        workspace_bytes < select_keys_bytes(total_q, H_kv, max_pages, budget))
-        return ATTN_ERR_WORKSPACE;
+    const size_t need = select_keys_bytes(total_q, H_kv, max_pages, budget);
+    if (max_pages > budget && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return ATTN_ERR_WORKSPACE;
     DeviceState* ds = nullptr;
     st = device_state(&ds);
     if (st != ATTN_OK) return st;
@@ -793,7 +803,8 @@ attn_status_t attn_paged_sparse_fwd(const void* q, const void* k_cache, const vo
     if (num_pages < 1 || (long long)num_pages * page_size > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
     const SparsePlan pl = sparse_plan(total_q, H, H_kv, d, page_size, max_pages, budget);
     if ((long long)total_q * H_kv * pl.n_splits > 0x3fffffffLL) return ATTN_ERR_INVALID_ARG;
-    if (!workspace || workspace_bytes < pl.bytes || !aligned16(workspace)) return ATTN_ERR_WORKSPACE;
+    const bool fused = sparse_fused_ok(d, H / H_kv, max_pages, budget);
+    if (!fused && (!workspace || workspace_bytes < pl.bytes || !aligned16(workspace))) return ATTN_ERR_WORKSPACE;
     DeviceState* ds = nullptr;
     st = device_state(&ds);
     if (st != ATTN_OK) return st;
@@ -807,7 +818,7 @@ attn_status_t attn_paged_sparse_fwd(const void* q, const void* k_cache, const vo
                 num_pages, budget, first, last);
     s.tables = tables;
     s.sel_lens = sel_lens;
-    if (sparse_fused_ok(d, G, max_pages, budget)) {
+    if (fused) {
         SparseParams p;
         std::memset(&p, 0, sizeof p);
         const int R = page_size < 16 ? page_size : 16;

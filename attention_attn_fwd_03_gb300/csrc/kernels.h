@@ -4,6 +4,7 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 
 namespace attn {
@@ -229,6 +230,10 @@ cudaError_t launch_bwd(int d, const BwdParams& p, int sm_count, cudaStream_t str
 #include "attn.h"
 
 namespace attn {
+
+// cudaFuncAttributeMaxDynamicSharedMemorySize of a kernel, set once per device
+// (`done` is the kernel's own bit mask of devices, zero at first).
+cudaError_t opt_in_smem(const void* kernel, int bytes, std::atomic<unsigned long long>& done);
 
 // Device address of the calling device's status word (api.cu).
 attn_status_t status_word_address(unsigned** out);

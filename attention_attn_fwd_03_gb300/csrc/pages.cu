@@ -381,8 +381,9 @@ attn_status_t attn_paged_plan(const int32_t* ctx_lens, const int32_t* new_lens, 
     p.num_pages = num_pages;
     p.n_free = n_free;
     const int smem = (3 * B + 1) * (int)sizeof(int);
-    if (cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (3 * kPlanMaxB + 1) * (int)sizeof(int)) != cudaSuccess)
+    static std::atomic<unsigned long long> opted{0};
+    if (opt_in_smem(reinterpret_cast<const void*>(paged_plan_kernel), (3 * kPlanMaxB + 1) * (int)sizeof(int), opted) !=
+        cudaSuccess)
         return ATTN_ERR_CUDA;
     int ctas = (total_q + kPlanThreads - 1) / kPlanThreads;
     ctas = ctas >= kPlanMaxCluster ? kPlanMaxCluster : ctas > 2 ? 4 : ctas;

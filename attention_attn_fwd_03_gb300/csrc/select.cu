@@ -157,8 +157,9 @@ cudaError_t launch_d(SelectParams& p, cudaStream_t stream) {
 }  // namespace
 
 size_t select_keys_bytes(int total_q, int H_kv, int max_pages, int budget) {
-    if (max_pages <= budget) return 256;
-    return ((size_t)total_q * H_kv * max_pages * sizeof(uint32_t) + 255) / 256 * 256;
+    if (max_pages <= budget) return 256;  // none needed
+    const size_t n = ((size_t)total_q * H_kv * max_pages * sizeof(uint32_t) + 255) / 256 * 256;
+    return n < 512 ? 512 : n;
 }
 
 cudaError_t launch_select(int d, SelectParams p, cudaStream_t stream) {

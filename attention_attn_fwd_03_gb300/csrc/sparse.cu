@@ -478,7 +478,8 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1) sparse_kernel
 template <int D, int NT>
 cudaError_t launch_t(const SparseParams& p, int cluster, cudaStream_t stream) {
     using C = SCfg<D>;
-    cudaError_t e = cudaFuncSetAttribute(sparse_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    static std::atomic<unsigned long long> opted{0};
+    const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(sparse_kernel<D, NT>), C::SMEM_BYTES, opted);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;

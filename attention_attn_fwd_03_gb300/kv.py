@@ -97,6 +97,12 @@ def attn_paged_sparse_fwd(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_le
 
 # ---------------------------------------------------------------- torch helpers
 
+# The helpers below run once per call of a decode step, whose kernels take a few microseconds: they
+# look up each attribute once and take the slow path only to say what is wrong.
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _device(t, name):
     """Index of the current CUDA device, which t has to be on."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -108,6 +114,12 @@ def _device(t, name):
 
 
 def _check(t, name, dtype, dev, shape, dense=True):
+    """Address of t, a tensor of this dtype, device and shape."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.shape == shape and (not dense or t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
     if t.dtype is not dtype:
@@ -116,22 +128,23 @@ def _check(t, name, dtype, dev, shape, dense=True):
         raise ValueError("%s is on cuda:%d, the call runs on cuda:%d" % (name, t.get_device(), dev))
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if dense and not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr()
+    raise ValueError("%s must be contiguous" % name)
 
 
 def _handle(stream, dev):
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return _raw_stream(dev)
     if stream.device.index != dev:
         raise ValueError("stream is on %s, the tensors are on cuda:%d" % (stream.device, dev))
     return stream.cuda_stream
 
 
+_no_context = contextlib.nullcontext()
+
+
 def _on(stream):
     """Allocations inside belong to the call's stream."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _no_context if stream is None else torch.cuda.stream(stream)
 
 
 def _freqs(inv_freq, dev):
@@ -210,7 +223,7 @@ def rope(q, k=None, *, inv_freq, positions=None, interleaved=False, inverse=Fals
             pp, pb = _check(positions, "positions", torch.int32, dev, (B, N)), N
         else:
             pp = _check(positions, "positions", torch.int32, dev, (N,))
-    st = attn_rope(qp, qop, kp, kop, pp, pb, fp, bits, dt.itemsize, B, H, H_k, N, d, rot,
+    st = lib().attn_rope(qp, qop, kp, kop, pp, pb, fp, bits, dt.itemsize, B, H, H_k, N, d, rot,
                    (ctypes.c_longlong * 12)(*qs, *qos, *ks, *kos), int(bool(interleaved)),
                    int(bool(inverse)), float(amplitude), _handle(stream, dev))
     _raise(st, "attn_rope")
@@ -233,18 +246,15 @@ def paged_plan(ctx_lens, block_table, free_pages, free_count, page_size, num_pag
     if total_q < 1:
         raise ValueError("total_q must be at least 1")
     B, max_pages = ctx_lens.shape[0], block_table.shape[1]
-    given = (cu_seqlens_q, seq_lens, positions, slots, free_left)
     sizes = (B + 1, B, total_q, total_q, 1)
-    if all(t is None for t in given):  # one allocation
-        with _on(stream):
-            given = torch.empty(sum(sizes), dtype=i32, device=ctx_lens.device).split(sizes)
-    else:
-        with _on(stream):
-            given = [torch.empty(n, dtype=i32, device=ctx_lens.device) if t is None else t
-                     for t, n in zip(given, sizes)]
+    given = [cu_seqlens_q, seq_lens, positions, slots, free_left]
+    with _on(stream):
+        for i in range(5):
+            if given[i] is None:
+                given[i] = torch.empty(sizes[i], dtype=i32, device=ctx_lens.device)
     names = ("cu_seqlens_q", "seq_lens", "positions", "slots", "free_left")
     outs = [_check(t, name, i32, dev, (n,)) for t, name, n in zip(given, names, sizes)]
-    st = attn_paged_plan(_check(ctx_lens, "ctx_lens", i32, dev, (B,)),
+    st = lib().attn_paged_plan(_check(ctx_lens, "ctx_lens", i32, dev, (B,)),
                          None if new_lens is None else _check(new_lens, "new_lens", i32, dev, (B,)),
                          _check(block_table, "block_table", i32, dev, (B, max_pages)),
                          _check(free_pages, "free_pages", i32, dev, (free_pages.shape[0],)),
@@ -291,7 +301,7 @@ def paged_append(q, k, v, k_cache, v_cache, slots, positions=None, inv_freq=None
     if inv_freq is not None:
         fp, bits, rot = _freqs(inv_freq, dev)
         pp = _check(positions, "positions", torch.int32, dev, (T,))
-    st = attn_paged_append(qp, qop, kp, vp, _check(k_cache, "k_cache", bf, dev, cache),
+    st = lib().attn_paged_append(qp, qop, kp, vp, _check(k_cache, "k_cache", bf, dev, cache),
                            _check(v_cache, "v_cache", bf, dev, cache), _check(slots, "slots", torch.int32, dev, (T,)),
                            pp, fp, bits, T, H, H_kv, d, rot, page_size, num_pages,
                            (ctypes.c_longlong * 8)(*qs, *qos, *ks, *vs), int(bool(interleaved)),
@@ -311,7 +321,7 @@ def page_sketch(k_cache, block_table, seq_lens, sketch, amp, cu_seqlens_q=None, 
     num_pages, page_size, H_kv, d = k_cache.shape
     B, max_pages = block_table.shape
     i32 = torch.int32
-    st = attn_page_sketch(_check(k_cache, "k_cache", torch.bfloat16, dev, k_cache.shape),
+    st = lib().attn_page_sketch(_check(k_cache, "k_cache", torch.bfloat16, dev, k_cache.shape),
                           _check(block_table, "block_table", i32, dev, (B, max_pages)),
                           None if cu_seqlens_q is None else _check(cu_seqlens_q, "cu_seqlens_q", i32, dev, (B + 1,)),
                           _check(seq_lens, "seq_lens", i32, dev, (B,)), B, int(max_q_len), H_kv, d, page_size,
@@ -339,12 +349,15 @@ def _selection_args(q, sketch, amp, block_table, seq_lens, cu_seqlens_q, dev):
 
 
 def _workspace(workspace, need, dev, stream, device, what):
+    """(address, bytes, tensor) of a workspace of `need` bytes; none is made where 256 say that it is not used."""
     if need == 0:
         raise AttnError(ATTN_ERR_UNSUPPORTED, what)
     if workspace is None:
+        if need <= 256:
+            return None, 0, None
         with _on(stream):
             workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    return _check(workspace, "workspace", torch.uint8, dev, (workspace.numel(),)), workspace
+    return _check(workspace, "workspace", torch.uint8, dev, (workspace.numel(),)), workspace.numel(), workspace
 
 
 def page_select(q, sketch, amp, block_table, seq_lens, page_size, budget, first=1, last=1, cu_seqlens_q=None,
@@ -366,10 +379,10 @@ def page_select(q, sketch, amp, block_table, seq_lens, page_size, budget, first=
             sel_lens = torch.empty((T,), dtype=torch.int32, device=q.device)
     tp = _check(tables, "tables", torch.int32, dev, (T, H_kv, budget))
     lp = _check(sel_lens, "sel_lens", torch.int32, dev, (T,))
-    wp, workspace = _workspace(workspace, attn_page_select_workspace_size(T, H_kv, max_pages, budget), dev, stream,
-                               q.device, "attn_page_select_workspace_size")
-    st = attn_page_select(*ptrs, B, T, H, H_kv, d, int(page_size), max_pages, num_pages, budget, int(first), int(last),
-                          tp, lp, wp, workspace.numel(), _handle(stream, dev))
+    need = lib().attn_page_select_workspace_size(T, H_kv, max_pages, budget)
+    wp, wn, workspace = _workspace(workspace, need, dev, stream, q.device, "attn_page_select_workspace_size")
+    st = lib().attn_page_select(*ptrs, B, T, H, H_kv, d, int(page_size), max_pages, num_pages, budget, int(first), int(last),
+                          tp, lp, wp, wn, _handle(stream, dev))
     _raise(st, "attn_page_select")
     return tables, sel_lens
 
@@ -402,13 +415,12 @@ def paged_sparse_fwd(q, k_cache, v_cache, block_table, seq_lens, sketch, amp, bu
             sel_lens = torch.empty((T,), dtype=torch.int32, device=q.device)
     op = _check(out, "out", bf, dev, (T, H, d))
     lp = None if lse is None else _check(lse, "lse", torch.float32, dev, (T, H))
-    need = attn_paged_sparse_fwd_workspace_size(T, H, H_kv, d, page_size, max_pages, budget)
-    wp, workspace = _workspace(workspace, need, dev, stream, q.device, "attn_paged_sparse_fwd_workspace_size")
+    need = lib().attn_paged_sparse_fwd_workspace_size(T, H, H_kv, d, page_size, max_pages, budget)
+    wp, wn, workspace = _workspace(workspace, need, dev, stream, q.device, "attn_paged_sparse_fwd_workspace_size")
     qp, sp, ap, bp, cp, np_ = ptrs
-    st = attn_paged_sparse_fwd(qp, kp, vp, bp, cp, np_, sp, ap, B, T, H, H_kv, d, page_size, max_pages, num_pages,
+    st = lib().attn_paged_sparse_fwd(qp, kp, vp, bp, cp, np_, sp, ap, B, T, H, H_kv, d, page_size, max_pages, num_pages,
                                budget, int(first), int(last), float(scale) if scale is not None else 1.0 / math.sqrt(d),
                                op, lp, None if tables is None else tables.data_ptr(),
-                               None if sel_lens is None else sel_lens.data_ptr(), wp, workspace.numel(),
-                               _handle(stream, dev))
+                               None if sel_lens is None else sel_lens.data_ptr(), wp, wn, _handle(stream, dev))
     _raise(st, "attn_paged_sparse_fwd")
     return (out, lse, tables, sel_lens) if return_tables else (out, lse)

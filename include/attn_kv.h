@@ -171,7 +171,9 @@ attn_status_t attn_page_sketch(const void* k_cache, const int32_t* block_table, 
  *   behind the last request, and tokens that see no key, get 0 and -1.
  *   H / H_kv <= 128; budget >= 1; first >= 0, last >= 1, first + last <=
  *   budget; total_q * H_kv * max(max_pages, budget) < 2^31.
- *   workspace: attn_page_select_workspace_size bytes, 16-byte aligned. */
+ *   workspace: attn_page_select_workspace_size bytes, 16-byte aligned, no
+ *   initialisation; where that is 256 (budget >= max_pages) none is used and
+ *   NULL will do. */
 size_t attn_page_select_workspace_size(int total_q, int H_kv, int max_pages, int budget);
 attn_status_t attn_page_select(const void* q, const int8_t* sketch, const float* amp, const int32_t* block_table,
                                const int32_t* cu_seqlens_q, const int32_t* seq_lens, int B, int total_q, int H,
@@ -191,8 +193,12 @@ attn_status_t attn_page_select(const void* q, const int8_t* sketch, const float*
  * Each token gathers its own pages: meant for decode steps and the few tokens
  * per request of a drafted continuation; a long prompt is better served by
  * attn_paged_fwd, whose tiles share the keys among 128 rows.
+ * Groups of up to 32 heads with a budget of up to 1024 pages and tables of up
+ * to 15000 (d = 64) or 22000 pages run as one kernel that keeps everything on
+ * chip; the others as a selection and the kernel of attn_paged_fwd.
  *   workspace: attn_paged_sparse_fwd_workspace_size bytes, 16-byte aligned,
- *   no initialisation; calls that may overlap need distinct workspaces. */
+ *   no initialisation; calls that may overlap need distinct workspaces.  Where
+ *   the size is 256 (one kernel) none is used and NULL will do. */
 size_t attn_paged_sparse_fwd_workspace_size(int total_q, int H, int H_kv, int d, int page_size, int max_pages,
                                             int budget);
 attn_status_t attn_paged_sparse_fwd(const void* q, const void* k_cache, const void* v_cache,

@@ -312,10 +312,11 @@ def test_helpers_refuse():
                dict(seq_lens=g["lens"].repeat(2))):
         with pytest.raises(ValueError):
             attn.paged_sparse_fwd(**dict(args, **kw))
-    for kw in (dict(budget=0), dict(budget=4, first=4), dict(last=0), dict(scale=-1.0),
-               dict(workspace=torch.zeros(16, dtype=torch.uint8, device=DEV))):
+    for kw in (dict(budget=0), dict(budget=4, first=4), dict(last=0), dict(scale=-1.0)):
         with pytest.raises(attn.AttnError):
             attn.paged_sparse_fwd(**dict(args, **kw))
+    with pytest.raises(attn.AttnError):  # scores do not fit
+        _select(c, g, 4, 1, 1, workspace=torch.zeros(16, dtype=torch.uint8, device=DEV))
 
 
 def test_serving_steps():

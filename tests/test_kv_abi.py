@@ -213,8 +213,8 @@ def _sparse(**kw):
 @pytest.mark.parametrize("kw,code", SELECTION + [
     (dict(k_cache=None), BAD), (dict(v_cache=FAKE + 8), BAD), (dict(o=None), BAD), (dict(o=FAKE + 4), BAD),
     (dict(lse=FAKE + 2), BAD), (dict(tables=FAKE), BAD), (dict(sel_lens=FAKE), BAD), (dict(scale=0.0), BAD),
-    (dict(scale=float("nan")), BAD), (dict(workspace=None), WS), (dict(workspace_bytes=255), WS),
-    (dict(H=80, workspace_bytes=4000), WS)])
+    (dict(scale=float("nan")), BAD), (dict(H=80, workspace=None), WS), (dict(H=80, workspace_bytes=4000), WS),
+    (dict(H=80, workspace=FAKE + 8), WS)])
 def test_sparse_refusals(kw, code):
     assert _sparse(**kw) == code
 
