@@ -22,18 +22,20 @@ namespace cg = cooperative_groups;
 // everything: token t belongs to the last request r with cu[r] <= t, and the
 // i-th new page of request r is the (before[r] + i)-th taken from the stack.
 //
-// One cluster does the call.  Every CTA computes both sums for itself into
-// shared memory (a few words per request, read through L2), then the tokens
-// are dealt to the cluster's threads, each finding its request by bisection in
-// shared memory.  The barrier between the two lets outputs replace inputs:
-// every CTA has read the lengths and the free count before CTA 0 writes
-// seq_lens and free_left.  A token that starts a page enters it in the table,
-// so table writes are as balanced as the tokens.  Latency-bound: the largest
-// calls write 8 bytes per token, the smallest a few hundred bytes.
+// Every CTA computes both sums for itself into shared memory (a few words per
+// request, read through L2), then the tokens are dealt to all threads, each
+// finding its request by bisection in shared memory.  A token that starts a
+// page enters it in the table, so table writes are as balanced as the tokens.
+// A call whose outputs replace inputs runs in one cluster: its barrier lets
+// every CTA read the lengths and the free count before CTA 0 writes seq_lens
+// and free_left; any other call uses as many CTAs as it has tokens for.
+// Latency-bound: the largest calls write 8 bytes per token, the smallest a few
+// hundred bytes.
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanMaxB = 16384;
 constexpr int kPlanMaxCluster = 8;
+constexpr int kPlanMaxCtas = 152;
 
 struct PlanParams {
     const int32_t* ctx;
@@ -44,6 +46,7 @@ struct PlanParams {
     int32_t *cu, *seq_lens, *positions, *slots, *free_left;
     unsigned* status;
     int B, total_q, page_size, max_pages, num_pages, n_free;
+    int in_place;  // an output replaces an input: the grid is one cluster
 };
 
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_constant__ PlanParams p) {
@@ -54,9 +57,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
     __shared__ long long s_tok[32], s_pg[32];
     __shared__ int s_count;
     __shared__ long long s_demand;
-    cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rank = (int)cluster.block_rank(), n_ctas = (int)cluster.num_blocks();
+    const int rank = (int)blockIdx.x, n_ctas = (int)gridDim.x;
     const int ps = p.page_size;
     const long long cap = (long long)p.max_pages * ps;
     bool bad = false;
@@ -136,8 +138,10 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
             bad |= tok > p.total_q;
         }
     }
-    // all inputs that an output may replace have been read, by every CTA
-    cluster.sync();
+    if (p.in_place)  // all inputs that an output may replace have been read, by every CTA
+        cg::this_cluster().sync();
+    else
+        __syncthreads();
     const int count = s_count;
     const int owned = s_cu[p.B];
     if (rank == 0) {
@@ -145,7 +149,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
         for (int r = tid; r <= p.B; r += kPlanThreads) p.cu[r] = s_cu[r];
         if (tid == 0) *p.free_left = s_demand < count ? count - (int)s_demand : 0;
     }
-    for (long long t64 = rank * kPlanThreads + tid; t64 < p.total_q; t64 += n_ctas * kPlanThreads) {
+    for (long long t64 = (long long)rank * kPlanThreads + tid; t64 < p.total_q; t64 += (long long)n_ctas * kPlanThreads) {
         const int t = (int)t64;
         int pos = 0, slot = -1;
         if (t < owned) {
@@ -190,13 +194,18 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
 // (divide, multiply) and one to an integer, so a page's sketch is a function
 // of its keys alone.
 //
-// Bound by reading the keys once.  A CTA takes one page (up to 1024 channels
-// of it): a thread owns 8 channels and every RG-th row, so that a row of the
-// page is read whole, 16 bytes per thread with eight rows in flight; row
-// groups combine through shared memory.
+// Bound by reading the keys once.  A CTA takes one page, or a block of its
+// channels: a thread owns 8 channels and every RG-th row, 16 bytes per load;
+// row groups combine through shared memory.  With many pages a CTA takes up to
+// LANES = 128 pieces of a row (1024 channels), so that the page is read in
+// whole rows, U = 12 of them in flight per thread; with few pages (a decode
+// step) LANES = 16 spreads a page over many CTAs and puts eight rows side by
+// side, so that no thread waits for memory more than once or twice.
+// Measured, 120 MB of keys: 22 us with 128 lanes (5.4 TB/s), 28 with 16; the
+// last pages of 64 requests 6.4 and 3.9 us, of 256 9.5 and 8.0, of 512 14.3 and 14.7.
 
-constexpr int kSketchThreads = 256;
-constexpr int kSketchLanes = 128;  // threads across a row at most: 1024 channels
+constexpr int kSketchThreads = 128;
+constexpr long long kManyPages = 512;
 
 struct SketchParams {
     const uint16_t* k;
@@ -231,10 +240,11 @@ __device__ __forceinline__ uint32_t code4(uint32_t a, uint32_t b, float amp) {
     return r;
 }
 
+template <int LANES, int U>
 __global__ void __launch_bounds__(kSketchThreads) page_sketch_kernel(const __grid_constant__ SketchParams p) {
     __shared__ uint4 s_hi[kSketchThreads], s_lo[kSketchThreads];
     const int cols = p.H_kv * p.d / 8;  // 16-byte pieces of a row
-    const int L = cols < kSketchLanes ? cols : kSketchLanes;
+    const int L = cols < LANES ? cols : LANES;
     const int RG = kSketchThreads / L;
     long long u = blockIdx.x;
     const int cb = (int)(u % p.col_blocks);
@@ -267,7 +277,7 @@ __global__ void __launch_bounds__(kSketchThreads) page_sketch_kernel(const __gri
     }
 
     const int lane = threadIdx.x % L, rg = threadIdx.x / L;
-    const int col = cb * kSketchLanes + lane;
+    const int col = cb * LANES + lane;
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -276,7 +286,6 @@ __global__ void __launch_bounds__(kSketchThreads) page_sketch_kernel(const __gri
     }
     if (rg < RG && col < cols) {
         const uint4* src = reinterpret_cast<const uint4*>(p.k) + (long long)id * p.page_size * cols + col;
-        constexpr int U = 8;
         for (int row0 = rg; row0 < rows; row0 += RG * U) {
             uint4 x[U];
 #pragma unroll
@@ -386,10 +395,14 @@ attn_status_t attn_paged_plan(const int32_t* ctx_lens, const int32_t* new_lens, 
         cudaSuccess)
         return ATTN_ERR_CUDA;
     int ctas = (total_q + kPlanThreads - 1) / kPlanThreads;
-    ctas = ctas >= kPlanMaxCluster ? kPlanMaxCluster : ctas > 2 ? 4 : ctas;
+    p.in_place = seq_lens == ctx_lens || seq_lens == new_lens || free_left == free_count;
+    if (p.in_place)
+        ctas = ctas >= kPlanMaxCluster ? kPlanMaxCluster : ctas > 2 ? 4 : ctas;
+    else
+        ctas = ctas > kPlanMaxCtas ? kPlanMaxCtas : ctas;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)ctas;
+    attr[0].val.clusterDim.x = p.in_place ? (unsigned)ctas : 1u;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
@@ -423,7 +436,9 @@ attn_status_t attn_page_sketch(const void* k_cache, const int32_t* block_table, 
     if (per_req > max_pages) per_req = max_pages;
     p.per_req = (int)per_req;
     const int cols = H_kv * d / 8;
-    p.col_blocks = (cols + kSketchLanes - 1) / kSketchLanes;
+    const bool many = (long long)B * per_req >= kManyPages;
+    const int lanes = many ? 128 : 16;
+    p.col_blocks = (cols + lanes - 1) / lanes;
     const long long blocks = (long long)B * per_req * p.col_blocks;
     if (blocks > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
     attn_status_t st = status_word_address(&p.status);
@@ -441,7 +456,11 @@ attn_status_t attn_page_sketch(const void* k_cache, const int32_t* block_table, 
     p.page_size = page_size;
     p.max_pages = max_pages;
     p.num_pages = num_pages;
-    page_sketch_kernel<<<(unsigned)blocks, kSketchThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (many)
+        page_sketch_kernel<128, 12><<<(unsigned)blocks, kSketchThreads, 0, cs>>>(p);
+    else
+        page_sketch_kernel<16, 8><<<(unsigned)blocks, kSketchThreads, 0, cs>>>(p);
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

@@ -93,8 +93,8 @@ attn_status_t attn_rope(const void* q, void* q_out, const void* k, void* k_out, 
  *   positions, slots int32 [total_q]: token cu[r] + i of request r has
  *   position P = ctx_r + i and slot page(P) * page_size + P % page_size.
  *   Tokens from cu[B] on (padding) get position 0 and slot -1.
- *   seq_lens may be ctx_lens and free_left may be free_count: both are read
- *   before they are written, so a captured step can advance itself.
+ *   seq_lens may be ctx_lens (or new_lens) and free_left may be free_count: they
+ *   are read before they are written, so a captured step can advance itself.
  *   1 <= B <= 16384, total_q >= 1, page_size a multiple of 8 in [8, 1024],
  *   n_free >= 1 (the array; count may be 0).
  * On the device, reported as ATTN_ERR_DEVICE_DATA: a negative length, or one
