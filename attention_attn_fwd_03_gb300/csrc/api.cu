@@ -821,7 +821,7 @@ attn_status_t attn_paged_sparse_fwd(const void* q, const void* k_cache, const vo
     if (fused) {
         SparseParams p;
         std::memset(&p, 0, sizeof p);
-        const int R = page_size < 16 ? page_size : 16;
+        const int R = page_size < sparse_chunk_keys(d) ? page_size : sparse_chunk_keys(d);
         if (!make_paged_map(&p.tm_k, k_cache, d, H_kv, slots, 1, R) || !make_paged_map(&p.tm_v, v_cache, d, H_kv, slots, 1, R))
             return ATTN_ERR_CUDA;
         p.sel = s;

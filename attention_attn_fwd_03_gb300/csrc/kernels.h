@@ -174,7 +174,7 @@ cudaError_t launch_select(int d, SelectParams p, cudaStream_t stream);
 // Page-sparse attention in one kernel (sparse.cu): selection and attention of
 // single tokens, for groups, contexts and budgets that sparse_fused_ok admits.
 struct SparseParams {
-    CUtensorMap tm_k;        // cache [num_pages * page_size, H_kv, d]: box (64, 1, min(page_size, 16)), 128-B swizzle
+    CUtensorMap tm_k;        // cache [num_pages * page_size, H_kv, d]: box (64, 1, min(page_size, chunk keys)), 128-B swizzle
     CUtensorMap tm_v;
     SelectParams sel;        // keys, cu_out, sched: unused; tables, sel_lens: both or neither
     uint16_t* o;             // bf16 [total_q, H, d]
@@ -182,6 +182,7 @@ struct SparseParams {
     int kv_rows;             // first row past the cache: reads zeros
     float c_scale;           // scale * log2(e)
 };
+constexpr int sparse_chunk_keys(int d) { return d == 128 ? 16 : 32; }
 bool sparse_fused_ok(int d, int G, int max_pages, int budget);
 cudaError_t launch_sparse(int d, const SparseParams& p, cudaStream_t stream);
 

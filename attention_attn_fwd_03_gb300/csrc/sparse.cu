@@ -12,19 +12,19 @@
 //      the sketches are small and their loads latency-bound);
 //   2. every CTA selects for itself from the whole list (the scores are the
 //      same bits everywhere, so are the choices);
-//   3. the chosen keys are cut into chunks of 16 and dealt to four warps of each
-//      CTA.  Each warp is its own pipeline, with no barrier between warps: one
-//      lane keeps STAGES chunks in flight into the warp's own shared-memory ring
-//      (TMA boxes of up to 16 rows, two boxes where pages hold 8), and the warp
-//      runs the online softmax on the chunk that has landed;
+//   3. the chosen keys are cut into chunks of 16 (d = 64: 32) and dealt to four
+//      warps of each CTA.  Each warp is its own pipeline, with no barrier between
+//      warps: one lane keeps STAGES chunks of 8 KB in flight into the warp's own
+//      shared-memory ring (one TMA box per page and panel of a chunk), and the
+//      warp runs the online softmax on the chunk that has landed;
 //   4. the warps' partials (O, m, l) meet in shared memory, across the cluster
 //      through distributed shared memory, in one merge.
 // So a token occupies up to eight SMs without scores, tables or partials in
 // device memory, and a CTA is small enough that two share an SM and cover each
 // other's phases.
 //
-// The products run transposed, S^T = K Q^T and O^T = V^T P^T: the 16 keys of
-// a chunk (or 16 dims of V) fill the 16 rows of the warp-level matrix
+// The products run transposed, S^T = K Q^T and O^T = V^T P^T: 16 keys (or 16
+// dims of V) fill the 16 rows of the warp-level matrix
 // instruction and the query heads are its 8 columns, so a group of up to 8
 // heads wastes nothing that 128 rows of a whole-CTA tile would.  In this
 // orientation a thread holds the same two heads in S^T and in O^T: the
@@ -53,7 +53,6 @@ constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kWarps = 4;       // warps that attend
 constexpr int kAllWarps = 8;    // and all of a CTA's: scores, selection and merge
 constexpr int kThreads = kAllWarps * 32;
-constexpr int kKeys = 16;     // keys per chunk
 constexpr int kMaxCluster = 8;
 constexpr int kMaxG = 32;       // query heads per KV head: four column tiles
 constexpr int kMaxBudget = 1024;  // pages in a CTA's list
@@ -61,11 +60,13 @@ constexpr long long kSms = 152;
 
 template <int D>
 struct SCfg {
+    static constexpr int KEYS = sparse_chunk_keys(D); // keys per chunk
+    static constexpr int KT = KEYS / 16;              // row tiles of a chunk
     static constexpr int NPANEL = D / 64;             // 128-byte panels of the head dim
-    static constexpr int PANEL_BYTES = kKeys * 128;   // 16 rows x 128 B, 128-byte swizzle
+    static constexpr int PANEL_BYTES = KEYS * 128;    // KEYS rows x 128 B, 128-byte swizzle
     static constexpr int TILE_BYTES = NPANEL * PANEL_BYTES;
     static constexpr int STAGE_BYTES = 2 * TILE_BYTES;  // K and V
-    static constexpr int STAGES = D == 128 ? 3 : 4;
+    static constexpr int STAGES = 3;
     static constexpr int RING_BYTES = STAGES * STAGE_BYTES;  // per warp
     static constexpr int O_ROW = D + 4;               // floats per head of a warp's partial O: no bank conflicts
     // before the first load the rings hold the query codes and the scores
@@ -253,14 +254,14 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1) sparse_kernel
     }
 
     // ---- 3: this warp's chunks: gw, gw + W, gw + 2 W, ..
-    const int chunks = (n_keys + kKeys - 1) / kKeys;
+    const int chunks = (n_keys + C::KEYS - 1) / C::KEYS;
     const int mine = warp < kWarps && chunks > gw ? (chunks - gw + W - 1) / W : 0;
-    const int boxes = ps < kKeys ? kKeys / ps : 1;  // boxes per panel of a chunk
+    const int boxes = ps < C::KEYS ? C::KEYS / ps : 1;  // boxes per panel of a chunk
 
     // cache row of box x of the warp's chunk i: a box past the last page, or of a page that does not exist,
     // starts behind the cache and reads zeros
     auto cache_row = [&](int i, int x) {
-        const int k = (gw + i * W) * kKeys + x * ps;
+        const int k = (gw + i * W) * C::KEYS + x * ps;
         if (k >= n_keys) return p.kv_rows;
         const int id = s_list[k >> sp.page_shift];
         if (id >= 0 && id < sp.num_pages) return (id << sp.page_shift) + (k & (ps - 1));
@@ -270,17 +271,16 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1) sparse_kernel
     auto load = [&](int i) {  // the warp's chunk i into its stage (one lane)
         const int s = i % C::STAGES;
         uint8_t* dst = smem + warp * C::RING_BYTES + s * C::STAGE_BYTES;
-        const int r0 = cache_row(i, 0), r1 = boxes == 2 ? cache_row(i, 1) : 0;
         bar_arrive_expect_tx(&bars[s], C::STAGE_BYTES);
+        for (int x = 0; x < boxes; ++x) {
+            const int r = cache_row(i, x);
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv)
+            for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
-            for (int pn = 0; pn < C::NPANEL; ++pn) {
-                uint8_t* to = dst + kv * C::TILE_BYTES + pn * C::PANEL_BYTES;
-                const CUtensorMap* map = kv ? &p.tm_v : &p.tm_k;
-                tma_load_3d(to, map, &bars[s], pn * 64, kvh, r0);
-                if (boxes == 2) tma_load_3d(to + C::PANEL_BYTES / 2, map, &bars[s], pn * 64, kvh, r1);
-            }
+                for (int pn = 0; pn < C::NPANEL; ++pn)
+                    tma_load_3d(dst + kv * C::TILE_BYTES + pn * C::PANEL_BYTES + x * ps * 128, kv ? &p.tm_v : &p.tm_k, &bars[s],
+                                pn * 64, kvh, r);
+        }
     };
     int loaded = min(C::STAGES, mine);
     if (lane == 0)
@@ -306,10 +306,10 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1) sparse_kernel
         ok = __all_sync(0xffffffffu, wait_bar(&bars[s], (uint32_t)((i / C::STAGES) & 1), abort_flag, sp.status));
         if (!ok) break;
         const uint32_t kt = ring + s * C::STAGE_BYTES, vt = kt + C::TILE_BYTES;
-        const int key0 = (gw + i * W) * kKeys;
-        if (key0 + kKeys > n_keys) {
+        const int key0 = (gw + i * W) * C::KEYS;
+        if (key0 + C::KEYS > n_keys) {
             // cache rows behind the token's last key may hold anything, and 0 times NaN would reach O
-            for (int z = n_keys - key0 + (lane >> 3); z < kKeys; z += 4)
+            for (int z = n_keys - key0 + (lane >> 3); z < C::KEYS; z += 4)
 #pragma unroll
                 for (int pn = 0; pn < C::NPANEL; ++pn)
                     asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vt + pn * C::PANEL_BYTES + z * 128 +
@@ -318,28 +318,39 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1) sparse_kernel
                                  : "memory");
             __syncwarp();
         }
-        float sc[NT][4];
+        float sc[C::KT][NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+        for (int y = 0; y < C::KT; ++y)
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-            uint32_t a[4];
-            const int c = kk * 2 + k_chunk;
-            ldsm4(a, kt + (c >> 3) * C::PANEL_BYTES + k_key * 128 + (((c & 7) ^ (k_key & 7)) << 4));
+            for (int n = 0; n < NT; ++n) sc[y][n][0] = sc[y][n][1] = sc[y][n][2] = sc[y][n][3] = 0.f;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816(sc[n], a, qf[n][kk][0], qf[n][kk][1]);
-        }
-        // sc[n][0..1]: key lane / 4, heads 2 (lane % 4), + 1; [2..3]: key + 8
-        const bool in0 = key0 + (lane >> 2) < n_keys, in1 = key0 + (lane >> 2) + 8 < n_keys;
-        uint32_t pt[NT][2];
+        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+            for (int y = 0; y < C::KT; ++y) {
+                uint32_t a[4];
+                const int c = kk * 2 + k_chunk;
+                ldsm4(a, kt + (c >> 3) * C::PANEL_BYTES + (y * 16 + k_key) * 128 + (((c & 7) ^ (k_key & 7)) << 4));
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16816(sc[y][n], a, qf[n][kk][0], qf[n][kk][1]);
+            }
+        // sc[y][n][0..1]: key 16 y + lane / 4, heads 2 (lane % 4), + 1; [2..3]: key + 8
+        uint32_t pt[C::KT][NT][2];
         bool moved = false;
         float alpha[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float x0 = in0 ? sc[n][e] * p.c_scale : -INFINITY, x1 = in1 ? sc[n][2 + e] * p.c_scale : -INFINITY;
-                float top = fmaxf(x0, x1);
+                float top = -INFINITY;
+#pragma unroll
+                for (int y = 0; y < C::KT; ++y)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const bool in = key0 + y * 16 + x * 8 + (lane >> 2) < n_keys;
+                        float& v = sc[y][n][2 * x + e];
+                        v = in ? v * p.c_scale : -INFINITY;
+                        top = fmaxf(top, v);
+                    }
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
@@ -351,12 +362,18 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1) sparse_kernel
                     moved = true;
                 }
                 const float mu = m[n][e] == -INFINITY ? 0.f : m[n][e];
-                sc[n][e] = ex2(x0 - mu);
-                sc[n][2 + e] = ex2(x1 - mu);
-                l[n][e] += sc[n][e] + sc[n][2 + e];
+#pragma unroll
+                for (int y = 0; y < C::KT; ++y) {
+                    sc[y][n][e] = ex2(sc[y][n][e] - mu);
+                    sc[y][n][2 + e] = ex2(sc[y][n][2 + e] - mu);
+                    l[n][e] += sc[y][n][e] + sc[y][n][2 + e];
+                }
             }
-            pt[n][0] = transpose8(pack_bf16(sc[n][0], sc[n][1]));
-            pt[n][1] = transpose8(pack_bf16(sc[n][2], sc[n][3]));
+#pragma unroll
+            for (int y = 0; y < C::KT; ++y) {
+                pt[y][n][0] = transpose8(pack_bf16(sc[y][n][0], sc[y][n][1]));
+                pt[y][n][1] = transpose8(pack_bf16(sc[y][n][2], sc[y][n][3]));
+            }
         }
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
@@ -370,13 +387,15 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1) sparse_kernel
                 }
         }
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x) {
-            uint32_t a[4];
-            const int c = x * 2 + v_chunk;
-            ldsm4_t(a, vt + (c >> 3) * C::PANEL_BYTES + v_key * 128 + (((c & 7) ^ (v_key & 7)) << 4));
+        for (int y = 0; y < C::KT; ++y)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816(o[n][x], a, pt[n][0], pt[n][1]);
-        }
+            for (int x = 0; x < D / 16; ++x) {
+                uint32_t a[4];
+                const int c = x * 2 + v_chunk;
+                ldsm4_t(a, vt + (c >> 3) * C::PANEL_BYTES + (y * 16 + v_key) * 128 + (((c & 7) ^ (v_key & 7)) << 4));
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16816(o[n][x], a, pt[y][n][0], pt[y][n][1]);
+            }
         __syncwarp();  // every lane has read the stage
         if (loaded < mine) {
             if (lane == 0) load(loaded);
@@ -520,7 +539,8 @@ cudaError_t launch_sparse(int d, const SparseParams& p, cudaStream_t stream) {
     const SelectParams& s = p.sel;
     const long long rows = (long long)s.total_q * s.H_kv;
     const long long keys = (long long)(s.budget < s.max_pages ? s.budget : s.max_pages) << s.page_shift;
-    const long long chunks = (keys + kKeys - 1) / kKeys;
+    const int chunk = sparse_chunk_keys(d);
+    const long long chunks = (keys + chunk - 1) / chunk;
     const long long resident = kSms * ((s.G + 7) / 8 * d <= 128 ? 2 : 1);
     int cluster = 1;
     while (cluster < kMaxCluster && rows * cluster * 2 <= resident && chunks >= (long long)cluster * 4 * kWarps)

@@ -95,6 +95,9 @@ CASES = [
     ([2500, 300], None, 10, 2, 128, 128, 3, 0, 1),               # pages of several chunks
     ([9000], None, 8, 8, 64, 1024, 4, 1, 1),                     # G = 1, large pages
     ([9000, 100], None, 4, 2, 64, 8, 1030, 3, 5),                # a budget beyond the fused kernel's list
+    ([300, 2000], None, 8, 2, 128, 16, 3, 1, 2),                 # nothing left for the scores to decide
+    ([160000], None, 2, 1, 64, 8, 40, 1, 1),                     # 20000 pages
+    ([200000], None, 2, 1, 64, 8, 40, 1, 1),                     # more scores than the fused kernel's shared memory holds
     ([20000], None, 2, 1, 64, 8, 700, 3, 5),                     # 2500 pages: several selection runs per thread
 ]
 
@@ -141,7 +144,7 @@ def test_many_scored_pages_and_unsplit_units():
 
 
 def test_more_pages_than_a_selection_caches():
-    """20000 pages: the selection reads its scores through L2, and the page-sparse call is not fused."""
+    """20000 pages: the selection reads its scores through L2."""
     lens, page = [160000], 8
     c = _case(5, [800], None, 2, 1, 64, page)
     g = torch.Generator().manual_seed(11)
