@@ -1,6 +1,6 @@
 // sparse.cu -- page-sparse attention of single query tokens in one kernel:
 // scores, selection and attention of one (token, KV head) at a time, the
-// G <= 32 query heads of the group against the pages chosen for them.
+// G <= 24 (d = 64: 32) query heads of the group against the chosen pages.
 //
 // Bound by memory: 4 d bytes of K and V per key serve 4 d G flops, and the
 // sketches are 1/64 of a 64-row page's keys, so the kernel has to keep loads in
@@ -521,15 +521,21 @@ cudaError_t launch_d(const SparseParams& p, int cluster, cudaStream_t stream) {
     case 1: return launch_t<D, 1>(p, cluster, stream);
     case 2: return launch_t<D, 2>(p, cluster, stream);
     case 3: return launch_t<D, 3>(p, cluster, stream);
-    case 4: return launch_t<D, 4>(p, cluster, stream);
+    case 4:
+        if constexpr (D == 64) return launch_t<D, 4>(p, cluster, stream);
     }
     return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
+// Larger groups run on the paged kernel's tiles of 128 rows, whose cost does
+// not grow with the group.  Measured there and here, us, 32 tokens of 4 KV heads
+// over 4096 of 16384 - 32768 keys (d = 128): G = 8: 74 and 58, 16: 77 and 66,
+// 24: 83 and 74, 32: 85 and 108 (its registers spill over one CTA per SM);
+// d = 64, G = 32: 66 and 48.
 bool sparse_fused_ok(int d, int G, int max_pages, int budget) {
-    return G <= kMaxG && budget <= kMaxBudget && max_pages <= (d == 128 ? SCfg<128>::MAX_PAGES : SCfg<64>::MAX_PAGES);
+    return G <= (d == 128 ? 24 : kMaxG) && budget <= kMaxBudget && max_pages <= (d == 128 ? SCfg<128>::MAX_PAGES : SCfg<64>::MAX_PAGES);
 }
 
 cudaError_t launch_sparse(int d, const SparseParams& p, cudaStream_t stream) {

@@ -193,9 +193,9 @@ attn_status_t attn_page_select(const void* q, const int8_t* sketch, const float*
  * Each token gathers its own pages: meant for decode steps and the few tokens
  * per request of a drafted continuation; a long prompt is better served by
  * attn_paged_fwd, whose tiles share the keys among 128 rows.
- * Groups of up to 32 heads with a budget of up to 1024 pages and tables of up
- * to 22000 pages run as one kernel that keeps everything on
- * chip; the others as a selection and the kernel of attn_paged_fwd.
+ * Groups of up to 24 heads (d = 64: 32) with a budget of up to 1024 pages and
+ * tables of up to 22000 pages run as one kernel that keeps everything on chip;
+ * the others as a selection and the kernel of attn_paged_fwd.
  *   workspace: attn_paged_sparse_fwd_workspace_size bytes, 16-byte aligned,
  *   no initialisation; calls that may overlap need distinct workspaces.  Where
  *   the size is 256 (one kernel) none is used and NULL will do. */

@@ -92,6 +92,8 @@ CASES = [
     ([500, 1], None, 32, 1, 64, 8, 33, 1, 1),                    # G = 32
     ([3000, 20, 1], [2, 1, 1], 12, 1, 128, 8, 50, 2, 1),         # G = 12, two boxes per chunk
     ([700, 2000], None, 33, 1, 64, 32, 12, 1, 1),                # G = 33: the tiles of 128 rows
+    ([1700, 400], None, 48, 2, 128, 16, 14, 1, 1),               # G = 24 ..
+    ([1700, 400], None, 50, 2, 128, 16, 14, 1, 1),               # .. and 25
     ([2500, 300], None, 10, 2, 128, 128, 3, 0, 1),               # pages of several chunks
     ([9000], None, 8, 8, 64, 1024, 4, 1, 1),                     # G = 1, large pages
     ([9000, 100], None, 4, 2, 64, 8, 1030, 3, 5),                # a budget beyond the fused kernel's list

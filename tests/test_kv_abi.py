@@ -226,9 +226,10 @@ def test_workspace_sizes():
     assert size(0, 2, 64, 8) == 0 and size(4, 2, 64, 0) == 0 and size(1 << 16, 1 << 10, 64, 8) == 0
     size = attn.attn_paged_sparse_fwd_workspace_size
     assert size(4, 8, 2, 128, 64, 64, 8) == 256  # one kernel, nothing in device memory
-    # groups of more than 32 heads, budgets of more than 1024 pages, tables of more pages than shared memory
+    # groups of more than 24 heads (d = 64: 32), budgets of more than 1024 pages, tables of more pages than shared memory
     # holds scores for: scores, selection and work list
-    for H, max_pages, budget in ((80, 64, 8), (8, 2000, 1025), (8, 30000, 8)):
+    assert size(4, 64, 2, 64, 64, 64, 8) == 256 and size(4, 48, 2, 128, 64, 64, 8) == 256
+    for H, max_pages, budget in ((50, 64, 8), (8, 2000, 1025), (8, 30000, 8)):
         assert size(4, H, 2, 128, 64, max_pages, budget) > attn.attn_page_select_workspace_size(4, 2, max_pages, budget)
     assert size(4, 9, 2, 128, 64, 64, 8) == 0 and size(4, 8, 2, 96, 64, 64, 8) == 0 and size(4, 8, 2, 128, 48, 64, 8) == 0
 
