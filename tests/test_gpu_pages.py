@@ -107,6 +107,23 @@ def test_captured_plan_advances_itself():
     attn.device_status()
 
 
+@pytest.mark.parametrize("over", ["ctx", "new"])
+def test_plan_in_place_with_many_tokens(over):
+    """Outputs over inputs, more tokens than one CTA has threads: the cluster reads all before it writes."""
+    ctx, new, table, free, num_pages = _state(8, 700, 90, 0, 60, 16)
+    total = sum(new) + 5
+    want = ref.plan(ctx, new, table, free, len(free), 16, total)
+    for _ in range(3):
+        bt, c, n, count = torch.from_numpy(table.copy()).to(DEV), _i32(ctx), _i32(new), _i32([len(free)])
+        cu, lens, pos, slots, left = attn.paged_plan(c, bt, torch.from_numpy(free).to(DEV), count, 16, num_pages, total,
+                                                     new_lens=n, seq_lens=c if over == "ctx" else n, free_left=count)
+        attn.device_status()
+        assert lens is (c if over == "ctx" else n) and left is count
+        for name, a, b in zip(("cu", "lens", "positions", "slots"), (cu, lens, pos, slots), want[:4]):
+            assert a.tolist() == b, name
+        assert np.array_equal(bt.cpu().numpy(), np.array(want[4])) and count.tolist() == [want[5]]
+
+
 @pytest.mark.parametrize("what", ["too few pages", "negative length", "past the table", "too many tokens", "count", "page id"])
 def test_plan_reports_bad_data(what):
     ctx, new, table, free, num_pages = _state(5, 6, 50, 3, 20, 8)

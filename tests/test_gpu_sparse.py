@@ -386,3 +386,97 @@ def test_serving_steps():
             rows = slice(37, 42)
             assert np.all(np.abs(dense[rows].double().cpu().numpy() - ro[rows]) <= bo[rows])
     assert int(count) == num_pages - sum(-(-(p + steps - 1) // page) for p in prompts)
+
+
+def test_captured_decode_step():
+    """One decode step (plan in place, append, sketch, sparse attention) captured once and replayed: every
+    replay is the next step, to the bits of the same calls made one by one."""
+    B, H, H_kv, d, page, budget, steps = 5, 8, 2, 128, 16, 4, 20
+    ctx = [0, 15, 40, 100, 63]
+    max_pages = 9
+    num_pages = 64
+    f = attn.rope_inv_freq(d)[0].to(DEV)
+
+    def state():
+        g = torch.Generator().manual_seed(3)
+        held = [-(-c // page) for c in ctx]
+        perm = torch.randperm(num_pages, generator=g).to(torch.int32)
+        table = torch.full((B, max_pages), -1, dtype=torch.int32)
+        at = 0
+        for r in range(B):
+            table[r, :held[r]] = perm[at:at + held[r]]
+            at += held[r]
+        k, v = (torch.randn((num_pages, page, H_kv, d), generator=g).to(torch.bfloat16).to(DEV) for _ in range(2))
+        s = dict(lens=torch.tensor(ctx, dtype=torch.int32, device=DEV), bt=table.to(DEV), free=perm[at:].contiguous().to(DEV),
+                 count=torch.tensor([num_pages - at], dtype=torch.int32, device=DEV), k=k, v=v,
+                 sk=torch.zeros((num_pages, H_kv, 2 * d), dtype=torch.int8, device=DEV),
+                 amp=torch.zeros((num_pages, H_kv), device=DEV), fused=torch.zeros((B, (H + 2 * H_kv) * d), dtype=torch.bfloat16, device=DEV),
+                 o=torch.zeros((B, H, d), dtype=torch.bfloat16, device=DEV), lse=torch.zeros((B, H), device=DEV))
+        attn.page_sketch(s["k"], s["bt"], s["lens"], s["sk"], s["amp"], max_q_len=max_pages * page)
+        s["tmp"] = [torch.empty(n, dtype=torch.int32, device=DEV) for n in (B + 1, B, B)]
+        return s
+
+    def step(s):
+        cu, pos, slots = s["tmp"]
+        attn.paged_plan(s["lens"], s["bt"], s["free"], s["count"], page, num_pages, B, cu_seqlens_q=cu, seq_lens=s["lens"],
+                        positions=pos, slots=slots, free_left=s["count"])
+        q, k, v = (x.unflatten(1, (-1, d)) for x in s["fused"].split([H * d, H_kv * d, H_kv * d], 1))
+        attn.paged_append(q, k, v, s["k"], s["v"], slots, positions=pos, inv_freq=f, q_out=q)
+        attn.page_sketch(s["k"], s["bt"], s["lens"], s["sk"], s["amp"])
+        attn.paged_sparse_fwd(q.contiguous(), s["k"], s["v"], s["bt"], s["lens"], s["sk"], s["amp"], budget, out=s["o"], lse=s["lse"])
+    eager, kept, replayed = state(), state(), state()
+    step(kept)  # warm-up
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        step(replayed)
+    torch.cuda.current_stream().wait_stream(side)
+    for i in range(steps):
+        x = torch.randn(eager["fused"].shape, generator=torch.Generator().manual_seed(100 + i)).to(torch.bfloat16).to(DEV)
+        for s in (eager, replayed):
+            s["fused"].copy_(x)
+        step(eager)
+        graph.replay()
+        torch.cuda.synchronize()
+        for name in ("lens", "bt", "count", "k", "v", "sk", "amp", "o", "lse"):
+            assert torch.equal(eager[name], replayed[name]), (i, name)
+    attn.device_status()
+    assert eager["lens"].tolist() == [c + steps for c in ctx]
+
+
+def test_recorded_timeout_leaves_outputs_alone():
+    """While a bounded wait's timeout is recorded, page-sparse attention returns without work, as the other
+    attention calls do; once the word is read it computes again."""
+    c = _case(16, [900, 300], None, 8, 2, 64, 16)
+    g = _gpu(c)
+    args = (g["q"], g["k"], g["v"], g["bt"], g["lens"], g["sk"], g["amp"], 6)
+    o_ref, l_ref = attn.paged_sparse_fwd(*args)
+    attn.device_status()
+    o, l = torch.full_like(o_ref, 3.0), torch.full_like(l_ref, 3.0)
+    assert attn.attn_selftest_wait_timeout(torch.cuda.current_stream().cuda_stream) == attn.ATTN_OK
+    attn.paged_sparse_fwd(*args, out=o, lse=l)
+    with pytest.raises(attn.AttnError) as e:
+        attn.device_status()
+    assert e.value.status == attn.ATTN_ERR_TIMEOUT
+    assert bool((o == 3).all()) and bool((l == 3).all())
+    attn.paged_sparse_fwd(*args, out=o, lse=l)
+    attn.device_status()
+    assert torch.equal(o, o_ref) and torch.equal(l, l_ref)
+
+
+def test_caches_past_32_bit_offsets():
+    """Pages at the end of caches of more than 2^32 elements."""
+    pages, page, H_kv, d, n = 66000, 64, 8, 128, 40
+    c = _case(17, [n * page - 7], None, 8, H_kv, d, page)
+    ids = c["table"][0, :n].long()
+    k, v = (torch.empty((pages, page, H_kv, d), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    sk, amp = torch.zeros((pages, H_kv, 2 * d), dtype=torch.int8, device=DEV), torch.zeros((pages, H_kv), device=DEV)
+    far = pages - 1 - 3 * torch.arange(n)
+    k[far.to(DEV)], v[far.to(DEV)] = c["k"][ids].to(DEV), c["v"][ids].to(DEV)
+    sk[far.to(DEV)], amp[far.to(DEV)] = torch.from_numpy(c["sk"])[ids].to(DEV), torch.from_numpy(c["amp"])[ids].to(DEV)
+    g = _gpu(c)
+    want = attn.paged_sparse_fwd(g["q"], g["k"], g["v"], g["bt"], g["lens"], g["sk"], g["amp"], 9)
+    got = attn.paged_sparse_fwd(g["q"], k, v, far.to(torch.int32)[None].contiguous().to(DEV), g["lens"], sk, amp, 9)
+    attn.device_status()
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
