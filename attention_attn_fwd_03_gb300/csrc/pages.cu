@@ -198,14 +198,18 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
 // channels: a thread owns 8 channels and every RG-th row, 16 bytes per load;
 // row groups combine through shared memory.  With many pages a CTA takes up to
 // LANES = 128 pieces of a row (1024 channels), so that the page is read in
-// whole rows, U = 12 of them in flight per thread; with few pages (a decode
+// whole rows, U = 24 of them in flight per thread; with few pages (a decode
 // step) LANES = 16 spreads a page over many CTAs and puts eight rows side by
 // side, so that no thread waits for memory more than once or twice.
-// Measured, 120 MB of keys: 22 us with 128 lanes (5.4 TB/s), 28 with 16; the
-// last pages of 64 requests 6.4 and 3.9 us, of 256 9.5 and 8.0, of 512 14.3 and 14.7.
+// Measured, 120 MB of keys: 20.9 us with 128 lanes (5.7 TB/s), 28 with 16; the
+// last pages of 64 requests 6.4 and 3.9 us, of 256 9.5 and 8.0, of 512 12.5 and 14.7.
+// Many small pages of narrow rows (up to 32 pieces a row, 512 a page) take a
+// warp each: 2 KB pages of 16 x 8192 keys 23.5 -> 8.2 us, 8 KB pages 14.3 ->
+// 8.8, while 16 KB ones are equal and 32 KB ones slower (9.0 -> 16.0).
 
 constexpr int kSketchThreads = 128;
 constexpr long long kManyPages = 512;
+constexpr long long kNarrowPieces = 512;
 
 struct SketchParams {
     const uint16_t* k;
@@ -240,18 +244,14 @@ __device__ __forceinline__ uint32_t code4(uint32_t a, uint32_t b, float amp) {
     return r;
 }
 
-template <int LANES, int U>
-__global__ void __launch_bounds__(kSketchThreads) page_sketch_kernel(const __grid_constant__ SketchParams p) {
-    __shared__ uint4 s_hi[kSketchThreads], s_lo[kSketchThreads];
-    const int cols = p.H_kv * p.d / 8;  // 16-byte pieces of a row
-    const int L = cols < LANES ? cols : LANES;
-    const int RG = kSketchThreads / L;
-    long long u = blockIdx.x;
-    const int cb = (int)(u % p.col_blocks);
-    u /= p.col_blocks;
+// The page of unit u (request, its nth page from the first new key on); id -1: nothing to do.
+struct SketchPage {
+    int id, rows;
+};
+__device__ __forceinline__ SketchPage sketch_page(const SketchParams& p, long long u, bool report) {
+    SketchPage g = {-1, 0};
     const int nth = (int)(u % p.per_req);
     const int r = (int)(u / p.per_req);
-
     const long long cap = (long long)p.max_pages * p.page_size;
     long long len = __ldg(p.seq_lens + r);
     long long fresh = p.max_q_len;
@@ -265,78 +265,148 @@ __global__ void __launch_bounds__(kSketchThreads) page_sketch_kernel(const __gri
         }
     }
     if (fresh > len) fresh = len;
-    if (bad && threadIdx.x == 0 && nth == 0 && cb == 0) atomicOr(p.status, 1u << kStatusDeviceData);
-    if (fresh <= 0) return;
+    if (bad && report && nth == 0) atomicOr(p.status, 1u << kStatusDeviceData);
+    if (fresh <= 0) return g;
     const long long page = (len - fresh) / p.page_size + nth;
-    if (page * p.page_size >= len) return;
-    const int rows = (int)min((long long)p.page_size, len - page * p.page_size);
+    if (page * p.page_size >= len) return g;
     const int id = __ldg(p.table + (long long)r * p.max_pages + page);
     if (id < 0 || id >= p.num_pages) {
-        if (threadIdx.x == 0) atomicOr(p.status, 1u << kStatusDeviceData);
-        return;
+        if (report) atomicOr(p.status, 1u << kStatusDeviceData);
+        return g;
     }
+    g.id = id;
+    g.rows = (int)min((long long)p.page_size, len - page * p.page_size);
+    return g;
+}
 
-    const int lane = threadIdx.x % L, rg = threadIdx.x / L;
-    const int col = cb * LANES + lane;
+// Extremes of 8 channels of one thread, as packed bf16 pairs.
+struct Extremes {
     uint32_t hi[4], lo[4];
+    __device__ __forceinline__ Extremes() {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        hi[i] = 0xff80ff80u;  // -inf
-        lo[i] = 0x7f807f80u;  // +inf
-    }
-    if (rg < RG && col < cols) {
-        const uint4* src = reinterpret_cast<const uint4*>(p.k) + (long long)id * p.page_size * cols + col;
-        for (int row0 = rg; row0 < rows; row0 += RG * U) {
-            uint4 x[U];
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-                // past the last row the first one is read again: extremes do not change
-                const int row = row0 + i * RG < rows ? row0 + i * RG : row0;
-                x[i] = src[(long long)row * cols];
-            }
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-                hi[0] = max2(hi[0], x[i].x); lo[0] = min2(lo[0], x[i].x);
-                hi[1] = max2(hi[1], x[i].y); lo[1] = min2(lo[1], x[i].y);
-                hi[2] = max2(hi[2], x[i].z); lo[2] = min2(lo[2], x[i].z);
-                hi[3] = max2(hi[3], x[i].w); lo[3] = min2(lo[3], x[i].w);
-            }
+        for (int i = 0; i < 4; ++i) {
+            hi[i] = 0xff80ff80u;  // -inf
+            lo[i] = 0x7f807f80u;  // +inf
         }
     }
-    s_hi[threadIdx.x] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    s_lo[threadIdx.x] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    __syncthreads();
-    if (rg == 0) {
-        const int groups = RG < rows ? RG : rows;  // groups that read a row
-        for (int g = 1; g < groups; ++g) {
-            const uint4 a = s_hi[g * L + lane], b = s_lo[g * L + lane];
-            hi[0] = max2(hi[0], a.x); hi[1] = max2(hi[1], a.y); hi[2] = max2(hi[2], a.z); hi[3] = max2(hi[3], a.w);
-            lo[0] = min2(lo[0], b.x); lo[1] = min2(lo[1], b.y); lo[2] = min2(lo[2], b.z); lo[3] = min2(lo[3], b.w);
-        }
+    __device__ __forceinline__ void add(const uint4& a, const uint4& b) {  // a for the largest, b for the smallest
+        hi[0] = max2(hi[0], a.x); lo[0] = min2(lo[0], b.x);
+        hi[1] = max2(hi[1], a.y); lo[1] = min2(lo[1], b.y);
+        hi[2] = max2(hi[2], a.z); lo[2] = min2(lo[2], b.z);
+        hi[3] = max2(hi[3], a.w); lo[3] = min2(lo[3], b.w);
     }
-    // largest magnitude over the head's channels, as bf16 bits without the sign: the order of
-    // the integers is that of the magnitudes, infinities and NaN above every number
+};
+
+// 16 bytes that nobody reads again; volatile, so that U of them are issued before the first is used
+// (plain loads were interleaved with their uses).
+__device__ __forceinline__ uint4 ld_once(const uint4* p) {
+    uint4 r;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+
+// Rows row0, row0 + step, .. below rows of one 16-byte column: with ONCE in batches of U loads while they
+// are whole, the rest (else all) in eights.
+template <int U, bool ONCE>
+__device__ __forceinline__ void scan_rows(const uint4* src, int cols, int row0, int step, int rows, Extremes& e) {
+    for (; ONCE && row0 + step * (U - 1) < rows; row0 += step * U) {
+        uint4 x[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) x[i] = ld_once(src + (long long)(row0 + i * step) * cols);
+#pragma unroll
+        for (int i = 0; i < U; ++i) e.add(x[i], x[i]);
+    }
+    constexpr int V = 8;
+    for (; row0 < rows; row0 += step * V) {
+        uint4 x[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            // past the last row the first one is read again: extremes do not change
+            const int row = row0 + i * step < rows ? row0 + i * step : row0;
+            x[i] = __ldg(src + (long long)row * cols);
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) e.add(x[i], x[i]);
+    }
+}
+
+// The largest magnitude over the head's channels, then the codes (whole warps call it; `write`: this thread's are stored).
+__device__ __forceinline__ void store_sketch(const SketchParams& p, const Extremes& e, int id, int col, bool write) {
+    // as bf16 bits without the sign: the order of the integers is that of the magnitudes, infinities and
+    // NaN above every number
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t a = hi[i] & 0x7fff7fffu, b = lo[i] & 0x7fff7fffu;
+        const uint32_t a = e.hi[i] & 0x7fff7fffu, b = e.lo[i] & 0x7fff7fffu;
         top = max(top, max(max(a & 0xffffu, a >> 16), max(b & 0xffffu, b >> 16)));
     }
-    const int lanes_per_head = p.d / 8;  // 8 or 16 neighbouring lanes of a warp, whole heads of L
+    const int lanes_per_head = p.d / 8;  // 8 or 16 neighbouring lanes of a warp
     for (int o = 1; o < lanes_per_head; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (rg != 0 || col >= cols) return;
+    if (!write) return;
     const bool finite = top < 0x7f80u;
     const float amp = finite ? __uint_as_float(top << 16) : INFINITY;
     uint2 ch = make_uint2(0u, 0u), cl = make_uint2(0u, 0u);
     if (finite && top != 0u) {
-        ch = make_uint2(code4(hi[0], hi[1], amp), code4(hi[2], hi[3], amp));
-        cl = make_uint2(code4(lo[0], lo[1], amp), code4(lo[2], lo[3], amp));
+        ch = make_uint2(code4(e.hi[0], e.hi[1], amp), code4(e.hi[2], e.hi[3], amp));
+        cl = make_uint2(code4(e.lo[0], e.lo[1], amp), code4(e.lo[2], e.lo[3], amp));
     }
     const int head = col / lanes_per_head, c0 = (col % lanes_per_head) * 8;
     const long long rec = (long long)id * p.H_kv + head;
     *reinterpret_cast<uint2*>(p.sketch + rec * (2 * p.d) + c0) = ch;
     *reinterpret_cast<uint2*>(p.sketch + rec * (2 * p.d) + p.d + c0) = cl;
     if (c0 == 0) p.amp[rec] = amp;
+}
+
+template <int LANES, int U>
+__global__ void __launch_bounds__(kSketchThreads) page_sketch_kernel(const __grid_constant__ SketchParams p) {
+    __shared__ uint4 s_hi[kSketchThreads], s_lo[kSketchThreads];
+    const int cols = p.H_kv * p.d / 8;  // 16-byte pieces of a row
+    const int L = cols < LANES ? cols : LANES;
+    const int RG = kSketchThreads / L;
+    const int cb = (int)(blockIdx.x % p.col_blocks);
+    const SketchPage g = sketch_page(p, blockIdx.x / p.col_blocks, threadIdx.x == 0 && cb == 0);
+    if (g.id < 0) return;
+    const int lane = threadIdx.x % L, rg = threadIdx.x / L;
+    const int col = cb * LANES + lane;
+    Extremes e;
+    if (rg < RG && col < cols)
+        scan_rows<U, (LANES > 16)>(reinterpret_cast<const uint4*>(p.k) + (long long)g.id * p.page_size * cols + col, cols, rg, RG, g.rows, e);
+    s_hi[threadIdx.x] = make_uint4(e.hi[0], e.hi[1], e.hi[2], e.hi[3]);
+    s_lo[threadIdx.x] = make_uint4(e.lo[0], e.lo[1], e.lo[2], e.lo[3]);
+    __syncthreads();
+    if (rg == 0) {
+        const int groups = RG < g.rows ? RG : g.rows;  // groups that read a row
+        for (int x = 1; x < groups; ++x) e.add(s_hi[x * L + lane], s_lo[x * L + lane]);
+    }
+    store_sketch(p, e, g.id, col, rg == 0 && col < cols);
+}
+
+// Rows of at most 32 pieces: a warp takes a page, L lanes across a row, and
+// combines its 32 / L row groups by shuffles.  L is the power of two at or
+// above the pieces of a row.
+template <int U>
+__global__ void __launch_bounds__(kSketchThreads) page_sketch_warp_kernel(const __grid_constant__ SketchParams p) {
+    const int lane = threadIdx.x & 31;
+    const long long u = (long long)blockIdx.x * (kSketchThreads / 32) + (threadIdx.x >> 5);
+    if (u >= (long long)p.B * p.per_req) return;
+    const SketchPage g = sketch_page(p, u, lane == 0);
+    if (g.id < 0) return;
+    const int cols = p.H_kv * p.d / 8;
+    int L = 8;
+    while (L < cols) L <<= 1;
+    const int RG = 32 / L, rg = lane / L, col = lane % L;
+    Extremes e;
+    if (col < cols)
+        scan_rows<U, false>(reinterpret_cast<const uint4*>(p.k) + (long long)g.id * p.page_size * cols + col, cols, rg, RG, g.rows, e);
+    for (int o = L; o < 32; o <<= 1) {
+        uint4 a, b;
+        a.x = __shfl_xor_sync(0xffffffffu, e.hi[0], o); b.x = __shfl_xor_sync(0xffffffffu, e.lo[0], o);
+        a.y = __shfl_xor_sync(0xffffffffu, e.hi[1], o); b.y = __shfl_xor_sync(0xffffffffu, e.lo[1], o);
+        a.z = __shfl_xor_sync(0xffffffffu, e.hi[2], o); b.z = __shfl_xor_sync(0xffffffffu, e.lo[2], o);
+        a.w = __shfl_xor_sync(0xffffffffu, e.hi[3], o); b.w = __shfl_xor_sync(0xffffffffu, e.lo[3], o);
+        e.add(a, b);
+    }
+    store_sketch(p, e, g.id, col, rg == 0 && col < cols);
 }
 
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -437,9 +507,11 @@ attn_status_t attn_page_sketch(const void* k_cache, const int32_t* block_table, 
     p.per_req = (int)per_req;
     const int cols = H_kv * d / 8;
     const bool many = (long long)B * per_req >= kManyPages;
+    const bool narrow = many && cols <= 32 && (long long)page_size * cols <= kNarrowPieces;
     const int lanes = many ? 128 : 16;
-    p.col_blocks = (cols + lanes - 1) / lanes;
-    const long long blocks = (long long)B * per_req * p.col_blocks;
+    p.col_blocks = narrow ? 1 : (cols + lanes - 1) / lanes;
+    const int pages_per_cta = narrow ? kSketchThreads / 32 : 1;
+    const long long blocks = ((long long)B * per_req * p.col_blocks + pages_per_cta - 1) / pages_per_cta;
     if (blocks > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
     attn_status_t st = status_word_address(&p.status);
     if (st != ATTN_OK) return st;
@@ -457,8 +529,10 @@ attn_status_t attn_page_sketch(const void* k_cache, const int32_t* block_table, 
     p.max_pages = max_pages;
     p.num_pages = num_pages;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    if (many)
-        page_sketch_kernel<128, 12><<<(unsigned)blocks, kSketchThreads, 0, cs>>>(p);
+    if (narrow)
+        page_sketch_warp_kernel<8><<<(unsigned)blocks, kSketchThreads, 0, cs>>>(p);
+    else if (many)
+        page_sketch_kernel<128, 24><<<(unsigned)blocks, kSketchThreads, 0, cs>>>(p);
     else
         page_sketch_kernel<16, 8><<<(unsigned)blocks, kSketchThreads, 0, cs>>>(p);
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;

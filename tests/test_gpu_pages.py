@@ -171,6 +171,10 @@ def _cache(seed, pages, page, H_kv, d):
     (16, 128, 32, [70, 33], 64),              # more than 1024 channels: two channel blocks
     (9, 128, 16, [50, 20], 20),               # the second channel block partial
     (5, 64, 1024, [1500, 1], 700),
+    (1, 64, 8, [4100, 100, 0, 7], 5000),      # many pages of narrow rows: a warp per page
+    (3, 64, 8, [4099, 90], 5000),             # 24 of 32 lanes across a row
+    (2, 128, 16, [9000, 41], 9000),
+    (5, 64, 16, [8500, 200], 9000),           # many pages of wider rows
 ])
 def test_sketch_matches_definition(H_kv, d, page, lens, fresh):
     B, max_pages = len(lens), max(-(-n // page) for n in lens) + 1
