@@ -307,7 +307,11 @@ attn_status_t select_sizes_ok(int B, int total_q, int H, int H_kv, int d, int pa
 // none; 256 bytes stand for it.  Otherwise the selection kernels and the paged
 // kernel run: with one unit per (token, KV head) too few to occupy the SMs, a
 // token's keys are cut into runs of whole 128-key blocks until about three
-// units per SM exist, with a work list and partials of the runs.
+// units per SM exist, with a work list and partials of the runs.  Measured with
+// groups of 4 (before they had a kernel of their own), runs of at least 1, 2, 4
+// blocks: 2048 keys of 8 heads 19.2, 18.6, 19.9 us; 8192 keys of 32 rows with
+// 304, 456, 912, 1824 units wanted 65, 66, 68, 73 us, 4096 keys of 256 rows 121,
+// 121, 117, 121.
 struct SparsePlan {
     int n_splits, split_blocks;
     size_t tables, lens, cu, list, part_o, part_ml, bytes;  // byte offsets; list: the 256-byte header, then the entries

@@ -16,11 +16,14 @@
 // heads: the TOK * rot / 2 angles are computed once, by all threads, into
 // shared memory; each thread then keeps the cosines and sines of its few
 // pairs in registers and walks over the heads, 32 bytes of a head vector at a
-// time (two 16-byte loads), three heads in flight.  Outputs of more than half
-// of L2 are stored evict-first, so that they do not push out lines that loads
+// time (two 16-byte loads), three heads in flight.  Outputs of more than L2
+// holds are stored evict-first, so that they do not push out lines that loads
 // share.  Measured, [1, 32 + 8, 32768, 128] bf16: 100 us, 6.7 TB/s, 0.98 of a
 // copy (2, 4, 5 heads in flight: 105, 110, 117 us; plain stores: 114; 8 tokens
-// per CTA instead of 4: 102, but 48 for 44 us on fp32).
+// per CTA instead of 4: 102, but 48 for 44 us on fp32).  With a reader of q
+// behind it: 80 MB out 51.8 us evict-first and 49.2 plain, 160 MB 95.4 and 94.6.
+// Few tokens take a CTA or more each: 64 tokens of 40 heads 2.8 us (four to a
+// CTA: 4.1), 512 both 4.4, 1024 7.0 (5.4), 4096 23 (17).
 #include <cmath>
 #include <cstring>
 
@@ -34,7 +37,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kInFlight = 3;  // heads whose loads a thread issues before it uses the first
-constexpr long long kStreamBytes = 64LL << 20;  // half of L2
+constexpr long long kStreamBytes = 128LL << 20;  // L2
+constexpr int kManyTokens = 512;
 
 struct RopeSide {
     const char* in;
@@ -259,7 +263,7 @@ cudaError_t launch(const RopeParams& p, long long blocks, int smem, cudaStream_t
 void plan(RopeParams& p, int elem_bytes, long long* blocks) {
     const int units = p.d / (32 / elem_bytes);
     const int rows = kThreads / units;  // head vectors side by side in a CTA
-    p.tok = p.n_tokens >= 2048 ? 4 : 1;
+    p.tok = p.n_tokens >= kManyTokens ? 4 : 1;
     if (p.tok > rows) p.tok = rows;
     const int lanes = rows / p.tok;
     p.splits = 1;

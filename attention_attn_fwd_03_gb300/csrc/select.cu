@@ -5,8 +5,11 @@
 // 1/64 of a 64-row page's keys: four lanes take a page, up to sixteen 16-byte
 // loads in flight per lane, and go to the matrix units from registers.
 //
-// The selection kernel takes one (token, KV head) per CTA, works from shared
-// memory (or through L2 above kCached pages) and is latency-bound.
+// The selection kernel takes one (token, KV head) per CTA and is latency-bound.
+// It reads the scores through L1, a few times each: a copy in shared memory
+// first was no faster (4096 pages: 17.2 us for both kernels with it, 15.9
+// without).  Score CTAs of 64 pages instead of 128 gained 0.5 us at 512 pages
+// of one token and lost 3 to 20% everywhere else.
 #include <cmath>
 #include <cstring>
 
@@ -21,12 +24,12 @@ namespace {
 
 constexpr int kScoreWarps = 4;
 constexpr int kSelectThreads = 512;
-constexpr int kCached = 10240;  // scores a selection keeps in shared memory (40 KB: no opt-in size)
 
-// 8 STEPS pages per warp.
-template <int D, int STEPS>
+constexpr int kSteps = 4;  // 32 pages per warp
+
+template <int D>
 __global__ void __launch_bounds__(kScoreWarps * 32) page_score_kernel(const __grid_constant__ SelectParams p) {
-    constexpr int PAGES = kScoreWarps * STEPS * 8;
+    constexpr int PAGES = kScoreWarps * kSteps * 8;
     extern __shared__ uint4 s_codes[];  // [G][pieces], then the heads' scalars [G]
     float2* s_heads = reinterpret_cast<float2*>(s_codes + p.G * kPieces<D>);
     griddep_launch_dependents();
@@ -42,17 +45,17 @@ __global__ void __launch_bounds__(kScoreWarps * 32) page_score_kernel(const __gr
     if (n_vis <= p.budget || chunk * PAGES >= n_vis) return;  // everything is taken, or nothing is here
 
     // the sketches are on their way while the codes are made
-    const int first = chunk * PAGES + warp * STEPS * 8;
-    SketchLoads<D, STEPS> loads;
+    const int first = chunk * PAGES + warp * kSteps * 8;
+    SketchLoads<D, kSteps> loads;
     loads.look_up(p.table + (long long)k.r * p.max_pages, first, n_vis, lane);
     loads.fetch(p, kvh, first, n_vis, lane, bad);
     make_codes<D>(p.q + ((long long)t * p.H + kvh * p.G) * D, p.G, s_codes, s_heads, warp, kScoreWarps, lane);
     __syncthreads();
-    uint32_t key[STEPS];
+    uint32_t key[kSteps];
     loads.template keys<2>(s_codes, s_heads, p.G, lane, key);
     uint32_t* keys = p.keys + ((long long)t * p.H_kv + kvh) * p.max_pages;
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
+    for (int s = 0; s < kSteps; ++s) {
         const int page = first + s * 8 + (lane >> 2);
         if ((lane & 3) == 0 && page < n_vis) keys[page] = key[s];
     }
@@ -60,7 +63,6 @@ __global__ void __launch_bounds__(kScoreWarps * 32) page_score_kernel(const __gr
 }
 
 __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(const __grid_constant__ SelectParams p) {
-    extern __shared__ uint32_t s_keys[];  // [kCached] or less
     __shared__ SelectScratch<kSelectThreads> scratch;
     __shared__ int s_bins[kBins];
     griddep_launch_dependents();
@@ -112,42 +114,27 @@ __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(const __gri
     for (int i = tid; i < p.last; i += kSelectThreads) out[p.budget - p.last + i] = __ldg(table + n_vis - p.last + i);
     if (need == 0) return;
     const uint32_t* keys = p.keys + ((long long)t * p.H_kv + kvh) * p.max_pages + p.first;
-    if (n <= kCached) {
-        for (int i = tid; i < n; i += kSelectThreads) s_keys[i] = keys[i];
-        keys = s_keys;
-    }
     select_best<kSelectThreads>(keys, n, need, s_bins, scratch,
                                 [&](int place, int i) { out[p.first + place] = __ldg(table + p.first + i); });
 }
-
-// Below this many CTAs of 128 pages the score kernel takes 64 pages per CTA.
-constexpr long long kFewChunks = 608;  // four per SM
 
 template <int D>
 cudaError_t launch_d(SelectParams& p, cudaStream_t stream) {
     const long long rows = (long long)p.total_q * p.H_kv;
     const int smem = p.G * (2 * D + 8);
     if (p.max_pages > p.budget) {
-        const int wide = kScoreWarps * 32, narrow = kScoreWarps * 16;
-        const long long chunks = (p.max_pages + wide - 1) / wide;
-        if (rows * chunks >= kFewChunks) {
-            p.n_chunks = (int)chunks;
-            page_score_kernel<D, 4><<<(unsigned)(rows * chunks), kScoreWarps * 32, smem, stream>>>(p);
-        } else {
-            p.n_chunks = (p.max_pages + narrow - 1) / narrow;
-            page_score_kernel<D, 2><<<(unsigned)(rows * p.n_chunks), kScoreWarps * 32, smem, stream>>>(p);
-        }
+        const int pages = kScoreWarps * kSteps * 8;
+        p.n_chunks = (p.max_pages + pages - 1) / pages;
+        page_score_kernel<D><<<(unsigned)(rows * p.n_chunks), kScoreWarps * 32, smem, stream>>>(p);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    const int n = p.max_pages < kCached ? p.max_pages : kCached;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)rows);
     cfg.blockDim = dim3(kSelectThreads);
-    cfg.dynamicSmemBytes = p.max_pages > p.budget ? (size_t)n * 4 : 0;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = p.max_pages > p.budget ? 1 : 0;

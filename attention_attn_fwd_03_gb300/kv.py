@@ -100,7 +100,8 @@ def attn_paged_sparse_fwd(q, k_cache, v_cache, block_table, cu_seqlens_q, seq_le
 # The helpers below run once per call of a decode step, whose kernels take a few microseconds: they
 # look up each attribute once and take the slow path only to say what is wrong.
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _device(t, name):

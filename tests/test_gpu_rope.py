@@ -56,7 +56,9 @@ def _heads_inside(x):
     (2, 5, 1, 7, 64, 64, True, 1.0),
     (3, 4, 2, 61, 128, 48, False, 1.25),       # part of the head
     (1, 32, 8, 65, 128, 16, True, 0.5),
-    (2, 3, 3, 1031, 64, 32, False, 1.0),       # 2048 tokens or more: four to a CTA, the last CTA partial
+    (2, 3, 3, 1031, 64, 32, False, 1.0),       # 512 tokens or more: four to a CTA, the last CTA partial
+    (3, 2, 1, 171, 64, 64, True, 1.0),         # 513
+    (1, 2, 1, 511, 128, 64, False, 1.0),
     (1, 7, 2, 2051, 128, 128, True, 1.1),
     (1, 40, 0, 5, 128, 112, False, -2.0),      # q alone
 ])

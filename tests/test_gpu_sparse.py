@@ -145,8 +145,8 @@ def test_many_scored_pages_and_unsplit_units():
     assert np.all(np.abs(o.double().cpu().numpy() - ro) <= bo) and np.all(np.abs(lse.double().cpu().numpy() - rl) <= bl)
 
 
-def test_more_pages_than_a_selection_caches():
-    """20000 pages: the selection reads its scores through L2."""
+def test_selection_from_many_pages():
+    """20000 pages of scores that tie a lot, budgets of a few to all but one."""
     lens, page = [160000], 8
     c = _case(5, [800], None, 2, 1, 64, page)
     g = torch.Generator().manual_seed(11)
