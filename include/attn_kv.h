@@ -145,7 +145,9 @@ attn_status_t attn_paged_append(const void* q, void* q_out, const void* k, const
  *   With cu_seqlens_q, max_q_len bounds the tokens of a request (more are cut
  *   to the last max_q_len and set ATTN_ERR_DEVICE_DATA).
  *   d in {64, 128}; page_size a power of two in [8, 1024].
- * Rows of a page past the request's last key are not read. */
+ * Rows of a page past the request's last key are not read.  Requests that
+ * share a page (a common prefix) renew it alike as long as the page is full;
+ * one that is still being filled belongs to one request. */
 attn_status_t attn_page_sketch(const void* k_cache, const int32_t* block_table, const int32_t* cu_seqlens_q,
                                const int32_t* seq_lens, int B, int max_q_len, int H_kv, int d, int page_size,
                                int max_pages, int num_pages, int8_t* sketch, float* amp, void* stream);
