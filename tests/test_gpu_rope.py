@@ -293,3 +293,44 @@ def test_helpers_refuse():
         attn.rope(q[..., :64].contiguous(), inv_freq=f)
     with pytest.raises(ValueError):
         attn.paged_append(None, q[0], q[0], q, q, torch.zeros(4, dtype=torch.int32, device=DEV), inv_freq=f)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_shapes(seed):
+    """Seeded shapes, strides and types of rope, and the same rotation through the cache append."""
+    rng = np.random.default_rng(seed)
+    g = torch.Generator().manual_seed(seed)
+    dt = torch.bfloat16 if seed % 3 else torch.float32
+    d = int(rng.choice([64, 128]))
+    rot = int(rng.integers(1, d // 16 + 1)) * 16
+    B, N, H, H_k = int(rng.integers(1, 4)), int(rng.choice([1, 3, 30, 400])), int(rng.integers(1, 20)), int(rng.integers(1, 6))
+    interleaved, inverse, amp = bool(rng.integers(2)), bool(rng.integers(2)), float(rng.uniform(-2, 2))
+    f = attn.rope_inv_freq(rot, base=float(rng.choice([10000.0, 500000.0])))[0]
+    pos = torch.randint(-10, 200000, (B, N), generator=g, dtype=torch.int32)
+    order = [(0, 1, 2, 3), (0, 2, 1, 3), (2, 0, 1, 3), (1, 0, 2, 3)][int(rng.integers(4))]
+
+    def tensor(heads):  # [B, heads, N, d] stored in another order, inside a wider row
+        dims = [(B, heads, N, d + 16)[i] for i in order]
+        x = torch.randn(dims, generator=g).to(dt).to(DEV)
+        return x.permute([order.index(i) for i in range(4)])[..., :d]
+    q, k = tensor(H), tensor(H_k)
+    q_out, k_out = tensor(H), None
+    qo, ko = attn.rope(q, k, inv_freq=f.to(DEV), positions=pos.to(DEV), interleaved=interleaved, inverse=inverse, amplitude=amp,
+                       q_out=q_out, k_out=k_out)
+    attn.device_status()
+    assert qo is q_out
+    for name, x, y in (("q", q, qo), ("k", k, ko)):
+        want = ref.rope(_heads_inside(x), pos.numpy(), f.numpy(), rot, interleaved, inverse, amp).transpose(0, 2, 1, 3)
+        _check(name, y, x, want, rot, interleaved, amp)
+    if dt is torch.bfloat16 and not inverse:
+        page, T = int(rng.choice([8, 24, 64, 1024])), B * N
+        pages = -(-T // page) + 1
+        slots = torch.randperm(pages * page, generator=g)[:T].to(torch.int32).to(DEV)
+        kc, vc = (torch.zeros((pages, page, H_k, d), dtype=dt, device=DEV) for _ in range(2))
+        rows = k.permute(0, 2, 1, 3).reshape(T, H_k, d)
+        got = attn.paged_append(q.permute(0, 2, 1, 3).reshape(T, H, d), rows, rows, kc, vc, slots, positions=pos.reshape(-1).to(DEV),
+                                inv_freq=f.to(DEV), interleaved=interleaved, amplitude=amp)
+        attn.device_status()
+        assert torch.equal(got, qo.permute(0, 2, 1, 3).reshape(T, H, d))
+        assert torch.equal(kc.flatten(0, 1)[slots.long()], ko.permute(0, 2, 1, 3).reshape(T, H_k, d))
+        assert torch.equal(vc.flatten(0, 1)[slots.long()], rows)

@@ -480,3 +480,39 @@ def test_caches_past_32_bit_offsets():
     got = attn.paged_sparse_fwd(g["q"], k, v, far.to(torch.int32)[None].contiguous().to(DEV), g["lens"], sk, amp, 9)
     attn.device_status()
     assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
+@pytest.mark.parametrize("seed", range(30))
+def test_random_shapes(seed):
+    """Seeded shapes over the whole range: groups on both kernels, every page size, budgets below and above
+    the pages in use, requests that are empty or shorter than their new tokens."""
+    rng = np.random.default_rng(1000 + seed)
+    d = int(rng.choice([64, 128]))
+    page = int(rng.choice([8, 16, 32, 64, 128, 256, 512, 1024]))
+    H_kv = int(rng.choice([1, 2, 3, 5]))
+    G = int(rng.choice([1, 2, 5, 7, 8, 11, 16, 21, 30, 40]))
+    B = int(rng.integers(1, 6))
+    top = int(rng.choice([3, 40, 150])) * page
+    lens = rng.integers(0, max(2, min(top, 12000)), B).tolist()
+    q_lens = None if rng.random() < 0.5 else rng.integers(0, 7, B).tolist()
+    if q_lens is not None and sum(q_lens) == 0:
+        q_lens[-1] = 2
+    if sum(lens) == 0:
+        lens[0] = 1
+    first, last = int(rng.integers(0, 3)), int(rng.integers(1, 4))
+    budget = first + last + int(rng.integers(0, 20))
+    c = _case(seed, lens, q_lens, G * H_kv, H_kv, d, page, extra_pages=int(rng.integers(0, 4)))
+    g = _gpu(c)
+    want, want_sel = _want(c, budget, first, last)
+    tables, sel = _select(c, g, budget, first, last)
+    assert np.array_equal(tables.cpu().numpy(), want) and np.array_equal(sel.cpu().numpy(), want_sel)
+    scale = float(np.float32(rng.uniform(0.02, 0.3)))
+    o, lse, t2, s2 = attn.paged_sparse_fwd(g["q"], g["k"], g["v"], g["bt"], g["lens"], g["sk"], g["amp"], budget, first, last,
+                                           cu_seqlens_q=g["cu"], scale=scale, return_tables=True)
+    attn.device_status()
+    assert torch.equal(t2, tables) and torch.equal(s2, sel)
+    ro, rl, bo, bl = ref.attend(c["q"].float().numpy(), c["k"].float().numpy(), c["v"].float().numpy(), want, want_sel, scale)
+    o, lse = o.double().cpu().numpy(), lse.double().cpu().numpy()
+    empty = np.isneginf(rl)
+    assert np.array_equal(np.isneginf(lse), empty) and np.all(o[empty] == 0)
+    assert np.all(np.abs(o - ro) <= bo) and np.all(np.abs(lse[~empty] - rl[~empty]) <= bl[~empty])
