@@ -7,9 +7,11 @@
 //
 // The selection kernel takes one (token, KV head) per CTA and is latency-bound.
 // It reads the scores through L1, a few times each: a copy in shared memory
-// first was no faster (4096 pages: 17.2 us for both kernels with it, 15.9
-// without).  Score CTAs of 64 pages instead of 128 gained 0.5 us at 512 pages
-// of one token and lost 3 to 20% everywhere else.
+// first was no faster.  Score CTAs of 64 pages instead of 128 gained 0.5 us at
+// 512 pages of one token and lost 3 to 20% elsewhere.  Both kernels, 8 KV heads:
+// one token of 512 pages 10.0 us, of 4096 16.9, 64 tokens of 1024 43.5 (20 of
+// them for the bytes); selection by 512 threads 10.9, 15.7, 53.7, by 128 9.9,
+// 27.9, 45.9.
 #include <cmath>
 #include <cstring>
 
@@ -23,7 +25,7 @@ namespace attn {
 namespace {
 
 constexpr int kScoreWarps = 4;
-constexpr int kSelectThreads = 512;
+constexpr int kSelectThreads = 256;
 
 constexpr int kSteps = 4;  // 32 pages per warp
 

@@ -244,8 +244,9 @@ def test_rows_behind_the_last_request_stay():
         assert bool((tables[5:] == -1).all()) and sel.tolist()[5:] == [0] * 4
 
 
-def test_replay_other_stream_and_two_at_once():
-    c = _case(12, [3000, 500, 0, 1700], None, 16, 4, 128, 16)
+@pytest.mark.parametrize("H", [16, 120])  # the fused kernel; the selection kernels and the paged kernel
+def test_replay_other_stream_and_two_at_once(H):
+    c = _case(12, [3000, 500, 0, 1700], None, H, 4, 128, 16)
     g = _gpu(c)
     args = (g["q"], g["k"], g["v"], g["bt"], g["lens"], g["sk"], g["amp"], 24, 1, 2)
     o_ref, l_ref = attn.paged_sparse_fwd(*args)
@@ -259,7 +260,7 @@ def test_replay_other_stream_and_two_at_once():
     torch.cuda.synchronize()
     for o, l in outs:
         assert torch.equal(o, o_ref) and torch.equal(l, l_ref)
-    need = attn.attn_paged_sparse_fwd_workspace_size(4, 16, 4, 128, 16, c["table"].shape[1], 24)
+    need = attn.attn_paged_sparse_fwd_workspace_size(4, H, 4, 128, 16, c["table"].shape[1], 24)
     ws = torch.full((need,), 0xAB, dtype=torch.uint8, device=DEV)
     o, l = torch.zeros_like(o_ref), torch.zeros_like(l_ref)
     graphs = []
