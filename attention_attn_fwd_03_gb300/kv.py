@@ -16,7 +16,7 @@ import math
 
 import torch
 
-from . import ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, AttnError, _raise, lib
+from . import ATTN_ERR_INVALID_ARG, ATTN_ERR_WORKSPACE, AttnError, _raise, lib
 
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
 
@@ -349,16 +349,18 @@ def _selection_args(q, sketch, amp, block_table, seq_lens, cu_seqlens_q, dev):
     return ptrs, (B, T, H, H_kv, d), max_pages, num_pages
 
 
-def _workspace(workspace, need, dev, stream, device, what):
-    """(address, bytes, tensor) of a workspace of `need` bytes; none is made where 256 say that it is not used."""
-    if need == 0:
-        raise AttnError(ATTN_ERR_UNSUPPORTED, what)
-    if workspace is None:
-        if need <= 256:
-            return None, 0, None
-        with _on(stream):
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    return _check(workspace, "workspace", torch.uint8, dev, (workspace.numel(),)), workspace.numel(), workspace
+def _with_workspace(call, size, workspace, dev, stream, device, what):
+    """Runs call(address, bytes) with the workspace given, else with none, and where that is refused with one of
+    size() bytes: most calls need none, and asking for the size first would cost each of them."""
+    if workspace is not None:
+        st = call(_check(workspace, "workspace", torch.uint8, dev, (workspace.numel(),)), workspace.numel())
+    else:
+        st = call(None, 0)
+        if st == ATTN_ERR_WORKSPACE:
+            with _on(stream):
+                workspace = torch.empty(size(), dtype=torch.uint8, device=device)
+            st = call(workspace.data_ptr(), workspace.numel())
+    _raise(st, what)
 
 
 def page_select(q, sketch, amp, block_table, seq_lens, page_size, budget, first=1, last=1, cu_seqlens_q=None,
@@ -380,11 +382,11 @@ def page_select(q, sketch, amp, block_table, seq_lens, page_size, budget, first=
             sel_lens = torch.empty((T,), dtype=torch.int32, device=q.device)
     tp = _check(tables, "tables", torch.int32, dev, (T, H_kv, budget))
     lp = _check(sel_lens, "sel_lens", torch.int32, dev, (T,))
-    need = lib().attn_page_select_workspace_size(T, H_kv, max_pages, budget)
-    wp, wn, workspace = _workspace(workspace, need, dev, stream, q.device, "attn_page_select_workspace_size")
-    st = lib().attn_page_select(*ptrs, B, T, H, H_kv, d, int(page_size), max_pages, num_pages, budget, int(first), int(last),
-                          tp, lp, wp, wn, _handle(stream, dev))
-    _raise(st, "attn_page_select")
+    h = _handle(stream, dev)
+    _with_workspace(lambda wp, wn: lib().attn_page_select(*ptrs, B, T, H, H_kv, d, int(page_size), max_pages, num_pages, budget,
+                                                          int(first), int(last), tp, lp, wp, wn, h),
+                    lambda: attn_page_select_workspace_size(T, H_kv, max_pages, budget), workspace, dev, stream, q.device,
+                    "attn_page_select")
     return tables, sel_lens
 
 
@@ -416,12 +418,13 @@ def paged_sparse_fwd(q, k_cache, v_cache, block_table, seq_lens, sketch, amp, bu
             sel_lens = torch.empty((T,), dtype=torch.int32, device=q.device)
     op = _check(out, "out", bf, dev, (T, H, d))
     lp = None if lse is None else _check(lse, "lse", torch.float32, dev, (T, H))
-    need = lib().attn_paged_sparse_fwd_workspace_size(T, H, H_kv, d, page_size, max_pages, budget)
-    wp, wn, workspace = _workspace(workspace, need, dev, stream, q.device, "attn_paged_sparse_fwd_workspace_size")
-    qp, sp, ap, bp, cp, np_ = ptrs
-    st = lib().attn_paged_sparse_fwd(qp, kp, vp, bp, cp, np_, sp, ap, B, T, H, H_kv, d, page_size, max_pages, num_pages,
-                               budget, int(first), int(last), float(scale) if scale is not None else 1.0 / math.sqrt(d),
-                               op, lp, None if tables is None else tables.data_ptr(),
-                               None if sel_lens is None else sel_lens.data_ptr(), wp, wn, _handle(stream, dev))
-    _raise(st, "attn_paged_sparse_fwd")
+    tp = None if tables is None else tables.data_ptr()
+    sp = None if sel_lens is None else sel_lens.data_ptr()
+    sc, h = float(scale) if scale is not None else 1.0 / math.sqrt(d), _handle(stream, dev)
+    qp, skp, ap, bp, cp, np_ = ptrs
+    _with_workspace(lambda wp, wn: lib().attn_paged_sparse_fwd(qp, kp, vp, bp, cp, np_, skp, ap, B, T, H, H_kv, d, page_size,
+                                                               max_pages, num_pages, budget, int(first), int(last), sc, op, lp,
+                                                               tp, sp, wp, wn, h),
+                    lambda: attn_paged_sparse_fwd_workspace_size(T, H, H_kv, d, page_size, max_pages, budget), workspace, dev,
+                    stream, q.device, "attn_paged_sparse_fwd")
     return (out, lse, tables, sel_lens) if return_tables else (out, lse)

@@ -250,3 +250,34 @@ def test_sketch_past_32_bit_offsets():
     code, amp = ref.sketch(last[0].float().numpy())
     assert np.array_equal(s[pages - 1].cpu().numpy(), code) and np.array_equal(a[pages - 1].cpu().numpy(), amp)
     assert int(s[:pages - 1].abs().max()) == 0
+
+
+def test_other_stream():
+    """The whole chain on a side stream, outputs allocated by the calls: the bits of the default stream."""
+    page, H, H_kv, d = 16, 4, 2, 64
+    ctx, new, table, free, num_pages = _state(3, 9, 60, 0, 20, page)
+    total = sum(new) + 2
+    f = attn.rope_inv_freq(d)[0].to(DEV)
+    x = torch.randn((total, H + 2 * H_kv, d), generator=torch.Generator().manual_seed(0)).to(torch.bfloat16).to(DEV)
+    side = torch.cuda.Stream()
+    out = []
+    for stream in (None, side):
+        bt = torch.from_numpy(np.where(table == -7, -1, table)).to(DEV)
+        kc, vc = (torch.zeros((num_pages, page, H_kv, d), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        sk, amp = torch.zeros((num_pages, H_kv, 2 * d), dtype=torch.int8, device=DEV), torch.zeros((num_pages, H_kv), device=DEV)
+        args = _i32(ctx), bt, torch.from_numpy(free).to(DEV), _i32([len(free)])
+        fresh = _i32(new)
+        torch.cuda.synchronize()
+        cu, lens, pos, slots, left = attn.paged_plan(*args, page, num_pages, total, new_lens=fresh, stream=stream)
+        with torch.cuda.stream(side if stream is not None else torch.cuda.current_stream()):
+            qo = torch.zeros((total, H, d), dtype=torch.bfloat16, device=DEV)
+        attn.paged_append(x[:, :H], x[:, H:H + H_kv], x[:, H + H_kv:], kc, vc, slots, positions=pos, inv_freq=f, q_out=qo, stream=stream)
+        attn.page_sketch(kc, bt, lens, sk, amp, cu_seqlens_q=cu, max_q_len=20, stream=stream)
+        qr, kr = attn.rope(x[:, :H], x[:, H:H + H_kv], inv_freq=f, positions=pos, stream=stream)
+        tables, sel = attn.page_select(qo, sk, amp, bt, lens, page, 2, cu_seqlens_q=cu, stream=stream)
+        torch.cuda.synchronize()
+        attn.device_status()
+        out.append((cu, lens, pos, slots, left, bt, kc, vc, qo, sk, amp, qr, kr, tables, sel))
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+    with pytest.raises(ValueError):
+        attn.paged_plan(*args, page, num_pages, total, new_lens=fresh[:-1])
