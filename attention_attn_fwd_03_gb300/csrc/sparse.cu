@@ -546,17 +546,24 @@ bool sparse_fused_ok(int d, int G, int max_pages, int budget) {
 }
 
 cudaError_t launch_sparse(int d, const SparseParams& p, cudaStream_t stream) {
-    // CTAs per (token, KV head): as many as let the whole launch reside on the GPU at once (two CTAs to
-    // an SM, one where a group takes more registers), and no more than there is work for (two chunks
-    // per warp)
+    // CTAs per (token, KV head): no more than let the whole launch reside on the GPU at once (two CTAs to an
+    // SM, one where a group takes more registers), and no more than there is work for.  Up to one CTA per SM
+    // that is a chunk of keys for each attending warp, or a group of pages for each scoring warp; beyond, where
+    // CTAs begin to share SMs, four chunks.  Measured (d = 128, 32 heads over 8, us, CTAs per row 1, 2, 4, 8):
+    // one token, 4 of 500 64-row pages 13.4, 12.5, 11.4, 11.4; 8 of 2000 16-row pages 19.7, 15.9, 13.9, 12.6;
+    // 4 tokens, 16 of 500 64-row pages 22.7, 17.0, 13.8, 14.3; 128 of 4000: 146, 82, 49, 48; more than fit:
+    // 16 tokens, 32 of 500 pages 38.4, 37.3, 47.7, 69.3.
     const SelectParams& s = p.sel;
     const long long rows = (long long)s.total_q * s.H_kv;
     const long long keys = (long long)(s.budget < s.max_pages ? s.budget : s.max_pages) << s.page_shift;
     const int chunk = sparse_chunk_keys(d);
     const long long chunks = (keys + chunk - 1) / chunk;
+    const long long groups = s.budget < s.max_pages ? (s.max_pages + 15) / 16 : 0;  // of pages to score
     const long long resident = kSms * ((s.G + 7) / 8 * d <= 128 ? 2 : 1);
     int cluster = 1;
-    while (cluster < kMaxCluster && rows * cluster * 2 <= resident && chunks >= (long long)cluster * 4 * kWarps)
+    while (cluster < kMaxCluster && rows * cluster * 2 <= resident &&
+           (rows * cluster * 2 <= kSms ? chunks >= (long long)cluster * 2 * kWarps || groups >= (long long)cluster * 2 * kAllWarps
+                                       : chunks >= (long long)cluster * 8 * kWarps))
         cluster *= 2;
     if (d == 128) return launch_d<128>(p, cluster, stream);
     if (d == 64) return launch_d<64>(p, cluster, stream);
