@@ -36,9 +36,9 @@
 // in log2 units, and at the end the (m, l, O) merge over the warps.
 //
 // Measured, d = 128, 32 query heads over 8, 64-row pages: one token of 32000
-// keys, 32 pages chosen: 13.5 us (1.3 to the token's position, 2.8 scores, 2.3
+// keys, 32 pages chosen: 13.7 us (1.3 to the token's position, 2.8 scores, 2.3
 // selection, 3.6 attention, 2.6 merge, the rest launch and barriers); 32 tokens
-// of up to 65536 keys, 64 pages chosen: 99 us, 0.86 of what its bytes take at
+// of up to 65536 keys, 64 pages chosen: 101 us, 0.83 of what its bytes take at
 // the copy rate (14 scores, 3 selection, 66 - 90 attention, 3 merge); 4 tokens
 // of 200000 - 262144 keys, 128 pages chosen: 47 us.
 #include <cooperative_groups.h>
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1) sparse_kernel
                 for (int n = 0; n < NT; ++n) mma16816(sc[y][n], a, qf[n][kk][0], qf[n][kk][1]);
             }
         // sc[y][n][0..1]: key 16 y + lane / 4, heads 2 (lane % 4), + 1; [2..3]: key + 8
-        uint32_t pt[C::KT][NT][2];
+        uint32_t pt[C::KT][NT][2], pr[C::KT][NT][2];  // P^T in bf16, and what that rounding left out
         bool moved = false;
         float alpha[NT][2];
 #pragma unroll
@@ -377,10 +377,14 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1) sparse_kernel
                 }
             }
 #pragma unroll
-            for (int y = 0; y < C::KT; ++y) {
-                pt[y][n][0] = transpose8(pack_bf16(sc[y][n][0], sc[y][n][1]));
-                pt[y][n][1] = transpose8(pack_bf16(sc[y][n][2], sc[y][n][3]));
-            }
+            for (int y = 0; y < C::KT; ++y)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float p0 = sc[y][n][2 * x], p1 = sc[y][n][2 * x + 1];
+                    const uint32_t w = pack_bf16(p0, p1);
+                    pt[y][n][x] = transpose8(w);
+                    pr[y][n][x] = transpose8(pack_bf16(p0 - bf16lo_to_f32(w), p1 - bf16hi_to_f32(w)));
+                }
         }
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
@@ -401,7 +405,10 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1) sparse_kernel
                 const int c = x * 2 + v_chunk;
                 ldsm4_t(a, vt + (c >> 3) * C::PANEL_BYTES + (y * 16 + v_key) * 128 + (((c & 7) ^ (v_key & 7)) << 4));
 #pragma unroll
-                for (int n = 0; n < NT; ++n) mma16816(o[n][x], a, pt[y][n][0], pt[y][n][1]);
+                for (int n = 0; n < NT; ++n) {
+                    mma16816(o[n][x], a, pt[y][n][0], pt[y][n][1]);
+                    mma16816(o[n][x], a, pr[y][n][0], pr[y][n][1]);
+                }
             }
         __syncwarp();  // every lane has read the stage
         if (loaded < mine) {

@@ -197,7 +197,11 @@ attn_status_t attn_page_select(const void* q, const int8_t* sketch, const float*
  * attn_paged_fwd, whose tiles share the keys among 128 rows.
  * Groups of up to 24 heads (d = 64: 32) with a budget of up to 1024 pages and
  * tables of up to 22000 pages run as one kernel that keeps everything on chip;
- * the others as a selection and the kernel of attn_paged_fwd.
+ * the others as a selection and the kernel of attn_paged_fwd.  Scores, maxima
+ * and sums are fp32 on both.  The one kernel takes the probabilities to 2^-16
+ * (as two bf16 numbers each), so O is off by little more than its own rounding
+ * to bf16; the other rounds them to bf16 before the product with V, as
+ * attn_paged_fwd does.
  *   workspace: attn_paged_sparse_fwd_workspace_size bytes, 16-byte aligned,
  *   no initialisation; calls that may overlap need distinct workspaces.  Where
  *   the size is 256 (one kernel) none is used and NULL will do. */
