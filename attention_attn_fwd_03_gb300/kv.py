@@ -164,11 +164,14 @@ def _dense_heads(t, name):
     return s[:-1]
 
 
-def rope_inv_freq(rot, base=10000.0, scaling="none", factor=1.0, orig_len=8192, low=1.0, high=4.0):
+def rope_inv_freq(rot, base=10000.0, scaling="none", factor=1.0, orig_len=8192, low=1.0, high=None):
     """Angle per position of each of the rot / 2 rotated pairs, a float64 CPU tensor, and the amplitude
-    that goes with them (see attn_rope_scaling_t; ``low`` and ``high`` are turns over ``orig_len``)."""
+    that goes with them (see attn_rope_scaling_t; ``low`` and ``high`` are turns over ``orig_len``: 1 and, where
+    ``high`` is None, the end that each kind was published with, 4 for bands and 32 for yarn)."""
     if scaling not in ROPE_SCALINGS:
         raise ValueError("scaling must be one of %s" % ", ".join(ROPE_SCALINGS))
+    if high is None:
+        high = 32.0 if scaling == "yarn" else 4.0
     out = torch.empty(max(int(rot), 0) // 2, dtype=torch.float64)
     amplitude = ctypes.c_double()
     st = attn_rope_inv_freq(out.data_ptr(), ctypes.addressof(amplitude), int(rot), float(base), ROPE_SCALINGS[scaling],

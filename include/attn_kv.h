@@ -43,7 +43,8 @@ typedef enum {
  *   inv_freq: HOST array of rot / 2 doubles (written); amplitude: HOST double
  *   or NULL (written: the factor on rotated vectors, 1 except for YARN).
  *   rot even, in [2, 1024]; base > 1; factor >= 1 (read by the four stretched
- *   kinds); orig_len >= 1 and 0 < low < high (read by BANDS and YARN).
+ *   kinds); orig_len >= 1 and 0 < low < high (read by BANDS and YARN;
+ *   their published ends are 1 and 4 turns for BANDS, 1 and 32 for YARN).
  * Errors: ATTN_ERR_INVALID_ARG. */
 attn_status_t attn_rope_inv_freq(double* inv_freq, double* amplitude, int rot, double base, int scaling,
                                  double factor, int orig_len, double low, double high);
