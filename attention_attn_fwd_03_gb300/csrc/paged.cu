@@ -106,11 +106,13 @@ struct PUnit {
 
 // Query tokens and key count of request r, checked against the launch's
 // bounds.  Offsets out of range drop the request's queries (q_len = 0); a
-// length out of range is clamped.  Either marks the unit bad.
+// length out of range is clamped.  Either marks the unit bad.  Where a
+// selection has listed the units, it writes offsets, lengths and tables while
+// the paged kernel and the merge may already run (ld_dependent).
 __device__ __forceinline__ void request_extent(const PagedParams& p, int r, PUnit& g) {
     g.bad = false;
     if (p.cu_q != nullptr) {
-        const int a = __ldg(p.cu_q + r), b = __ldg(p.cu_q + r + 1);
+        const int a = ld_dependent(p.cu_q + r), b = ld_dependent(p.cu_q + r + 1);
         g.q_start = a;
         g.q_len = b - a;
         if (a < 0 || b < a || b > p.total_q || g.q_len > p.max_q_len) {
@@ -131,7 +133,7 @@ __device__ __forceinline__ void request_extent(const PagedParams& p, int r, PUni
             g.kv_len = 0;
         }
     } else {
-        g.kv_len = __ldg(p.seq_lens + r);
+        g.kv_len = ld_dependent(p.seq_lens + r);
     }
     if (g.kv_len < 0 || g.kv_len > cap) {
         g.bad = true;
@@ -325,7 +327,7 @@ __device__ void producer_role(const PagedParams& p, uint8_t* smem, const PBars& 
                         } else {
                             const int pg = (int)(key / p.page_size);
                             const size_t trow = (size_t)g.r * p.table_heads + (p.table_heads > 1 ? g.kvh : 0);
-                            const int id = __ldg(p.block_table + trow * p.max_pages + pg);
+                            const int id = ld_dependent(p.block_table + trow * p.max_pages + pg);
                             if (id >= 0 && id < p.num_pages)
                                 row = id * p.page_size + (int)(key % p.page_size);
                             else
@@ -871,7 +873,7 @@ __global__ void __launch_bounds__(512) paged_merge_kernel(const PagedParams p) {
         int lo = 0, hi = p.B - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (__ldg(p.cu_q + mid) <= tok)
+            if (ld_dependent(p.cu_q + mid) <= tok)
                 lo = mid;
             else
                 hi = mid - 1;
@@ -882,7 +884,7 @@ __global__ void __launch_bounds__(512) paged_merge_kernel(const PagedParams p) {
     request_extent(p, r, g);
     const int t = tok - g.q_start;
     if (t < 0 || t >= g.q_len) return;  // token not owned by a valid request (reported by the main kernel)
-    if (p.whole != nullptr && __ldg(p.whole + r)) return;  // written by its unit
+    if (p.whole != nullptr && ld_dependent(p.whole + r)) return;  // written by its unit
     const int t0 = (t / p.T) * p.T;
     const int nb = tile_kv_blocks(p, g.q_len, g.kv_len, min(t0 + p.T, g.q_len) - 1);
     const int ns = (nb + p.split_blocks - 1) / p.split_blocks;

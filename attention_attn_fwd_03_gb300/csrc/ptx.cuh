@@ -113,6 +113,14 @@ __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wa
 __device__ __forceinline__ void griddep_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+// A word that the preceding grid may write while this one already runs: read
+// after griddep_wait, and by an ordinary load.  The read-only path (__ldg) asks
+// for data that nobody writes for as long as this kernel lives.
+__device__ __forceinline__ int ld_dependent(const int* p) {
+    int v;
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
 
 // Wait that ignores the abort flag (used only to drain in-flight async work
 // before the CTA releases its shared and tensor memory); bounded in time.
