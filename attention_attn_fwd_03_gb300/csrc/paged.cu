@@ -864,6 +864,7 @@ __global__ void __launch_bounds__(512) paged_merge_kernel(const PagedParams p) {
     constexpr int PER = D / 32;
     static_assert(PER == 4 || PER == 2, "head dim");
     griddep_wait();  // launched early: the partials are complete past this point
+    const bool skip = timeout_recorded(p.status);  // then there are no partials
     const long long gw = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
     const int lane = threadIdx.x & 31;
     if (gw >= (long long)p.total_q * p.H) return;
@@ -883,7 +884,7 @@ __global__ void __launch_bounds__(512) paged_merge_kernel(const PagedParams p) {
     PUnit g;
     request_extent(p, r, g);
     const int t = tok - g.q_start;
-    if (t < 0 || t >= g.q_len) return;  // token not owned by a valid request (reported by the main kernel)
+    if (t < 0 || t >= g.q_len || skip) return;  // token not owned by a valid request (reported by the main kernel)
     if (p.whole != nullptr && ld_dependent(p.whole + r)) return;  // written by its unit
     const int t0 = (t / p.T) * p.T;
     const int nb = tile_kv_blocks(p, g.q_len, g.kv_len, min(t0 + p.T, g.q_len) - 1);

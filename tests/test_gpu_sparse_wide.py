@@ -81,6 +81,26 @@ def test_bad_device_data_is_reported(H, H_kv, d, what):
     attn.device_status()
 
 
+@pytest.mark.parametrize("H,H_kv,d", GROUPS)
+@pytest.mark.parametrize("budget,split", [(8, False), (40, True)])
+def test_recorded_timeout_leaves_outputs_alone(H, H_kv, d, budget, split):
+    c = _case(16, [900, 300], None, H, H_kv, d, 16)
+    g = _gpu(c)
+    _on_wide_path(2, H, H_kv, d, 16, c["table"].shape[1], budget, split)
+    o_ref, l_ref = _sparse(c, g, budget)
+    attn.device_status()
+    o, l = torch.full_like(o_ref, 3.0), torch.full_like(l_ref, 3.0)
+    assert attn.attn_selftest_wait_timeout(torch.cuda.current_stream().cuda_stream) == attn.ATTN_OK
+    _sparse(c, g, budget, out=o, lse=l)
+    with pytest.raises(attn.AttnError) as e:
+        attn.device_status()
+    assert e.value.status == attn.ATTN_ERR_TIMEOUT
+    assert bool((o == 3).all()) and bool((l == 3).all())
+    _sparse(c, g, budget, out=o, lse=l)
+    attn.device_status()
+    assert torch.equal(o, o_ref) and torch.equal(l, l_ref)
+
+
 def test_caches_past_32_bit_offsets():
     """Pages at the end of a cache of more than 2^32 elements (one cache for K and V)."""
     pages, page, H, H_kv, d, n = 66000, 64, 30 * 8, 8, 128, 40
