@@ -225,6 +225,11 @@ __device__ __forceinline__ void st_global_v4(void* ptr, uint32_t a, uint32_t b, 
                  : "memory");
 }
 
+// 1 / l and the LSE of a row.  l = 0: no visible key, O = 0 and LSE = -inf.  A
+// NaN among the visible scores makes l NaN, and both outputs with it.
+__device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float log_sum(float m, float l) { return l == 0.f ? -INFINITY : (m + lg2(l)) * kLn2; }
+
 __device__ __forceinline__ void st_shared_zero16(uint32_t addr) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
 }
@@ -613,7 +618,7 @@ __device__ void softmax_role(const PagedParams& p, uint8_t* smem, const PBars& b
         const float m_use = (m == -INFINITY) ? 0.f : m;
         if (p.n_splits == 1 || g.split < 0) {
             if (!row_ok) continue;
-            const float inv = (l > 0.f) ? 1.f / l : 0.f;
+            const float inv = inverse_sum(l);
             uint16_t* dst = p.o + grow * D;
 #pragma unroll
             for (int c = 0; c < D; c += 8)
@@ -621,13 +626,13 @@ __device__ void softmax_role(const PagedParams& p, uint8_t* smem, const PBars& b
                              pack_bf16(__uint_as_float(o[c + 2]) * inv, __uint_as_float(o[c + 3]) * inv),
                              pack_bf16(__uint_as_float(o[c + 4]) * inv, __uint_as_float(o[c + 5]) * inv),
                              pack_bf16(__uint_as_float(o[c + 6]) * inv, __uint_as_float(o[c + 7]) * inv));
-            if (p.lse != nullptr) p.lse[grow] = (l > 0.f) ? (m_use + lg2(l)) * kLn2 : -INFINITY;
+            if (p.lse != nullptr) p.lse[grow] = log_sum(m_use, l);
         } else if (row_ok) {
             const size_t rec = grow * (size_t)p.n_splits + (size_t)g.split;
             float* po = p.part_o + rec * D;
 #pragma unroll
             for (int c = 0; c < D; c += 4) st_global_v4(po + c, o[c], o[c + 1], o[c + 2], o[c + 3]);
-            *reinterpret_cast<float2*>(p.part_ml + rec * 2) = make_float2((l > 0.f) ? m_use : -INFINITY, l);
+            *reinterpret_cast<float2*>(p.part_ml + rec * 2) = make_float2(l == 0.f ? -INFINITY : m_use, l);
         }
     }
 }
@@ -941,14 +946,14 @@ __global__ void __launch_bounds__(512) paged_merge_kernel(const PagedParams p) {
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    const float inv = (l > 0.f) ? 1.f / l : 0.f;
+    const float inv = inverse_sum(l);
     uint16_t* dst = p.o + (size_t)gw * D + lane * PER;
     if (PER == 4)
         *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv),
                                                     pack_bf16(acc[2] * inv, acc[3] * inv));
     else
         *reinterpret_cast<uint32_t*>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
-    if (lane == 0 && p.lse != nullptr) p.lse[gw] = (l > 0.f) ? (m + lg2(l)) * kLn2 : -INFINITY;
+    if (lane == 0 && p.lse != nullptr) p.lse[gw] = log_sum(m, l);
 }
 
 template <int D>

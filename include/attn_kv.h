@@ -191,8 +191,9 @@ attn_status_t attn_page_select(const void* q, const int8_t* sketch, const float*
  *   cu_seqlens_q (NULL: one token per request, total_q = B) as for
  *   attn_paged_fwd; sketch, amp, budget, first, last as for attn_page_select;
  *   tables, sel_lens: the selection, written when not NULL (both or neither).
- * A token that sees no key gets O = 0 and lse = -inf; rows behind the last
- * request are left as they were.
+ * A token that sees no key gets O = 0 and lse = -inf, one with a NaN among the
+ * scores of its chosen keys NaN in both; rows behind the last request are left
+ * as they were.
  * Each token gathers its own pages: meant for decode steps and the few tokens
  * per request of a drafted continuation; a long prompt is better served by
  * attn_paged_fwd, whose tiles share the keys among 128 rows.
