@@ -103,21 +103,32 @@ __global__ void __launch_bounds__(kSelectThreads) page_select_kernel(const __gri
             p.sched_list[unit] = make_int4(unit, t, k.owned ? 1 : 0, sel_len);
         }
     }
+    auto page_id = [&](int i) {  // of the request's page i; -1 and reported where the table names none
+        const int id = __ldg(table + i);
+        if (id >= 0 && id < p.num_pages) return id;
+        atomicOr(p.status, 1u << kStatusDeviceData);
+        return -1;
+    };
     for (int i = n_sel + tid; i < p.budget; i += kSelectThreads) out[i] = -1;
     if (n_vis <= p.budget) {
-        for (int i = tid; i < n_vis; i += kSelectThreads) out[i] = __ldg(table + i);
+        for (int i = tid; i < n_vis; i += kSelectThreads) out[i] = page_id(i);
         return;
     }
 
     // more pages than the budget: `first` in front, `last` behind, the best of [first, n_vis - last)
     const int need = p.budget - p.first - p.last;
     const int n = n_vis - p.first - p.last;  // > need
-    for (int i = tid; i < p.first; i += kSelectThreads) out[i] = __ldg(table + i);
-    for (int i = tid; i < p.last; i += kSelectThreads) out[p.budget - p.last + i] = __ldg(table + n_vis - p.last + i);
+    for (int i = tid; i < p.first; i += kSelectThreads) out[i] = page_id(i);
+    for (int i = tid; i < p.last; i += kSelectThreads) out[p.budget - p.last + i] = page_id(n_vis - p.last + i);
     if (need == 0) return;
     const uint32_t* keys = p.keys + ((long long)t * p.H_kv + kvh) * p.max_pages + p.first;
-    select_best<kSelectThreads>(keys, n, need, s_bins, scratch,
-                                [&](int place, int i) { out[p.first + place] = __ldg(table + p.first + i); });
+    const uint32_t lowest = select_best<kSelectThreads>(
+        keys, n, need, s_bins, scratch, [&](int place, int i) { out[p.first + place] = __ldg(table + p.first + i); });
+    if (lowest == ordered(-INFINITY)) {  // rare: pages that do not exist may be among the chosen (the scores reported them)
+        __syncthreads();
+        for (int i = p.first + tid; i < p.budget - p.last; i += kSelectThreads)
+            if (out[i] < 0 || out[i] >= p.num_pages) out[i] = -1;
+    }
 }
 
 template <int D>

@@ -324,8 +324,9 @@ __device__ __forceinline__ void for_keys(const uint32_t* keys, int n, F f) {
 }
 
 // Calls emit(place, i) for the `need` (1 <= need < n) best of keys[0 .. n - 1],
-// ties to the smaller i, place = 0 .. need - 1 in the order of i.  bins: kBins
-// words of shared memory.  All NTHREADS threads call it.
+// ties to the smaller i, place = 0 .. need - 1 in the order of i, and returns the
+// smallest key among them.  bins: kBins words of shared memory.  All NTHREADS
+// threads call it.
 //
 // The keys between the smallest and the largest are counted in up to kBins
 // equal intervals, which leaves a few contenders in the interval where the
@@ -333,7 +334,7 @@ __device__ __forceinline__ void for_keys(const uint32_t* keys, int n, F f) {
 // interval with more of them (outliers had stretched the range, or scores tie)
 // is divided again, ten bits of the range at a time, until it holds one value.
 template <int NTHREADS, class Emit>
-__device__ __forceinline__ void select_best(const uint32_t* keys, int n, int need, int* bins,
+__device__ __forceinline__ uint32_t select_best(const uint32_t* keys, int n, int need, int* bins,
                                             SelectScratch<NTHREADS>& s, Emit emit) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint32_t lo = 0xffffffffu, hi = 0u;
@@ -473,6 +474,7 @@ __device__ __forceinline__ void select_best(const uint32_t* keys, int n, int nee
             equal += __popc(eq);
         }
     }
+    return value;
 }
 
 }  // namespace

@@ -256,7 +256,10 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1) sparse_kernel
     const int n_keys = skip ? 0 : sel_len;
     if (sp.tables != nullptr && rank == 0) {
         int32_t* out = sp.tables + (long long)row * sp.budget;
-        for (int i = tid; i < sp.budget; i += kThreads) out[i] = i < n_sel ? s_list[i] : -1;
+        for (int i = tid; i < sp.budget; i += kThreads) {  // an id out of range becomes -1 (its loads report it)
+            const int id = i < n_sel ? s_list[i] : -1;
+            out[i] = id < sp.num_pages ? max(id, -1) : -1;
+        }
         if (tid == 0 && kvh == 0) sp.sel_lens[t] = sel_len;
     }
 

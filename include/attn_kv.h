@@ -168,7 +168,7 @@ attn_status_t attn_page_sketch(const void* k_cache, const int32_t* block_table, 
  * scores and non-finite sketches count as +inf; |q_h|max infinite or NaN makes
  * that head's score +inf.)
  *   tables: int32 [total_q, H_kv, budget], the chosen pages' physical ids in
- *   the order of their keys, -1 behind them; sel_lens: int32 [total_q], the
+ *   the order of their keys (-1 for one out of range), -1 behind them; sel_lens: int32 [total_q], the
  *   keys they hold for the token: the same for every KV head, since a token's
  *   own page, the only one that may be partial, is always chosen.  Tokens
  *   behind the last request, and tokens that see no key, get 0 and -1.
