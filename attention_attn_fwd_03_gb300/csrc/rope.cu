@@ -4,12 +4,14 @@
 //   a' = s (a cos t - b sin t),  b' = s (a sin t + b cos t).
 //
 // The angle.  In units of a whole turn it is P f_i / 2 pi, of which only the
-// fraction matters.  f_i / 2 pi is held as a 64-bit binary fraction, so that
-// the integer product with P, taken modulo 2^64, is that fraction exactly
-// reduced, for any 32-bit P and either sign, without float64 arithmetic per
-// angle (one conversion per frequency and CTA).  Converted to fp32
-// in (-1, 1] half turns it feeds sincospif: the angle is off by at most 2^-25
-// half turns however far the position.
+// fraction matters.  f_i / 2 pi is held as a 64-bit binary fraction, so that the
+// integer product with P, taken modulo 2^64, is that fraction to |P| 2^-63 turns
+// for any 32-bit P and either sign, without float64 arithmetic.  Its first 24
+// bits, as fp32 half turns in [-1, 1), feed sincospif; the angle e of the next
+// 32 (below 2^-23 half turns) turns the result once more: (cos - e sin, sin + e
+// cos), off by e^2 / 2 < 2^-43 of either.  So the cosine and sine are those
+// functions' own (1 ulp) and one more rounding, however far the position, and
+// small ones keep their relative accuracy.
 //
 // Work.  Bound by memory: each element is read and written once, 3 flops
 // each.  A CTA takes TOK consecutive tokens and all (or a share) of their
@@ -81,11 +83,28 @@ __device__ __forceinline__ void st16(char* p, const uint4& v, bool stream) {
                      : "memory");
 }
 
-// f / 2 pi modulo 1 as a 64-bit binary fraction.
+// f / 2 pi modulo 1 as a 64-bit binary fraction, from the bits of f = +- m 2^e
+// with m shifted to the top of 64 bits: m / 2 pi by 128 bits of 1 / 2 pi, as
+// whole + part 2^-64, then shifted to units of 2^-64 turns.  Good to two units for
+// |f| < 2^63 (beyond: 0).  Integers, because float64 is slow here: a product carried
+// in two doubles cost every call 0.2 us.
+__device__ __forceinline__ unsigned long long turn_fraction(unsigned long long m, int e, bool negative) {
+    constexpr unsigned long long kHi = 0x28be60db9391054aULL, kLo = 0x7f09d5f47d4d3770ULL;
+    const unsigned long long low = m * kHi, carry = __umul64hi(m, kLo), part = low + carry;
+    const unsigned long long whole = __umul64hi(m, kHi) + (part < low ? 1ULL : 0ULL);
+    const int s = 64 + e;
+    const unsigned long long turns = s <= -64 ? 0ULL : s <= 0 ? whole >> -s : s < 64 ? whole << s | part >> (64 - s) : 0ULL;
+    return negative ? 0ULL - turns : turns;
+}
 __device__ __forceinline__ unsigned long long turn_fraction(double f) {
-    double t = f * 0.15915494309189533577;
-    t -= floor(t);
-    return __double2ull_rn(t * 18446744073709551616.0);
+    const unsigned long long b = (unsigned long long)__double_as_longlong(f);
+    const int x = (int)(b >> 52) & 0x7ff;
+    return turn_fraction(((b << 11) & 0x7fffffffffffffffULL) | (x ? 1ULL << 63 : 0ULL), (x ? x : 1) - 1086, (b >> 63) != 0);
+}
+__device__ __forceinline__ unsigned long long turn_fraction(float f) {
+    const unsigned b = __float_as_uint(f);
+    const int x = (int)(b >> 23) & 0xff;
+    return turn_fraction(((unsigned long long)(b << 8 & 0x7fffffffu) << 32) | (x ? 1ULL << 63 : 0ULL), (x ? x : 1) - 190, (b >> 31) != 0);
 }
 
 template <int EB>
@@ -134,8 +153,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     const int t0 = tile * p.tok;  // within n_tokens < 2^31 by the grid
 
     for (int i = tid; i < half; i += kThreads)
-        s_turn[i] = turn_fraction(p.freq64 ? static_cast<const double*>(p.freq)[i]
-                                           : (double)static_cast<const float*>(p.freq)[i]);
+        s_turn[i] = p.freq64 ? turn_fraction(static_cast<const double*>(p.freq)[i])
+                             : turn_fraction(static_cast<const float*>(p.freq)[i]);
     const int units = p.d / (2 * VN);        // units of a head vector: 4, 8 or 16
     const int r_units = p.rot / (2 * VN);    // of which this many rotate
     __syncthreads();
@@ -153,8 +172,12 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
             pos = t % p.N;
         }
         const unsigned long long phase = s_turn[i] * (unsigned long long)(long long)pos;
-        float sn, cs;
-        sincospif((float)(long long)phase * 1.0842021724855044e-19f, &sn, &cs);  // 2^-63: half turns
+        // half turns: 24 bits exactly in fp32, and the 32 bits below them, in radians
+        const int top = (int)(phase >> 32) & ~0xff;
+        const float e = (float)(unsigned)(phase >> 8) * 8.7196712450215807e-17f;  // 2^-55 pi
+        float s0, c0;
+        sincospif((float)top * 4.6566128730773926e-10f, &s0, &c0);  // 2^-31
+        const float cs = fmaf(-e, s0, c0), sn = fmaf(e, c0, s0);
         const int at = k * half + (VN == 8 ? ((i >> 2) & 1) * (half >> 1) : 0) + (i / VN) * 4 + (i & 3);
         s_cos[at] = cs * p.amplitude;
         s_sin[at] = sn * p.sign * p.amplitude;

@@ -70,9 +70,9 @@ attn_status_t attn_rope_inv_freq(double* inv_freq, double* amplitude, int rot, d
  *   inv_freq: DEVICE array of rot / 2 float64 (freq_bits 64) or fp32 (32).
  *   d in {64, 128}; rot a multiple of 16 in [16, d]; B, H, N >= 1;
  *   B * N < 2^31, H and H_k at most 65535; amplitude finite.
- * P f_i / 2 pi is taken modulo 1 in 64-bit fixed point, so far positions lose
- * no more than float64 arithmetic would; the rotation is fp32 and rounds once
- * to the output type.
+ * P f_i / 2 pi is taken modulo 1 in 64-bit fixed point, good to |P| 2^-63 turns
+ * (|f_i| < 2^63), and its cosine and sine are fp32, good to 2 ulp (or 2^-44) at any
+ * position; the rotation is fp32 and rounds once to the output type.
  * Errors: ATTN_ERR_INVALID_ARG / ATTN_ERR_UNSUPPORTED before the launch;
  * ATTN_ERR_CUDA when it fails. */
 attn_status_t attn_rope(const void* q, void* q_out, const void* k, void* k_out, const int32_t* positions,
