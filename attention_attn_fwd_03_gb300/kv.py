@@ -104,6 +104,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
+def _dims(t, name, n):
+    """Refuses what is not a tensor of n dims (its dtype, device and shape are checked with the others')."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.dim() != n:
+        raise ValueError("%s must have %d dims" % (name, n))
+
+
 def _device(t, name):
     """Index of the current CUDA device, which t has to be on."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -150,6 +158,7 @@ def _on(stream):
 
 def _freqs(inv_freq, dev):
     """(address, bits, rotated dims) of the frequencies."""
+    _dims(inv_freq, "inv_freq", 1)
     if inv_freq.dtype not in (torch.float64, torch.float32):
         raise TypeError("inv_freq must be float64 or float32, got %s" % inv_freq.dtype)
     return (_check(inv_freq, "inv_freq", inv_freq.dtype, dev, (inv_freq.numel(),)),
@@ -199,8 +208,7 @@ def rope(q, k=None, *, inv_freq, positions=None, interleaved=False, inverse=Fals
     shape = q.shape
     H_k = 0
     if k is not None:
-        if not isinstance(k, torch.Tensor) or k.dim() != q.dim():
-            raise ValueError("k must have the dims of q")
+        _dims(k, "k", q.dim())
         H_k = k.shape[1]
     with _on(stream):
         if q_out is None:
@@ -223,6 +231,8 @@ def rope(q, k=None, *, inv_freq, positions=None, interleaved=False, inverse=Fals
     fp, bits, rot = _freqs(inv_freq, dev)
     pp, pb = None, 0
     if positions is not None:
+        if not isinstance(positions, torch.Tensor):
+            raise TypeError("positions must be a CUDA tensor")
         if positions.dim() == 2 and len(shape) == 4:
             pp, pb = _check(positions, "positions", torch.int32, dev, (B, N)), N
         else:
@@ -245,8 +255,9 @@ def paged_plan(ctx_lens, block_table, free_pages, free_count, page_size, num_pag
     Returns (cu_seqlens_q [B + 1], seq_lens [B], positions [total_q], slots [total_q], free_left [1])."""
     dev = _device(ctx_lens, "ctx_lens")
     i32, total_q = torch.int32, int(total_q)
-    if ctx_lens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
-        raise ValueError("ctx_lens and free_pages must have 1 dim, block_table 2")
+    _dims(ctx_lens, "ctx_lens", 1)
+    _dims(block_table, "block_table", 2)
+    _dims(free_pages, "free_pages", 1)
     if total_q < 1:
         raise ValueError("total_q must be at least 1")
     B, max_pages = ctx_lens.shape[0], block_table.shape[1]
@@ -278,8 +289,8 @@ def paged_append(q, k, v, k_cache, v_cache, slots, positions=None, inv_freq=None
     None: nothing rotates.  q_out may be q.  Returns q_out."""
     dev = _device(k, "k")
     bf = torch.bfloat16
-    if k.dim() != 3 or k_cache.dim() != 4:
-        raise ValueError("k must have 3 dims and k_cache 4")
+    _dims(k, "k", 3)
+    _dims(k_cache, "k_cache", 4)
     if (positions is None) != (inv_freq is None):
         raise ValueError("positions and inv_freq go together")
     T, H_kv, d = k.shape
@@ -288,8 +299,7 @@ def paged_append(q, k, v, k_cache, v_cache, slots, positions=None, inv_freq=None
     qp = qop = None
     qs = qos = (0, 0)
     if q is not None:
-        if not isinstance(q, torch.Tensor) or q.dim() != 3:
-            raise ValueError("q must have 3 dims")
+        _dims(q, "q", 3)
         H = q.shape[1]
         if q_out is None:
             with _on(stream):
@@ -320,8 +330,8 @@ def page_sketch(k_cache, block_table, seq_lens, sketch, amp, cu_seqlens_q=None, 
     ``max_q_len``).  k_cache bf16 [num_pages, page_size, H_kv, d]; block_table int32 [B, max_pages];
     seq_lens int32 [B]; sketch int8 [num_pages, H_kv, 2 d]; amp fp32 [num_pages, H_kv]."""
     dev = _device(k_cache, "k_cache")
-    if k_cache.dim() != 4 or block_table.dim() != 2:
-        raise ValueError("k_cache must have 4 dims and block_table 2")
+    _dims(k_cache, "k_cache", 4)
+    _dims(block_table, "block_table", 2)
     num_pages, page_size, H_kv, d = k_cache.shape
     B, max_pages = block_table.shape
     i32 = torch.int32
@@ -337,8 +347,9 @@ def page_sketch(k_cache, block_table, seq_lens, sketch, amp, cu_seqlens_q=None, 
 
 def _selection_args(q, sketch, amp, block_table, seq_lens, cu_seqlens_q, dev):
     """Checked pointers and sizes that selection and sparse attention share."""
-    if q.dim() != 3 or block_table.dim() != 2 or sketch.dim() != 3:
-        raise ValueError("q and sketch must have 3 dims, block_table 2")
+    _dims(q, "q", 3)
+    _dims(block_table, "block_table", 2)
+    _dims(sketch, "sketch", 3)
     T, H, d = q.shape
     B, max_pages = block_table.shape
     num_pages, H_kv = sketch.shape[0], sketch.shape[1]
@@ -405,8 +416,7 @@ def paged_sparse_fwd(q, k_cache, v_cache, block_table, seq_lens, sketch, amp, bu
     ptrs, (B, T, H, H_kv, d), max_pages, num_pages = _selection_args(q, sketch, amp, block_table, seq_lens,
                                                                      cu_seqlens_q, dev)
     bf = torch.bfloat16
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache must have 4 dims")
+    _dims(k_cache, "k_cache", 4)
     page_size, budget = k_cache.shape[1], int(budget)
     cache = (num_pages, page_size, H_kv, d)
     kp, vp = _check(k_cache, "k_cache", bf, dev, cache), _check(v_cache, "v_cache", bf, dev, cache)
