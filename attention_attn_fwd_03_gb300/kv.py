@@ -210,6 +210,8 @@ def rope(q, k=None, *, inv_freq, positions=None, interleaved=False, inverse=Fals
     if k is not None:
         _dims(k, "k", q.dim())
         H_k = k.shape[1]
+    elif k_out is not None:
+        raise ValueError("k_out without k")
     with _on(stream):
         if q_out is None:
             q_out = torch.empty(shape, dtype=dt, device=q.device)

@@ -56,3 +56,11 @@ def test_what_is_no_tensor_is_a_type_error(name):
         for arg in ("positions", "inv_freq"):
             with pytest.raises(ValueError):
                 call(**dict(kw, **{arg: None}))
+
+
+def test_k_out_without_k_is_refused():
+    call, kw = _calls()["rope"]
+    out = torch.full((2, 2, 3, 64), 5.0, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError):
+        call(**dict(kw, k=None, k_out=out))
+    assert bool((out == 5).all())
