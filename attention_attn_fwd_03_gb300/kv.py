@@ -112,6 +112,14 @@ def _dims(t, name, n):
         raise ValueError("%s must have %d dims" % (name, n))
 
 
+def _size(x, name):
+    """x as a C int, which would take its low 32 bits without a word."""
+    x = int(x)
+    if not -0x80000000 <= x <= 0x7fffffff:
+        raise ValueError("%s = %d does not fit 32 bits" % (name, x))
+    return x
+
+
 def _device(t, name):
     """Index of the current CUDA device, which t has to be on."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -181,10 +189,11 @@ def rope_inv_freq(rot, base=10000.0, scaling="none", factor=1.0, orig_len=8192, 
         raise ValueError("scaling must be one of %s" % ", ".join(ROPE_SCALINGS))
     if high is None:
         high = 32.0 if scaling == "yarn" else 4.0
-    out = torch.empty(max(int(rot), 0) // 2, dtype=torch.float64)
+    rot, orig_len = _size(rot, "rot"), _size(orig_len, "orig_len")
+    out = torch.empty(max(rot, 0) // 2, dtype=torch.float64)
     amplitude = ctypes.c_double()
-    st = attn_rope_inv_freq(out.data_ptr(), ctypes.addressof(amplitude), int(rot), float(base), ROPE_SCALINGS[scaling],
-                            float(factor), int(orig_len), float(low), float(high))
+    st = attn_rope_inv_freq(out.data_ptr(), ctypes.addressof(amplitude), rot, float(base), ROPE_SCALINGS[scaling],
+                            float(factor), orig_len, float(low), float(high))
     _raise(st, "attn_rope_inv_freq")
     return out, amplitude.value
 
@@ -256,7 +265,7 @@ def paged_plan(ctx_lens, block_table, free_pages, free_count, page_size, num_pag
     seq_lens may be ctx_lens and free_left may be free_count.
     Returns (cu_seqlens_q [B + 1], seq_lens [B], positions [total_q], slots [total_q], free_left [1])."""
     dev = _device(ctx_lens, "ctx_lens")
-    i32, total_q = torch.int32, int(total_q)
+    i32, total_q = torch.int32, _size(total_q, "total_q")
     _dims(ctx_lens, "ctx_lens", 1)
     _dims(block_table, "block_table", 2)
     _dims(free_pages, "free_pages", 1)
@@ -275,8 +284,8 @@ def paged_plan(ctx_lens, block_table, free_pages, free_count, page_size, num_pag
                          None if new_lens is None else _check(new_lens, "new_lens", i32, dev, (B,)),
                          _check(block_table, "block_table", i32, dev, (B, max_pages)),
                          _check(free_pages, "free_pages", i32, dev, (free_pages.shape[0],)),
-                         _check(free_count, "free_count", i32, dev, (1,)), B, total_q, int(page_size), max_pages,
-                         int(num_pages), free_pages.shape[0], *outs, _handle(stream, dev))
+                         _check(free_count, "free_count", i32, dev, (1,)), B, total_q, _size(page_size, "page_size"), max_pages,
+                         _size(num_pages, "num_pages"), free_pages.shape[0], *outs, _handle(stream, dev))
     _raise(st, "attn_paged_plan")
     return tuple(given)
 
@@ -295,7 +304,7 @@ def paged_append(q, k, v, k_cache, v_cache, slots, positions=None, inv_freq=None
     _dims(k_cache, "k_cache", 4)
     if (positions is None) != (inv_freq is None):
         raise ValueError("positions and inv_freq go together")
-    T, H_kv, d = k.shape
+    T, H_kv, d = _size(k.shape[0], "the number of tokens"), k.shape[1], k.shape[2]
     num_pages, page_size = k_cache.shape[0], k_cache.shape[1]
     H = 0
     qp = qop = None
@@ -340,7 +349,7 @@ def page_sketch(k_cache, block_table, seq_lens, sketch, amp, cu_seqlens_q=None, 
     st = lib().attn_page_sketch(_check(k_cache, "k_cache", torch.bfloat16, dev, k_cache.shape),
                           _check(block_table, "block_table", i32, dev, (B, max_pages)),
                           None if cu_seqlens_q is None else _check(cu_seqlens_q, "cu_seqlens_q", i32, dev, (B + 1,)),
-                          _check(seq_lens, "seq_lens", i32, dev, (B,)), B, int(max_q_len), H_kv, d, page_size,
+                          _check(seq_lens, "seq_lens", i32, dev, (B,)), B, _size(max_q_len, "max_q_len"), H_kv, d, page_size,
                           max_pages, num_pages, _check(sketch, "sketch", torch.int8, dev, (num_pages, H_kv, 2 * d)),
                           _check(amp, "amp", torch.float32, dev, (num_pages, H_kv)), _handle(stream, dev))
     _raise(st, "attn_page_sketch")
@@ -388,7 +397,8 @@ def page_select(q, sketch, amp, block_table, seq_lens, page_size, budget, first=
     dev = _device(q, "q")
     ptrs, (B, T, H, H_kv, d), max_pages, num_pages = _selection_args(q, sketch, amp, block_table, seq_lens,
                                                                      cu_seqlens_q, dev)
-    budget = int(budget)
+    page_size, budget = _size(page_size, "page_size"), _size(budget, "budget")
+    first, last = _size(first, "first"), _size(last, "last")
     if budget < 1:
         raise AttnError(ATTN_ERR_INVALID_ARG, "attn_page_select")
     with _on(stream):
@@ -399,8 +409,8 @@ def page_select(q, sketch, amp, block_table, seq_lens, page_size, budget, first=
     tp = _check(tables, "tables", torch.int32, dev, (T, H_kv, budget))
     lp = _check(sel_lens, "sel_lens", torch.int32, dev, (T,))
     h = _handle(stream, dev)
-    _with_workspace(lambda wp, wn: lib().attn_page_select(*ptrs, B, T, H, H_kv, d, int(page_size), max_pages, num_pages, budget,
-                                                          int(first), int(last), tp, lp, wp, wn, h),
+    _with_workspace(lambda wp, wn: lib().attn_page_select(*ptrs, B, T, H, H_kv, d, page_size, max_pages, num_pages, budget,
+                                                          first, last, tp, lp, wp, wn, h),
                     lambda: attn_page_select_workspace_size(T, H_kv, max_pages, budget), workspace, dev, stream, q.device,
                     "attn_page_select")
     return tables, sel_lens
@@ -419,7 +429,8 @@ def paged_sparse_fwd(q, k_cache, v_cache, block_table, seq_lens, sketch, amp, bu
                                                                      cu_seqlens_q, dev)
     bf = torch.bfloat16
     _dims(k_cache, "k_cache", 4)
-    page_size, budget = k_cache.shape[1], int(budget)
+    page_size, budget = k_cache.shape[1], _size(budget, "budget")
+    first, last = _size(first, "first"), _size(last, "last")
     cache = (num_pages, page_size, H_kv, d)
     kp, vp = _check(k_cache, "k_cache", bf, dev, cache), _check(v_cache, "v_cache", bf, dev, cache)
     tables = sel_lens = None
@@ -438,7 +449,7 @@ def paged_sparse_fwd(q, k_cache, v_cache, block_table, seq_lens, sketch, amp, bu
     sc, h = float(scale) if scale is not None else 1.0 / math.sqrt(d), _handle(stream, dev)
     qp, skp, ap, bp, cp, np_ = ptrs
     _with_workspace(lambda wp, wn: lib().attn_paged_sparse_fwd(qp, kp, vp, bp, cp, np_, skp, ap, B, T, H, H_kv, d, page_size,
-                                                               max_pages, num_pages, budget, int(first), int(last), sc, op, lp,
+                                                               max_pages, num_pages, budget, first, last, sc, op, lp,
                                                                tp, sp, wp, wn, h),
                     lambda: attn_paged_sparse_fwd_workspace_size(T, H, H_kv, d, page_size, max_pages, budget), workspace, dev,
                     stream, q.device, "attn_paged_sparse_fwd")

@@ -64,3 +64,16 @@ def test_k_out_without_k_is_refused():
     with pytest.raises(ValueError):
         call(**dict(kw, k=None, k_out=out))
     assert bool((out == 5).all())
+
+
+@pytest.mark.parametrize("name,arg", [("paged_plan", "page_size"), ("paged_plan", "num_pages"), ("paged_plan", "total_q"),
+                                      ("page_sketch", "max_q_len"), ("page_select", "page_size"), ("page_select", "budget"),
+                                      ("page_select", "first"), ("page_select", "last"), ("paged_sparse_fwd", "budget"),
+                                      ("paged_sparse_fwd", "first"), ("paged_sparse_fwd", "last")])
+def test_sizes_past_32_bits_do_not_wrap(name, arg):
+    """2^32 more than a good value is not that value."""
+    call, kw = _calls()[name]
+    good = dict(dict(first=0, last=1, max_q_len=1), **kw)[arg]
+    with pytest.raises((ValueError, attn.AttnError)):
+        call(**dict(kw, **{arg: good + 2 ** 32}))
+    attn.device_status()

@@ -37,3 +37,9 @@ def test_yarn_by_default_matches_its_formula():
         keep = 1.0 - min(max((i - lo) / (hi - lo), 0.0), 1.0)
         assert abs(g - (keep * f + (1 - keep) * f / factor)) <= 1e-13 * f
     assert abs(amp - (0.1 * math.log(factor) + 1.0)) < 1e-15
+
+
+@pytest.mark.parametrize("kw", [dict(orig_len=2 ** 32 + 8192), dict(orig_len=-2 ** 31 - 1), dict(rot=2 ** 32 + 64)])
+def test_sizes_past_32_bits_do_not_wrap(kw):
+    with pytest.raises(ValueError):
+        attn.rope_inv_freq(**dict(dict(rot=64, scaling="yarn", factor=2.0), **kw))
