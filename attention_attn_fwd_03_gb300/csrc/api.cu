@@ -833,7 +833,7 @@ attn_status_t attn_paged_sparse_fwd(const void* q, const void* k_cache, const vo
         p.lse = lse;
         p.kv_rows = (int)slots;
         p.c_scale = c_scale;
-        return from_cuda(launch_sparse(d, p, cs));
+        return from_cuda(launch_sparse(d, p, ds->sm_count, cs));
     }
     char* ws = static_cast<char*>(workspace);
     s.keys = reinterpret_cast<uint32_t*>(ws);

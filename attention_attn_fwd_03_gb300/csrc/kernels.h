@@ -184,7 +184,7 @@ struct SparseParams {
 };
 constexpr int sparse_chunk_keys(int d) { return d == 128 ? 16 : 32; }
 bool sparse_fused_ok(int d, int G, int max_pages, int budget);
-cudaError_t launch_sparse(int d, const SparseParams& p, cudaStream_t stream);
+cudaError_t launch_sparse(int d, const SparseParams& p, int sm_count, cudaStream_t stream);
 
 // Failure-handling test: a bounded wait that nothing completes (selftest.cu).
 cudaError_t launch_selftest_timeout(unsigned* status, cudaStream_t stream);

@@ -63,7 +63,6 @@ constexpr int kThreads = kAllWarps * 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxG = 32;       // query heads per KV head: four column tiles
 constexpr int kMaxBudget = 1024;  // pages in a CTA's list
-constexpr long long kSms = 152;
 
 template <int D>
 struct SCfg {
@@ -512,34 +511,87 @@ __global__ void __launch_bounds__(kThreads, NT * D <= 128 ? 2 : 1) sparse_kernel
 }
 
 template <int D, int NT>
-cudaError_t launch_t(const SparseParams& p, int cluster, cudaStream_t stream) {
-    using C = SCfg<D>;
-    static std::atomic<unsigned long long> opted{0};
-    const cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(sparse_kernel<D, NT>), C::SMEM_BYTES, opted);
-    if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr[1];
+cudaLaunchConfig_t launch_config(int cluster, cudaLaunchAttribute* attr) {
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)cluster;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)p.sel.total_q * p.sel.H_kv * cluster));
+    cfg.gridDim = dim3((unsigned)cluster);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = C::SMEM_BYTES;
-    cfg.stream = stream;
+    cfg.dynamicSmemBytes = SCfg<D>::SMEM_BYTES;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    return cfg;
+}
+
+// Clusters of 2^log2 CTAs that the device holds at once, asked once per device: a cluster stays within a
+// group of SMs, so these are fewer than the SMs' CTAs make up (groups of 18 SMs hold two clusters of
+// eight with one CTA to an SM).
+template <int D, int NT>
+cudaError_t resident_clusters(int log2, int* n) {
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices][4];  // the number + 1; 0: not asked yet
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
+    std::atomic<int>& k = known[dev][log2];
+    *n = k.load(std::memory_order_acquire) - 1;
+    if (*n >= 0) return cudaSuccess;
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = launch_config<D, NT>(1 << log2, attr);
+    e = cudaOccupancyMaxActiveClusters(n, sparse_kernel<D, NT>, &cfg);
+    if (e == cudaSuccess) k.store(*n + 1, std::memory_order_release);
+    return e;
+}
+
+// CTAs per (token, KV head): no more than let the whole launch reside on the GPU at once, and no more than there
+// is work for.  Up to one CTA per SM that is a chunk of keys for each attending warp, or a group of pages for
+// each scoring warp; beyond, where CTAs begin to share SMs, four chunks.  Measured (d = 128, us, CTAs per row
+// 1, 2, 4, 8; 32 heads over 8): one token, 4 of 500 64-row pages 13.4, 12.5, 11.4, 11.4; 8 of 2000 16-row pages
+// 19.7, 15.9, 13.9, 12.6; 4 tokens, 16 of 500 64-row pages 22.7, 17.0, 13.8, 14.3; 128 of 4000: 146, 82, 49, 48;
+// more than fit: 16 tokens, 32 of 500 pages 38.4, 37.3, 47.7, 69.3.
+// Pages are counted by the table's width, since the lengths are on the device: one token of 2000 keys in 16-row
+// pages, 8 of them, takes 10.3, 11.0, 11.7, 11.8 and 11.0 by the rule in a table of its own 125 pages, 11.8 in
+// one of 1024 to 16384.
+template <int D, int NT>
+cudaError_t launch_t(const SparseParams& p, int sm_count, cudaStream_t stream) {
+    static std::atomic<unsigned long long> opted{0};
+    cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(sparse_kernel<D, NT>), SCfg<D>::SMEM_BYTES, opted);
+    if (e != cudaSuccess) return e;
+    const SelectParams& s = p.sel;
+    const long long rows = (long long)s.total_q * s.H_kv;
+    const long long keys = (long long)(s.budget < s.max_pages ? s.budget : s.max_pages) << s.page_shift;
+    const long long chunks = (keys + SCfg<D>::KEYS - 1) / SCfg<D>::KEYS;
+    const long long groups = s.budget < s.max_pages ? (s.max_pages + 15) / 16 : 0;  // of pages to score
+    int log2 = 0;
+    while ((1 << log2) < kMaxCluster) {
+        const int next = 1 << (log2 + 1);
+        if (rows * next <= sm_count ? chunks < (long long)next * kWarps && groups < (long long)next * kAllWarps
+                                    : chunks < (long long)next * 4 * kWarps)
+            break;
+        int fit = 0;
+        e = resident_clusters<D, NT>(log2 + 1, &fit);
+        if (e != cudaSuccess) return e;
+        if (rows > fit) break;
+        ++log2;
+    }
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = launch_config<D, NT>(1 << log2, attr);
+    cfg.gridDim = dim3((unsigned)(rows << log2));
+    cfg.stream = stream;
     return cudaLaunchKernelEx(&cfg, sparse_kernel<D, NT>, p);
 }
 
 template <int D>
-cudaError_t launch_d(const SparseParams& p, int cluster, cudaStream_t stream) {
+cudaError_t launch_d(const SparseParams& p, int sm_count, cudaStream_t stream) {
     switch ((p.sel.G + 7) / 8) {
-    case 1: return launch_t<D, 1>(p, cluster, stream);
-    case 2: return launch_t<D, 2>(p, cluster, stream);
-    case 3: return launch_t<D, 3>(p, cluster, stream);
+    case 1: return launch_t<D, 1>(p, sm_count, stream);
+    case 2: return launch_t<D, 2>(p, sm_count, stream);
+    case 3: return launch_t<D, 3>(p, sm_count, stream);
     case 4:
-        if constexpr (D == 64) return launch_t<D, 4>(p, cluster, stream);
+        if constexpr (D == 64) return launch_t<D, 4>(p, sm_count, stream);
     }
     return cudaErrorInvalidValue;
 }
@@ -547,36 +599,19 @@ cudaError_t launch_d(const SparseParams& p, int cluster, cudaStream_t stream) {
 }  // namespace
 
 // Larger groups run on the paged kernel's tiles of 128 rows, whose cost does
-// not grow with the group.  Measured there and here, us, 32 tokens of 4 KV heads
-// over 4096 of 16384 - 32768 keys (d = 128): G = 8: 74 and 58, 16: 77 and 66,
-// 24: 83 and 74, 32: 85 and 108 (four column tiles need all registers);
-// d = 64, G = 32: 66 and 48.
+// not grow with the group.  Measured there and here, us, tokens of 4 KV heads
+// over 4096 of 16384 - 32768 keys: d = 128, 32 tokens, G = 8: 79 and 60, 12: 80
+// and 73, 16: 82 and 74, 24: 89 and 86, 32: 91 and 117 (four column tiles need all
+// registers); 4 tokens, G = 16: 31 and 29, 24: 33 and 35; d = 64, 32 tokens, G = 16:
+// 66 and 48 (two column tiles at 128 registers spill 56 bytes), 24: 68 and 50,
+// 32: 69 and 57; 4 tokens, G = 32: 30 and 26.
 bool sparse_fused_ok(int d, int G, int max_pages, int budget) {
     return G <= (d == 128 ? 24 : kMaxG) && budget <= kMaxBudget && max_pages <= (d == 128 ? SCfg<128>::MAX_PAGES : SCfg<64>::MAX_PAGES);
 }
 
-cudaError_t launch_sparse(int d, const SparseParams& p, cudaStream_t stream) {
-    // CTAs per (token, KV head): no more than let the whole launch reside on the GPU at once (two CTAs to an
-    // SM, one where a group takes more registers), and no more than there is work for.  Up to one CTA per SM
-    // that is a chunk of keys for each attending warp, or a group of pages for each scoring warp; beyond, where
-    // CTAs begin to share SMs, four chunks.  Measured (d = 128, 32 heads over 8, us, CTAs per row 1, 2, 4, 8):
-    // one token, 4 of 500 64-row pages 13.4, 12.5, 11.4, 11.4; 8 of 2000 16-row pages 19.7, 15.9, 13.9, 12.6;
-    // 4 tokens, 16 of 500 64-row pages 22.7, 17.0, 13.8, 14.3; 128 of 4000: 146, 82, 49, 48; more than fit:
-    // 16 tokens, 32 of 500 pages 38.4, 37.3, 47.7, 69.3.
-    const SelectParams& s = p.sel;
-    const long long rows = (long long)s.total_q * s.H_kv;
-    const long long keys = (long long)(s.budget < s.max_pages ? s.budget : s.max_pages) << s.page_shift;
-    const int chunk = sparse_chunk_keys(d);
-    const long long chunks = (keys + chunk - 1) / chunk;
-    const long long groups = s.budget < s.max_pages ? (s.max_pages + 15) / 16 : 0;  // of pages to score
-    const long long resident = kSms * ((s.G + 7) / 8 * d <= 128 ? 2 : 1);
-    int cluster = 1;
-    while (cluster < kMaxCluster && rows * cluster * 2 <= resident &&
-           (rows * cluster * 2 <= kSms ? chunks >= (long long)cluster * 2 * kWarps || groups >= (long long)cluster * 2 * kAllWarps
-                                       : chunks >= (long long)cluster * 8 * kWarps))
-        cluster *= 2;
-    if (d == 128) return launch_d<128>(p, cluster, stream);
-    if (d == 64) return launch_d<64>(p, cluster, stream);
+cudaError_t launch_sparse(int d, const SparseParams& p, int sm_count, cudaStream_t stream) {
+    if (d == 128) return launch_d<128>(p, sm_count, stream);
+    if (d == 64) return launch_d<64>(p, sm_count, stream);
     return cudaErrorInvalidValue;
 }
 
