@@ -495,12 +495,13 @@ cudaError_t opt_in_smem(const void* kernel, int bytes, std::atomic<unsigned long
     return e;
 }
 
-// Device address of the calling device's status word (set-up on first use).
-attn_status_t status_word_address(unsigned** out) {
+// Device address of the calling device's status word (set-up on first use), and its SM count where asked for.
+attn_status_t status_word_address(unsigned** out, int* sm_count) {
     DeviceState* ds = nullptr;
     attn_status_t st = device_state(&ds);
     if (st != ATTN_OK) return st;
     *out = ds->status;
+    if (sm_count) *sm_count = ds->sm_count;
     return ATTN_OK;
 }
 

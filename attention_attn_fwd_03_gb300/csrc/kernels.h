@@ -237,6 +237,6 @@ namespace attn {
 cudaError_t opt_in_smem(const void* kernel, int bytes, std::atomic<unsigned long long>& done);
 
 // Device address of the calling device's status word (api.cu).
-attn_status_t status_word_address(unsigned** out);
+attn_status_t status_word_address(unsigned** out, int* sm_count = nullptr);
 
 }  // namespace attn

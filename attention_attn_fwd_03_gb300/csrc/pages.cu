@@ -35,7 +35,6 @@ namespace cg = cooperative_groups;
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanMaxB = 16384;
 constexpr int kPlanMaxCluster = 8;
-constexpr int kPlanMaxCtas = 152;
 
 struct PlanParams {
     const int32_t* ctx;
@@ -441,7 +440,8 @@ attn_status_t attn_paged_plan(const int32_t* ctx_lens, const int32_t* new_lens, 
 
     PlanParams p;
     std::memset(&p, 0, sizeof p);
-    attn_status_t st = status_word_address(&p.status);
+    int sm_count = 0;
+    attn_status_t st = status_word_address(&p.status, &sm_count);
     if (st != ATTN_OK) return st;
     p.ctx = ctx_lens;
     p.fresh = new_lens;
@@ -469,7 +469,7 @@ attn_status_t attn_paged_plan(const int32_t* ctx_lens, const int32_t* new_lens, 
     if (p.in_place)
         ctas = ctas >= kPlanMaxCluster ? kPlanMaxCluster : ctas > 2 ? 4 : ctas;
     else
-        ctas = ctas > kPlanMaxCtas ? kPlanMaxCtas : ctas;
+        ctas = ctas > sm_count ? sm_count : ctas;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = p.in_place ? (unsigned)ctas : 1u;

@@ -41,6 +41,7 @@ constexpr int kThreads = 256;
 constexpr int kInFlight = 3;  // heads whose loads a thread issues before it uses the first
 constexpr long long kStreamBytes = 128LL << 20;  // L2
 constexpr int kManyTokens = 512;
+constexpr int kFewCtas = 304;  // for fewer tokens: two CTAs to each of the chip's 152 SMs
 
 struct RopeSide {
     const char* in;
@@ -292,7 +293,7 @@ void plan(RopeParams& p, int elem_bytes, long long* blocks) {
     p.splits = 1;
     if (p.tok == 1) {
         const int most = (p.n_heads + lanes - 1) / lanes;  // more would leave CTAs without a head
-        const int want = (304 + p.n_tokens - 1) / p.n_tokens;
+        const int want = (kFewCtas + p.n_tokens - 1) / p.n_tokens;
         p.splits = want < most ? want : most;
         if (p.splits < 1) p.splits = 1;
     }
