@@ -197,10 +197,15 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
 // channels: a thread owns 8 channels and every RG-th row, 16 bytes per load;
 // row groups combine through shared memory.  With many pages a CTA takes up to
 // LANES = 128 pieces of a row (1024 channels), so that the page is read in
-// whole rows, U = 24 of them in flight per thread; with few pages (a decode
+// whole rows, in batches of U = 12 per thread; with few pages (a decode
 // step) LANES = 16 spreads a page over many CTAs and puts eight rows side by
 // side, so that no thread waits for memory more than once or twice.
-// Measured, 120 MB of keys: 20.9 us with 128 lanes (5.7 TB/s), 28 with 16; the
+// The loads of a batch keep their order, but the extremes between them move up:
+// for U = 8, 12 and 24 alike 47 registers are used, room for about eight loads in
+// flight.  120 MB of keys, us with U = 8, 12, 24: 8 requests of 6144 - 8192 in
+// 64-row pages 20.0, 19.4, 21.1; of 7168 19.2, 18.4, 17.5, in 16-row pages 24.0,
+// 22.7, 29.4, in 128-row pages 25.5 each; 64 requests (940 MB) 137, 138, 143.
+// Measured, 120 MB of keys: 19.4 us with 128 lanes (6.1 TB/s), 28 with 16; the
 // last pages of 64 requests 6.4 and 3.9 us, of 256 9.5 and 8.0, of 512 12.5 and 14.7.
 // Many small pages of narrow rows (up to 32 pieces a row, 512 a page) take a
 // warp each: 2 KB pages of 16 x 8192 keys 23.5 -> 8.2 us, 8 KB pages 14.3 ->
@@ -296,8 +301,7 @@ struct Extremes {
     }
 };
 
-// 16 bytes that nobody reads again; volatile, so that U of them are issued before the first is used
-// (plain loads were interleaved with their uses).
+// 16 bytes that nobody reads again; volatile, so that the loads are issued in the order of the rows.
 __device__ __forceinline__ uint4 ld_once(const uint4* p) {
     uint4 r;
     asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
@@ -532,7 +536,7 @@ attn_status_t attn_page_sketch(const void* k_cache, const int32_t* block_table, 
     if (narrow)
         page_sketch_warp_kernel<8><<<(unsigned)blocks, kSketchThreads, 0, cs>>>(p);
     else if (many)
-        page_sketch_kernel<128, 24><<<(unsigned)blocks, kSketchThreads, 0, cs>>>(p);
+        page_sketch_kernel<128, 12><<<(unsigned)blocks, kSketchThreads, 0, cs>>>(p);
     else
         page_sketch_kernel<16, 8><<<(unsigned)blocks, kSketchThreads, 0, cs>>>(p);
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
