@@ -307,11 +307,15 @@ attn_status_t select_sizes_ok(int B, int total_q, int H, int H_kv, int d, int pa
 // none; 256 bytes stand for it.  Otherwise the selection kernels and the paged
 // kernel run: with one unit per (token, KV head) too few to occupy the SMs, a
 // token's keys are cut into runs of whole 128-key blocks until about three
-// units per SM exist, with a work list and partials of the runs.  Measured with
-// groups of 4 (before they had a kernel of their own), runs of at least 1, 2, 4
-// blocks: 2048 keys of 8 heads 19.2, 18.6, 19.9 us; 8192 keys of 32 rows with
-// 304, 456, 912, 1824 units wanted 65, 66, 68, 73 us, 4096 keys of 256 rows 121,
-// 121, 117, 121.
+// units per SM exist, with a work list and partials of the runs.  (The size is
+// asked for without a device, so the number is the chip's: 3 x 152.)  Measured on
+// the groups, budgets and tables that come here, us with 152, 304, 456, 912 units
+// wanted: G = 32, 32 tokens of 4 KV heads over 4096 keys 87.6, 89.7, 91.8, 93.0, 8
+// tokens 43, 42, 44, 46; G = 128, 32 tokens of one KV head 70, 68, 76, 80; 256
+// tokens over 2048 keys 122, 123, 123, 148; G = 4 with 2048 16-row pages of 65000
+// keys 225, 179, 151, 158; and with 456 wanted and runs of at least 1, 2, 4 blocks:
+// one token of 8 KV heads over 2048 keys 26.9, 25.4, 26.9, of 30000 16-row pages 48,
+// 49, 52, 8 tokens 44, 44, 41.
 struct SparsePlan {
     int n_splits, split_blocks;
     size_t tables, lens, cu, list, part_o, part_ml, bytes;  // byte offsets; list: the 256-byte header, then the entries
