@@ -9,7 +9,7 @@
 // It reads the scores through L1, a few times each: a copy in shared memory
 // first was no faster.  Score CTAs of 64 pages instead of 128 gained 0.5 us at
 // 512 pages of one token and lost 3 to 20% elsewhere.  Both kernels, 8 KV heads:
-// one token of 512 pages 10.0 us, of 4096 16.9, 64 tokens of 1024 43.5 (20 of
+// one token of 512 pages 10.0 us, of 4096 17.0, 64 tokens of 1024 44.2 (20 of
 // them for the bytes); selection by 512 threads 10.9, 15.7, 53.7, by 128 9.9,
 // 27.9, 45.9.
 #include <cmath>
