@@ -109,6 +109,7 @@ def lib():
             L.attn_status_string.restype = ctypes.c_char_p
             L.attn_status_string.argtypes = [i]
             kv._declare(L)
+            kv8._declare(L)
             _lib = L
         return _lib
 
@@ -507,3 +508,7 @@ from .kv import (  # noqa: E402,F401
     attn_page_select, attn_page_select_workspace_size, attn_page_sketch, attn_paged_append, attn_paged_plan,
     attn_paged_sparse_fwd, attn_paged_sparse_fwd_workspace_size, attn_rope, attn_rope_inv_freq, page_select,
     page_sketch, paged_append, paged_plan, paged_sparse_fwd, rope, rope_inv_freq)
+from . import kv8  # noqa: E402
+from .kv8 import (  # noqa: E402,F401
+    attn_paged_append_fp8, attn_paged_fwd_fp8, attn_paged_fwd_fp8_workspace_size, attn_paged_read_fp8, paged_append_fp8,
+    paged_fwd_fp8, paged_read_fp8)

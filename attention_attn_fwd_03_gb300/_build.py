@@ -17,7 +17,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB_NAME = "libattn_gb300.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["api.cu", "prefill.cu", "prefill_sp.cu", "decode.cu", "paged.cu", "backward.cu", "rope.cu", "pages.cu",
-           "select.cu", "sparse.cu", "selftest.cu"]
+           "select.cu", "sparse.cu", "append8.cu", "paged8.cu", "selftest.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -45,7 +45,7 @@ def build(force=False, verbose=False, extra_flags=()):
     os.makedirs(BUILD, exist_ok=True)
     nvcc = nvcc_path()
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    headers += [os.path.join(INCLUDE, f) for f in ("attn.h", "attn_kv.h")]
+    headers += [os.path.join(INCLUDE, f) for f in ("attn.h", "attn_kv.h", "attn_kv8.h")]
     objs, jobs = [], []
     for src in SOURCES:
         s = os.path.join(CSRC, src)

@@ -1,5 +1,6 @@
 // api.cu -- the extern "C" entry points declared in include/attn.h, and the
-// page selection and page-sparse attention of include/attn_kv.h.
+// page selection and page-sparse attention of include/attn_kv.h and the attention
+// of include/attn_kv8.h.
 //
 // Host-side only: argument validation (nothing is enqueued on a bad
 // argument), TMA tensor-map encoding, per-device cached state (the device
@@ -12,6 +13,7 @@
 
 #include "attn.h"
 #include "attn_kv.h"
+#include "attn_kv8.h"
 #include "kernels.h"
 
 namespace attn {
@@ -753,6 +755,63 @@ attn_status_t attn_varlen_fwd(const void* q, const void* k, const void* v, const
     p.n_ctas = grid;
     p.table_heads = 1;
     return from_cuda(launch_paged(d, p, grid, static_cast<cudaStream_t>(stream)));
+}
+
+size_t attn_paged_fwd_fp8_workspace_size(int B, int total_q, int max_q_len, int H, int H_kv, int d, int page_size,
+                                         int max_pages) {
+    if (paged_sizes_ok(B, total_q, max_q_len, H, H_kv, d, page_size, max_pages) != ATTN_OK) return 0;
+    return 256;
+}
+
+attn_status_t attn_paged_fwd_fp8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                                 const float* v_scale, const int32_t* block_table, const int32_t* cu_seqlens_q,
+                                 const int32_t* seq_lens, int B, int total_q, int max_q_len, int H, int H_kv, int d,
+                                 int page_size, int block, int max_pages, int num_pages, float scale, int causal,
+                                 void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_table || !seq_lens || !o) return ATTN_ERR_INVALID_ARG;
+    if (!cu_seqlens_q && (total_q != B || max_q_len != 1)) return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = paged_sizes_ok(B, total_q, max_q_len, H, H_kv, d, page_size, max_pages);
+    if (st != ATTN_OK) return st;
+    st = blocks_ok(page_size, block, num_pages);
+    if (st != ATTN_OK) return st;
+    if (!(std::isfinite(scale) && scale > 0.f)) return ATTN_ERR_INVALID_ARG;
+    if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o)) return ATTN_ERR_INVALID_ARG;
+    auto a4 = [](const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 3u) == 0; };
+    if (!a4(k_scale) || !a4(v_scale) || !a4(block_table) || !a4(seq_lens) || !a4(cu_seqlens_q) || !a4(lse))
+        return ATTN_ERR_INVALID_ARG;
+    const size_t need = attn_paged_fwd_fp8_workspace_size(B, total_q, max_q_len, H, H_kv, d, page_size, max_pages);
+    if (!workspace || workspace_bytes < need || !aligned16(workspace)) return ATTN_ERR_WORKSPACE;
+    DeviceState* ds = nullptr;
+    st = device_state(&ds);
+    if (st != ATTN_OK) return st;
+
+    Paged8Params p;
+    std::memset(&p, 0, sizeof p);
+    p.q = static_cast<const uint16_t*>(q);
+    p.k_cache = static_cast<const uint8_t*>(k_cache);
+    p.v_cache = static_cast<const uint8_t*>(v_cache);
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.block_table = block_table;
+    p.cu_q = cu_seqlens_q;
+    p.seq_lens = seq_lens;
+    p.o = static_cast<uint16_t*>(o);
+    p.lse = lse;
+    p.status = ds->status;
+    p.B = B;
+    p.H = H;
+    p.H_kv = H_kv;
+    p.G = H / H_kv;
+    p.total_q = total_q;
+    p.max_q_len = max_q_len;
+    while ((1 << p.page_shift) < page_size) ++p.page_shift;
+    while ((1 << p.block_shift) < block) ++p.block_shift;
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    p.causal = causal;
+    p.c_scale = scale * 1.4426950408889634f;
+    return from_cuda(launch_paged8(d, p, static_cast<cudaStream_t>(stream)));
 }
 
 size_t attn_page_select_workspace_size(int total_q, int H_kv, int max_pages, int budget) {

@@ -1,0 +1,541 @@
+// append8.cu -- the append that quantises, and the read that undoes it, for a
+// paged cache of e4m3 codes with a scale for each block of rows and KV head.
+//
+// A block's scale is a power of two, 2^e with amax <= 448 2^e: e4m3 keeps its 4
+// significant bits wherever in its range a number lies, so rounding the scale up
+// costs no accuracy, x 2^-e is exact, and when a later token needs a larger scale
+// the older codes move by whole binades: exactly, but for those that become
+// subnormal.
+//
+// Work.  Tokens of one block follow one another in the call (a run).  A CTA owns
+// the runs that begin among its 32 tokens, for K or for V, and a share of the
+// heads; the last run may reach past them.  A thread holds 16 dims of one row (8
+// pairs of the rotation: their cosines and sines, computed once, serve all heads).
+// First pass: every head's rows are rotated and each run's largest magnitude found
+// (lanes of a row by shuffles, rows by an atomic maximum in shared memory, whose
+// order does not matter).  Then the scales; second pass: the rows, from L1 or L2,
+// rotated again and stored as codes.  Rows that a block held before are requantised
+// by the whole CTA where the scale grew.
+#include <cmath>
+#include <cstring>
+
+#include "attn_kv8.h"
+#include "kernels.h"
+#include "ptx.cuh"
+#include "rope.cuh"
+
+namespace attn {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWindow = 32;  // tokens whose runs a CTA owns
+constexpr int kMaxHeads = 16;  // heads a CTA walks over
+
+struct Append8Params {
+    const char* in[2];       // k, v: bf16 through byte strides
+    long long it[2], ih[2];  // token, head
+    uint8_t* codes[2];
+    float* scale[2];
+    const int32_t* slots;
+    const int32_t* positions;
+    const void* freq;
+    unsigned* status;
+    long long n_slots;
+    int freq64, T, H_kv, d, rot;
+    int page_shift, block_shift;
+    int hpc, splits;         // heads per CTA, CTAs that share a window's heads
+    float amplitude;
+};
+
+// Four fp32 -> four e4m3 bytes.  The magnitudes are at most 448 by the choice of the scale;
+// an infinity or NaN becomes the code of NaN (x - x is NaN for both, 0 otherwise).
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float inv) {
+    return pack_e4m3x4(fmaf(a, inv, a - a), fmaf(b, inv, b - b), fmaf(c, inv, c - c), fmaf(d, inv, d - d));
+}
+
+__device__ __forceinline__ uint32_t codes4_div(float a, float b, float c, float d, float s) {
+    return pack_e4m3x4(a / s + (a - a), b / s + (b - b), c / s + (c - c), d / s + (d - d));
+}
+
+// Two e4m3 bytes -> two fp32 (exact).
+__device__ __forceinline__ float2 values2(uint16_t x) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(x));
+    float lo, hi;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(h));
+    return make_float2(lo, hi);
+}
+
+// The smallest power of two s >= 2^-126 with amax <= 448 s, for a finite amax >= 0: 448 = 1.75 2^8,
+// so a significand above 1.75 (the carry) takes one binade more.
+__device__ __forceinline__ float scale_for(float amax) {
+    const int e = (int)((__float_as_uint(amax) + 0x1fffffu) >> 23) - 8;  // biased by 127
+    return __uint_as_float((unsigned)max(e, 1) << 23);
+}
+
+__device__ __forceinline__ bool is_pow2(float s) { return (__float_as_uint(s) & 0x807fffffu) == 0u && s > 0.f; }
+
+__device__ __forceinline__ uint4 ld16(const char* p) { return *reinterpret_cast<const uint4*>(p); }
+
+// The slot of token t, -1 where there is none.
+__device__ __forceinline__ int slot_of(const Append8Params& p, int t) {
+    const int s = __ldg(p.slots + t);
+    return s < 0 || s >= p.n_slots ? -1 : s;
+}
+
+// Whether token t, which has slot s, begins a run.
+__device__ __forceinline__ bool begins(const Append8Params& p, int t, int s) {
+    return t == 0 || (s & ((1 << p.block_shift) - 1)) == 0 || __ldg(p.slots + t - 1) != s - 1;
+}
+
+template <bool INTERLEAVED>
+struct Turn {  // 8 pairs of one row
+    float cs[8], sn[8];
+    __device__ __forceinline__ void rotate(float* a, float* c) const {
+        if (INTERLEAVED) {  // pieces hold pairs (0, 1), (2, 3), ..
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                const float x0 = a[e], x1 = a[e + 1], y0 = c[e], y1 = c[e + 1];
+                a[e] = x0 * cs[e / 2] - x1 * sn[e / 2];
+                a[e + 1] = x0 * sn[e / 2] + x1 * cs[e / 2];
+                c[e] = y0 * cs[4 + e / 2] - y1 * sn[4 + e / 2];
+                c[e + 1] = y0 * sn[4 + e / 2] + y1 * cs[4 + e / 2];
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float x = a[e], y = c[e];
+                a[e] = x * cs[e] - y * sn[e];
+                c[e] = x * sn[e] + y * cs[e];
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ void unpack8(const uint4& v, float* x) {
+    x[0] = bf16lo_to_f32(v.x); x[1] = bf16hi_to_f32(v.x);
+    x[2] = bf16lo_to_f32(v.y); x[3] = bf16hi_to_f32(v.y);
+    x[4] = bf16lo_to_f32(v.z); x[5] = bf16hi_to_f32(v.z);
+    x[6] = bf16lo_to_f32(v.w); x[7] = bf16hi_to_f32(v.w);
+}
+
+__device__ __forceinline__ float finite_abs(float x) {
+    const float a = fabsf(x);
+    return a < INFINITY ? a : 0.f;
+}
+
+template <int D, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads) append8_kernel(const __grid_constant__ Append8Params p) {
+    constexpr int UPR = D / 16;            // threads of a row
+    constexpr int ROWS = kThreads / UPR;   // rows side by side
+    __shared__ unsigned long long s_turn[D / 2];
+    __shared__ int s_amax[kMaxHeads][kWindow];     // by run, named by its first token's place in the window
+    __shared__ float s_scale[kMaxHeads][kWindow];
+    __shared__ float s_ratio[kMaxHeads][kWindow];  // before / now of the rows already there, 1: as they are
+    __shared__ unsigned s_lead;
+    __shared__ int s_end;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int side = blockIdx.y;  // 0: K, 1: V
+    const int window = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
+    const int t0 = window * kWindow;
+    const int h0 = split * p.hpc, nh = min(p.hpc, p.H_kv - h0);
+    const int bmask = (1 << p.block_shift) - 1;
+
+    if (tid < 32) {  // which of the window's tokens begin runs
+        const int t = t0 + lane;
+        bool lead = false;
+        if (t < p.T) {
+            const int s = slot_of(p, t);
+            lead = s >= 0 && begins(p, t, s);
+            if (s < 0 && __ldg(p.slots + t) >= 0 && side == 0 && split == 0) atomicOr(p.status, 1u << kStatusDeviceData);
+        }
+        const unsigned m = __ballot_sync(0xffffffffu, lead);
+        if (lane == 0) {
+            s_lead = m;
+            s_end = p.T;
+        }
+    }
+    for (int i = tid; i < kMaxHeads * kWindow; i += kThreads) (&s_amax[0][0])[i] = 0;
+    const bool turning = side == 0 && p.rot > 0;
+    if (turning)
+        for (int i = tid; i < p.rot / 2; i += kThreads)
+            s_turn[i] = p.freq64 ? turn_fraction(static_cast<const double*>(p.freq)[i])
+                                 : turn_fraction(static_cast<const float*>(p.freq)[i]);
+    __syncthreads();
+    const unsigned lead = s_lead;
+    if (lead == 0u) return;  // the tokens here belong to a run that began before, or to none
+    const int first = t0 + __ffs(lead) - 1, last_lead = t0 + 31 - __clz(lead);
+    {  // the end of the last run: its first token that does not follow on
+        const int s0 = slot_of(p, last_lead);
+        const int room = bmask + 1 - (s0 & bmask);  // rows of the block from the run's first on
+        for (int i = 1 + tid; i <= room; i += kThreads) {
+            const int t = last_lead + i;
+            if (t >= p.T) break;
+            if (i == room || __ldg(p.slots + t) != s0 + i) {
+                atomicMin(&s_end, t);
+                break;
+            }
+        }
+    }
+    __syncthreads();
+    const int end = s_end;
+
+    const int j = tid % UPR, row = tid / UPR;
+    const bool turns = turning && j * 16 < p.rot;
+    const bool split_halves = turns && !INTERLEAVED;
+    const int off_a = split_halves ? j * 8 : j * 16;  // elements of the thread's two pieces
+    const int off_b = split_halves ? p.rot / 2 + j * 8 : j * 16 + 8;
+    // the run of token t: the last of the window's runs to begin at or before it
+    auto run_of = [&](int t) {
+        const int i = min(t - t0, 31);
+        return 31 - __clz(lead & (0xffffffffu >> (31 - i)));
+    };
+    auto turn_for = [&](int t, Turn<INTERLEAVED>& w) {
+        if (!turns) return;
+        const int pos = __ldg(p.positions + t);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float c, s;
+            turned_cos_sin(s_turn[j * 8 + e], pos, &c, &s);
+            w.cs[e] = c * p.amplitude;
+            w.sn[e] = s * p.amplitude;
+        }
+    };
+    auto load = [&](int t, int h, const Turn<INTERLEAVED>& w, float* a, float* c) {
+        const char* src = p.in[side] + t * p.it[side] + (h0 + h) * p.ih[side];
+        unpack8(ld16(src + off_a * 2), a);
+        unpack8(ld16(src + off_b * 2), c);
+        if (turns) w.rotate(a, c);
+    };
+
+    Turn<INTERLEAVED> w;
+    for (int base = first; base < end; base += ROWS) {  // the largest magnitudes
+        const int t = base + row;
+        const bool in = t < end && slot_of(p, min(t, p.T - 1)) >= 0;
+        if (in) turn_for(t, w);
+        for (int h = 0; h < nh; ++h) {
+            float top = 0.f;
+            if (in) {
+                float a[8], c[8];
+                load(t, h, w, a, c);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = fmaxf(top, fmaxf(finite_abs(a[e]), finite_abs(c[e])));
+            }
+#pragma unroll
+            for (int o = UPR / 2; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (in && j == 0) atomicMax(&s_amax[h][run_of(t)], __float_as_int(top));
+        }
+    }
+    __syncthreads();
+    for (int x = tid; x < nh * kWindow; x += kThreads) {  // the scales
+        const int h = x / kWindow, i = x % kWindow;
+        if (!(lead >> i & 1u)) continue;
+        const int s = slot_of(p, t0 + i);
+        const int per_page = 1 << (p.page_shift - p.block_shift);
+        const long long at = ((long long)(s >> p.page_shift) * p.H_kv + h0 + h) * per_page +
+                             ((s & ((1 << p.page_shift) - 1)) >> p.block_shift);
+        const float need = scale_for(__int_as_float(s_amax[h][i]));
+        float now = need, ratio = 1.f;
+        if ((s & bmask) != 0) {
+            const float before = p.scale[side][at];
+            now = fmaxf(before, need);
+            if (!(before >= now)) ratio = before / now;
+        }
+        s_scale[h][i] = now;
+        s_ratio[h][i] = ratio;
+        p.scale[side][at] = now;
+    }
+    __syncthreads();
+    for (int base = first; base < end; base += ROWS) {  // the codes
+        const int t = base + row;
+        if (t >= end) break;
+        const int s = slot_of(p, t);
+        if (s < 0) continue;
+        if (base != first || end - first > ROWS) turn_for(t, w);
+        const int run = run_of(t);
+        for (int h = 0; h < nh; ++h) {
+            float a[8], c[8];
+            load(t, h, w, a, c);
+            const float now = s_scale[h][run];
+            uint2 x, y;
+            if (is_pow2(now)) {
+                const float inv = 1.f / now;
+                x = make_uint2(codes4(a[0], a[1], a[2], a[3], inv), codes4(a[4], a[5], a[6], a[7], inv));
+                y = make_uint2(codes4(c[0], c[1], c[2], c[3], inv), codes4(c[4], c[5], c[6], c[7], inv));
+            } else {  // a scale that another writer left
+                x = make_uint2(codes4_div(a[0], a[1], a[2], a[3], now), codes4_div(a[4], a[5], a[6], a[7], now));
+                y = make_uint2(codes4_div(c[0], c[1], c[2], c[3], now), codes4_div(c[4], c[5], c[6], c[7], now));
+            }
+            uint8_t* dst = p.codes[side] + ((long long)s * p.H_kv + h0 + h) * D;
+            *reinterpret_cast<uint2*>(dst + off_a) = x;
+            *reinterpret_cast<uint2*>(dst + off_b) = y;
+        }
+    }
+    for (unsigned left = lead; left != 0u; left &= left - 1) {  // rows that were there, under a larger scale now
+        const int i = __ffs(left) - 1;
+        const int s = slot_of(p, t0 + i), held = s & bmask;
+        if (held == 0) continue;
+        for (int h = 0; h < nh; ++h) {
+            const float ratio = s_ratio[h][i];
+            if (ratio == 1.f) continue;
+            for (int r = row; r < held; r += ROWS) {
+                uint4* at = reinterpret_cast<uint4*>(p.codes[side] + ((long long)(s - held + r) * p.H_kv + h0 + h) * D + j * 16);
+                uint4 x = *at;
+                uint32_t* word = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 lo = values2((uint16_t)word[e]), hi = values2((uint16_t)(word[e] >> 16));
+                    word[e] = pack_e4m3x4(lo.x * ratio, lo.y * ratio, hi.x * ratio, hi.y * ratio);
+                }
+                *at = x;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- reading back
+
+struct Read8Params {
+    const uint8_t* codes[2];
+    const float* scale[2];
+    char* out[2];
+    const int32_t* table;
+    const int32_t* cu;
+    unsigned* status;
+    int B, total, H_kv, d, page_shift, block_shift, max_pages, num_pages;
+    int sides;               // 2: K and V; 1: one of them, in place 0
+};
+
+constexpr int kReadRows = 8;  // rows of a CTA
+
+// Bound by memory: a code is read, two bytes (or four) written.  A CTA takes 8 rows of K and V: their
+// requests and cache rows are looked up once, then each thread moves 16 codes at a time.
+template <int EB>
+__global__ void __launch_bounds__(kThreads) read8_kernel(const __grid_constant__ Read8Params p) {
+    __shared__ int s_row[kReadRows];  // cache row, -1: left as it is, -2: zeros
+    const int tid = threadIdx.x;
+    const int t0 = blockIdx.x * kReadRows;
+    if (tid < kReadRows) {
+        const int t = t0 + tid;
+        int row = -1;
+        if (t < p.total) {
+            int lo = 0, hi = p.B - 1;  // the last request that begins at or before t
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (__ldg(p.cu + mid) <= t)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            const int a = __ldg(p.cu + lo), b = __ldg(p.cu + lo + 1);
+            if (a < 0 || b < a || b > p.total || ((long long)p.max_pages << p.page_shift) < (long long)b - a) {
+                atomicOr(p.status, 1u << kStatusDeviceData);
+            } else if (t >= a && t < b) {
+                const int key = t - a;
+                const int id = __ldg(p.table + (long long)lo * p.max_pages + (key >> p.page_shift));
+                if (id >= 0 && id < p.num_pages) {
+                    row = (id << p.page_shift) + (key & ((1 << p.page_shift) - 1));
+                } else {
+                    row = -2;
+                    atomicOr(p.status, 1u << kStatusDeviceData);
+                }
+            }
+        }
+        s_row[tid] = row;
+    }
+    __syncthreads();
+    const int units = p.H_kv * (p.d / 16);  // pieces of 16 codes in a row
+    const int per_page = 1 << (p.page_shift - p.block_shift);
+    for (int x = tid; x < kReadRows * units; x += kThreads) {
+        const int i = x / units, u = x - i * units;
+        const int row = s_row[i];
+        if (row == -1) continue;
+        const int h = u / (p.d / 16);
+        for (int side = 0; side < p.sides; ++side) {
+            uint4 c = make_uint4(0u, 0u, 0u, 0u);
+            float s = 0.f;
+            if (row >= 0) {
+                c = __ldcs(reinterpret_cast<const uint4*>(p.codes[side] + (long long)row * units * 16 + u * 16));
+                s = __ldg(p.scale[side] + ((long long)(row >> p.page_shift) * p.H_kv + h) * per_page +
+                          ((row & ((1 << p.page_shift) - 1)) >> p.block_shift));
+            }
+            const uint32_t* word = reinterpret_cast<const uint32_t*>(&c);
+            char* dst = p.out[side] + ((long long)(t0 + i) * units + u) * 16 * EB;
+            float f[16];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 lo = values2((uint16_t)word[e]), hi = values2((uint16_t)(word[e] >> 16));
+                f[4 * e] = lo.x * s;
+                f[4 * e + 1] = lo.y * s;
+                f[4 * e + 2] = hi.x * s;
+                f[4 * e + 3] = hi.y * s;
+            }
+            if (EB == 2) {
+#pragma unroll
+                for (int e = 0; e < 16; e += 8)
+                    *reinterpret_cast<uint4*>(dst + e * 2) = make_uint4(pack_bf16(f[e], f[e + 1]), pack_bf16(f[e + 2], f[e + 3]),
+                                                                        pack_bf16(f[e + 4], f[e + 5]), pack_bf16(f[e + 6], f[e + 7]));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; e += 4)
+                    *reinterpret_cast<float4*>(dst + e * 4) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+            }
+        }
+    }
+}
+
+bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+bool pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
+int shift_of(int x) {
+    int s = 0;
+    while ((1 << s) < x) ++s;
+    return s;
+}
+
+}  // namespace
+
+attn_status_t blocks_ok(int page_size, int block, int num_pages) {
+    if (num_pages < 1 || page_size < 1 || block < 1 || block > page_size) return ATTN_ERR_INVALID_ARG;
+    if (!pow2(page_size) || page_size < 8 || page_size > 1024 || !pow2(block)) return ATTN_ERR_UNSUPPORTED;
+    if ((long long)num_pages * page_size > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+    return ATTN_OK;
+}
+
+}  // namespace attn
+
+using namespace attn;
+
+extern "C" {
+
+attn_status_t attn_paged_append_fp8(const void* q, void* q_out, const void* k, const void* v, void* k_cache,
+                                    void* v_cache, float* k_scale, float* v_scale, const int32_t* slots,
+                                    const int32_t* positions, const void* inv_freq, int freq_bits, int T, int H,
+                                    int H_kv, int d, int rot, int page_size, int block, int num_pages,
+                                    const long long* strides, int interleaved, float amplitude, void* stream) {
+    attn_status_t st = append_args_ok(q, q_out, k, v, k_cache, v_cache, slots, positions, inv_freq, freq_bits, T, H, H_kv,
+                                      d, rot, page_size, num_pages, strides, interleaved, amplitude);
+    if (st != ATTN_OK) return st;
+    st = blocks_ok(page_size, block, num_pages);
+    if (st != ATTN_OK) return st;
+    if (T > 0x7fffffff - 2048) return ATTN_ERR_INVALID_ARG;  // a run reaches at most 1024 tokens past its window
+    if (!k_scale || !v_scale || !aligned(k_scale, 4) || !aligned(v_scale, 4)) return ATTN_ERR_INVALID_ARG;
+    unsigned* status = nullptr;
+    st = status_word_address(&status);
+    if (st != ATTN_OK) return st;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+
+    Append8Params p;
+    std::memset(&p, 0, sizeof p);
+    const void* in[2] = {k, v};
+    void* out[2] = {k_cache, v_cache};
+    float* scale[2] = {k_scale, v_scale};
+    for (int i = 0; i < 2; ++i) {
+        p.in[i] = static_cast<const char*>(in[i]);
+        p.it[i] = strides[4 + 2 * i] * 2;
+        p.ih[i] = strides[5 + 2 * i] * 2;
+        p.codes[i] = static_cast<uint8_t*>(out[i]);
+        p.scale[i] = scale[i];
+    }
+    p.slots = slots;
+    p.positions = positions;
+    p.freq = inv_freq;
+    p.status = status;
+    p.n_slots = (long long)num_pages * page_size;
+    p.freq64 = freq_bits == 64;
+    p.T = T;
+    p.H_kv = H_kv;
+    p.d = d;
+    p.rot = rot;
+    p.page_shift = shift_of(page_size);
+    p.block_shift = shift_of(block);
+    p.amplitude = amplitude;
+    p.hpc = H_kv < kMaxHeads ? H_kv : kMaxHeads;
+    const long long windows = ((long long)T + kWindow - 1) / kWindow;
+    while (p.hpc > 1 && windows * ((H_kv + p.hpc - 1) / p.hpc) < 304) p.hpc = (p.hpc + 1) / 2;
+    p.splits = (H_kv + p.hpc - 1) / p.hpc;
+    if (windows * p.splits > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+    const dim3 grid((unsigned)(windows * p.splits), 2);
+    if (d == 128) {
+        if (interleaved)
+            append8_kernel<128, true><<<grid, kThreads, 0, cs>>>(p);
+        else
+            append8_kernel<128, false><<<grid, kThreads, 0, cs>>>(p);
+    } else {
+        if (interleaved)
+            append8_kernel<64, true><<<grid, kThreads, 0, cs>>>(p);
+        else
+            append8_kernel<64, false><<<grid, kThreads, 0, cs>>>(p);
+    }
+    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+    if (!q) return ATTN_OK;
+    AppendQ a;
+    a.q = q;
+    a.q_out = q_out;
+    a.strides = strides;
+    a.slots = slots;
+    a.positions = positions;
+    a.inv_freq = inv_freq;
+    a.status = status;
+    a.n_slots = p.n_slots;
+    a.freq_bits = freq_bits;
+    a.T = T;
+    a.H = H;
+    a.d = d;
+    a.rot = rot;
+    a.interleaved = interleaved;
+    a.amplitude = amplitude;
+    return launch_append_q(a, cs) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+attn_status_t attn_paged_read_fp8(const void* k_cache, const void* v_cache, const float* k_scale,
+                                  const float* v_scale, const int32_t* block_table, const int32_t* cu_seqlens_k,
+                                  int B, int total_k, int H_kv, int d, int page_size, int block, int max_pages,
+                                  int num_pages, void* k, void* v, int elem_bytes, void* stream) {
+    if (!block_table || !cu_seqlens_k || (!k && !v)) return ATTN_ERR_INVALID_ARG;
+    if ((k && (!k_cache || !k_scale)) || (v && (!v_cache || !v_scale))) return ATTN_ERR_INVALID_ARG;
+    if (B < 1 || total_k < 1 || total_k > 0x7fffffff - kReadRows || H_kv < 1 || H_kv > 65535 || max_pages < 1)
+        return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = blocks_ok(page_size, block, num_pages);
+    if (st != ATTN_OK) return st;
+    if ((d != 64 && d != 128) || (elem_bytes != 2 && elem_bytes != 4)) return ATTN_ERR_UNSUPPORTED;
+    if ((long long)max_pages * page_size > 0x7fffffffLL || (long long)B * max_pages > 0x7fffffffLL)
+        return ATTN_ERR_INVALID_ARG;
+    for (const void* ptr : {static_cast<const void*>(k), static_cast<const void*>(v), k ? k_cache : nullptr,
+                            v ? v_cache : nullptr})
+        if (!aligned(ptr, 16)) return ATTN_ERR_INVALID_ARG;
+    if (!aligned(block_table, 4) || !aligned(cu_seqlens_k, 4) || (k && !aligned(k_scale, 4)) || (v && !aligned(v_scale, 4)))
+        return ATTN_ERR_INVALID_ARG;
+    Read8Params p;
+    std::memset(&p, 0, sizeof p);
+    st = status_word_address(&p.status);
+    if (st != ATTN_OK) return st;
+    auto add = [&](const void* codes, const float* scale, void* out) {
+        p.codes[p.sides] = static_cast<const uint8_t*>(codes);
+        p.scale[p.sides] = scale;
+        p.out[p.sides++] = static_cast<char*>(out);
+    };
+    if (k) add(k_cache, k_scale, k);
+    if (v) add(v_cache, v_scale, v);
+    p.table = block_table;
+    p.cu = cu_seqlens_k;
+    p.B = B;
+    p.total = total_k;
+    p.H_kv = H_kv;
+    p.d = d;
+    p.page_shift = shift_of(page_size);
+    p.block_shift = shift_of(block);
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    const unsigned blocks = (unsigned)((total_k + kReadRows - 1) / kReadRows);
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (elem_bytes == 2)
+        read8_kernel<2><<<blocks, kThreads, 0, cs>>>(p);
+    else
+        read8_kernel<4><<<blocks, kThreads, 0, cs>>>(p);
+    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // extern "C"

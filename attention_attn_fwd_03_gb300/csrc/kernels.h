@@ -186,6 +186,45 @@ constexpr int sparse_chunk_keys(int d) { return d == 128 ? 16 : 32; }
 bool sparse_fused_ok(int d, int G, int max_pages, int budget);
 cudaError_t launch_sparse(int d, const SparseParams& p, int sm_count, cudaStream_t stream);
 
+// The q side of a cache append (rope.cu): q rotated for the tokens that have a slot.
+struct AppendQ {
+    const void* q;             // bf16 [T, H, d] through strides
+    void* q_out;
+    const long long* strides;  // (t, h) of q and of q_out, in elements
+    const int32_t* slots;
+    const int32_t* positions;
+    const void* inv_freq;
+    unsigned* status;
+    long long n_slots;
+    int freq_bits, T, H, d, rot, interleaved;
+    float amplitude;
+};
+cudaError_t launch_append_q(const AppendQ& a, cudaStream_t stream);
+
+// Attention over a cache of e4m3 codes with block scales (paged8.cu).  Query rows of a request
+// and KV head are numbered token * G + head of the group and cut into tiles of R.
+struct Paged8Params {
+    CUtensorMap tm_k;            // codes [slots, H_kv, d]: dims (d, H_kv, slots), box (d, 1, rows_per_box), swizzle d bytes
+    CUtensorMap tm_v;
+    const uint16_t* q;           // bf16 [total_q, H, d]
+    const uint8_t* k_cache;
+    const uint8_t* v_cache;
+    const float* k_scale;        // [num_pages, H_kv, page_size / block]
+    const float* v_scale;
+    const int32_t* block_table;  // [B, max_pages]
+    const int32_t* cu_q;         // [B + 1] or nullptr: one token per request
+    const int32_t* seq_lens;     // [B]
+    uint16_t* o;
+    float* lse;                  // [total_q, H] or nullptr
+    unsigned* status;
+    int B, H, H_kv, G;
+    int total_q, max_q_len;
+    int page_shift, block_shift, max_pages, num_pages;
+    int causal;
+    float c_scale;               // scale * log2(e)
+};
+cudaError_t launch_paged8(int d, const Paged8Params& p, cudaStream_t stream);
+
 // Failure-handling test: a bounded wait that nothing completes (selftest.cu).
 cudaError_t launch_selftest_timeout(unsigned* status, cudaStream_t stream);
 // Tensor-core rate check: n_ctas CTAs (one per SM), each timing 4 * n_groups
@@ -235,6 +274,16 @@ namespace attn {
 // cudaFuncAttributeMaxDynamicSharedMemorySize of a kernel, set once per device
 // (`done` is the kernel's own bit mask of devices, zero at first).
 cudaError_t opt_in_smem(const void* kernel, int bytes, std::atomic<unsigned long long>& done);
+
+// Checks shared by the appends (rope.cu).
+attn_status_t append_args_ok(const void* q, const void* q_out, const void* k, const void* v, const void* k_cache,
+                             const void* v_cache, const int32_t* slots, const int32_t* positions,
+                             const void* inv_freq, int freq_bits, int T, int H, int H_kv, int d, int rot,
+                             int page_size, int num_pages, const long long* strides, int interleaved,
+                             float amplitude);
+
+// Page and block sizes of a cache of codes (append8.cu).
+attn_status_t blocks_ok(int page_size, int block, int num_pages);
 
 // Device address of the calling device's status word (api.cu).
 attn_status_t status_word_address(unsigned** out, int* sm_count = nullptr);

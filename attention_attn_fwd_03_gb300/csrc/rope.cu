@@ -32,6 +32,7 @@
 #include "attn_kv.h"
 #include "kernels.h"
 #include "ptx.cuh"
+#include "rope.cuh"
 
 namespace attn {
 
@@ -82,30 +83,6 @@ __device__ __forceinline__ void st16(char* p, const uint4& v, bool stream) {
     else
         asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                      : "memory");
-}
-
-// f / 2 pi modulo 1 as a 64-bit binary fraction, from the bits of f = +- m 2^e
-// with m shifted to the top of 64 bits: m / 2 pi by 128 bits of 1 / 2 pi, as
-// whole + part 2^-64, then shifted to units of 2^-64 turns.  Good to two units for
-// |f| < 2^63 (beyond: 0).  Integers, because float64 is slow here: a product carried
-// in two doubles cost every call 0.2 us.
-__device__ __forceinline__ unsigned long long turn_fraction(unsigned long long m, int e, bool negative) {
-    constexpr unsigned long long kHi = 0x28be60db9391054aULL, kLo = 0x7f09d5f47d4d3770ULL;
-    const unsigned long long low = m * kHi, carry = __umul64hi(m, kLo), part = low + carry;
-    const unsigned long long whole = __umul64hi(m, kHi) + (part < low ? 1ULL : 0ULL);
-    const int s = 64 + e;
-    const unsigned long long turns = s <= -64 ? 0ULL : s <= 0 ? whole >> -s : s < 64 ? whole << s | part >> (64 - s) : 0ULL;
-    return negative ? 0ULL - turns : turns;
-}
-__device__ __forceinline__ unsigned long long turn_fraction(double f) {
-    const unsigned long long b = (unsigned long long)__double_as_longlong(f);
-    const int x = (int)(b >> 52) & 0x7ff;
-    return turn_fraction(((b << 11) & 0x7fffffffffffffffULL) | (x ? 1ULL << 63 : 0ULL), (x ? x : 1) - 1086, (b >> 63) != 0);
-}
-__device__ __forceinline__ unsigned long long turn_fraction(float f) {
-    const unsigned b = __float_as_uint(f);
-    const int x = (int)(b >> 23) & 0xff;
-    return turn_fraction(((unsigned long long)(b << 8 & 0x7fffffffu) << 32) | (x ? 1ULL << 63 : 0ULL), (x ? x : 1) - 190, (b >> 31) != 0);
 }
 
 template <int EB>
@@ -172,13 +149,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         } else {
             pos = t % p.N;
         }
-        const unsigned long long phase = s_turn[i] * (unsigned long long)(long long)pos;
-        // half turns: 24 bits exactly in fp32, and the 32 bits below them, in radians
-        const int top = (int)(phase >> 32) & ~0xff;
-        const float e = (float)(unsigned)(phase >> 8) * 8.7196712450215807e-17f;  // 2^-55 pi
-        float s0, c0;
-        sincospif((float)top * 4.6566128730773926e-10f, &s0, &c0);  // 2^-31
-        const float cs = fmaf(-e, s0, c0), sn = fmaf(e, c0, s0);
+        float cs, sn;
+        turned_cos_sin(s_turn[i], pos, &cs, &sn);
         const int at = k * half + (VN == 8 ? ((i >> 2) & 1) * (half >> 1) : 0) + (i / VN) * 4 + (i & 3);
         s_cos[at] = cs * p.amplitude;
         s_sin[at] = sn * p.sign * p.amplitude;
@@ -343,6 +315,58 @@ void set_side(RopeSide& s, const void* in, void* out, const long long* si, const
 
 }  // namespace
 
+attn_status_t append_args_ok(const void* q, const void* q_out, const void* k, const void* v, const void* k_cache,
+                             const void* v_cache, const int32_t* slots, const int32_t* positions,
+                             const void* inv_freq, int freq_bits, int T, int H, int H_kv, int d, int rot,
+                             int page_size, int num_pages, const long long* strides, int interleaved,
+                             float amplitude) {
+    if (!k || !v || !k_cache || !v_cache || !slots || !strides || (q == nullptr) != (q_out == nullptr))
+        return ATTN_ERR_INVALID_ARG;
+    if (!q) H = 0;
+    if (T < 1 || T > 0x7fffffff - 8 || H < 0 || H > 65535 || H_kv < 1 || H_kv > 65535 || (q && H < 1) || num_pages < 1 ||
+        page_size < 1)
+        return ATTN_ERR_INVALID_ARG;
+    if (rot != 0 && (!positions || !inv_freq || (freq_bits != 32 && freq_bits != 64))) return ATTN_ERR_INVALID_ARG;
+    if ((interleaved & ~1) || !std::isfinite(amplitude)) return ATTN_ERR_INVALID_ARG;
+    if ((d != 64 && d != 128) || rot < 0 || rot > d || rot % 16 != 0) return ATTN_ERR_UNSUPPORTED;
+    if (page_size < 8 || page_size > 1024 || page_size % 8 != 0) return ATTN_ERR_UNSUPPORTED;
+    if ((long long)num_pages * page_size > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+    for (const void* ptr : {q, static_cast<const void*>(q_out), k, v, static_cast<const void*>(k_cache),
+                            static_cast<const void*>(v_cache)})
+        if (!aligned(ptr, 16)) return ATTN_ERR_INVALID_ARG;
+    if (!aligned(slots, 4) || !aligned(positions, 4) || (rot != 0 && !aligned(inv_freq, freq_bits / 8)))
+        return ATTN_ERR_INVALID_ARG;
+    const long long nq[2] = {T, H}, nk[2] = {T, H_kv};
+    if (q && (!strides_ok(strides, nq, 2, d, 2, false) || !strides_ok(strides + 2, nq, 2, d, 2, true)))
+        return ATTN_ERR_INVALID_ARG;
+    if (!strides_ok(strides + 4, nk, 2, d, 2, false) || !strides_ok(strides + 6, nk, 2, d, 2, false))
+        return ATTN_ERR_INVALID_ARG;
+    return ATTN_OK;
+}
+
+// The rotation of q on its way past the cache: tokens with a slot only.
+cudaError_t launch_append_q(const AppendQ& a, cudaStream_t stream) {
+    RopeParams p;
+    std::memset(&p, 0, sizeof p);
+    const long long i3[3] = {0, a.strides[1], a.strides[0]}, o3[3] = {0, a.strides[3], a.strides[2]};
+    set_side(p.q, a.q, a.q_out, i3, o3, 2);
+    p.positions = a.positions;
+    p.freq = a.inv_freq;
+    p.freq64 = a.freq_bits == 64;
+    p.slots = a.slots;
+    p.n_slots = a.n_slots;
+    p.status = a.status;
+    p.n_tokens = a.T;
+    p.N = a.T;
+    p.H = a.H;
+    p.n_heads = a.H;
+    p.d = a.d;
+    p.rot = a.rot;
+    p.amplitude = a.amplitude;
+    p.sign = 1.f;
+    return run(p, 2, a.interleaved != 0, true, stream);
+}
+
 }  // namespace attn
 
 using namespace attn;
@@ -436,29 +460,12 @@ attn_status_t attn_paged_append(const void* q, void* q_out, const void* k, const
                                 const void* inv_freq, int freq_bits, int T, int H, int H_kv, int d, int rot,
                                 int page_size, int num_pages, const long long* strides, int interleaved,
                                 float amplitude, void* stream) {
-    if (!k || !v || !k_cache || !v_cache || !slots || !strides || (q == nullptr) != (q_out == nullptr))
-        return ATTN_ERR_INVALID_ARG;
+    attn_status_t st = append_args_ok(q, q_out, k, v, k_cache, v_cache, slots, positions, inv_freq, freq_bits, T, H, H_kv,
+                                      d, rot, page_size, num_pages, strides, interleaved, amplitude);
+    if (st != ATTN_OK) return st;
     if (!q) H = 0;
-    if (T < 1 || T > 0x7fffffff - 8 || H < 0 || H > 65535 || H_kv < 1 || H_kv > 65535 || (q && H < 1) || num_pages < 1 ||
-        page_size < 1)
-        return ATTN_ERR_INVALID_ARG;
-    if (rot != 0 && (!positions || !inv_freq || (freq_bits != 32 && freq_bits != 64))) return ATTN_ERR_INVALID_ARG;
-    if ((interleaved & ~1) || !std::isfinite(amplitude)) return ATTN_ERR_INVALID_ARG;
-    if ((d != 64 && d != 128) || rot < 0 || rot > d || rot % 16 != 0) return ATTN_ERR_UNSUPPORTED;
-    if (page_size < 8 || page_size > 1024 || page_size % 8 != 0) return ATTN_ERR_UNSUPPORTED;
-    if ((long long)num_pages * page_size > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
-    for (const void* ptr : {q, static_cast<const void*>(q_out), k, v, static_cast<const void*>(k_cache),
-                            static_cast<const void*>(v_cache)})
-        if (!aligned(ptr, 16)) return ATTN_ERR_INVALID_ARG;
-    if (!aligned(slots, 4) || !aligned(positions, 4) || (rot != 0 && !aligned(inv_freq, freq_bits / 8)))
-        return ATTN_ERR_INVALID_ARG;
-    const long long nq[2] = {T, H}, nk[2] = {T, H_kv};
-    if (q && (!strides_ok(strides, nq, 2, d, 2, false) || !strides_ok(strides + 2, nq, 2, d, 2, true)))
-        return ATTN_ERR_INVALID_ARG;
-    if (!strides_ok(strides + 4, nk, 2, d, 2, false) || !strides_ok(strides + 6, nk, 2, d, 2, false))
-        return ATTN_ERR_INVALID_ARG;
     unsigned* status = nullptr;
-    attn_status_t st = status_word_address(&status);
+    st = status_word_address(&status);
     if (st != ATTN_OK) return st;
 
     RopeParams p;
