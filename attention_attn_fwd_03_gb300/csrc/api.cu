@@ -209,6 +209,19 @@ bool make_paged_map(CUtensorMap* map, const void* base, int d, long long heads, 
     return r == CUDA_SUCCESS;
 }
 
+// Map of e4m3 codes [slots, H_kv, d]: box (d bytes, 1 head, R rows), swizzle of d bytes, zero fill outside the tensor.
+bool make_codes_map(CUtensorMap* map, const void* base, int d, long long heads, long long rows, int box_rows) {
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {(cuuint64_t)d, (cuuint64_t)heads * d};
+    cuuint32_t box[3] = {(cuuint32_t)d, 1u, (cuuint32_t)box_rows};
+    cuuint32_t estr[3] = {1u, 1u, 1u};
+    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 // ---- ragged prefill: the prefill kernel over variable-length sequences.
 //
 // Launches whose sequences bring at least kRaggedMinQ query tokens run on
@@ -760,7 +773,7 @@ attn_status_t attn_varlen_fwd(const void* q, const void* k, const void* v, const
 size_t attn_paged_fwd_fp8_workspace_size(int B, int total_q, int max_q_len, int H, int H_kv, int d, int page_size,
                                          int max_pages) {
     if (paged_sizes_ok(B, total_q, max_q_len, H, H_kv, d, page_size, max_pages) != ATTN_OK) return 0;
-    return 256;
+    return paged8_plan(B, max_q_len, H / H_kv, d).bytes;
 }
 
 attn_status_t attn_paged_fwd_fp8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
@@ -780,17 +793,27 @@ attn_status_t attn_paged_fwd_fp8(const void* q, const void* k_cache, const void*
     auto a4 = [](const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 3u) == 0; };
     if (!a4(k_scale) || !a4(v_scale) || !a4(block_table) || !a4(seq_lens) || !a4(cu_seqlens_q) || !a4(lse))
         return ATTN_ERR_INVALID_ARG;
-    const size_t need = attn_paged_fwd_fp8_workspace_size(B, total_q, max_q_len, H, H_kv, d, page_size, max_pages);
-    if (!workspace || workspace_bytes < need || !aligned16(workspace)) return ATTN_ERR_WORKSPACE;
+    const Paged8Plan pl = paged8_plan(B, max_q_len, H / H_kv, d);
+    if (!workspace || workspace_bytes < pl.bytes || !aligned16(workspace)) return ATTN_ERR_WORKSPACE;
     DeviceState* ds = nullptr;
     st = device_state(&ds);
     if (st != ATTN_OK) return st;
 
     Paged8Params p;
     std::memset(&p, 0, sizeof p);
+    const long long slots = (long long)num_pages * page_size;
+    p.rows_per_box = page_size < 128 ? page_size : 128;
+    if (!make_codes_map(&p.tm_k, k_cache, d, H_kv, slots, p.rows_per_box) ||
+        !make_codes_map(&p.tm_v, v_cache, d, H_kv, slots, p.rows_per_box))
+        return ATTN_ERR_CUDA;
+    p.kv_rows = (int)slots;
+    char* ws = static_cast<char*>(workspace);
+    p.plan = reinterpret_cast<long long*>(ws);
+    p.part_ml = reinterpret_cast<float*>(ws + pl.part_ml);
+    p.part_o = reinterpret_cast<float*>(ws + pl.part_o);
+    p.R = pl.R;
+    p.n_ctas = 2 * ds->sm_count < kPaged8Ctas ? 2 * ds->sm_count : kPaged8Ctas;
     p.q = static_cast<const uint16_t*>(q);
-    p.k_cache = static_cast<const uint8_t*>(k_cache);
-    p.v_cache = static_cast<const uint8_t*>(v_cache);
     p.k_scale = k_scale;
     p.v_scale = v_scale;
     p.block_table = block_table;

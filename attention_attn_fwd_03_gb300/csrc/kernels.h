@@ -207,8 +207,6 @@ struct Paged8Params {
     CUtensorMap tm_k;            // codes [slots, H_kv, d]: dims (d, H_kv, slots), box (d, 1, rows_per_box), swizzle d bytes
     CUtensorMap tm_v;
     const uint16_t* q;           // bf16 [total_q, H, d]
-    const uint8_t* k_cache;
-    const uint8_t* v_cache;
     const float* k_scale;        // [num_pages, H_kv, page_size / block]
     const float* v_scale;
     const int32_t* block_table;  // [B, max_pages]
@@ -216,13 +214,26 @@ struct Paged8Params {
     const int32_t* seq_lens;     // [B]
     uint16_t* o;
     float* lse;                  // [total_q, H] or nullptr
+    long long* plan;             // workspace: [0] tiles per CTA, [1 ..] first tile of each request
+    float* part_ml;              // [2 n_ctas, R, 2]: (m in log2 units, l) of a CTA's first and last piece
+    float* part_o;               // [2 n_ctas, R, d]: unnormalised O
     unsigned* status;
-    int B, H, H_kv, G;
+    int B, H, H_kv, G, R;
     int total_q, max_q_len;
     int page_shift, block_shift, max_pages, num_pages;
+    int rows_per_box;            // min(page_size, 128)
+    int kv_rows;                 // first row past the cache: reads zeros
     int causal;
+    int n_ctas;
     float c_scale;               // scale * log2(e)
 };
+// Workspace of the call: byte offsets of the plan's parts.
+struct Paged8Plan {
+    int R;                       // query rows of a tile
+    size_t part_ml, part_o, bytes;
+};
+constexpr int kPaged8Ctas = 304;  // at most: two to each of the chip's 152 SMs
+Paged8Plan paged8_plan(int B, int max_q_len, int G, int d);
 cudaError_t launch_paged8(int d, const Paged8Params& p, cudaStream_t stream);
 
 // Failure-handling test: a bounded wait that nothing completes (selftest.cu).

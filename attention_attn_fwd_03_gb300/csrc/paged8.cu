@@ -1,7 +1,40 @@
 // paged8.cu -- attention over a paged cache of e4m3 codes with block scales.
 //
-// A CTA per (query token, query head); a warp per key: its lanes hold d / 32 dims each.  Online
-// softmax per warp (running max m, sum l, unnormalised O), the warps merged at the end.
+//   s_j = scale ks_j (q . kc_j),  p_j = e^(s_j),  O = sum p_j vs_j vc_j / sum p_j,  LSE = ln sum p_j
+//
+// (kc, vc: codes; ks, vs: the scales of key j's block), by the one-pass online
+// softmax (running maximum, sum and unnormalised O, one final division).
+//
+// What bounds it.  A decode step reads every code once and computes 4 G d flops for
+// 2 d bytes (G query heads to a KV head): HBM.  At its rate an SM gets some 23 bytes a
+// cycle, too many to convert to 16 bits on the way: so the codes go from the cache to the
+// matrix units as they are, by TMA into swizzled shared memory and from there as e4m3
+// operands of tcgen05.mma (kind::f8f6f4).  The other operands have few rows, so their
+// precision is bought with more rows:
+//   q = 2^x (hi + lo / 16): a bf16 number has 8 significant bits, two e4m3 numbers hold
+//       them; x by the head vector's largest element.
+//   P vs / 2^(running maximum) = hi + mid / 16 + lo / 256: an fp16 number's 11 bits.
+// Both products are transposed, so that keys (or channels) fill the 128 rows of the
+// matrix instruction and query rows its columns:
+//   S^T [128 keys, 2 R] = Kc [128, d] Q^T,    O^T [d, 3 R] += Vc^T [d, 128 keys] P^T,
+// R = 8, 16 or 32 query rows (tokens times the heads of a group).  A thread of the softmax
+// then has one key and all rows: no thread is idle, and the row sums stay per thread until
+// the end.  It takes 32 / R tiles of 128 keys (a step, 32 scores a thread) at a time:
+// one test per step, over all threads, whether a row's maximum grew by more than kTau.
+//
+// Work split.  Requests, KV heads, row tiles and key tiles in a row, cut into equal shares,
+// one for each CTA (two to an SM, so that one's softmax runs during the other's loads).  Each
+// CTA computes the cut from the lengths.  A unit (request, head, row tile) that lies in one
+// CTA is finished there; pieces of others leave (m, l, O), merged by a second kernel.
+//
+// A CTA, 224 threads:
+//   warp 0    TMA producer: the units, their pages, K and V tiles into a ring, in the order
+//             K of step n + 1, V of step n.
+//   warp 1    MMA issuer (one lane); the warp clears V rows past the request's keys.
+//   warps 2-5 softmax and epilogue: thread = key, then thread = channel.
+//   warp 6    query rows as e4m3 pairs, and the scales of the steps' keys.
+#include <cuda_fp16.h>
+
 #include <cmath>
 
 #include "kernels.h"
@@ -11,24 +44,963 @@ namespace attn {
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr float kTau = 1.f;       // log2 units: how far a row's maximum may lag behind
+constexpr float kBase = 7.f;      // P is scaled by 2^7: at most 2^(kBase + kTau) = 256 of e4m3's 448
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr int kThreads8 = 224;
+constexpr int kQN = 4;            // unit queue between the producer and the other warps
+constexpr int kUnitInts = 10;
+constexpr int kMinShare = 2;      // tiles
 
-__device__ __forceinline__ float value(uint8_t x) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)x));
-    float f;
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.f32.f16 %0, l;\n\t}" : "=f"(f) : "r"(h));
-    return f;
+template <int D, int R>
+struct Cfg {
+    static constexpr int SB = 32 / R;                  // key tiles of a step
+    static constexpr int NQ = 2 * R;                   // columns of S^T per tile: hi, lo
+    static constexpr int NPV = R == 8 ? 32 : 3 * R;    // columns of O^T: hi, mid, lo (a multiple of 16)
+    static constexpr int TILE = 128 * D;               // bytes of a K or V tile
+    static constexpr int NST = D == 64 ? 10 : R == 32 ? 4 : 5;  // ring stages
+    static constexpr int QBYTES = NQ * D;
+    static constexpr int PTILE = NPV * 128;
+    static constexpr uint32_t TM_O = 128;              // S: two buffers of 64 columns
+    static constexpr uint32_t TM_COLS = 256;
+    static constexpr int OFF_KV = 0;
+    static constexpr int OFF_P = OFF_KV + NST * TILE;
+    static constexpr int OFF_Q = OFF_P + SB * PTILE;
+    static constexpr int OFF_SC = OFF_Q + 2 * QBYTES;                 // float2 [2][SB][128]: ks, log2 vs
+    static constexpr int OFF_ROW = OFF_SC + 2 * SB * 128 * 8;         // int4 [2][R]: factor, last visible key, output row
+    static constexpr int OFF_STAT = OFF_ROW + 2 * R * 16;             // float2 [R]: running maxima of s and of s + log2 vs
+    static constexpr int OFF_ALPHA = OFF_STAT + R * 8;                // float2 [R]
+    static constexpr int OFF_EXCH = OFF_ALPHA + R * 8;                // float2 [4][R]
+    static constexpr int OFF_SUM = OFF_EXCH + 4 * R * 8;              // float [4][R]
+    static constexpr int OFF_NAN = OFF_SUM + 4 * R * 4;               // int [D]: first row that sees a NaN in this channel
+    static constexpr int OFF_BAR = OFF_NAN + D * 4;
+    static constexpr int N_BARS = 2 * NST + 13 + 2 * kQN;
+    static constexpr int OFF_UQ = OFF_BAR + 8 * N_BARS;
+    static constexpr int OFF_MISC = OFF_UQ + 4 * kQN * kUnitInts;
+    static constexpr int SMEM_BYTES = OFF_MISC + 128 + 1024;
+    static_assert(SMEM_BYTES <= 115712, "two CTAs to an SM");
+    static_assert(OFF_P % 1024 == 0 && PTILE % 1024 == 0 && OFF_Q % 1024 == 0 && QBYTES % 1024 == 0, "swizzle atoms");
+};
+
+struct Bars {
+    uint64_t* kv_full;   // [NST]
+    uint64_t* kv_empty;  // [NST]
+    uint64_t* q_full;    // [2] query rows prepared
+    uint64_t* q_empty;   // [2] the unit's last S product, and the four softmax warps
+    uint64_t* sc_full;   // [2] scales of a step
+    uint64_t* sc_empty;  // [2] four softmax warps
+    uint64_t* s_full;    // [2]
+    uint64_t* p_full;    // 128 arrivals per step
+    uint64_t* o_full;    // PV products of a step, and the issuing lane
+    uint64_t* done;
+    uint64_t* uq_full;   // [kQN]
+    uint64_t* uq_empty;  // [kQN] six readers
+};
+
+// A piece of a unit: key tiles [tile0, tile0 + nt) for rows [row0, row0 + nr) of request r and KV head kvh.
+// Row x is query token x / G of the request, head x % G of the group.
+struct Unit {
+    int r;  // -1: no more
+    int kvh, q_start, q_len, kv_len, row0, nr, tile0, nt;
+    int slot;  // partial record, -1: the whole unit
+};
+
+struct Extent {
+    int q_start, q_len, kv_len;
+    bool bad;
+};
+
+__device__ __forceinline__ Extent extent(const Paged8Params& p, int r) {
+    Extent e;
+    e.bad = false;
+    e.q_start = r;
+    e.q_len = 1;
+    if (p.cu_q != nullptr) {
+        const int a = __ldg(p.cu_q + r), b = __ldg(p.cu_q + r + 1);
+        e.q_start = a;
+        e.q_len = b - a;
+        if (a < 0 || b < a || b > p.total_q || e.q_len > p.max_q_len) {
+            e.bad = true;
+            e.q_start = 0;
+            e.q_len = 0;
+        }
+    }
+    e.kv_len = __ldg(p.seq_lens + r);
+    const int cap = p.max_pages << p.page_shift;
+    if (e.kv_len < 0 || e.kv_len > cap) {
+        e.bad = true;
+        e.kv_len = e.kv_len < 0 ? 0 : cap;
+    }
+    return e;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) paged8_simple_kernel(const __grid_constant__ Paged8Params p) {
-    constexpr int PER = D / 32;
-    __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][D];
-    const int tok = blockIdx.x, head = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int r = tok, q_start = tok, q_len = 1;
+// Key tiles of every unit of a request (one at least, so that its rows are written), and its row tiles.
+__device__ __forceinline__ int key_tiles(const Extent& e) { return max(1, (int)(((long long)e.kv_len + 127) / 128)); }
+__device__ __forceinline__ int row_tiles(const Paged8Params& p, const Extent& e) { return (e.q_len * p.G + p.R - 1) / p.R; }
+__device__ __forceinline__ long long work_of(const Paged8Params& p, const Extent& e) {
+    return (long long)p.H_kv * row_tiles(p, e) * key_tiles(e);
+}
+
+__device__ __forceinline__ void publish(volatile int* q, const Unit& u) {
+    q[0] = u.r; q[1] = u.kvh; q[2] = u.q_start; q[3] = u.q_len; q[4] = u.kv_len;
+    q[5] = u.row0; q[6] = u.nr; q[7] = u.tile0; q[8] = u.nt; q[9] = u.slot;
+}
+__device__ __forceinline__ Unit read_unit(const volatile int* q) {
+    Unit u;
+    u.r = q[0]; u.kvh = q[1]; u.q_start = q[2]; u.q_len = q[3]; u.kv_len = q[4];
+    u.row0 = q[5]; u.nr = q[6]; u.tile0 = q[7]; u.nt = q[8]; u.slot = q[9];
+    return u;
+}
+
+// Position of row x of a unit's request in the request, and with the causal mask its last visible key.
+__device__ __forceinline__ int last_key(const Paged8Params& p, const Unit& u, int x) {
+    if (!p.causal) return u.kv_len - 1;
+    return (int)min((long long)u.kv_len - 1, (long long)u.kv_len - u.q_len + x / p.G);
+}
+
+// A whole warp's wait: every lane gets the same answer.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* status) {
+    return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, status));
+}
+
+__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool softmax_any(bool x) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"((uint32_t)x)
+                 : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ void st_u8(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_zero16(uint32_t addr) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
+}
+
+// Two fp16 numbers <-> two e4m3 numbers (nearest, saturating; NaN stays NaN).
+__device__ __forceinline__ uint32_t e4m3_of(uint32_t h2) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
+    return r;
+}
+__device__ __forceinline__ uint32_t half2_of(uint32_t e) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)e));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t h2_mul16(uint32_t a) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0x4c004c00u));  // 16
+    return r;
+}
+
+// Shared-memory descriptor of an operand tile: rows of W bytes with a swizzle of W bytes, 8-row groups 8 W bytes
+// apart.  The same bytes serve as a K-major operand (rows are M or N) and as an MN-major one (rows are K).
+template <int W>
+__device__ __forceinline__ uint64_t desc(uint32_t addr) {
+    uint64_t d = (uint64_t)((addr >> 4) & 0x3FFFu);
+    d |= (uint64_t)1u << 16;
+    d |= (uint64_t)((8 * W) >> 4) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)(W == 128 ? 2u : 4u) << 61;
+    return d;
+}
+
+// The smallest power of two s >= 2^-126 with amax <= 448 s (a finite amax).
+__device__ __forceinline__ float scale_for(float amax) {
+    const int e = (int)((__float_as_uint(amax) + 0x1fffffu) >> 23) - 8;
+    return __uint_as_float((unsigned)max(e, 1) << 23);
+}
+
+// ---------------------------------------------------------------- producer (whole warp)
+
+template <int D, int R>
+__device__ void producer_role(const Paged8Params& p, uint8_t* smem, const Bars& b, volatile int* uq, volatile int* abort_flag,
+                              int lane, int r, long long w, long long w1, long long start) {
+    using C = Cfg<D, R>;
+    if (lane == 0) {
+        tma_prefetch_map(&p.tm_k);
+        tma_prefetch_map(&p.tm_v);
+    }
+    const int rows = p.rows_per_box, per_tile = 128 / rows;  // boxes of a tile: 1 .. 16
+    const long long w0 = w;
+    int kv_idx = 0, pub = 0;
+    bool ok = true;
+    // lane i: extent of request base + i
+    int base = r;
+    Extent mine = extent(p, min(base + lane, p.B - 1));
+    int prev_rows[2] = {0, 0}, prev_nt = 0;
+
+    // tiles of one step into the ring: box x of the step in lane x % 32, register x / 32
+    auto load_tiles = [&](const CUtensorMap* map, const int* row_of, int nt, int kvh) {
+        for (int t = 0; ok && t < nt; ++t) {
+            const int slot = kv_idx % C::NST, round = kv_idx / C::NST;
+            if (lane == 0) {
+                if (round > 0) ok = wait_bar(&b.kv_empty[slot], (uint32_t)((round - 1) & 1), abort_flag, p.status);
+                if (ok) bar_arrive_expect_tx(&b.kv_full[slot], C::TILE);
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            const int first = t * per_tile;  // per_tile divides 32: the tile's boxes lie in one register
+            const int i = lane - (first & 31);
+            if (i >= 0 && i < per_tile)
+                tma_load_3d(smem + C::OFF_KV + slot * C::TILE + i * rows * D, map, &b.kv_full[slot], 0, kvh,
+                            first < 32 ? row_of[0] : row_of[1]);
+            ++kv_idx;
+        }
+    };
+    int prev_kvh = 0;
+    for (;;) {
+        Unit u;
+        u.r = -1;
+        u.nt = 0;
+        while (w < w1) {
+            if (r >= base + 32) {
+                base = r;
+                mine = extent(p, min(base + lane, p.B - 1));
+            }
+            Extent e;
+            e.q_start = __shfl_sync(0xffffffffu, mine.q_start, r - base);
+            e.q_len = __shfl_sync(0xffffffffu, mine.q_len, r - base);
+            e.kv_len = __shfl_sync(0xffffffffu, mine.kv_len, r - base);
+            const long long work = work_of(p, e);
+            if (w - start >= work) {
+                start += work;
+                ++r;
+                continue;
+            }
+            const int nb = key_tiles(e), nqt = row_tiles(p, e);
+            const long long off = w - start;
+            const int unit = (int)(off / nb), tile = (int)(off - (long long)unit * nb);
+            const int n = (int)min((long long)(nb - tile), w1 - w);
+            u.r = r;
+            u.kvh = unit / nqt;
+            u.q_start = e.q_start;
+            u.q_len = e.q_len;
+            u.kv_len = e.kv_len;
+            u.row0 = (unit - u.kvh * nqt) * R;
+            u.nr = min(R, e.q_len * p.G - u.row0);
+            u.tile0 = tile;
+            const long long seen = (last_key(p, u, u.row0 + u.nr - 1) + 128LL) / 128;  // tiles that the last row sees
+            u.nt = (int)max(0LL, min((long long)n, seen - tile));
+            u.slot = n == nb ? -1 : 2 * (int)blockIdx.x + (w == w0 ? 0 : 1);
+            w += n;
+            break;
+        }
+        if (lane == 0) {
+            const int slot = pub % kQN;
+            if (pub >= kQN) ok = wait_bar(&b.uq_empty[slot], (uint32_t)((pub / kQN - 1) & 1), abort_flag, p.status);
+            if (ok) {
+                publish(uq + slot * kUnitInts, u);
+                bar_arrive(&b.uq_full[slot]);
+            }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok || u.r < 0) break;
+        ++pub;
+        if (u.nt == 0) {  // as in mma_role: no step follows that the pending values could come after
+            load_tiles(&p.tm_v, prev_rows, prev_nt, prev_kvh);
+            prev_nt = 0;
+        }
+        for (int s = 0; ok && s < u.nt; s += C::SB) {
+            const int nt = min(C::SB, u.nt - s);
+            int row_of[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int x = k * 32 + lane;
+                row_of[k] = p.kv_rows;
+                const long long key = (long long)(u.tile0 + s) * 128 + (long long)x * rows;
+                if (x < nt * per_tile && key < u.kv_len) {
+                    const int id = __ldg(p.block_table + (size_t)u.r * p.max_pages + (key >> p.page_shift));
+                    if (id >= 0 && id < p.num_pages)
+                        row_of[k] = (id << p.page_shift) + (int)(key & ((1 << p.page_shift) - 1));
+                    else
+                        atomicOr(p.status, 1u << kStatusDeviceData);
+                }
+            }
+            load_tiles(&p.tm_k, row_of, nt, u.kvh);
+            load_tiles(&p.tm_v, prev_rows, prev_nt, prev_kvh);
+            prev_rows[0] = row_of[0];
+            prev_rows[1] = row_of[1];
+            prev_nt = nt;
+            prev_kvh = u.kvh;
+        }
+        if (!ok) break;
+    }
+    load_tiles(&p.tm_v, prev_rows, prev_nt, prev_kvh);
+    // every copy that this warp started must land before the CTA exits
+    if (lane == 0)
+        for (int idx = kv_idx - C::NST > 0 ? kv_idx - C::NST : 0; idx < kv_idx; ++idx)
+            drain_wait(&b.kv_full[idx % C::NST], (uint32_t)((idx / C::NST) & 1), p.status);
+    __syncwarp();
+}
+
+// ---------------------------------------------------------------- MMA issuer (whole warp, lane 0 issues)
+
+template <int D, int R>
+__device__ void mma_role(const Paged8Params& p, uint8_t* smem, const Bars& b, volatile int* uq, volatile int* abort_flag,
+                         uint32_t tmem, int lane) {
+    using C = Cfg<D, R>;
+    constexpr uint32_t ID_S = idesc_make(128, C::NQ, 0u, false, false);
+    constexpr uint32_t ID_PV = idesc_make(D, C::NPV, 0u, true, false);
+    const uint32_t sbase = smem_u32(smem);
+    volatile int* s_nan = reinterpret_cast<volatile int*>(smem + C::OFF_NAN);
+    auto tile_addr = [&](int idx) { return sbase + C::OFF_KV + (uint32_t)((idx % C::NST) * C::TILE); };
+    int kv_idx = 0, units = 0;
+    uint32_t n = 0;  // steps issued
+    struct Step {
+        Unit u;
+        int s, nt;
+    } prev;
+    prev.nt = 0;
+
+    auto product_pv = [&](uint32_t step) -> bool {  // of prev, step number `step`
+        const Unit& u = prev.u;
+        if (!warp_wait(b.p_full, step & 1u, abort_flag, p.status)) return false;
+        for (int t = 0; t < prev.nt; ++t, ++kv_idx) {
+            if (!warp_wait(&b.kv_full[kv_idx % C::NST], (uint32_t)((kv_idx / C::NST) & 1), abort_flag, p.status)) return false;
+            const int tile = u.tile0 + prev.s + t;
+            const int left = (int)min(128LL, (long long)u.kv_len - (long long)tile * 128);
+            const uint32_t v = tile_addr(kv_idx);
+            bool touched = false;
+            if (left < 128) {
+                // rows past the request's keys may hold anything, and 0 * NaN would reach every row
+                for (int x = left * (D / 16) + lane; x < 128 * (D / 16); x += 32) st_zero16(v + (uint32_t)x * 16u);
+                touched = true;
+            }
+            if (p.causal && u.nr > 1) {
+                // Keys that only some of the rows see: a NaN among their values must not reach the others
+                // through 0 * NaN.  It is taken out and noted, by channel, for the rows from the first that sees it.
+                const long long pos0 = (long long)u.kv_len - u.q_len;
+                const int from = (int)max(0LL, min(128LL, last_key(p, u, u.row0) + 1LL - (long long)tile * 128));
+                for (int x = from * (D / 4) + lane; x < left * (D / 4); x += 32) {
+                    const int key = x / (D / 4), word = x % (D / 4);  // stored word of the row, swizzled
+                    const int chunk = (word >> 2) ^ (D == 128 ? key & 7 : (key >> 1) & 3);
+                    const uint32_t at = v + (uint32_t)(key * D + word * 4);
+                    uint32_t c;
+                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(c) : "r"(at) : "memory");
+                    uint32_t keep = c;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (((c >> (8 * k)) & 0x7fu) == 0x7fu) {
+                            keep &= ~(0xffu << (8 * k));
+                            // token of the first row that sees the key
+                            const long long tok = (long long)tile * 128 + key - pos0;
+                            const int row = (int)max(0LL, tok * p.G - u.row0);
+                            atomicMin(const_cast<int*>(s_nan) + chunk * 16 + (word & 3) * 4 + k, row);
+                        }
+                    if (keep != c) st_u32(at, keep);
+                }
+                touched = touched || from < left;
+            }
+            if (touched) {
+                fence_async_smem();
+                __syncwarp();
+            }
+            if (lane == 0) {
+                tc_fence_after();
+                const uint32_t o = tmem + C::TM_O;
+                const uint64_t a = desc<D>(v), q = desc<128>(sbase + C::OFF_P + (uint32_t)(t * C::PTILE));
+                constexpr uint64_t VS = (32 * D) >> 4;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_f8_ss(o, a + k * VS, q + 2 * k, ID_PV, (prev.s > 0 || t > 0 || k > 0) ? 1u : 0u);
+                tc_commit(&b.kv_empty[kv_idx % C::NST]);
+            }
+        }
+        __syncwarp();
+        if (lane == 0) {
+            tc_commit(b.o_full);
+            bar_arrive(b.o_full);  // what the warp noted of NaNs
+        }
+        return true;
+    };
+
+    for (int k = 0;; ++k) {
+        const int slot = k % kQN;
+        if (!warp_wait(&b.uq_full[slot], (uint32_t)((k / kQN) & 1), abort_flag, p.status)) return;
+        const Unit u = read_unit(uq + slot * kUnitInts);
+        __syncwarp();
+        if (lane == 0) bar_arrive(&b.uq_empty[slot]);
+        if (u.r < 0) break;
+        const int qb = units & 1;
+        if (!warp_wait(&b.q_full[qb], (uint32_t)((units >> 1) & 1), abort_flag, p.status)) return;
+        ++units;
+        const uint64_t q_desc = desc<D>(sbase + C::OFF_Q + (uint32_t)(qb * C::QBYTES));
+        if (u.nt == 0) {
+            // Nothing to compute.  The products of the step before must not wait for a later unit: its query rows
+            // would wait for the buffer that the unit of that step still holds.
+            if (prev.nt > 0 && !product_pv(n - 1u)) return;
+            prev.nt = 0;
+            if (lane == 0) bar_arrive(&b.q_empty[qb]);
+        }
+        for (int s = 0; s < u.nt; s += C::SB) {
+            const int nt = min(C::SB, u.nt - s);
+            for (int t = 0; t < nt; ++t, ++kv_idx) {
+                if (!warp_wait(&b.kv_full[kv_idx % C::NST], (uint32_t)((kv_idx / C::NST) & 1), abort_flag, p.status)) return;
+                if (lane == 0) {
+                    tc_fence_after();
+                    const uint32_t d = tmem + (n & 1u) * 64u + (uint32_t)(t * C::NQ);
+                    const uint64_t a = desc<D>(tile_addr(kv_idx));
+#pragma unroll
+                    for (int x = 0; x < D / 32; ++x) mma_f8_ss(d, a + 2 * x, q_desc + 2 * x, ID_S, x > 0 ? 1u : 0u);
+                    tc_commit(&b.kv_empty[kv_idx % C::NST]);
+                }
+            }
+            if (lane == 0) {
+                tc_commit(&b.s_full[n & 1u]);
+                if (s + nt == u.nt) tc_commit(&b.q_empty[qb]);
+            }
+            __syncwarp();
+            if (prev.nt > 0 && !product_pv(n - 1u)) return;
+            prev.u = u;
+            prev.s = s;
+            prev.nt = nt;
+            ++n;
+        }
+    }
+    if (prev.nt > 0) product_pv(n - 1u);
+}
+
+// ---------------------------------------------------------------- query rows and scales (one warp)
+
+template <int D, int R>
+__device__ void aux_role(const Paged8Params& p, uint8_t* smem, const Bars& b, volatile int* uq, volatile int* abort_flag,
+                         int lane) {
+    using C = Cfg<D, R>;
+    constexpr int PER = D / 32;  // elements of a query row in a lane
+    const uint32_t sbase = smem_u32(smem);
+    const int per_page = p.page_shift - p.block_shift;
+    int units = 0;
+    uint32_t n = 0;
+    for (int k = 0;; ++k) {
+        const int slot = k % kQN;
+        if (!warp_wait(&b.uq_full[slot], (uint32_t)((k / kQN) & 1), abort_flag, p.status)) return;
+        const Unit u = read_unit(uq + slot * kUnitInts);
+        __syncwarp();
+        if (lane == 0) bar_arrive(&b.uq_empty[slot]);
+        if (u.r < 0) return;
+        const int qb = units & 1;
+        if (units >= 2 && !warp_wait(&b.q_empty[qb], (uint32_t)(((units >> 1) - 1) & 1), abort_flag, p.status)) return;
+        ++units;
+        const uint32_t q_at = sbase + C::OFF_Q + (uint32_t)(qb * C::QBYTES);
+        int4* s_row = reinterpret_cast<int4*>(smem + C::OFF_ROW) + qb * R;
+#pragma unroll
+        for (int g0 = 0; g0 < R; g0 += 8) {  // eight rows' loads in flight
+            uint32_t x[8][PER / 2];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int row = u.row0 + g0 + i;
+                const int tok = row / p.G;
+                const int out = (u.q_start + tok) * p.H + u.kvh * p.G + (row - tok * p.G);
+#pragma unroll
+                for (int c = 0; c < PER / 2; ++c) x[i][c] = 0u;
+                if (g0 + i < u.nr) {
+                    const uint16_t* src = p.q + (size_t)out * D + lane * PER;
+                    if (PER == 4) {
+                        const uint2 y = *reinterpret_cast<const uint2*>(src);
+                        x[i][0] = y.x;
+                        x[i][PER / 2 - 1] = y.y;
+                    } else {
+                        x[i][0] = *reinterpret_cast<const uint32_t*>(src);
+                    }
+                }
+                if (lane == i) s_row[g0 + i] = make_int4(0, last_key(p, u, row), out, 0);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float f[PER], top = 0.f;
+#pragma unroll
+                for (int c = 0; c < PER; ++c) {
+                    f[c] = c & 1 ? bf16hi_to_f32(x[i][c / 2]) : bf16lo_to_f32(x[i][c / 2]);
+                    const float a = fabsf(f[c]);
+                    top = fmaxf(top, a < INFINITY ? a : 0.f);
+                }
+#pragma unroll
+                for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const float qs = scale_for(top), inv = 1.f / qs;
+                uint32_t hi = 0u, lo = 0u;
+#pragma unroll
+                for (int c = 0; c < PER; c += 2) {
+                    // an infinity or NaN: x - x makes a NaN of it
+                    const float a = fmaf(f[c], inv, f[c] - f[c]), d = fmaf(f[c + 1], inv, f[c + 1] - f[c + 1]);
+                    uint16_t e;
+                    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e) : "f"(d), "f"(a));
+                    const uint32_t back = half2_of(e);
+                    const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&back));
+                    uint16_t e2;
+                    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e2) : "f"((d - w.y) * 16.f), "f"((a - w.x) * 16.f));
+                    hi |= (uint32_t)e << (8 * c);
+                    lo |= (uint32_t)e2 << (8 * c);
+                }
+                const int r0 = g0 + i, r1 = R + g0 + i, byte = lane * PER;
+                auto at = [&](int r) {
+                    const int chunk = (byte >> 4) ^ (D == 128 ? r & 7 : (r >> 1) & 3);
+                    return q_at + (uint32_t)(r * D + chunk * 16 + (byte & 15));
+                };
+                if (PER == 4) {
+                    st_u32(at(r0), hi);
+                    st_u32(at(r1), lo);
+                } else {
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(at(r0)), "h"((uint16_t)hi) : "memory");
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(at(r1)), "h"((uint16_t)lo) : "memory");
+                }
+                if (lane == 0) s_row[g0 + i].x = __float_as_int(qs * p.c_scale);
+            }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&b.q_full[qb]);
+        for (int s = 0; s < u.nt; s += C::SB, ++n) {
+            const int nt = min(C::SB, u.nt - s);
+            const uint32_t buf = n & 1u;
+            // lane: four keys of each tile, all in one page
+            int id[C::SB];
+            float ks[C::SB][4], vs[C::SB][4];
+#pragma unroll
+            for (int t = 0; t < C::SB; ++t) {
+                const long long key = (long long)(u.tile0 + s + t) * 128 + lane * 4;
+                id[t] = -1;
+                if (t < nt && key < u.kv_len) id[t] = __ldg(p.block_table + (size_t)u.r * p.max_pages + (key >> p.page_shift));
+            }
+#pragma unroll
+            for (int t = 0; t < C::SB; ++t) {
+                const long long key = (long long)(u.tile0 + s + t) * 128 + lane * 4;
+                const bool ok = id[t] >= 0 && id[t] < p.num_pages;
+                const size_t at = (((size_t)(unsigned)(ok ? id[t] : 0) * p.H_kv + u.kvh) << per_page) +
+                                  (((int)key & ((1 << p.page_shift) - 1)) >> p.block_shift);
+                if (p.block_shift >= 2) {
+                    const float x = ok ? __ldg(p.k_scale + at) : 0.f, y = ok ? __ldg(p.v_scale + at) : 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        ks[t][i] = x;
+                        vs[t][i] = y;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool in = ok && key + i < u.kv_len;
+                        ks[t][i] = in ? __ldg(p.k_scale + at + (i >> p.block_shift)) : 0.f;
+                        vs[t][i] = in ? __ldg(p.v_scale + at + (i >> p.block_shift)) : 0.f;
+                    }
+                }
+            }
+            if (n >= 2 && !warp_wait(&b.sc_empty[buf], ((n >> 1) - 1u) & 1u, abort_flag, p.status)) return;
+            float4* dst = reinterpret_cast<float4*>(smem + C::OFF_SC) + (buf * C::SB * 128 + lane * 4) / 2;
+#pragma unroll
+            for (int t = 0; t < C::SB; ++t) {
+                dst[t * 64] = make_float4(ks[t][0], lg2(vs[t][0]), ks[t][1], lg2(vs[t][1]));
+                dst[t * 64 + 1] = make_float4(ks[t][2], lg2(vs[t][2]), ks[t][3], lg2(vs[t][3]));
+            }
+            __syncwarp();
+            if (lane == 0) bar_arrive(&b.sc_full[buf]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- softmax + epilogue (four warps)
+
+__device__ __forceinline__ float warp_max(float x) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+template <int D, int R>
+__device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b, volatile int* uq, volatile int* abort_flag,
+                             uint32_t tmem, int wq, int lane) {
+    using C = Cfg<D, R>;
+    constexpr int SB = C::SB;
+    const int tid = wq * 32 + lane;  // key within a tile, TMEM lane
+    const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
+    const uint32_t tS = tmem + lane_off, tO = tmem + lane_off + C::TM_O;
+    const uint32_t p_at = smem_u32(smem + C::OFF_P) + (uint32_t)tid;  // this key's byte of P's row 0, before the swizzle
+    const float2* s_scale = reinterpret_cast<const float2*>(smem + C::OFF_SC);
+    float2* s_stat = reinterpret_cast<float2*>(smem + C::OFF_STAT);
+    float2* s_alpha = reinterpret_cast<float2*>(smem + C::OFF_ALPHA);
+    float2* s_exch = reinterpret_cast<float2*>(smem + C::OFF_EXCH);
+    float* s_sum = reinterpret_cast<float*>(smem + C::OFF_SUM);
+    int* s_nan = reinterpret_cast<int*>(smem + C::OFF_NAN);
+    uint32_t n = 0;  // step
+    // A failed wait leaves this warp on the common path, so that no barrier lacks a warp; all leave together where
+    // they next agree on it.
+    bool fail = false;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!fail) fail = !warp_wait(bar, parity, abort_flag, p.status);
+    };
+
+    for (int k = 0;; ++k) {
+        const int slot = k % kQN, qb = k & 1;
+        wait(&b.uq_full[slot], (uint32_t)((k / kQN) & 1));
+        if (softmax_any(fail)) return;
+        const Unit u = read_unit(uq + slot * kUnitInts);
+        __syncwarp();
+        if (lane == 0) bar_arrive(&b.uq_empty[slot]);
+        if (u.r < 0) return;
+        wait(&b.q_full[qb], (uint32_t)((k >> 1) & 1));
+        const int4* s_row = reinterpret_cast<const int4*>(smem + C::OFF_ROW) + qb * R;
+        float l[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) l[r] = 0.f;
+
+        for (int s = 0; s < u.nt; s += SB, ++n) {
+            const int nt = min(SB, u.nt - s);
+            const uint32_t buf = n & 1u;
+            wait(&b.sc_full[buf], (n >> 1) & 1u);
+            float2 sc[SB];
+#pragma unroll
+            for (int t = 0; t < SB; ++t) sc[t] = s_scale[(buf * SB + t) * 128 + tid];
+            wait(&b.s_full[buf], (n >> 1) & 1u);
+            __syncwarp();
+            if (lane == 0) bar_arrive(&b.sc_empty[buf]);
+            tc_fence_after();
+            float e[32];
+            {
+                uint32_t x[64];
+                tmem_ld32(tS + buf * 64u, x);
+                tmem_ld32(tS + buf * 64u + 32u, x + 32);
+                tmem_ld_wait();
+                reg_after_wait<64>(x);
+#pragma unroll
+                for (int t = 0; t < SB; ++t)
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        e[t * R + r] = fmaf(__uint_as_float(x[t * C::NQ + R + r]), 0.0625f, __uint_as_float(x[t * C::NQ + r]));
+            }
+            const long long key0 = (long long)(u.tile0 + s) * 128;
+            // whether a key of the step lies past the last one that the unit's first row sees
+            const bool masked = key0 + nt * 128 - 1 > last_key(p, u, u.row0) || nt < SB;
+            bool grew = false;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int4 row = s_row[r];
+                const float2 stat = s_stat[r];
+                const float f = __int_as_float(row.x);
+                float top = -INFINITY, top_v = -INFINITY;
+#pragma unroll
+                for (int t = 0; t < SB; ++t) {
+                    float x = e[t * R + r] * (f * sc[t].x);
+                    if (masked && (t >= nt || key0 + t * 128 + tid > row.y)) x = -INFINITY;
+                    e[t * R + r] = x;
+                    top = fmaxf(top, x);
+                    top_v = fmaxf(top_v, x + sc[t].y);
+                }
+                grew = grew || top > stat.x + kTau || top_v > stat.y + kTau;
+            }
+            if (softmax_any(grew || fail || s == 0)) {
+                if (softmax_any(fail)) return;
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    float top = -INFINITY, top_v = -INFINITY;
+#pragma unroll
+                    for (int t = 0; t < SB; ++t) {
+                        top = fmaxf(top, e[t * R + r]);
+                        top_v = fmaxf(top_v, e[t * R + r] + sc[t].y);
+                    }
+                    top = warp_max(top);
+                    top_v = warp_max(top_v);
+                    if (lane == 0) s_exch[wq * R + r] = make_float2(top, top_v);
+                }
+                softmax_sync();
+                if (tid < R) {
+                    const float2 old = s == 0 ? make_float2(-INFINITY, -INFINITY) : s_stat[tid];
+                    float2 now = old;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        now.x = fmaxf(now.x, s_exch[w * R + tid].x);
+                        now.y = fmaxf(now.y, s_exch[w * R + tid].y);
+                    }
+                    s_stat[tid] = now;
+                    s_alpha[tid] = make_float2(old.x == -INFINITY ? 1.f : ex2(old.x - now.x),
+                                               old.y == -INFINITY ? 1.f : ex2(old.y - now.y));
+                }
+                softmax_sync();
+                if (s > 0) {
+                    wait(b.o_full, (n - 1u) & 1u);
+                    tc_fence_after();
+#pragma unroll
+                    for (int r = 0; r < R; ++r) l[r] *= s_alpha[r].x;
+#pragma unroll
+                    for (int c0 = 0; c0 < 3; ++c0) {  // hi, mid, lo
+#pragma unroll
+                        for (int r0 = 0; r0 < R; r0 += 8) {
+                            uint32_t x[8];
+                            tmem_ld8(tO + (uint32_t)(c0 * R + r0), x);
+                            tmem_ld_wait();
+                            reg_after_wait<8>(x);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * s_alpha[r0 + i].y);
+                            tmem_st8(tO + (uint32_t)(c0 * R + r0), x);
+                        }
+                    }
+                    tmem_st_wait();
+                } else if (n > 0) {
+                    wait(b.o_full, (n - 1u) & 1u);
+                }
+            } else {
+                wait(b.o_full, (n - 1u) & 1u);  // the products of the step before have read P
+            }
+            // probabilities; pairs of them share the conversions
+#pragma unroll
+            for (int r = 0; r < R; r += (SB > 1 ? 1 : 2)) {
+                constexpr int PAIRS = SB > 1 ? SB / 2 : 1;
+                const float2 st0 = s_stat[r], st1 = s_stat[SB > 1 ? r : r + 1];
+                const float m0 = st0.x == -INFINITY ? 0.f : st0.x, m1 = st1.x == -INFINITY ? 0.f : st1.x;
+                const float v0 = st0.y == -INFINITY ? -kBase : st0.y - kBase, v1 = st1.y == -INFINITY ? -kBase : st1.y - kBase;
+#pragma unroll
+                for (int q = 0; q < PAIRS; ++q) {
+                    const int t0 = SB > 1 ? 2 * q : 0, t1 = SB > 1 ? 2 * q + 1 : 0, r1 = SB > 1 ? r : r + 1;
+                    const float a = e[t0 * R + r], c = e[t1 * R + r1];
+                    if (SB > 1) {
+                        l[r] += ex2(a - m0) + ex2(c - m1);
+                    } else {
+                        l[r] += ex2(a - m0);
+                        l[r1] += ex2(c - m1);
+                    }
+                    const uint32_t h = pack_half(ex2(a + sc[t0].y - v0), ex2(c + sc[t1].y - v1));
+                    const uint32_t hi = e4m3_of(h);
+                    const uint32_t rest = h2_mul16(h2_sub(h, half2_of(hi)));
+                    const uint32_t mid = e4m3_of(rest);
+                    const uint32_t lo = e4m3_of(h2_mul16(h2_sub(rest, half2_of(mid))));
+                    const uint32_t a0 = (p_at ^ (uint32_t)((r & 7) << 4)) + (uint32_t)(t0 * C::PTILE + r * 128);
+                    const uint32_t a1 = (p_at ^ (uint32_t)((r1 & 7) << 4)) + (uint32_t)(t1 * C::PTILE + r1 * 128);
+                    st_u8(a0, hi);
+                    st_u8(a1, hi >> 8);
+                    st_u8(a0 + R * 128, mid);
+                    st_u8(a1 + R * 128, mid >> 8);
+                    st_u8(a0 + 2 * R * 128, lo);
+                    st_u8(a1 + 2 * R * 128, lo >> 8);
+                }
+            }
+            fence_async_smem();
+            tc_fence_before();
+            bar_arrive(b.p_full);
+        }
+
+        // ---- the unit's end: sums over the threads, O by channel
+        if (u.nt > 0) wait(b.o_full, (n - 1u) & 1u);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float x = l[r];
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+            if (lane == 0) s_sum[wq * R + r] = x;
+        }
+        softmax_sync();
+        const int chan = D == 128 ? tid : wq * 16 + (lane & 15);
+        const bool mine = !fail && (D == 128 || lane < 16);
+        const int nan_from = s_nan[chan];
+        tc_fence_after();
+#pragma unroll 1
+        for (int r0 = 0; r0 < u.nr; r0 += 8) {
+            uint32_t x[24];
+            if (u.nt > 0) {
+                tmem_ld8(tO + (uint32_t)r0, x);
+                tmem_ld8(tO + (uint32_t)(R + r0), x + 8);
+                tmem_ld8(tO + (uint32_t)(2 * R + r0), x + 16);
+                tmem_ld_wait();
+                reg_after_wait<24>(x);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 24; ++i) x[i] = 0u;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = r0 + i;
+                if (r >= u.nr) break;
+                const float2 st = u.nt > 0 ? s_stat[r] : make_float2(-INFINITY, -INFINITY);
+                const float sum = s_sum[r] + s_sum[R + r] + s_sum[2 * R + r] + s_sum[3 * R + r];
+                const float m = st.x == -INFINITY ? 0.f : st.x;
+                const float f = st.y == -INFINITY ? 0.f : ex2(st.y - kBase - m);
+                float v = fmaf(__uint_as_float(x[16 + i]), 0.00390625f, fmaf(__uint_as_float(x[8 + i]), 0.0625f, __uint_as_float(x[i]))) * f;
+                if (r >= nan_from) v = __int_as_float(0x7fffffff);
+                if (u.slot < 0) {
+                    const size_t out = (size_t)(unsigned)s_row[r].z;
+                    const float y = sum == 0.f ? 0.f : v / sum;
+                    if (mine) p.o[out * D + chan] = (uint16_t)pack_bf16(y, y);
+                    if (!fail && tid == r && p.lse != nullptr) p.lse[out] = sum == 0.f ? -INFINITY : (m + lg2(sum)) * kLn2;
+                } else {
+                    const size_t rec = (size_t)u.slot * R + r;
+                    if (mine) p.part_o[rec * D + chan] = v;
+                    if (!fail && tid == r) *reinterpret_cast<float2*>(p.part_ml + rec * 2) = make_float2(sum == 0.f ? -INFINITY : m, sum);
+                }
+            }
+        }
+        if (mine) s_nan[chan] = 0x7fffffff;
+        tc_fence_before();
+        softmax_sync();  // s_stat, s_sum and the rows have been read
+        if (lane == 0) bar_arrive(&b.q_empty[qb]);
+    }
+}
+
+// ---------------------------------------------------------------- kernels
+
+template <int D, int R>
+__global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_constant__ Paged8Params p) {
+    using C = Cfg<D, R>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    Bars b;
+    b.kv_full = bars;
+    b.kv_empty = b.kv_full + C::NST;
+    b.q_full = b.kv_empty + C::NST;
+    b.q_empty = b.q_full + 2;
+    b.sc_full = b.q_empty + 2;
+    b.sc_empty = b.sc_full + 2;
+    b.s_full = b.sc_empty + 2;
+    b.p_full = b.s_full + 2;
+    b.o_full = b.p_full + 1;
+    b.done = b.o_full + 1;
+    b.uq_full = b.done + 1;
+    b.uq_empty = b.uq_full + kQN;
+    volatile int* uq = reinterpret_cast<volatile int*>(smem + C::OFF_UQ);
+    int* misc = reinterpret_cast<int*>(smem + C::OFF_MISC);  // tmem, abort, skip, r0; 8-byte: total, start, warp sums
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(misc);
+    volatile int* abort_flag = misc + 1;
+    long long* wide = reinterpret_cast<long long*>(misc + 4);  // [0] start of request r0, [1 .. 7] sums of the warps
+
+    griddep_launch_dependents();  // the merge may be scheduled; it waits for this grid
+    // ---- the cut: tiles of all requests, in order, in shares of equal size
+    const int per = (p.B + kThreads8 - 1) / kThreads8;
+    const int ra = min(p.B, tid * per), rb = min(p.B, ra + per);
+    long long sum = 0;
     bool bad = false;
-    if (p.cu_q != nullptr) {
+    for (int r = ra; r < rb; ++r) {
+        const Extent e = extent(p, r);
+        bad |= e.bad;
+        sum += work_of(p, e);
+    }
+    if (bad && blockIdx.x == 0) atomicOr(p.status, 1u << kStatusDeviceData);
+    long long before = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += y;
+    }
+    if (lane == 31) wide[1 + warp] = before;
+    if (tid == 0) {
+        for (int s = 0; s < C::NST; ++s) {
+            bar_init(&b.kv_full[s], 1);
+            bar_init(&b.kv_empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&b.q_full[i], 1);
+            bar_init(&b.q_empty[i], 5);
+            bar_init(&b.sc_full[i], 1);
+            bar_init(&b.sc_empty[i], 4);
+            bar_init(&b.s_full[i], 1);
+        }
+        bar_init(b.p_full, 128);
+        bar_init(b.o_full, 2);
+        bar_init(b.done, 1);
+        for (int i = 0; i < kQN; ++i) {
+            bar_init(&b.uq_full[i], 1);
+            bar_init(&b.uq_empty[i], 6);
+        }
+        *abort_flag = 0;
+        misc[2] = timeout_recorded(p.status) ? 1 : 0;  // an earlier launch gave up
+        bar_init_fence();
+    }
+    for (int i = tid; i < D; i += kThreads8) reinterpret_cast<int*>(smem + C::OFF_NAN)[i] = 0x7fffffff;
+    // columns of O^T that pad 3 R to 32: their rows of P read as zeros
+    if (R == 8)
+        for (int i = tid; i < C::SB * 8 * 8; i += kThreads8)
+            st_zero16(smem_u32(smem + C::OFF_P) + (uint32_t)((i / 64) * C::PTILE + 24 * 128 + (i % 64) * 16));
+    fence_async_smem();
+    if (warp == 0) {
+        tmem_alloc(tmem_holder, C::TM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    long long total = 0;
+    before -= sum;
+#pragma unroll
+    for (int w = 0; w < kThreads8 / 32; ++w) {
+        if (w < warp) before += wide[1 + w];
+        total += wide[1 + w];
+    }
+    const long long share = max((long long)kMinShare, (total + gridDim.x - 1) / gridDim.x);
+    const long long w0 = (long long)blockIdx.x * share, w1 = min(total, w0 + share);
+    if (blockIdx.x == 0) {  // for the merge
+        if (tid == 0) p.plan[0] = share;
+        long long at = before;
+        for (int r = ra; r < rb; ++r) {
+            p.plan[1 + r] = at;
+            at += work_of(p, extent(p, r));
+        }
+    }
+    if (w0 >= before && w0 < before + sum) {  // this thread's requests hold the CTA's first tile
+        long long at = before;
+        for (int r = ra; r < rb; ++r) {
+            const long long work = work_of(p, extent(p, r));
+            if (w0 < at + work) {
+                misc[3] = r;
+                wide[0] = at;
+                break;
+            }
+            at += work;
+        }
+    }
+    __syncthreads();
+    const uint32_t tmem = *tmem_holder;
+    if (misc[2] == 0 && w0 < total) {
+        if (warp >= 2 && warp < 6) {
+            softmax_role<D, R>(p, smem, b, uq, abort_flag, tmem, warp & 3, lane);
+        } else if (warp == 1) {
+            mma_role<D, R>(p, smem, b, uq, abort_flag, tmem, lane);
+            __syncwarp();
+            if (lane == 0) {
+                tc_commit(b.done);  // every issued MMA finishes before tensor memory is released
+                drain_wait(b.done, 0, p.status);
+            }
+            __syncwarp();
+        } else if (warp == 0) {
+            producer_role<D, R>(p, smem, b, uq, abort_flag, lane, misc[3], w0, w1, wide[0]);
+        } else {
+            aux_role<D, R>(p, smem, b, uq, abort_flag, lane);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TM_COLS);
+    }
+}
+
+// One warp per output row (query token, head): where its unit was cut, its pieces by
+//   m = max m_i,  l = sum l_i 2^(m_i - m),  O = sum 2^(m_i - m) O_i / l.
+template <int D>
+__global__ void __launch_bounds__(256) paged8_merge_kernel(const __grid_constant__ Paged8Params p) {
+    constexpr int PER = D / 32;
+    griddep_wait();
+    const long long row = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    const int lane = threadIdx.x & 31;
+    if (row >= (long long)p.total_q * p.H || timeout_recorded(p.status)) return;
+    const int tok = (int)(row / p.H), head = (int)(row - (long long)tok * p.H);
+    int r = tok;
+    if (p.cu_q != nullptr) {  // the last request whose first token is <= tok
         int lo = 0, hi = p.B - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -38,86 +1010,89 @@ __global__ void __launch_bounds__(kWarps * 32) paged8_simple_kernel(const __grid
                 hi = mid - 1;
         }
         r = lo;
-        const int a = __ldg(p.cu_q + r), b = __ldg(p.cu_q + r + 1);
-        bad = a < 0 || b < a || b > p.total_q || b - a > p.max_q_len;
-        if (!bad && (tok < a || tok >= b)) return;
-        q_start = a;
-        q_len = b - a;
     }
-    int len = __ldg(p.seq_lens + r);
-    const int cap = p.max_pages << p.page_shift;
-    if (len < 0 || len > cap) {
-        bad = true;
-        len = len < 0 ? 0 : cap;
-    }
-    if (bad && threadIdx.x == 0) atomicOr(p.status, 1u << kStatusDeviceData);
-    const long long limit = p.causal ? (long long)len - q_len + (tok - q_start) + 1 : len;
-    const int n = (int)(limit < len ? limit : len);
-    const int kvh = head / p.G;
-    const int per_page = 1 << (p.page_shift - p.block_shift);
-    const size_t row = (size_t)tok * p.H + head;
-    float q[PER], o[PER], m = -INFINITY, l = 0.f;
+    const Extent e = extent(p, r);
+    const int t = tok - e.q_start;
+    if (t < 0 || t >= e.q_len) return;
+    const int kvh = head / p.G, x = t * p.G + head - kvh * p.G;
+    const int nb = key_tiles(e), qt = x / p.R;
+    const long long share = *(const volatile long long*)p.plan;
+    const long long first = *(const volatile long long*)(p.plan + 1 + r) + ((long long)kvh * row_tiles(p, e) + qt) * nb;
+    const int c0 = (int)(first / share), c1 = (int)((first + nb - 1) / share);
+    if (c0 == c1) return;
+    auto record = [&](int c) { return ((size_t)(2 * c + (c == c0 && first != c * share ? 1 : 0))) * p.R + (x - qt * p.R); };
+    float m = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, *(const volatile float*)(p.part_ml + record(c) * 2));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    float l = 0.f, acc[PER];
 #pragma unroll
-    for (int c = 0; c < PER; ++c) {
-        q[c] = __uint_as_float((uint32_t)p.q[row * D + lane * PER + c] << 16);
-        o[c] = 0.f;
-    }
-    for (int k = warp; k < n; k += kWarps) {
-        const int id = __ldg(p.block_table + (size_t)r * p.max_pages + (k >> p.page_shift));
-        const int in_page = k & ((1 << p.page_shift) - 1);
-        float s = 0.f, ks = 0.f, vs = 0.f;
-        const size_t at = ((((size_t)(unsigned)id << p.page_shift) + in_page) * p.H_kv + kvh) * D + lane * PER;
-        const bool ok = id >= 0 && id < p.num_pages;
-        if (ok) {
-            const size_t sc = ((size_t)id * p.H_kv + kvh) * per_page + (in_page >> p.block_shift);
-            ks = __ldg(p.k_scale + sc);
-            vs = __ldg(p.v_scale + sc);
-#pragma unroll
-            for (int c = 0; c < PER; ++c) s = fmaf(q[c], value(p.k_cache[at + c]), s);
-        } else if (lane == 0) {
-            atomicOr(p.status, 1u << kStatusDeviceData);
+    for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+    for (int base = c0; base <= c1; base += 32) {
+        float w = 0.f;
+        if (base + lane <= c1) {
+            const size_t rec = record(base + lane);
+            const float mi = *(const volatile float*)(p.part_ml + rec * 2);
+            // a piece without a visible key has no O
+            w = mi == -INFINITY ? 0.f : ex2(mi - m);
+            if (w != 0.f) l += *(const volatile float*)(p.part_ml + rec * 2 + 1) * w;
         }
+        const int n = min(32, c1 - base + 1);
+        for (int i = 0; i < n; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, w, i);
+            if (wi == 0.f) continue;
+            const volatile float* src = p.part_o + record(base + i) * D + lane * PER;
 #pragma unroll
-        for (int x = 16; x >= 1; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= ks * p.c_scale;
-        const float top = fmaxf(m, s), base = top == -INFINITY ? 0.f : top;
-        const float alpha = exp2f(m - base), w = exp2f(s - base);
-        m = top;
-        l = l * alpha + w;
-#pragma unroll
-        for (int c = 0; c < PER; ++c) o[c] = o[c] * alpha + (ok ? w * (vs * value(p.v_cache[at + c])) : 0.f);
-    }
-    if (lane == 0) {
-        s_m[warp] = m;
-        s_l[warp] = l;
+            for (int k = 0; k < PER; ++k) acc[k] = fmaf(wi, src[k], acc[k]);
+        }
     }
 #pragma unroll
-    for (int c = 0; c < PER; ++c) s_o[warp][lane * PER + c] = o[c];
-    __syncthreads();
-    if (threadIdx.x >= D) return;
-    float top = -INFINITY, sum = 0.f, acc = 0.f;
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w]);
-    const float base = top == -INFINITY ? 0.f : top;
-    for (int w = 0; w < kWarps; ++w) {
-        const float f = exp2f(s_m[w] - base);
-        sum += s_l[w] * f;
-        acc += s_o[w][threadIdx.x] * f;
-    }
-    const float out = sum == 0.f ? 0.f : acc / sum;
-    p.o[row * D + threadIdx.x] = (uint16_t)pack_bf16(out, out);
-    if (threadIdx.x == 0 && p.lse != nullptr)
-        p.lse[row] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * 0.69314718055994530942f;
+    for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D + lane * PER);
+#pragma unroll
+    for (int k = 0; k < PER; k += 2) dst[k / 2] = pack_bf16(acc[k] * inv, acc[k + 1] * inv);
+    if (lane == 0 && p.lse != nullptr) p.lse[row] = l == 0.f ? -INFINITY : (m + lg2(l)) * kLn2;
+}
+
+template <int D, int R>
+cudaError_t launch(const Paged8Params& p, cudaStream_t stream) {
+    static std::atomic<unsigned long long> opted{0};
+    cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(paged8_kernel<D, R>), Cfg<D, R>::SMEM_BYTES, opted);
+    if (e != cudaSuccess) return e;
+    paged8_kernel<D, R><<<p.n_ctas, kThreads8, Cfg<D, R>::SMEM_BYTES, stream>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(((long long)p.total_q * p.H + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged8_merge_kernel<D>, p);
 }
 
 }  // namespace
 
+Paged8Plan paged8_plan(int B, int max_q_len, int G, int d) {
+    Paged8Plan pl;
+    const long long rows = (long long)max_q_len * G;
+    pl.R = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+    pl.part_ml = (8 + (size_t)B * 8 + 255) / 256 * 256;
+    pl.part_o = pl.part_ml + (size_t)2 * kPaged8Ctas * pl.R * 2 * sizeof(float);
+    pl.bytes = pl.part_o + (size_t)2 * kPaged8Ctas * pl.R * d * sizeof(float);
+    return pl;
+}
+
 cudaError_t launch_paged8(int d, const Paged8Params& p, cudaStream_t stream) {
-    const dim3 grid((unsigned)p.total_q, (unsigned)p.H);
-    if (d == 128)
-        paged8_simple_kernel<128><<<grid, kWarps * 32, 0, stream>>>(p);
-    else
-        paged8_simple_kernel<64><<<grid, kWarps * 32, 0, stream>>>(p);
-    return cudaGetLastError();
+    if (d == 128) return p.R == 8 ? launch<128, 8>(p, stream) : p.R == 16 ? launch<128, 16>(p, stream) : launch<128, 32>(p, stream);
+    return p.R == 8 ? launch<64, 8>(p, stream) : p.R == 16 ? launch<64, 16>(p, stream) : launch<64, 32>(p, stream);
 }
 
 }  // namespace attn
