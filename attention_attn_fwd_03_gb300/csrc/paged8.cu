@@ -66,7 +66,7 @@ struct Cfg {
     static constexpr int OFF_KV = 0;
     static constexpr int OFF_P = OFF_KV + NST * TILE;
     static constexpr int OFF_Q = OFF_P + SB * PTILE;
-    static constexpr int OFF_SC = OFF_Q + 2 * QBYTES;                 // float2 [2][SB][128]: ks, log2 vs
+    static constexpr int OFF_SC = OFF_Q + 2 * QBYTES;                 // float2 [2][SB * 128]: ks, log2 vs of each key (or 2 .. 16 keys)
     static constexpr int OFF_ROW = OFF_SC + 2 * SB * 128 * 8;         // int4 [2][R]: factor, last visible key, output row
     static constexpr int OFF_STAT = OFF_ROW + 2 * R * 16;             // float2 [R]: running maxima of s and of s + log2 vs
     static constexpr int OFF_ALPHA = OFF_STAT + R * 8;                // float2 [R]
@@ -178,6 +178,9 @@ __device__ __forceinline__ void st_u8(uint32_t addr, uint32_t v) {
 }
 __device__ __forceinline__ void st_u32(uint32_t addr, uint32_t v) {
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_v2(uint32_t addr, uint32_t a, uint32_t b) {
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 __device__ __forceinline__ void st_zero16(uint32_t addr) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
@@ -484,9 +487,11 @@ template <int D, int R>
 __device__ void aux_role(const Paged8Params& p, uint8_t* smem, const Bars& b, volatile int* uq, volatile int* abort_flag,
                          int lane) {
     using C = Cfg<D, R>;
-    constexpr int PER = D / 32;  // elements of a query row in a lane
+    constexpr int LPR = D / 8;         // lanes of a query row, 8 elements each
+    constexpr int PASS = 8 * LPR / 32; // rounds for 8 rows
     const uint32_t sbase = smem_u32(smem);
     const int per_page = p.page_shift - p.block_shift;
+    const int gshift = min(p.block_shift, 4);  // keys that share an entry of s_scale: 1 to 16
     int units = 0;
     uint32_t n = 0;
     for (int k = 0;; ++k) {
@@ -501,113 +506,91 @@ __device__ void aux_role(const Paged8Params& p, uint8_t* smem, const Bars& b, vo
         ++units;
         const uint32_t q_at = sbase + C::OFF_Q + (uint32_t)(qb * C::QBYTES);
         int4* s_row = reinterpret_cast<int4*>(smem + C::OFF_ROW) + qb * R;
+        if (lane < R) {
+            const int row = u.row0 + min(lane, u.nr - 1), tok = row / p.G;
+            s_row[lane] = make_int4(0, max(last_key(p, u, row), -1),
+                                    (u.q_start + tok) * p.H + u.kvh * p.G + (row - tok * p.G), 0);
+        }
+        __syncwarp();
+#pragma unroll 1
+        for (int g0 = 0; g0 < R; g0 += 8) {
+            uint4 x[PASS];
 #pragma unroll
-        for (int g0 = 0; g0 < R; g0 += 8) {  // eight rows' loads in flight
-            uint32_t x[8][PER / 2];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int row = u.row0 + g0 + i;
-                const int tok = row / p.G;
-                const int out = (u.q_start + tok) * p.H + u.kvh * p.G + (row - tok * p.G);
-#pragma unroll
-                for (int c = 0; c < PER / 2; ++c) x[i][c] = 0u;
-                if (g0 + i < u.nr) {
-                    const uint16_t* src = p.q + (size_t)out * D + lane * PER;
-                    if (PER == 4) {
-                        const uint2 y = *reinterpret_cast<const uint2*>(src);
-                        x[i][0] = y.x;
-                        x[i][PER / 2 - 1] = y.y;
-                    } else {
-                        x[i][0] = *reinterpret_cast<const uint32_t*>(src);
-                    }
-                }
-                if (lane == i) s_row[g0 + i] = make_int4(0, last_key(p, u, row), out, 0);
+            for (int i = 0; i < PASS; ++i) {
+                const int r = g0 + (i * 32 + lane) / LPR;
+                x[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (r < u.nr)
+                    x[i] = *reinterpret_cast<const uint4*>(p.q + (size_t)(unsigned)s_row[r].z * D + lane % LPR * 8);
             }
-            __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float f[PER], top = 0.f;
+            for (int i = 0; i < PASS; ++i) {
+                const int r = g0 + (i * 32 + lane) / LPR;
+                const uint32_t* word = reinterpret_cast<const uint32_t*>(&x[i]);
+                float f[8], top = 0.f;
 #pragma unroll
-                for (int c = 0; c < PER; ++c) {
-                    f[c] = c & 1 ? bf16hi_to_f32(x[i][c / 2]) : bf16lo_to_f32(x[i][c / 2]);
+                for (int c = 0; c < 8; ++c) {
+                    f[c] = c & 1 ? bf16hi_to_f32(word[c / 2]) : bf16lo_to_f32(word[c / 2]);
                     const float a = fabsf(f[c]);
                     top = fmaxf(top, a < INFINITY ? a : 0.f);
                 }
 #pragma unroll
-                for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                for (int o = LPR / 2; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                 const float qs = scale_for(top), inv = 1.f / qs;
-                uint32_t hi = 0u, lo = 0u;
+                uint32_t hi[2], lo[2];
 #pragma unroll
-                for (int c = 0; c < PER; c += 2) {
+                for (int c = 0; c < 8; c += 2) {
                     // an infinity or NaN: x - x makes a NaN of it
                     const float a = fmaf(f[c], inv, f[c] - f[c]), d = fmaf(f[c + 1], inv, f[c + 1] - f[c + 1]);
-                    uint16_t e;
+                    uint16_t e, e2;
                     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e) : "f"(d), "f"(a));
                     const uint32_t back = half2_of(e);
                     const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&back));
-                    uint16_t e2;
                     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e2) : "f"((d - w.y) * 16.f), "f"((a - w.x) * 16.f));
-                    hi |= (uint32_t)e << (8 * c);
-                    lo |= (uint32_t)e2 << (8 * c);
+                    hi[c / 4] = c & 2 ? hi[c / 4] | (uint32_t)e << 16 : (uint32_t)e;
+                    lo[c / 4] = c & 2 ? lo[c / 4] | (uint32_t)e2 << 16 : (uint32_t)e2;
                 }
-                const int r0 = g0 + i, r1 = R + g0 + i, byte = lane * PER;
-                auto at = [&](int r) {
-                    const int chunk = (byte >> 4) ^ (D == 128 ? r & 7 : (r >> 1) & 3);
-                    return q_at + (uint32_t)(r * D + chunk * 16 + (byte & 15));
+                const int byte = lane % LPR * 8;
+                auto at = [&](int row) {
+                    const int chunk = (byte >> 4) ^ (D == 128 ? row & 7 : (row >> 1) & 3);
+                    return q_at + (uint32_t)(row * D + chunk * 16 + (byte & 15));
                 };
-                if (PER == 4) {
-                    st_u32(at(r0), hi);
-                    st_u32(at(r1), lo);
-                } else {
-                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(at(r0)), "h"((uint16_t)hi) : "memory");
-                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(at(r1)), "h"((uint16_t)lo) : "memory");
-                }
-                if (lane == 0) s_row[g0 + i].x = __float_as_int(qs * p.c_scale);
+                st_v2(at(r), hi[0], hi[1]);
+                st_v2(at(R + r), lo[0], lo[1]);
+                if (lane % LPR == 0) s_row[r].x = __float_as_int(qs * p.c_scale);
             }
         }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) bar_arrive(&b.q_full[qb]);
         for (int s = 0; s < u.nt; s += C::SB, ++n) {
-            const int nt = min(C::SB, u.nt - s);
             const uint32_t buf = n & 1u;
-            // lane: four keys of each tile, all in one page
-            int id[C::SB];
-            float ks[C::SB][4], vs[C::SB][4];
+            const int groups = (min(C::SB, u.nt - s) * 128) >> gshift;
+            float2* dst = reinterpret_cast<float2*>(smem + C::OFF_SC) + buf * C::SB * 128;
+            bool free = n < 2;
+#pragma unroll 1
+            for (int g0 = 0; g0 < groups; g0 += 128) {
+                float2 v[4];
 #pragma unroll
-            for (int t = 0; t < C::SB; ++t) {
-                const long long key = (long long)(u.tile0 + s + t) * 128 + lane * 4;
-                id[t] = -1;
-                if (t < nt && key < u.kv_len) id[t] = __ldg(p.block_table + (size_t)u.r * p.max_pages + (key >> p.page_shift));
-            }
-#pragma unroll
-            for (int t = 0; t < C::SB; ++t) {
-                const long long key = (long long)(u.tile0 + s + t) * 128 + lane * 4;
-                const bool ok = id[t] >= 0 && id[t] < p.num_pages;
-                const size_t at = (((size_t)(unsigned)(ok ? id[t] : 0) * p.H_kv + u.kvh) << per_page) +
-                                  (((int)key & ((1 << p.page_shift) - 1)) >> p.block_shift);
-                if (p.block_shift >= 2) {
-                    const float x = ok ? __ldg(p.k_scale + at) : 0.f, y = ok ? __ldg(p.v_scale + at) : 0.f;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        ks[t][i] = x;
-                        vs[t][i] = y;
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const bool in = ok && key + i < u.kv_len;
-                        ks[t][i] = in ? __ldg(p.k_scale + at + (i >> p.block_shift)) : 0.f;
-                        vs[t][i] = in ? __ldg(p.v_scale + at + (i >> p.block_shift)) : 0.f;
+                for (int i = 0; i < 4; ++i) {  // four groups' loads in flight
+                    const int g = g0 + i * 32 + lane;
+                    const long long key = (long long)(u.tile0 + s) * 128 + ((long long)g << gshift);
+                    v[i] = make_float2(0.f, 0.f);
+                    if (g < groups && key < u.kv_len) {
+                        const int id = __ldg(p.block_table + (size_t)u.r * p.max_pages + (key >> p.page_shift));
+                        if (id >= 0 && id < p.num_pages) {
+                            const size_t at = (((size_t)(unsigned)id * p.H_kv + u.kvh) << per_page) +
+                                              (((int)key & ((1 << p.page_shift) - 1)) >> p.block_shift);
+                            v[i] = make_float2(__ldg(p.k_scale + at), __ldg(p.v_scale + at));
+                        }
                     }
                 }
-            }
-            if (n >= 2 && !warp_wait(&b.sc_empty[buf], ((n >> 1) - 1u) & 1u, abort_flag, p.status)) return;
-            float4* dst = reinterpret_cast<float4*>(smem + C::OFF_SC) + (buf * C::SB * 128 + lane * 4) / 2;
+                if (!free) {
+                    if (!warp_wait(&b.sc_empty[buf], ((n >> 1) - 1u) & 1u, abort_flag, p.status)) return;
+                    free = true;
+                }
 #pragma unroll
-            for (int t = 0; t < C::SB; ++t) {
-                dst[t * 64] = make_float4(ks[t][0], lg2(vs[t][0]), ks[t][1], lg2(vs[t][1]));
-                dst[t * 64 + 1] = make_float4(ks[t][2], lg2(vs[t][2]), ks[t][3], lg2(vs[t][3]));
+                for (int i = 0; i < 4; ++i)
+                    if (g0 + i * 32 + lane < groups) dst[g0 + i * 32 + lane] = make_float2(v[i].x, lg2(v[i].y));
             }
             __syncwarp();
             if (lane == 0) bar_arrive(&b.sc_full[buf]);
@@ -623,6 +606,26 @@ __device__ __forceinline__ float warp_max(float x) {
     return r;
 }
 
+// Sums of eight values over the warp: lane i gets that of value 4 (i >> 4 & 1) + 2 (i >> 3 & 1) + (i >> 2 & 1).
+__device__ __forceinline__ float warp_sum8(const float* v, int lane) {
+    float a[4], c[2], x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool up = lane & 16;
+        a[i] = (up ? v[i + 4] : v[i]) + __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + 4], 16);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const bool up = lane & 8;
+        c[i] = (up ? a[i + 2] : a[i]) + __shfl_xor_sync(0xffffffffu, up ? a[i] : a[i + 2], 8);
+    }
+    x = (lane & 4 ? c[1] : c[0]) + __shfl_xor_sync(0xffffffffu, lane & 4 ? c[0] : c[1], 4);
+    x += __shfl_xor_sync(0xffffffffu, x, 2);
+    return x + __shfl_xor_sync(0xffffffffu, x, 1);
+}
+
+// The code is kept small (loops over tiles, scores read from tensor memory twice): with a step's 32 scores in
+// registers and everything unrolled, warps waited for instructions more than for data.
 template <int D, int R>
 __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b, volatile int* uq, volatile int* abort_flag,
                              uint32_t tmem, int wq, int lane) {
@@ -638,6 +641,7 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
     float2* s_exch = reinterpret_cast<float2*>(smem + C::OFF_EXCH);
     float* s_sum = reinterpret_cast<float*>(smem + C::OFF_SUM);
     int* s_nan = reinterpret_cast<int*>(smem + C::OFF_NAN);
+    const int gshift = min(p.block_shift, 4);
     uint32_t n = 0;  // step
     // A failed wait leaves this warp on the common path, so that no barrier lacks a warp; all leave together where
     // they next agree on it.
@@ -663,62 +667,61 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
         for (int s = 0; s < u.nt; s += SB, ++n) {
             const int nt = min(SB, u.nt - s);
             const uint32_t buf = n & 1u;
+            const int key0 = (u.tile0 + s) * 128;  // below kv_len
             wait(&b.sc_full[buf], (n >> 1) & 1u);
-            float2 sc[SB];
-#pragma unroll
-            for (int t = 0; t < SB; ++t) sc[t] = s_scale[(buf * SB + t) * 128 + tid];
             wait(&b.s_full[buf], (n >> 1) & 1u);
-            __syncwarp();
-            if (lane == 0) bar_arrive(&b.sc_empty[buf]);
             tc_fence_after();
-            float e[32];
-            {
-                uint32_t x[64];
-                tmem_ld32(tS + buf * 64u, x);
-                tmem_ld32(tS + buf * 64u + 32u, x + 32);
+            // scores of tile t and rows rb .. rb + 7 in log2 units, -inf where masked
+            auto scores = [&](int rb, int t, const float* f, const int* last, float* e) {
+                uint32_t x[16];
+                tmem_ld8(tS + buf * 64u + (uint32_t)(t * C::NQ + rb), x);
+                tmem_ld8(tS + buf * 64u + (uint32_t)(t * C::NQ + R + rb), x + 8);
+                const float2 sc = s_scale[buf * SB * 128 + ((t * 128 + tid) >> gshift)];
                 tmem_ld_wait();
-                reg_after_wait<64>(x);
+                reg_after_wait<16>(x);
 #pragma unroll
-                for (int t = 0; t < SB; ++t)
-#pragma unroll
-                    for (int r = 0; r < R; ++r)
-                        e[t * R + r] = fmaf(__uint_as_float(x[t * C::NQ + R + r]), 0.0625f, __uint_as_float(x[t * C::NQ + r]));
-            }
-            const long long key0 = (long long)(u.tile0 + s) * 128;
-            // whether a key of the step lies past the last one that the unit's first row sees
-            const bool masked = key0 + nt * 128 - 1 > last_key(p, u, u.row0) || nt < SB;
-            bool grew = false;
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int4 row = s_row[r];
-                const float2 stat = s_stat[r];
-                const float f = __int_as_float(row.x);
-                float top = -INFINITY, top_v = -INFINITY;
-#pragma unroll
-                for (int t = 0; t < SB; ++t) {
-                    float x = e[t * R + r] * (f * sc[t].x);
-                    if (masked && (t >= nt || key0 + t * 128 + tid > row.y)) x = -INFINITY;
-                    e[t * R + r] = x;
-                    top = fmaxf(top, x);
-                    top_v = fmaxf(top_v, x + sc[t].y);
+                for (int i = 0; i < 8; ++i) {
+                    const float y = fmaf(__uint_as_float(x[8 + i]), 0.0625f, __uint_as_float(x[i])) * (f[i] * sc.x);
+                    e[i] = t * 128 + tid > last[i] ? -INFINITY : y;
                 }
-                grew = grew || top > stat.x + kTau || top_v > stat.y + kTau;
-            }
-            if (softmax_any(grew || fail || s == 0)) {
-                if (softmax_any(fail)) return;
+                return sc.y;
+            };
+            auto rows = [&](int rb, float* f, int* last) {  // score factor and last visible key (from key0) of rows rb ..
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    float top = -INFINITY, top_v = -INFINITY;
+                for (int i = 0; i < 8; ++i) {
+                    const int2 row = *reinterpret_cast<const int2*>(s_row + rb + i);
+                    f[i] = __int_as_float(row.x);
+                    last[i] = row.y - key0;
+                }
+            };
+            bool grew = s == 0;
 #pragma unroll
-                    for (int t = 0; t < SB; ++t) {
-                        top = fmaxf(top, e[t * R + r]);
-                        top_v = fmaxf(top_v, e[t * R + r] + sc[t].y);
+            for (int rb = 0; rb < R; rb += 8) {
+                float f[8], top[8], top_v[8];
+                int last[8];
+                rows(rb, f, last);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top[i] = top_v[i] = -INFINITY;
+#pragma unroll 1
+                for (int t = 0; t < nt; ++t) {
+                    float e[8];
+                    const float lv = scores(rb, t, f, last, e);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        top[i] = fmaxf(top[i], e[i]);
+                        top_v[i] = fmaxf(top_v[i], e[i] + lv);
                     }
-                    top = warp_max(top);
-                    top_v = warp_max(top_v);
-                    if (lane == 0) s_exch[wq * R + r] = make_float2(top, top_v);
                 }
-                softmax_sync();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float a = warp_max(top[i]), c = warp_max(top_v[i]);
+                    const float2 stat = s_stat[rb + i];
+                    grew = grew || a > stat.x + kTau || c > stat.y + kTau;
+                    if (lane == i) s_exch[wq * R + rb + i] = make_float2(a, c);
+                }
+            }
+            if (softmax_any(grew || fail)) {
+                if (softmax_any(fail)) return;
                 if (tid < R) {
                     const float2 old = s == 0 ? make_float2(-INFINITY, -INFINITY) : s_stat[tid];
                     float2 now = old;
@@ -737,110 +740,102 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
                     tc_fence_after();
 #pragma unroll
                     for (int r = 0; r < R; ++r) l[r] *= s_alpha[r].x;
+#pragma unroll 1
+                    for (int c = 0; c < 3 * R; c += 8) {  // hi, mid, lo
+                        uint32_t x[8];
+                        tmem_ld8(tO + (uint32_t)c, x);
+                        tmem_ld_wait();
+                        reg_after_wait<8>(x);
 #pragma unroll
-                    for (int c0 = 0; c0 < 3; ++c0) {  // hi, mid, lo
-#pragma unroll
-                        for (int r0 = 0; r0 < R; r0 += 8) {
-                            uint32_t x[8];
-                            tmem_ld8(tO + (uint32_t)(c0 * R + r0), x);
-                            tmem_ld_wait();
-                            reg_after_wait<8>(x);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * s_alpha[r0 + i].y);
-                            tmem_st8(tO + (uint32_t)(c0 * R + r0), x);
-                        }
+                        for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * s_alpha[c % R + i].y);
+                        tmem_st8(tO + (uint32_t)c, x);
                     }
                     tmem_st_wait();
-                } else if (n > 0) {
-                    wait(b.o_full, (n - 1u) & 1u);
                 }
             } else {
                 wait(b.o_full, (n - 1u) & 1u);  // the products of the step before have read P
             }
-            // probabilities; pairs of them share the conversions
 #pragma unroll
-            for (int r = 0; r < R; r += (SB > 1 ? 1 : 2)) {
-                constexpr int PAIRS = SB > 1 ? SB / 2 : 1;
-                const float2 st0 = s_stat[r], st1 = s_stat[SB > 1 ? r : r + 1];
-                const float m0 = st0.x == -INFINITY ? 0.f : st0.x, m1 = st1.x == -INFINITY ? 0.f : st1.x;
-                const float v0 = st0.y == -INFINITY ? -kBase : st0.y - kBase, v1 = st1.y == -INFINITY ? -kBase : st1.y - kBase;
+            for (int rb = 0; rb < R; rb += 8) {
+                float f[8], m[8], mv[8];
+                int last[8];
+                rows(rb, f, last);
 #pragma unroll
-                for (int q = 0; q < PAIRS; ++q) {
-                    const int t0 = SB > 1 ? 2 * q : 0, t1 = SB > 1 ? 2 * q + 1 : 0, r1 = SB > 1 ? r : r + 1;
-                    const float a = e[t0 * R + r], c = e[t1 * R + r1];
-                    if (SB > 1) {
-                        l[r] += ex2(a - m0) + ex2(c - m1);
-                    } else {
-                        l[r] += ex2(a - m0);
-                        l[r1] += ex2(c - m1);
+                for (int i = 0; i < 8; ++i) {
+                    const float2 stat = s_stat[rb + i];
+                    m[i] = stat.x == -INFINITY ? 0.f : stat.x;
+                    mv[i] = stat.y == -INFINITY ? 0.f : stat.y - kBase;
+                }
+#pragma unroll 1
+                for (int t = 0; t < nt; ++t) {
+                    float e[8];
+                    const float lv = scores(rb, t, f, last, e);
+                    const uint32_t at = p_at + (uint32_t)(t * C::PTILE + rb * 128);
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) {  // two rows share the conversions
+                        l[rb + i] += ex2(e[i] - m[i]);
+                        l[rb + i + 1] += ex2(e[i + 1] - m[i + 1]);
+                        const uint32_t h = pack_half(ex2(e[i] + lv - mv[i]), ex2(e[i + 1] + lv - mv[i + 1]));
+                        const uint32_t hi = e4m3_of(h);
+                        const uint32_t rest = h2_mul16(h2_sub(h, half2_of(hi)));
+                        const uint32_t mid = e4m3_of(rest);
+                        const uint32_t lo = e4m3_of(h2_mul16(h2_sub(rest, half2_of(mid))));
+                        const uint32_t a0 = (at ^ (uint32_t)(i << 4)) + (uint32_t)(i * 128);
+                        const uint32_t a1 = (at ^ (uint32_t)((i + 1) << 4)) + (uint32_t)((i + 1) * 128);
+                        st_u8(a0, hi);
+                        st_u8(a1, hi >> 8);
+                        st_u8(a0 + R * 128, mid);
+                        st_u8(a1 + R * 128, mid >> 8);
+                        st_u8(a0 + 2 * R * 128, lo);
+                        st_u8(a1 + 2 * R * 128, lo >> 8);
                     }
-                    const uint32_t h = pack_half(ex2(a + sc[t0].y - v0), ex2(c + sc[t1].y - v1));
-                    const uint32_t hi = e4m3_of(h);
-                    const uint32_t rest = h2_mul16(h2_sub(h, half2_of(hi)));
-                    const uint32_t mid = e4m3_of(rest);
-                    const uint32_t lo = e4m3_of(h2_mul16(h2_sub(rest, half2_of(mid))));
-                    const uint32_t a0 = (p_at ^ (uint32_t)((r & 7) << 4)) + (uint32_t)(t0 * C::PTILE + r * 128);
-                    const uint32_t a1 = (p_at ^ (uint32_t)((r1 & 7) << 4)) + (uint32_t)(t1 * C::PTILE + r1 * 128);
-                    st_u8(a0, hi);
-                    st_u8(a1, hi >> 8);
-                    st_u8(a0 + R * 128, mid);
-                    st_u8(a1 + R * 128, mid >> 8);
-                    st_u8(a0 + 2 * R * 128, lo);
-                    st_u8(a1 + 2 * R * 128, lo >> 8);
                 }
             }
             fence_async_smem();
             tc_fence_before();
             bar_arrive(b.p_full);
+            __syncwarp();
+            if (lane == 0) bar_arrive(&b.sc_empty[buf]);
         }
 
         // ---- the unit's end: sums over the threads, O by channel
-        if (u.nt > 0) wait(b.o_full, (n - 1u) & 1u);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            float x = l[r];
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-            if (lane == 0) s_sum[wq * R + r] = x;
+        for (int rb = 0; rb < R; rb += 8) {
+            const float x = warp_sum8(l + rb, lane);
+            if ((lane & 3) == 0) s_sum[wq * R + rb + (lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1)] = x;
         }
         softmax_sync();
+        if (u.nt > 0) wait(b.o_full, (n - 1u) & 1u);
         const int chan = D == 128 ? tid : wq * 16 + (lane & 15);
         const bool mine = !fail && (D == 128 || lane < 16);
         const int nan_from = s_nan[chan];
         tc_fence_after();
 #pragma unroll 1
-        for (int r0 = 0; r0 < u.nr; r0 += 8) {
-            uint32_t x[24];
+        for (int r = 0; r < u.nr; ++r) {
+            float v = 0.f, m = 0.f;
+            const float sum = s_sum[r] + s_sum[R + r] + s_sum[2 * R + r] + s_sum[3 * R + r];
             if (u.nt > 0) {
-                tmem_ld8(tO + (uint32_t)r0, x);
-                tmem_ld8(tO + (uint32_t)(R + r0), x + 8);
-                tmem_ld8(tO + (uint32_t)(2 * R + r0), x + 16);
+                uint32_t x[3];
+                tmem_ld1(tO + (uint32_t)r, x);
+                tmem_ld1(tO + (uint32_t)(R + r), x + 1);
+                tmem_ld1(tO + (uint32_t)(2 * R + r), x + 2);
                 tmem_ld_wait();
-                reg_after_wait<24>(x);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 24; ++i) x[i] = 0u;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = r0 + i;
-                if (r >= u.nr) break;
-                const float2 st = u.nt > 0 ? s_stat[r] : make_float2(-INFINITY, -INFINITY);
-                const float sum = s_sum[r] + s_sum[R + r] + s_sum[2 * R + r] + s_sum[3 * R + r];
-                const float m = st.x == -INFINITY ? 0.f : st.x;
+                reg_after_wait<3>(x);
+                const float2 st = s_stat[r];
+                m = st.x == -INFINITY ? 0.f : st.x;
                 const float f = st.y == -INFINITY ? 0.f : ex2(st.y - kBase - m);
-                float v = fmaf(__uint_as_float(x[16 + i]), 0.00390625f, fmaf(__uint_as_float(x[8 + i]), 0.0625f, __uint_as_float(x[i]))) * f;
+                v = fmaf(__uint_as_float(x[2]), 0.00390625f, fmaf(__uint_as_float(x[1]), 0.0625f, __uint_as_float(x[0]))) * f;
                 if (r >= nan_from) v = __int_as_float(0x7fffffff);
-                if (u.slot < 0) {
-                    const size_t out = (size_t)(unsigned)s_row[r].z;
-                    const float y = sum == 0.f ? 0.f : v / sum;
-                    if (mine) p.o[out * D + chan] = (uint16_t)pack_bf16(y, y);
-                    if (!fail && tid == r && p.lse != nullptr) p.lse[out] = sum == 0.f ? -INFINITY : (m + lg2(sum)) * kLn2;
-                } else {
-                    const size_t rec = (size_t)u.slot * R + r;
-                    if (mine) p.part_o[rec * D + chan] = v;
-                    if (!fail && tid == r) *reinterpret_cast<float2*>(p.part_ml + rec * 2) = make_float2(sum == 0.f ? -INFINITY : m, sum);
-                }
+            }
+            if (u.slot < 0) {
+                const size_t out = (size_t)(unsigned)s_row[r].z;
+                const float y = sum == 0.f ? 0.f : v * (1.f / sum);
+                if (mine) p.o[out * D + chan] = (uint16_t)pack_bf16(y, y);
+                if (!fail && tid == r && p.lse != nullptr) p.lse[out] = sum == 0.f ? -INFINITY : (m + lg2(sum)) * kLn2;
+            } else {
+                const size_t rec = (size_t)u.slot * R + r;
+                if (mine) p.part_o[rec * D + chan] = v;
+                if (!fail && tid == r) *reinterpret_cast<float2*>(p.part_ml + rec * 2) = make_float2(sum == 0.f ? -INFINITY : m, sum);
             }
         }
         if (mine) s_nan[chan] = 0x7fffffff;
