@@ -36,6 +36,7 @@
 #include <cuda_fp16.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "kernels.h"
 #include "ptx.cuh"
@@ -51,6 +52,7 @@ constexpr int kThreads8 = 224;
 constexpr int kQN = 4;            // unit queue between the producer and the other warps
 constexpr int kUnitInts = 10;
 constexpr int kMinShare = 2;      // tiles
+constexpr int kUnitCost = 2;      // tiles
 
 template <int D, int R>
 struct Cfg {
@@ -134,11 +136,12 @@ __device__ __forceinline__ Extent extent(const Paged8Params& p, int r) {
     return e;
 }
 
-// Key tiles of every unit of a request (one at least, so that its rows are written), and its row tiles.
+// Key tiles of every unit of a request (one at least, so that its rows are written), its row tiles, and its
+// size in the cut, where each unit counts kUnitCost tiles more: what its start and end take.
 __device__ __forceinline__ int key_tiles(const Extent& e) { return max(1, (int)(((long long)e.kv_len + 127) / 128)); }
 __device__ __forceinline__ int row_tiles(const Paged8Params& p, const Extent& e) { return (e.q_len * p.G + p.R - 1) / p.R; }
 __device__ __forceinline__ long long work_of(const Paged8Params& p, const Extent& e) {
-    return (long long)p.H_kv * row_tiles(p, e) * key_tiles(e);
+    return (long long)p.H_kv * row_tiles(p, e) * (key_tiles(e) + kUnitCost);
 }
 
 __device__ __forceinline__ void publish(volatile int* q, const Unit& u) {
@@ -288,9 +291,16 @@ __device__ void producer_role(const Paged8Params& p, uint8_t* smem, const Bars& 
                 ++r;
                 continue;
             }
-            const int nb = key_tiles(e), nqt = row_tiles(p, e);
+            const int nb = key_tiles(e), nqt = row_tiles(p, e), size = nb + kUnitCost;
             const long long off = w - start;
-            const int unit = (int)(off / nb), tile = (int)(off - (long long)unit * nb);
+            const int unit = (int)(off / size);
+            int at = (int)(off - (long long)unit * size);  // place in the unit: kUnitCost, then its tiles
+            if (at < kUnitCost) {
+                w += kUnitCost - at;
+                at = kUnitCost;
+                if (w >= w1) break;
+            }
+            const int tile = at - kUnitCost;
             const int n = (int)min((long long)(nb - tile), w1 - w);
             u.r = r;
             u.kvh = unit / nqt;
@@ -302,7 +312,7 @@ __device__ void producer_role(const Paged8Params& p, uint8_t* smem, const Bars& 
             u.tile0 = tile;
             const long long seen = (last_key(p, u, u.row0 + u.nr - 1) + 128LL) / 128;  // tiles that the last row sees
             u.nt = (int)max(0LL, min((long long)n, seen - tile));
-            u.slot = n == nb ? -1 : 2 * (int)blockIdx.x + (w == w0 ? 0 : 1);
+            u.slot = n == nb ? -1 : 2 * (int)blockIdx.x + (w - tile <= w0 ? 0 : 1);
             w += n;
             break;
         }
@@ -984,16 +994,16 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
     }
 }
 
-// One warp per output row (query token, head): where its unit was cut, its pieces by
+// Four warps per output row (query token, head): where its unit was cut, its pieces by
 //   m = max m_i,  l = sum l_i 2^(m_i - m),  O = sum 2^(m_i - m) O_i / l.
+constexpr int kMergeWarps = 4;
 template <int D>
-__global__ void __launch_bounds__(256) paged8_merge_kernel(const __grid_constant__ Paged8Params p) {
+__global__ void __launch_bounds__(kMergeWarps * 32) paged8_merge_kernel(const __grid_constant__ Paged8Params p) {
     constexpr int PER = D / 32;
-    griddep_wait();
-    const long long row = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    const int lane = threadIdx.x & 31;
-    if (row >= (long long)p.total_q * p.H || timeout_recorded(p.status)) return;
-    const int tok = (int)(row / p.H), head = (int)(row - (long long)tok * p.H);
+    using Vec = typename std::conditional<PER == 4, float4, float2>::type;
+    __shared__ float s_o[kMergeWarps][D];
+    const int tok = (int)(blockIdx.x / (unsigned)p.H), head = (int)(blockIdx.x - (unsigned)tok * (unsigned)p.H);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int r = tok;
     if (p.cu_q != nullptr) {  // the last request whose first token is <= tok
         int lo = 0, hi = p.B - 1;
@@ -1011,46 +1021,63 @@ __global__ void __launch_bounds__(256) paged8_merge_kernel(const __grid_constant
     if (t < 0 || t >= e.q_len) return;
     const int kvh = head / p.G, x = t * p.G + head - kvh * p.G;
     const int nb = key_tiles(e), qt = x / p.R;
-    const long long share = *(const volatile long long*)p.plan;
-    const long long first = *(const volatile long long*)(p.plan + 1 + r) + ((long long)kvh * row_tiles(p, e) + qt) * nb;
+    const long long in_request = ((long long)kvh * row_tiles(p, e) + qt) * (nb + kUnitCost) + kUnitCost;
+    griddep_wait();
+    if (timeout_recorded(p.status)) return;
+    const long long share = __ldcg(p.plan), first = __ldcg(p.plan + 1 + r) + in_request;
     const int c0 = (int)(first / share), c1 = (int)((first + nb - 1) / share);
     if (c0 == c1) return;
     auto record = [&](int c) { return ((size_t)(2 * c + (c == c0 && first != c * share ? 1 : 0))) * p.R + (x - qt * p.R); };
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
     float m = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, *(const volatile float*)(p.part_ml + record(c) * 2));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, __ldcg(ml + record(c)).x);
+    m = warp_max(m);
     float l = 0.f, acc[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) acc[i] = 0.f;
     for (int base = c0; base <= c1; base += 32) {
         float w = 0.f;
         if (base + lane <= c1) {
-            const size_t rec = record(base + lane);
-            const float mi = *(const volatile float*)(p.part_ml + rec * 2);
-            // a piece without a visible key has no O
-            w = mi == -INFINITY ? 0.f : ex2(mi - m);
-            if (w != 0.f) l += *(const volatile float*)(p.part_ml + rec * 2 + 1) * w;
+            const float2 y = __ldcg(ml + record(base + lane));
+            w = y.x == -INFINITY ? 0.f : ex2(y.x - m);  // a piece without a visible key has no O
+            if (w != 0.f) l += y.y * w;
         }
         const int n = min(32, c1 - base + 1);
-        for (int i = 0; i < n; ++i) {
-            const float wi = __shfl_sync(0xffffffffu, w, i);
-            if (wi == 0.f) continue;
-            const volatile float* src = p.part_o + record(base + i) * D + lane * PER;
+        for (int i = warp; i < n; i += 4 * kMergeWarps) {  // four pieces of the warp in flight
+            Vec v[4];
+            float wi[4];
 #pragma unroll
-            for (int k = 0; k < PER; ++k) acc[k] = fmaf(wi, src[k], acc[k]);
+            for (int k = 0; k < 4; ++k) {
+                const int c = i + k * kMergeWarps;
+                wi[k] = __shfl_sync(0xffffffffu, w, c & 31);
+                if (c >= n) wi[k] = 0.f;
+                if (wi[k] != 0.f) v[k] = __ldcg(reinterpret_cast<const Vec*>(p.part_o + record(base + c) * D) + lane);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (wi[k] != 0.f) {
+                    const float* f = reinterpret_cast<const float*>(&v[k]);
+#pragma unroll
+                    for (int q = 0; q < PER; ++q) acc[q] = fmaf(wi[k], f[q], acc[q]);
+                }
         }
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D + lane * PER);
 #pragma unroll
-    for (int k = 0; k < PER; k += 2) dst[k / 2] = pack_bf16(acc[k] * inv, acc[k + 1] * inv);
-    if (lane == 0 && p.lse != nullptr) p.lse[row] = l == 0.f ? -INFINITY : (m + lg2(l)) * kLn2;
+    for (int q = 0; q < PER; ++q) s_o[warp][lane * PER + q] = acc[q];
+    __syncthreads();
+    if (threadIdx.x < D / 2) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        float y[2] = {0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kMergeWarps; ++w) {
+            y[0] += s_o[w][2 * threadIdx.x];
+            y[1] += s_o[w][2 * threadIdx.x + 1];
+        }
+        reinterpret_cast<uint32_t*>(p.o + (size_t)blockIdx.x * D)[threadIdx.x] = pack_bf16(y[0] * inv, y[1] * inv);
+        if (threadIdx.x == 0 && p.lse != nullptr) p.lse[blockIdx.x] = l == 0.f ? -INFINITY : (m + lg2(l)) * kLn2;
+    }
 }
 
 template <int D, int R>
@@ -1065,8 +1092,8 @@ cudaError_t launch(const Paged8Params& p, cudaStream_t stream) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(((long long)p.total_q * p.H + 7) / 8));
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3((unsigned)(p.total_q * p.H));
+    cfg.blockDim = dim3(kMergeWarps * 32);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
