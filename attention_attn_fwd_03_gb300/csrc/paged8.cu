@@ -18,8 +18,7 @@
 // matrix instruction and query rows its columns:
 //   S^T [128 keys, 2 R] = Kc [128, d] Q^T,    O^T [d, 3 R] += Vc^T [d, 128 keys] P^T,
 // R = 8, 16 or 32 query rows (tokens times the heads of a group).  A thread of the softmax
-// then has one key and all rows: no thread is idle, and the row sums stay per thread until
-// the end.  It takes 32 / R tiles of 128 keys (a step, 32 scores a thread) at a time:
+// then has one key and 8 rows: no thread is idle.  It takes 32 / R tiles of 128 keys (a step) at a time:
 // one test per step, over all threads, whether a row's maximum grew by more than kTau.
 //
 // Work split.  Requests, KV heads, row tiles and key tiles in a row, cut into equal shares,
@@ -27,12 +26,12 @@
 // CTA computes the cut from the lengths.  A unit (request, head, row tile) that lies in one
 // CTA is finished there; pieces of others leave (m, l, O), merged by a second kernel.
 //
-// A CTA, 224 threads:
+// A CTA, 352 threads:
 //   warp 0    TMA producer: the units, their pages, K and V tiles into a ring, in the order
 //             K of step n + 1, V of step n.
 //   warp 1    MMA issuer (one lane); the warp clears V rows past the request's keys.
-//   warps 2-5 softmax and epilogue: thread = key, then thread = channel.
-//   warp 6    query rows as e4m3 pairs, and the scales of the steps' keys.
+//   warps 2-9 softmax and epilogue: thread = key, then thread = channel.
+//   warp 10   query rows as e4m3 pairs, and the scales of the steps' keys.
 #include <cuda_fp16.h>
 
 #include <cmath>
@@ -48,9 +47,11 @@ namespace {
 constexpr float kTau = 1.f;       // log2 units: how far a row's maximum may lag behind
 constexpr float kBase = 7.f;      // P is scaled by 2^7: at most 2^(kBase + kTau) = 256 of e4m3's 448
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr int kThreads8 = 224;
+constexpr int kThreads8 = 352;
+constexpr float kHuge = 3e38f;
 constexpr int kQN = 4;            // unit queue between the producer and the other warps
 constexpr int kUnitInts = 10;
+constexpr int kMiscFirst = 28;   // place in the misc words of the first request's extent
 constexpr int kMinShare = 2;      // tiles
 constexpr int kUnitCost = 2;      // tiles
 
@@ -71,10 +72,11 @@ struct Cfg {
     static constexpr int OFF_SC = OFF_Q + 2 * QBYTES;                 // float2 [2][SB * 128]: ks, log2 vs of each key (or 2 .. 16 keys)
     static constexpr int OFF_ROW = OFF_SC + 2 * SB * 128 * 8;         // int4 [2][R]: factor, last visible key, output row
     static constexpr int OFF_STAT = OFF_ROW + 2 * R * 16;             // float2 [R]: running maxima of s and of s + log2 vs
-    static constexpr int OFF_ALPHA = OFF_STAT + R * 8;                // float2 [R]
-    static constexpr int OFF_EXCH = OFF_ALPHA + R * 8;                // float2 [4][R]
-    static constexpr int OFF_SUM = OFF_EXCH + 4 * R * 8;              // float [4][R]
-    static constexpr int OFF_NAN = OFF_SUM + 4 * R * 4;               // int [D]: first row that sees a NaN in this channel
+    static constexpr int OFF_PAR = OFF_STAT + R * 8;                  // float2 [R]: the maximum, and P's factor
+    static constexpr int OFF_ALPHA = OFF_PAR + R * 8;                 // float2 [R]
+    static constexpr int OFF_EXCH = OFF_ALPHA + R * 8;                // float2 [8][R]
+    static constexpr int OFF_SUM = OFF_EXCH + 8 * R * 8;              // float [8][R]
+    static constexpr int OFF_NAN = OFF_SUM + 8 * R * 4;               // int [D]: first row that sees a NaN in this channel
     static constexpr int OFF_BAR = OFF_NAN + D * 4;
     static constexpr int N_BARS = 2 * NST + 13 + 2 * kQN;
     static constexpr int OFF_UQ = OFF_BAR + 8 * N_BARS;
@@ -88,15 +90,15 @@ struct Bars {
     uint64_t* kv_full;   // [NST]
     uint64_t* kv_empty;  // [NST]
     uint64_t* q_full;    // [2] query rows prepared
-    uint64_t* q_empty;   // [2] the unit's last S product, and the four softmax warps
+    uint64_t* q_empty;   // [2] the unit's last S product, and the eight softmax warps
     uint64_t* sc_full;   // [2] scales of a step
-    uint64_t* sc_empty;  // [2] four softmax warps
+    uint64_t* sc_empty;  // [2] eight softmax warps
     uint64_t* s_full;    // [2]
-    uint64_t* p_full;    // 128 arrivals per step
+    uint64_t* p_full;    // 256 arrivals per step
     uint64_t* o_full;    // PV products of a step, and the issuing lane
     uint64_t* done;
     uint64_t* uq_full;   // [kQN]
-    uint64_t* uq_empty;  // [kQN] six readers
+    uint64_t* uq_empty;  // [kQN] ten readers
 };
 
 // A piece of a unit: key tiles [tile0, tile0 + nt) for rows [row0, row0 + nr) of request r and KV head kvh.
@@ -166,10 +168,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
     return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, status));
 }
 
-__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ bool softmax_any(bool x) {
     uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
                  : "=r"(r)
                  : "r"((uint32_t)x)
                  : "memory");
@@ -238,7 +240,7 @@ __device__ __forceinline__ float scale_for(float amax) {
 
 template <int D, int R>
 __device__ void producer_role(const Paged8Params& p, uint8_t* smem, const Bars& b, volatile int* uq, volatile int* abort_flag,
-                              int lane, int r, long long w, long long w1, long long start) {
+                              int lane, int r, long long w, long long w1, long long start, Extent e) {
     using C = Cfg<D, R>;
     if (lane == 0) {
         tma_prefetch_map(&p.tm_k);
@@ -248,7 +250,7 @@ __device__ void producer_role(const Paged8Params& p, uint8_t* smem, const Bars& 
     const long long w0 = w;
     int kv_idx = 0, pub = 0;
     bool ok = true;
-    // lane i: extent of request base + i
+    // lane i: extent of request base + i (that of the first is known: the loads are not waited for)
     int base = r;
     Extent mine = extent(p, min(base + lane, p.B - 1));
     int prev_rows[2] = {0, 0}, prev_nt = 0;
@@ -277,23 +279,21 @@ __device__ void producer_role(const Paged8Params& p, uint8_t* smem, const Bars& 
         u.r = -1;
         u.nt = 0;
         while (w < w1) {
-            if (r >= base + 32) {
-                base = r;
-                mine = extent(p, min(base + lane, p.B - 1));
-            }
-            Extent e;
-            e.q_start = __shfl_sync(0xffffffffu, mine.q_start, r - base);
-            e.q_len = __shfl_sync(0xffffffffu, mine.q_len, r - base);
-            e.kv_len = __shfl_sync(0xffffffffu, mine.kv_len, r - base);
             const long long work = work_of(p, e);
             if (w - start >= work) {
                 start += work;
-                ++r;
+                if (++r >= base + 32) {
+                    base = r;
+                    mine = extent(p, min(base + lane, p.B - 1));
+                }
+                e.q_start = __shfl_sync(0xffffffffu, mine.q_start, r - base);
+                e.q_len = __shfl_sync(0xffffffffu, mine.q_len, r - base);
+                e.kv_len = __shfl_sync(0xffffffffu, mine.kv_len, r - base);
                 continue;
             }
             const int nb = key_tiles(e), nqt = row_tiles(p, e), size = nb + kUnitCost;
             const long long off = w - start;
-            const int unit = (int)(off / size);
+            const int unit = off < 0x7fffffffLL ? (int)((unsigned)off / (unsigned)size) : (int)(off / size);
             int at = (int)(off - (long long)unit * size);  // place in the unit: kUnitCost, then its tiles
             if (at < kUnitCost) {
                 w += kUnitCost - at;
@@ -383,6 +383,14 @@ __device__ void mma_role(const Paged8Params& p, uint8_t* smem, const Bars& b, vo
     } prev;
     prev.nt = 0;
 
+    // Rows of a tile past the request's keys may hold anything: cleared, since a NaN there would reach every row of the
+    // second product (as 0 * NaN), and the softmax masks scores by adding -inf to them.
+    auto clear_rows = [&](uint32_t tile, long long left) {
+        if (left >= 128) return;
+        for (int x = (int)left * (D / 16) + lane; x < 128 * (D / 16); x += 32) st_zero16(tile + (uint32_t)x * 16u);
+        fence_async_smem();
+        __syncwarp();
+    };
     auto product_pv = [&](uint32_t step) -> bool {  // of prev, step number `step`
         const Unit& u = prev.u;
         if (!warp_wait(b.p_full, step & 1u, abort_flag, p.status)) return false;
@@ -391,13 +399,8 @@ __device__ void mma_role(const Paged8Params& p, uint8_t* smem, const Bars& b, vo
             const int tile = u.tile0 + prev.s + t;
             const int left = (int)min(128LL, (long long)u.kv_len - (long long)tile * 128);
             const uint32_t v = tile_addr(kv_idx);
-            bool touched = false;
-            if (left < 128) {
-                // rows past the request's keys may hold anything, and 0 * NaN would reach every row
-                for (int x = left * (D / 16) + lane; x < 128 * (D / 16); x += 32) st_zero16(v + (uint32_t)x * 16u);
-                touched = true;
-            }
-            if (p.causal && u.nr > 1) {
+            clear_rows(v, left);
+            if (p.causal && u.nr > 1 && tile * 128LL + left - 1 > last_key(p, u, u.row0)) {
                 // Keys that only some of the rows see: a NaN among their values must not reach the others
                 // through 0 * NaN.  It is taken out and noted, by channel, for the rows from the first that sees it.
                 const long long pos0 = (long long)u.kv_len - u.q_len;
@@ -420,9 +423,6 @@ __device__ void mma_role(const Paged8Params& p, uint8_t* smem, const Bars& b, vo
                         }
                     if (keep != c) st_u32(at, keep);
                 }
-                touched = touched || from < left;
-            }
-            if (touched) {
                 fence_async_smem();
                 __syncwarp();
             }
@@ -467,6 +467,7 @@ __device__ void mma_role(const Paged8Params& p, uint8_t* smem, const Bars& b, vo
             const int nt = min(C::SB, u.nt - s);
             for (int t = 0; t < nt; ++t, ++kv_idx) {
                 if (!warp_wait(&b.kv_full[kv_idx % C::NST], (uint32_t)((kv_idx / C::NST) & 1), abort_flag, p.status)) return;
+                clear_rows(tile_addr(kv_idx), (long long)u.kv_len - (long long)(u.tile0 + s + t) * 128);
                 if (lane == 0) {
                     tc_fence_after();
                     const uint32_t d = tmem + (n & 1u) * 64u + (uint32_t)(t * C::NQ);
@@ -608,7 +609,7 @@ __device__ void aux_role(const Paged8Params& p, uint8_t* smem, const Bars& b, vo
     }
 }
 
-// ---------------------------------------------------------------- softmax + epilogue (four warps)
+// ---------------------------------------------------------------- softmax + epilogue (eight warps)
 
 __device__ __forceinline__ float warp_max(float x) {
     float r;
@@ -634,19 +635,27 @@ __device__ __forceinline__ float warp_sum8(const float* v, int lane) {
     return x + __shfl_xor_sync(0xffffffffu, x, 1);
 }
 
-// The code is kept small (loops over tiles, scores read from tensor memory twice): with a step's 32 scores in
-// registers and everything unrolled, warps waited for instructions more than for data.
+// A step's 32 / R x R / 8 blocks of 128 keys x 8 rows go to two groups of four warps: two blocks to a thread, whose 16
+// scores stay in registers.  Few instructions, each used often: with 32 scores a thread, everything unrolled, warps
+// waited for instructions more than for data.
 template <int D, int R>
 __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b, volatile int* uq, volatile int* abort_flag,
-                             uint32_t tmem, int wq, int lane) {
+                             uint32_t tmem, int warp8, int wq, int lane) {
     using C = Cfg<D, R>;
     constexpr int SB = C::SB;
-    const int tid = wq * 32 + lane;  // key within a tile, TMEM lane
+    constexpr int SETS = R == 32 ? 2 : 1;        // sets of 8 rows that a thread sees
+    const int grp = warp8 >> 2;
+    const int tid = wq * 32 + lane;              // key within a tile, TMEM lane
+    const int gtid = warp8 * 32 + lane;          // 0 .. 255
+    // block k of this thread: tile tile_of(k), rows row_of(k) ..
+    auto tile_of = [&](int k) { return R == 8 ? grp + 2 * k : R == 16 ? k : 0; };
+    auto row_of = [&](int k) { return R == 8 ? 0 : R == 16 ? 8 * grp : 8 * grp + 16 * k; };
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t tS = tmem + lane_off, tO = tmem + lane_off + C::TM_O;
     const uint32_t p_at = smem_u32(smem + C::OFF_P) + (uint32_t)tid;  // this key's byte of P's row 0, before the swizzle
     const float2* s_scale = reinterpret_cast<const float2*>(smem + C::OFF_SC);
     float2* s_stat = reinterpret_cast<float2*>(smem + C::OFF_STAT);
+    float2* s_par = reinterpret_cast<float2*>(smem + C::OFF_PAR);
     float2* s_alpha = reinterpret_cast<float2*>(smem + C::OFF_ALPHA);
     float2* s_exch = reinterpret_cast<float2*>(smem + C::OFF_EXCH);
     float* s_sum = reinterpret_cast<float*>(smem + C::OFF_SUM);
@@ -670,88 +679,95 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
         if (u.r < 0) return;
         wait(&b.q_full[qb], (uint32_t)((k >> 1) & 1));
         const int4* s_row = reinterpret_cast<const int4*>(smem + C::OFF_ROW) + qb * R;
-        float l[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) l[r] = 0.f;
+        const int first_last = last_key(p, u, u.row0);  // the last key that the unit's first row sees
 
         for (int s = 0; s < u.nt; s += SB, ++n) {
             const int nt = min(SB, u.nt - s);
             const uint32_t buf = n & 1u;
             const int key0 = (u.tile0 + s) * 128;  // below kv_len
+            const bool diagonal = first_last < u.kv_len - 1 && (long long)key0 + nt * 128 - 1 > first_last;
             wait(&b.sc_full[buf], (n >> 1) & 1u);
             wait(&b.s_full[buf], (n >> 1) & 1u);
             tc_fence_after();
-            // scores of tile t and rows rb .. rb + 7 in log2 units, -inf where masked
-            auto scores = [&](int rb, int t, const float* f, const int* last, float* e) {
-                uint32_t x[16];
-                tmem_ld8(tS + buf * 64u + (uint32_t)(t * C::NQ + rb), x);
-                tmem_ld8(tS + buf * 64u + (uint32_t)(t * C::NQ + R + rb), x + 8);
-                const float2 sc = s_scale[buf * SB * 128 + ((t * 128 + tid) >> gshift)];
-                tmem_ld_wait();
-                reg_after_wait<16>(x);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float y = fmaf(__uint_as_float(x[8 + i]), 0.0625f, __uint_as_float(x[i])) * (f[i] * sc.x);
-                    e[i] = t * 128 + tid > last[i] ? -INFINITY : y;
-                }
-                return sc.y;
-            };
-            auto rows = [&](int rb, float* f, int* last) {  // score factor and last visible key (from key0) of rows rb ..
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int2 row = *reinterpret_cast<const int2*>(s_row + rb + i);
-                    f[i] = __int_as_float(row.x);
-                    last[i] = row.y - key0;
-                }
-            };
+            // ---- scores in log2 units, -inf where masked; the rows' maxima over the warp
+            float e[2][8], lv[2];
             bool grew = s == 0;
 #pragma unroll
-            for (int rb = 0; rb < R; rb += 8) {
-                float f[8], top[8], top_v[8];
-                int last[8];
-                rows(rb, f, last);
+            for (int j = 0; j < 2; ++j) {
+                const int t = tile_of(j), rb = row_of(j);
+                if (t < nt) {
+                    uint32_t x[16];
+                    tmem_ld8(tS + buf * 64u + (uint32_t)(t * C::NQ + rb), x);
+                    tmem_ld8(tS + buf * 64u + (uint32_t)(t * C::NQ + R + rb), x + 8);
+                    const float2 sc = s_scale[buf * SB * 128 + ((t * 128 + tid) >> gshift)];
+                    // the rows of keys past the request's end are zeros
+                    const float mask = (unsigned)key0 + (unsigned)(t * 128 + tid) < (unsigned)u.kv_len ? 0.f : -INFINITY;
+                    lv[j] = sc.y;
+                    float f[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) top[i] = top_v[i] = -INFINITY;
-#pragma unroll 1
-                for (int t = 0; t < nt; ++t) {
-                    float e[8];
-                    const float lv = scores(rb, t, f, last, e);
+                    for (int i = 0; i < 8; ++i) f[i] = __int_as_float(s_row[rb + i].x) * sc.x;
+                    tmem_ld_wait();
+                    reg_after_wait<16>(x);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        e[j][i] = fmaf(fmaf(__uint_as_float(x[8 + i]), 0.0625f, __uint_as_float(x[i])), f[i], mask);
+                    if (diagonal) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if ((long long)key0 + t * 128 + tid > s_row[rb + i].y) e[j][i] = -INFINITY;
+                    }
+                } else {
+                    lv[j] = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) e[j][i] = -INFINITY;
+                }
+                if (SETS == 2 || j == 1) {
+                    float a = 0.f, c = 0.f;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        top[i] = fmaxf(top[i], e[i]);
-                        top_v[i] = fmaxf(top_v[i], e[i] + lv);
+                        const float top = warp_max(SETS == 2 ? e[j][i] : fmaxf(e[0][i], e[j][i]));
+                        const float top_v = warp_max(SETS == 2 ? e[j][i] + lv[j] : fmaxf(e[0][i] + lv[0], e[j][i] + lv[j]));
+                        if (lane == i) {
+                            a = top;
+                            c = top_v;
+                        }
                     }
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float a = warp_max(top[i]), c = warp_max(top_v[i]);
-                    const float2 stat = s_stat[rb + i];
-                    grew = grew || a > stat.x + kTau || c > stat.y + kTau;
-                    if (lane == i) s_exch[wq * R + rb + i] = make_float2(a, c);
+                    if (lane < 8) {
+                        const float2 stat = s_stat[rb + lane];
+                        grew = grew || a > stat.x + kTau || c > stat.y + kTau;
+                        s_exch[warp8 * R + rb + lane] = make_float2(a, c);
+                    }
                 }
             }
             if (softmax_any(grew || fail)) {
                 if (softmax_any(fail)) return;
-                if (tid < R) {
-                    const float2 old = s == 0 ? make_float2(-INFINITY, -INFINITY) : s_stat[tid];
+                if (gtid < R) {
+                    const float2 old = s == 0 ? make_float2(-INFINITY, -INFINITY) : s_stat[gtid];
                     float2 now = old;
+                    // the warps that saw the row: of both groups, or of the one that has its eight
+                    const int from = R == 8 ? 0 : (gtid >> 3 & 1) * 4;
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        now.x = fmaxf(now.x, s_exch[w * R + tid].x);
-                        now.y = fmaxf(now.y, s_exch[w * R + tid].y);
+                    for (int w = 0; w < (R == 8 ? 8 : 4); ++w) {
+                        const float2 x = s_exch[(from + w) * R + gtid];
+                        now.x = fmaxf(now.x, x.x);
+                        now.y = fmaxf(now.y, x.y);
                     }
-                    s_stat[tid] = now;
-                    s_alpha[tid] = make_float2(old.x == -INFINITY ? 1.f : ex2(old.x - now.x),
-                                               old.y == -INFINITY ? 1.f : ex2(old.y - now.y));
+                    // (a bound on the factor below: values 2^-110 of the scores' weight are as good as zero)
+                    now.y = fmaxf(now.y, now.x - 110.f);
+                    const float m = now.x == -INFINITY ? 0.f : now.x;
+                    s_stat[gtid] = now;
+                    s_par[gtid] = make_float2(m, now.y == -INFINITY ? 0.f : ex2(m - now.y + kBase));
+                    s_alpha[gtid] = make_float2(old.x == -INFINITY ? 1.f : ex2(old.x - now.x),
+                                                old.y == -INFINITY ? 1.f : ex2(old.y - now.y));
                 }
                 softmax_sync();
                 if (s > 0) {
                     wait(b.o_full, (n - 1u) & 1u);
                     tc_fence_after();
-#pragma unroll
-                    for (int r = 0; r < R; ++r) l[r] *= s_alpha[r].x;
+                    if (lane < R) s_sum[warp8 * R + lane] *= s_alpha[lane].x;
+                    __syncwarp();
 #pragma unroll 1
-                    for (int c = 0; c < 3 * R; c += 8) {  // hi, mid, lo
+                    for (int c = 8 * grp; c < 3 * R; c += 16) {  // hi, mid, lo
                         uint32_t x[8];
                         tmem_ld8(tO + (uint32_t)c, x);
                         tmem_ld_wait();
@@ -765,40 +781,53 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
             } else {
                 wait(b.o_full, (n - 1u) & 1u);  // the products of the step before have read P
             }
+            // ---- probabilities
+            float l[8];
 #pragma unroll
-            for (int rb = 0; rb < R; rb += 8) {
-                float f[8], m[8], mv[8];
-                int last[8];
-                rows(rb, f, last);
+            for (int j = 0; j < 2; ++j) {
+                const int t = tile_of(j), rb = row_of(j);
+                if (SETS == 2 || j == 0) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 stat = s_stat[rb + i];
-                    m[i] = stat.x == -INFINITY ? 0.f : stat.x;
-                    mv[i] = stat.y == -INFINITY ? 0.f : stat.y - kBase;
+                    for (int i = 0; i < 8; ++i) l[i] = 0.f;
                 }
-#pragma unroll 1
-                for (int t = 0; t < nt; ++t) {
-                    float e[8];
-                    const float lv = scores(rb, t, f, last, e);
-                    const uint32_t at = p_at + (uint32_t)(t * C::PTILE + rb * 128);
+                if (t < nt) {
+                    const float vk = ex2(lv[j]);
+                    uint32_t h[4], hi[4], mid[4], lo[4];
 #pragma unroll
                     for (int i = 0; i < 8; i += 2) {  // two rows share the conversions
-                        l[rb + i] += ex2(e[i] - m[i]);
-                        l[rb + i + 1] += ex2(e[i + 1] - m[i + 1]);
-                        const uint32_t h = pack_half(ex2(e[i] + lv - mv[i]), ex2(e[i + 1] + lv - mv[i + 1]));
-                        const uint32_t hi = e4m3_of(h);
-                        const uint32_t rest = h2_mul16(h2_sub(h, half2_of(hi)));
-                        const uint32_t mid = e4m3_of(rest);
-                        const uint32_t lo = e4m3_of(h2_mul16(h2_sub(rest, half2_of(mid))));
-                        const uint32_t a0 = (at ^ (uint32_t)(i << 4)) + (uint32_t)(i * 128);
-                        const uint32_t a1 = (at ^ (uint32_t)((i + 1) << 4)) + (uint32_t)((i + 1) * 128);
-                        st_u8(a0, hi);
-                        st_u8(a1, hi >> 8);
-                        st_u8(a0 + R * 128, mid);
-                        st_u8(a1 + R * 128, mid >> 8);
-                        st_u8(a0 + 2 * R * 128, lo);
-                        st_u8(a1 + 2 * R * 128, lo >> 8);
+                        const float2 par0 = s_par[rb + i], par1 = s_par[rb + i + 1];
+                        const float p0 = ex2(e[j][i] - par0.x), p1 = ex2(e[j][i + 1] - par1.x);
+                        l[i] += p0;
+                        l[i + 1] += p1;
+                        h[i / 2] = pack_half(p0 * fminf(vk * par0.y, kHuge), p1 * fminf(vk * par1.y, kHuge));
                     }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) hi[i] = e4m3_of(h[i]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) h[i] = h2_mul16(h2_sub(h[i], half2_of(hi[i])));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mid[i] = e4m3_of(h[i]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) h[i] = h2_mul16(h2_sub(h[i], half2_of(mid[i])));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) lo[i] = e4m3_of(h[i]);
+                    const uint32_t at = p_at + (uint32_t)(t * C::PTILE + rb * 128);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t a0 = (at ^ (uint32_t)(2 * i << 4)) + (uint32_t)(2 * i * 128);
+                        const uint32_t a1 = (at ^ (uint32_t)((2 * i + 1) << 4)) + (uint32_t)((2 * i + 1) * 128);
+                        st_u8(a0, hi[i]);
+                        st_u8(a1, hi[i] >> 8);
+                        st_u8(a0 + R * 128, mid[i]);
+                        st_u8(a1 + R * 128, mid[i] >> 8);
+                        st_u8(a0 + 2 * R * 128, lo[i]);
+                        st_u8(a1 + 2 * R * 128, lo[i] >> 8);
+                    }
+                }
+                if (SETS == 2 || j == 1) {  // the rows' sums, one lane each
+                    const float x = warp_sum8(l, lane);
+                    float* sum = s_sum + warp8 * R + rb + (lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1);
+                    if ((lane & 3) == 0) *sum = x + (s > 0 ? *sum : 0.f);
                 }
             }
             fence_async_smem();
@@ -808,32 +837,29 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
             if (lane == 0) bar_arrive(&b.sc_empty[buf]);
         }
 
-        // ---- the unit's end: sums over the threads, O by channel
-#pragma unroll
-        for (int rb = 0; rb < R; rb += 8) {
-            const float x = warp_sum8(l + rb, lane);
-            if ((lane & 3) == 0) s_sum[wq * R + rb + (lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1)] = x;
-        }
-        softmax_sync();
+        // ---- the unit's end: O by channel, every other row by each group
+        softmax_sync();  // every warp's sums
         if (u.nt > 0) wait(b.o_full, (n - 1u) & 1u);
         const int chan = D == 128 ? tid : wq * 16 + (lane & 15);
         const bool mine = !fail && (D == 128 || lane < 16);
         const int nan_from = s_nan[chan];
         tc_fence_after();
 #pragma unroll 1
-        for (int r = 0; r < u.nr; ++r) {
-            float v = 0.f, m = 0.f;
-            const float sum = s_sum[r] + s_sum[R + r] + s_sum[2 * R + r] + s_sum[3 * R + r];
+        for (int r = grp; r < u.nr; r += 2) {
+            float v = 0.f, m = 0.f, sum = 0.f;
             if (u.nt > 0) {
                 uint32_t x[3];
                 tmem_ld1(tO + (uint32_t)r, x);
                 tmem_ld1(tO + (uint32_t)(R + r), x + 1);
                 tmem_ld1(tO + (uint32_t)(2 * R + r), x + 2);
-                tmem_ld_wait();
-                reg_after_wait<3>(x);
+                const int from = R == 8 ? 0 : (r >> 3 & 1) * 4;
+#pragma unroll
+                for (int w = 0; w < (R == 8 ? 8 : 4); ++w) sum += s_sum[(from + w) * R + r];
                 const float2 st = s_stat[r];
                 m = st.x == -INFINITY ? 0.f : st.x;
                 const float f = st.y == -INFINITY ? 0.f : ex2(st.y - kBase - m);
+                tmem_ld_wait();
+                reg_after_wait<3>(x);
                 v = fmaf(__uint_as_float(x[2]), 0.00390625f, fmaf(__uint_as_float(x[1]), 0.0625f, __uint_as_float(x[0]))) * f;
                 if (r >= nan_from) v = __int_as_float(0x7fffffff);
             }
@@ -848,9 +874,9 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
                 if (!fail && tid == r) *reinterpret_cast<float2*>(p.part_ml + rec * 2) = make_float2(sum == 0.f ? -INFINITY : m, sum);
             }
         }
-        if (mine) s_nan[chan] = 0x7fffffff;
         tc_fence_before();
-        softmax_sync();  // s_stat, s_sum and the rows have been read
+        softmax_sync();  // s_stat, s_sum, s_nan and the rows have been read
+        if (mine && grp == 0) s_nan[chan] = 0x7fffffff;
         if (lane == 0) bar_arrive(&b.q_empty[qb]);
     }
 }
@@ -878,19 +904,40 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
     b.uq_full = b.done + 1;
     b.uq_empty = b.uq_full + kQN;
     volatile int* uq = reinterpret_cast<volatile int*>(smem + C::OFF_UQ);
-    int* misc = reinterpret_cast<int*>(smem + C::OFF_MISC);  // tmem, abort, skip, r0; 8-byte: total, start, warp sums
+    int* misc = reinterpret_cast<int*>(smem + C::OFF_MISC);  // tmem, abort, skip, r0; then the words below
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(misc);
     volatile int* abort_flag = misc + 1;
-    long long* wide = reinterpret_cast<long long*>(misc + 4);  // [0] start of request r0, [1 .. 7] sums of the warps
+    long long* wide = reinterpret_cast<long long*>(misc + 4);  // [0] start of request r0, [1 .. 11] sums of the warps
 
     griddep_launch_dependents();  // the merge may be scheduled; it waits for this grid
     // ---- the cut: tiles of all requests, in order, in shares of equal size
     const int per = (p.B + kThreads8 - 1) / kThreads8;
     const int ra = min(p.B, tid * per), rb = min(p.B, ra + per);
+    Extent e = extent(p, min(ra, p.B - 1));  // its load is under way during the set-up
+    if (tid < C::N_BARS) {
+        uint64_t* x = bars + tid;
+        bar_init(x, x >= b.uq_empty ? 10 : x == b.o_full ? 2 : x == b.p_full ? 256 : x >= b.sc_empty && x < b.s_full ? 8
+                    : x >= b.q_empty && x < b.sc_full ? 9 : 1);
+        bar_init_fence();
+    }
+    if (tid == kThreads8 - 1) {
+        *abort_flag = 0;
+        misc[2] = timeout_recorded(p.status) ? 1 : 0;  // an earlier launch gave up
+    }
+    if (warp == 0) {
+        tmem_alloc(tmem_holder, C::TM_COLS);
+        tmem_relinquish();
+    }
+    for (int i = tid; i < D; i += kThreads8) reinterpret_cast<int*>(smem + C::OFF_NAN)[i] = 0x7fffffff;
+    // columns of O^T that pad 3 R to 32: their rows of P read as zeros
+    if (R == 8)
+        for (int i = tid; i < C::SB * 8 * 8; i += kThreads8)
+            st_zero16(smem_u32(smem + C::OFF_P) + (uint32_t)((i / 64) * C::PTILE + 24 * 128 + (i % 64) * 16));
+    fence_async_smem();
     long long sum = 0;
     bool bad = false;
     for (int r = ra; r < rb; ++r) {
-        const Extent e = extent(p, r);
+        if (r > ra) e = extent(p, r);
         bad |= e.bad;
         sum += work_of(p, e);
     }
@@ -902,39 +949,6 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
         if (lane >= o) before += y;
     }
     if (lane == 31) wide[1 + warp] = before;
-    if (tid == 0) {
-        for (int s = 0; s < C::NST; ++s) {
-            bar_init(&b.kv_full[s], 1);
-            bar_init(&b.kv_empty[s], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            bar_init(&b.q_full[i], 1);
-            bar_init(&b.q_empty[i], 5);
-            bar_init(&b.sc_full[i], 1);
-            bar_init(&b.sc_empty[i], 4);
-            bar_init(&b.s_full[i], 1);
-        }
-        bar_init(b.p_full, 128);
-        bar_init(b.o_full, 2);
-        bar_init(b.done, 1);
-        for (int i = 0; i < kQN; ++i) {
-            bar_init(&b.uq_full[i], 1);
-            bar_init(&b.uq_empty[i], 6);
-        }
-        *abort_flag = 0;
-        misc[2] = timeout_recorded(p.status) ? 1 : 0;  // an earlier launch gave up
-        bar_init_fence();
-    }
-    for (int i = tid; i < D; i += kThreads8) reinterpret_cast<int*>(smem + C::OFF_NAN)[i] = 0x7fffffff;
-    // columns of O^T that pad 3 R to 32: their rows of P read as zeros
-    if (R == 8)
-        for (int i = tid; i < C::SB * 8 * 8; i += kThreads8)
-            st_zero16(smem_u32(smem + C::OFF_P) + (uint32_t)((i / 64) * C::PTILE + 24 * 128 + (i % 64) * 16));
-    fence_async_smem();
-    if (warp == 0) {
-        tmem_alloc(tmem_holder, C::TM_COLS);
-        tmem_relinquish();
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -945,33 +959,41 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
         if (w < warp) before += wide[1 + w];
         total += wide[1 + w];
     }
-    const long long share = max((long long)kMinShare, (total + gridDim.x - 1) / gridDim.x);
+    // (32-bit division where it will do: the 64-bit one takes a noticeable part of a short call)
+    const long long even = total < 0x7fff0000LL ? ((unsigned)total + gridDim.x - 1) / gridDim.x : (total + gridDim.x - 1) / gridDim.x;
+    const long long share = max((long long)kMinShare, even);
     const long long w0 = (long long)blockIdx.x * share, w1 = min(total, w0 + share);
-    if (blockIdx.x == 0) {  // for the merge
-        if (tid == 0) p.plan[0] = share;
-        long long at = before;
-        for (int r = ra; r < rb; ++r) {
-            p.plan[1 + r] = at;
-            at += work_of(p, extent(p, r));
-        }
-    }
     if (w0 >= before && w0 < before + sum) {  // this thread's requests hold the CTA's first tile
         long long at = before;
         for (int r = ra; r < rb; ++r) {
-            const long long work = work_of(p, extent(p, r));
+            if (per > 1) e = extent(p, r);
+            const long long work = work_of(p, e);
             if (w0 < at + work) {
                 misc[3] = r;
                 wide[0] = at;
+                int* first = misc + kMiscFirst;
+                first[0] = e.q_start;
+                first[1] = e.q_len;
+                first[2] = e.kv_len;
                 break;
             }
             at += work;
         }
     }
+    if (blockIdx.x == 0) {  // for the merge
+        if (tid == 0) p.plan[0] = share;
+        long long at = before;
+        for (int r = ra; r < rb; ++r) {
+            if (per > 1) e = extent(p, r);
+            p.plan[1 + r] = at;
+            at += work_of(p, e);
+        }
+    }
     __syncthreads();
     const uint32_t tmem = *tmem_holder;
     if (misc[2] == 0 && w0 < total) {
-        if (warp >= 2 && warp < 6) {
-            softmax_role<D, R>(p, smem, b, uq, abort_flag, tmem, warp & 3, lane);
+        if (warp >= 2 && warp < 10) {
+            softmax_role<D, R>(p, smem, b, uq, abort_flag, tmem, warp - 2, warp & 3, lane);
         } else if (warp == 1) {
             mma_role<D, R>(p, smem, b, uq, abort_flag, tmem, lane);
             __syncwarp();
@@ -981,7 +1003,9 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
             }
             __syncwarp();
         } else if (warp == 0) {
-            producer_role<D, R>(p, smem, b, uq, abort_flag, lane, misc[3], w0, w1, wide[0]);
+            const int* first = misc + kMiscFirst;
+            producer_role<D, R>(p, smem, b, uq, abort_flag, lane, misc[3], w0, w1, wide[0],
+                                Extent{first[0], first[1], first[2], false});
         } else {
             aux_role<D, R>(p, smem, b, uq, abort_flag, lane);
         }
