@@ -13,7 +13,7 @@
 // precision is bought with more rows:
 //   q = 2^x (hi + lo / 16): a bf16 number has 8 significant bits, two e4m3 numbers hold
 //       them; x by the head vector's largest element.
-//   P vs / 2^(running maximum) = hi + mid / 16 + lo / 256: an fp16 number's 11 bits.
+//   P vs / 2^(running maximum) = hi + mid / 32 + lo / 1024: an fp16 number's 11 bits.
 // Both products are transposed, so that keys (or channels) fill the 128 rows of the
 // matrix instruction and query rows its columns:
 //   S^T [128 keys, 2 R] = Kc [128, d] Q^T,    O^T [d, 3 R] += Vc^T [d, 128 keys] P^T,
@@ -44,8 +44,11 @@ namespace attn {
 
 namespace {
 
-constexpr float kTau = 1.f;       // log2 units: how far a row's maximum may lag behind
-constexpr float kBase = 7.f;      // P is scaled by 2^7: at most 2^(kBase + kTau) = 256 of e4m3's 448
+// How far a row's maximum may lag behind, in log2 units, and the scale of P, at most 2^(kTau + kBase) = 256: hi is then
+// off by at most 8, mid = 32 times that by as much again.  What lies 2^-24 below the row's largest is lost.  (kTau 1,
+// kBase 7: a maximum grew in nearly every step of 32 rows.)
+constexpr float kTau = 4.f;
+constexpr float kBase = 4.f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kThreads8 = 352;
 constexpr float kHuge = 3e38f;
@@ -61,14 +64,15 @@ struct Cfg {
     static constexpr int NQ = 2 * R;                   // columns of S^T per tile: hi, lo
     static constexpr int NPV = R == 8 ? 32 : 3 * R;    // columns of O^T: hi, mid, lo (a multiple of 16)
     static constexpr int TILE = 128 * D;               // bytes of a K or V tile
-    static constexpr int NST = D == 64 ? 10 : R == 32 ? 4 : 5;  // ring stages
+    static constexpr int NST = (R == 8 ? 5 : 4) * 128 / D;  // ring stages
     static constexpr int QBYTES = NQ * D;
     static constexpr int PTILE = NPV * 128;
+    static constexpr int PBUF = R == 8 ? 1 : 2;        // steps' P held at once
     static constexpr uint32_t TM_O = 128;              // S: two buffers of 64 columns
     static constexpr uint32_t TM_COLS = 256;
     static constexpr int OFF_KV = 0;
     static constexpr int OFF_P = OFF_KV + NST * TILE;
-    static constexpr int OFF_Q = OFF_P + SB * PTILE;
+    static constexpr int OFF_Q = OFF_P + PBUF * SB * PTILE;
     static constexpr int OFF_SC = OFF_Q + 2 * QBYTES;                 // float2 [2][SB * 128]: ks, log2 vs of each key (or 2 .. 16 keys)
     static constexpr int OFF_ROW = OFF_SC + 2 * SB * 128 * 8;         // int4 [2][R]: factor, last visible key, output row
     static constexpr int OFF_STAT = OFF_ROW + 2 * R * 16;             // float2 [R]: running maxima of s and of s + log2 vs
@@ -78,7 +82,7 @@ struct Cfg {
     static constexpr int OFF_SUM = OFF_EXCH + 8 * R * 8;              // float [8][R]
     static constexpr int OFF_NAN = OFF_SUM + 8 * R * 4;               // int [D]: first row that sees a NaN in this channel
     static constexpr int OFF_BAR = OFF_NAN + D * 4;
-    static constexpr int N_BARS = 2 * NST + 13 + 2 * kQN;
+    static constexpr int N_BARS = 2 * NST + 14 + 2 * kQN;
     static constexpr int OFF_UQ = OFF_BAR + 8 * N_BARS;
     static constexpr int OFF_MISC = OFF_UQ + 4 * kQN * kUnitInts;
     static constexpr int SMEM_BYTES = OFF_MISC + 128 + 1024;
@@ -95,7 +99,7 @@ struct Bars {
     uint64_t* sc_empty;  // [2] eight softmax warps
     uint64_t* s_full;    // [2]
     uint64_t* p_full;    // 256 arrivals per step
-    uint64_t* o_full;    // PV products of a step, and the issuing lane
+    uint64_t* o_full;    // [2] PV products of a step, and the issuing lane
     uint64_t* done;
     uint64_t* uq_full;   // [kQN]
     uint64_t* uq_empty;  // [kQN] ten readers
@@ -212,9 +216,9 @@ __device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b) {
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ uint32_t h2_mul16(uint32_t a) {
+__device__ __forceinline__ uint32_t h2_mul32(uint32_t a) {
     uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0x4c004c00u));  // 16
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0x50005000u));  // 32
     return r;
 }
 
@@ -429,7 +433,7 @@ __device__ void mma_role(const Paged8Params& p, uint8_t* smem, const Bars& b, vo
             if (lane == 0) {
                 tc_fence_after();
                 const uint32_t o = tmem + C::TM_O;
-                const uint64_t a = desc<D>(v), q = desc<128>(sbase + C::OFF_P + (uint32_t)(t * C::PTILE));
+                const uint64_t a = desc<D>(v), q = desc<128>(sbase + C::OFF_P + (uint32_t)(((C::PBUF == 2 ? step & 1u : 0u) * C::SB + t) * C::PTILE));
                 constexpr uint64_t VS = (32 * D) >> 4;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
@@ -439,8 +443,8 @@ __device__ void mma_role(const Paged8Params& p, uint8_t* smem, const Bars& b, vo
         }
         __syncwarp();
         if (lane == 0) {
-            tc_commit(b.o_full);
-            bar_arrive(b.o_full);  // what the warp noted of NaNs
+            tc_commit(&b.o_full[step & 1u]);
+            bar_arrive(&b.o_full[step & 1u]);  // what the warp noted of NaNs
         }
         return true;
     };
@@ -669,6 +673,8 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
         if (!fail) fail = !warp_wait(bar, parity, abort_flag, p.status);
     };
 
+    auto wait_products = [&](uint32_t step) { wait(&b.o_full[step & 1u], (step >> 1) & 1u); };
+
     for (int k = 0;; ++k) {
         const int slot = k % kQN, qb = k & 1;
         wait(&b.uq_full[slot], (uint32_t)((k / kQN) & 1));
@@ -695,7 +701,7 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int t = tile_of(j), rb = row_of(j);
-                if (t < nt) {
+                if (t < nt && rb < u.nr) {
                     uint32_t x[16];
                     tmem_ld8(tS + buf * 64u + (uint32_t)(t * C::NQ + rb), x);
                     tmem_ld8(tS + buf * 64u + (uint32_t)(t * C::NQ + R + rb), x + 8);
@@ -762,7 +768,7 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
                 }
                 softmax_sync();
                 if (s > 0) {
-                    wait(b.o_full, (n - 1u) & 1u);
+                    wait_products(n - 1u);
                     tc_fence_after();
                     if (lane < R) s_sum[warp8 * R + lane] *= s_alpha[lane].x;
                     __syncwarp();
@@ -778,9 +784,9 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
                     }
                     tmem_st_wait();
                 }
-            } else {
-                wait(b.o_full, (n - 1u) & 1u);  // the products of the step before have read P
             }
+            // the products that read this buffer of P before (those of the unit before are complete)
+            if (s >= C::PBUF * SB) wait_products(n - C::PBUF);
             // ---- probabilities
             float l[8];
 #pragma unroll
@@ -790,7 +796,7 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
 #pragma unroll
                     for (int i = 0; i < 8; ++i) l[i] = 0.f;
                 }
-                if (t < nt) {
+                if (t < nt && rb < u.nr) {
                     const float vk = ex2(lv[j]);
                     uint32_t h[4], hi[4], mid[4], lo[4];
 #pragma unroll
@@ -804,14 +810,14 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
 #pragma unroll
                     for (int i = 0; i < 4; ++i) hi[i] = e4m3_of(h[i]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) h[i] = h2_mul16(h2_sub(h[i], half2_of(hi[i])));
+                    for (int i = 0; i < 4; ++i) h[i] = h2_mul32(h2_sub(h[i], half2_of(hi[i])));
 #pragma unroll
                     for (int i = 0; i < 4; ++i) mid[i] = e4m3_of(h[i]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) h[i] = h2_mul16(h2_sub(h[i], half2_of(mid[i])));
+                    for (int i = 0; i < 4; ++i) h[i] = h2_mul32(h2_sub(h[i], half2_of(mid[i])));
 #pragma unroll
                     for (int i = 0; i < 4; ++i) lo[i] = e4m3_of(h[i]);
-                    const uint32_t at = p_at + (uint32_t)(t * C::PTILE + rb * 128);
+                    const uint32_t at = p_at + (uint32_t)(((C::PBUF == 2 ? buf : 0u) * SB + t) * C::PTILE + rb * 128);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint32_t a0 = (at ^ (uint32_t)(2 * i << 4)) + (uint32_t)(2 * i * 128);
@@ -839,7 +845,7 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
 
         // ---- the unit's end: O by channel, every other row by each group
         softmax_sync();  // every warp's sums
-        if (u.nt > 0) wait(b.o_full, (n - 1u) & 1u);
+        if (u.nt > 0) wait_products(n - 1u);
         const int chan = D == 128 ? tid : wq * 16 + (lane & 15);
         const bool mine = !fail && (D == 128 || lane < 16);
         const int nan_from = s_nan[chan];
@@ -860,7 +866,7 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
                 const float f = st.y == -INFINITY ? 0.f : ex2(st.y - kBase - m);
                 tmem_ld_wait();
                 reg_after_wait<3>(x);
-                v = fmaf(__uint_as_float(x[2]), 0.00390625f, fmaf(__uint_as_float(x[1]), 0.0625f, __uint_as_float(x[0]))) * f;
+                v = fmaf(__uint_as_float(x[2]), 0x1p-10f, fmaf(__uint_as_float(x[1]), 0x1p-5f, __uint_as_float(x[0]))) * f;
                 if (r >= nan_from) v = __int_as_float(0x7fffffff);
             }
             if (u.slot < 0) {
@@ -900,7 +906,7 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
     b.s_full = b.sc_empty + 2;
     b.p_full = b.s_full + 2;
     b.o_full = b.p_full + 1;
-    b.done = b.o_full + 1;
+    b.done = b.o_full + 2;
     b.uq_full = b.done + 1;
     b.uq_empty = b.uq_full + kQN;
     volatile int* uq = reinterpret_cast<volatile int*>(smem + C::OFF_UQ);
@@ -916,7 +922,7 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
     Extent e = extent(p, min(ra, p.B - 1));  // its load is under way during the set-up
     if (tid < C::N_BARS) {
         uint64_t* x = bars + tid;
-        bar_init(x, x >= b.uq_empty ? 10 : x == b.o_full ? 2 : x == b.p_full ? 256 : x >= b.sc_empty && x < b.s_full ? 8
+        bar_init(x, x >= b.uq_empty ? 10 : x >= b.o_full && x < b.done ? 2 : x == b.p_full ? 256 : x >= b.sc_empty && x < b.s_full ? 8
                     : x >= b.q_empty && x < b.sc_full ? 9 : 1);
         bar_init_fence();
     }
