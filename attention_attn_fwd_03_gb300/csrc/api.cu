@@ -773,7 +773,7 @@ attn_status_t attn_varlen_fwd(const void* q, const void* k, const void* v, const
 size_t attn_paged_fwd_fp8_workspace_size(int B, int total_q, int max_q_len, int H, int H_kv, int d, int page_size,
                                          int max_pages) {
     if (paged_sizes_ok(B, total_q, max_q_len, H, H_kv, d, page_size, max_pages) != ATTN_OK) return 0;
-    return paged8_plan(B, max_q_len, H / H_kv, d).bytes;
+    return paged8_plan(max_q_len, H / H_kv, d).bytes;
 }
 
 attn_status_t attn_paged_fwd_fp8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
@@ -793,7 +793,7 @@ attn_status_t attn_paged_fwd_fp8(const void* q, const void* k_cache, const void*
     auto a4 = [](const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 3u) == 0; };
     if (!a4(k_scale) || !a4(v_scale) || !a4(block_table) || !a4(seq_lens) || !a4(cu_seqlens_q) || !a4(lse))
         return ATTN_ERR_INVALID_ARG;
-    const Paged8Plan pl = paged8_plan(B, max_q_len, H / H_kv, d);
+    const Paged8Plan pl = paged8_plan(max_q_len, H / H_kv, d);
     if (!workspace || workspace_bytes < pl.bytes || !aligned16(workspace)) return ATTN_ERR_WORKSPACE;
     DeviceState* ds = nullptr;
     st = device_state(&ds);
@@ -808,7 +808,7 @@ attn_status_t attn_paged_fwd_fp8(const void* q, const void* k_cache, const void*
         return ATTN_ERR_CUDA;
     p.kv_rows = (int)slots;
     char* ws = static_cast<char*>(workspace);
-    p.plan = reinterpret_cast<long long*>(ws);
+    p.cuts = reinterpret_cast<int4*>(ws);
     p.part_ml = reinterpret_cast<float*>(ws + pl.part_ml);
     p.part_o = reinterpret_cast<float*>(ws + pl.part_o);
     p.R = pl.R;

@@ -214,7 +214,8 @@ struct Paged8Params {
     const int32_t* seq_lens;     // [B]
     uint16_t* o;
     float* lse;                  // [total_q, H] or nullptr
-    long long* plan;             // workspace: [0] tiles per CTA, [1 ..] first tile of each request
+    int4* cuts;                  // [n_ctas, 2] the unit that a CTA begins and others go on with, for the merge:
+                                 // (last of those CTAs or -1, record, rows, KV head), (first token, first row, -, -)
     float* part_ml;              // [2 n_ctas, R, 2]: (m in log2 units, l) of a CTA's first and last piece
     float* part_o;               // [2 n_ctas, R, d]: unnormalised O
     unsigned* status;
@@ -233,7 +234,7 @@ struct Paged8Plan {
     size_t part_ml, part_o, bytes;
 };
 constexpr int kPaged8Ctas = 304;  // at most: two to each of the chip's 152 SMs
-Paged8Plan paged8_plan(int B, int max_q_len, int G, int d);
+Paged8Plan paged8_plan(int max_q_len, int G, int d);
 cudaError_t launch_paged8(int d, const Paged8Params& p, cudaStream_t stream);
 
 // Failure-handling test: a bounded wait that nothing completes (selftest.cu).

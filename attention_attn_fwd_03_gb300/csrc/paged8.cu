@@ -26,12 +26,13 @@
 // CTA computes the cut from the lengths.  A unit (request, head, row tile) that lies in one
 // CTA is finished there; pieces of others leave (m, l, O), merged by a second kernel.
 //
-// A CTA, 352 threads:
+// A CTA, 384 threads:
 //   warp 0    TMA producer: the units, their pages, K and V tiles into a ring, in the order
 //             K of step n + 1, V of step n.
 //   warp 1    MMA issuer (one lane); the warp clears V rows past the request's keys.
 //   warps 2-9 softmax and epilogue: thread = key, then thread = channel.
-//   warp 10   query rows as e4m3 pairs, and the scales of the steps' keys.
+//   warp 10   query rows as e4m3 pairs.
+//   warp 11   the scales of the steps' keys.
 #include <cuda_fp16.h>
 
 #include <cmath>
@@ -50,11 +51,11 @@ namespace {
 constexpr float kTau = 4.f;
 constexpr float kBase = 4.f;
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr int kThreads8 = 352;
+constexpr int kThreads8 = 384;
 constexpr float kHuge = 3e38f;
 constexpr int kQN = 4;            // unit queue between the producer and the other warps
 constexpr int kUnitInts = 10;
-constexpr int kMiscFirst = 28;   // place in the misc words of the first request's extent
+constexpr int kMiscFirst = 30;   // place in the misc words of the first request's extent
 constexpr int kMinShare = 2;      // tiles
 constexpr int kUnitCost = 2;      // tiles
 
@@ -85,7 +86,7 @@ struct Cfg {
     static constexpr int N_BARS = 2 * NST + 14 + 2 * kQN;
     static constexpr int OFF_UQ = OFF_BAR + 8 * N_BARS;
     static constexpr int OFF_MISC = OFF_UQ + 4 * kQN * kUnitInts;
-    static constexpr int SMEM_BYTES = OFF_MISC + 128 + 1024;
+    static constexpr int SMEM_BYTES = OFF_MISC + 144 + 1024;
     static_assert(SMEM_BYTES <= 115712, "two CTAs to an SM");
     static_assert(OFF_P % 1024 == 0 && PTILE % 1024 == 0 && OFF_Q % 1024 == 0 && QBYTES % 1024 == 0, "swizzle atoms");
 };
@@ -102,7 +103,7 @@ struct Bars {
     uint64_t* o_full;    // [2] PV products of a step, and the issuing lane
     uint64_t* done;
     uint64_t* uq_full;   // [kQN]
-    uint64_t* uq_empty;  // [kQN] ten readers
+    uint64_t* uq_empty;  // [kQN] eleven readers
 };
 
 // A piece of a unit: key tiles [tile0, tile0 + nt) for rows [row0, row0 + nr) of request r and KV head kvh.
@@ -148,6 +149,12 @@ __device__ __forceinline__ int key_tiles(const Extent& e) { return max(1, (int)(
 __device__ __forceinline__ int row_tiles(const Paged8Params& p, const Extent& e) { return (e.q_len * p.G + p.R - 1) / p.R; }
 __device__ __forceinline__ long long work_of(const Paged8Params& p, const Extent& e) {
     return (long long)p.H_kv * row_tiles(p, e) * (key_tiles(e) + kUnitCost);
+}
+
+// a / b (both positive, the quotient an int), by a 32-bit division where that will do: the 64-bit one takes a noticeable
+// part of a short call.
+__device__ __forceinline__ int quotient(long long a, long long b) {
+    return a < 0x7fffffffLL && b < 0x7fffffffLL ? (int)((unsigned)a / (unsigned)b) : (int)(a / b);
 }
 
 __device__ __forceinline__ void publish(volatile int* q, const Unit& u) {
@@ -244,7 +251,8 @@ __device__ __forceinline__ float scale_for(float amax) {
 
 template <int D, int R>
 __device__ void producer_role(const Paged8Params& p, uint8_t* smem, const Bars& b, volatile int* uq, volatile int* abort_flag,
-                              int lane, int r, long long w, long long w1, long long start, Extent e) {
+                              int lane, int r, long long w, long long w1, long long start, Extent e,
+                              long long share) {
     using C = Cfg<D, R>;
     if (lane == 0) {
         tma_prefetch_map(&p.tm_k);
@@ -297,7 +305,7 @@ __device__ void producer_role(const Paged8Params& p, uint8_t* smem, const Bars& 
             }
             const int nb = key_tiles(e), nqt = row_tiles(p, e), size = nb + kUnitCost;
             const long long off = w - start;
-            const int unit = off < 0x7fffffffLL ? (int)((unsigned)off / (unsigned)size) : (int)(off / size);
+            const int unit = quotient(off, size);
             int at = (int)(off - (long long)unit * size);  // place in the unit: kUnitCost, then its tiles
             if (at < kUnitCost) {
                 w += kUnitCost - at;
@@ -317,6 +325,11 @@ __device__ void producer_role(const Paged8Params& p, uint8_t* smem, const Bars& 
             const long long seen = (last_key(p, u, u.row0 + u.nr - 1) + 128LL) / 128;  // tiles that the last row sees
             u.nt = (int)max(0LL, min((long long)n, seen - tile));
             u.slot = n == nb ? -1 : 2 * (int)blockIdx.x + (w - tile <= w0 ? 0 : 1);
+            if (tile == 0 && n < nb && lane == 0) {  // for the merge: the unit goes on in the CTAs after this one
+                int4* cut = p.cuts + 2 * blockIdx.x;
+                cut[0] = make_int4(quotient(w + nb - 1, share), u.slot, u.nr, u.kvh);
+                cut[1] = make_int4(u.q_start, u.row0, 0, 0);
+            }
             w += n;
             break;
         }
@@ -335,21 +348,32 @@ __device__ void producer_role(const Paged8Params& p, uint8_t* smem, const Bars& 
             load_tiles(&p.tm_v, prev_rows, prev_nt, prev_kvh);
             prev_nt = 0;
         }
+        auto page_ids = [&](int s, int* id) {  // of the boxes of step s: loaded a step before they are used
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int x = k * 32 + lane;
+                const long long key = (long long)(u.tile0 + s) * 128 + (long long)x * rows;
+                id[k] = -1;
+                if (x < min(C::SB, u.nt - s) * per_tile && key < u.kv_len)
+                    id[k] = __ldg(p.block_table + (size_t)u.r * p.max_pages + (key >> p.page_shift));
+            }
+        };
+        int id[2], next_id[2];
+        if (u.nt > 0) page_ids(0, id);
         for (int s = 0; ok && s < u.nt; s += C::SB) {
             const int nt = min(C::SB, u.nt - s);
+            page_ids(s + C::SB, next_id);
             int row_of[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int x = k * 32 + lane;
-                row_of[k] = p.kv_rows;
                 const long long key = (long long)(u.tile0 + s) * 128 + (long long)x * rows;
-                if (x < nt * per_tile && key < u.kv_len) {
-                    const int id = __ldg(p.block_table + (size_t)u.r * p.max_pages + (key >> p.page_shift));
-                    if (id >= 0 && id < p.num_pages)
-                        row_of[k] = (id << p.page_shift) + (int)(key & ((1 << p.page_shift) - 1));
-                    else
-                        atomicOr(p.status, 1u << kStatusDeviceData);
-                }
+                row_of[k] = p.kv_rows;
+                if (id[k] >= 0 && id[k] < p.num_pages)
+                    row_of[k] = (id[k] << p.page_shift) + (int)(key & ((1 << p.page_shift) - 1));
+                else if (x < nt * per_tile && key < u.kv_len)
+                    atomicOr(p.status, 1u << kStatusDeviceData);
+                id[k] = next_id[k];
             }
             load_tiles(&p.tm_k, row_of, nt, u.kvh);
             load_tiles(&p.tm_v, prev_rows, prev_nt, prev_kvh);
@@ -496,19 +520,16 @@ __device__ void mma_role(const Paged8Params& p, uint8_t* smem, const Bars& b, vo
     if (prev.nt > 0) product_pv(n - 1u);
 }
 
-// ---------------------------------------------------------------- query rows and scales (one warp)
+// ---------------------------------------------------------------- query rows (one warp)
 
 template <int D, int R>
-__device__ void aux_role(const Paged8Params& p, uint8_t* smem, const Bars& b, volatile int* uq, volatile int* abort_flag,
+__device__ void query_role(const Paged8Params& p, uint8_t* smem, const Bars& b, volatile int* uq, volatile int* abort_flag,
                          int lane) {
     using C = Cfg<D, R>;
     constexpr int LPR = D / 8;         // lanes of a query row, 8 elements each
     constexpr int PASS = 8 * LPR / 32; // rounds for 8 rows
     const uint32_t sbase = smem_u32(smem);
-    const int per_page = p.page_shift - p.block_shift;
-    const int gshift = min(p.block_shift, 4);  // keys that share an entry of s_scale: 1 to 16
     int units = 0;
-    uint32_t n = 0;
     for (int k = 0;; ++k) {
         const int slot = k % kQN;
         if (!warp_wait(&b.uq_full[slot], (uint32_t)((k / kQN) & 1), abort_flag, p.status)) return;
@@ -577,6 +598,25 @@ __device__ void aux_role(const Paged8Params& p, uint8_t* smem, const Bars& b, vo
         fence_async_smem();
         __syncwarp();
         if (lane == 0) bar_arrive(&b.q_full[qb]);
+    }
+}
+
+// ---------------------------------------------------------------- scales of the steps' keys (one warp)
+
+template <int D, int R>
+__device__ void scale_role(const Paged8Params& p, uint8_t* smem, const Bars& b, volatile int* uq, volatile int* abort_flag,
+                           int lane) {
+    using C = Cfg<D, R>;
+    const int per_page = p.page_shift - p.block_shift;
+    const int gshift = min(p.block_shift, 4);  // keys that share an entry of s_scale: 1 to 16
+    uint32_t n = 0;
+    for (int k = 0;; ++k) {
+        const int slot = k % kQN;
+        if (!warp_wait(&b.uq_full[slot], (uint32_t)((k / kQN) & 1), abort_flag, p.status)) return;
+        const Unit u = read_unit(uq + slot * kUnitInts);
+        __syncwarp();
+        if (lane == 0) bar_arrive(&b.uq_empty[slot]);
+        if (u.r < 0) return;
         for (int s = 0; s < u.nt; s += C::SB, ++n) {
             const uint32_t buf = n & 1u;
             const int groups = (min(C::SB, u.nt - s) * 128) >> gshift;
@@ -913,7 +953,7 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
     int* misc = reinterpret_cast<int*>(smem + C::OFF_MISC);  // tmem, abort, skip, r0; then the words below
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(misc);
     volatile int* abort_flag = misc + 1;
-    long long* wide = reinterpret_cast<long long*>(misc + 4);  // [0] start of request r0, [1 .. 11] sums of the warps
+    long long* wide = reinterpret_cast<long long*>(misc + 4);  // [0] start of request r0, [1 .. 12] sums of the warps
 
     griddep_launch_dependents();  // the merge may be scheduled; it waits for this grid
     // ---- the cut: tiles of all requests, in order, in shares of equal size
@@ -922,7 +962,7 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
     Extent e = extent(p, min(ra, p.B - 1));  // its load is under way during the set-up
     if (tid < C::N_BARS) {
         uint64_t* x = bars + tid;
-        bar_init(x, x >= b.uq_empty ? 10 : x >= b.o_full && x < b.done ? 2 : x == b.p_full ? 256 : x >= b.sc_empty && x < b.s_full ? 8
+        bar_init(x, x >= b.uq_empty ? 11 : x >= b.o_full && x < b.done ? 2 : x == b.p_full ? 256 : x >= b.sc_empty && x < b.s_full ? 8
                     : x >= b.q_empty && x < b.sc_full ? 9 : 1);
         bar_init_fence();
     }
@@ -965,9 +1005,8 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
         if (w < warp) before += wide[1 + w];
         total += wide[1 + w];
     }
-    // (32-bit division where it will do: the 64-bit one takes a noticeable part of a short call)
-    const long long even = total < 0x7fff0000LL ? ((unsigned)total + gridDim.x - 1) / gridDim.x : (total + gridDim.x - 1) / gridDim.x;
-    const long long share = max((long long)kMinShare, even);
+    const long long share = total < 0x7fff0000LL ? max((unsigned)kMinShare, ((unsigned)total + gridDim.x - 1) / gridDim.x)
+                                                 : (total + gridDim.x - 1) / gridDim.x;
     const long long w0 = (long long)blockIdx.x * share, w1 = min(total, w0 + share);
     if (w0 >= before && w0 < before + sum) {  // this thread's requests hold the CTA's first tile
         long long at = before;
@@ -986,15 +1025,7 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
             at += work;
         }
     }
-    if (blockIdx.x == 0) {  // for the merge
-        if (tid == 0) p.plan[0] = share;
-        long long at = before;
-        for (int r = ra; r < rb; ++r) {
-            if (per > 1) e = extent(p, r);
-            p.plan[1 + r] = at;
-            at += work_of(p, e);
-        }
-    }
+    if (tid == 0) p.cuts[2 * blockIdx.x].x = -1;  // the producer (this thread) may put a cut in its place
     __syncthreads();
     const uint32_t tmem = *tmem_holder;
     if (misc[2] == 0 && w0 < total) {
@@ -1011,9 +1042,11 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
         } else if (warp == 0) {
             const int* first = misc + kMiscFirst;
             producer_role<D, R>(p, smem, b, uq, abort_flag, lane, misc[3], w0, w1, wide[0],
-                                Extent{first[0], first[1], first[2], false});
+                                Extent{first[0], first[1], first[2], false}, share);
+        } else if (warp == 10) {
+            query_role<D, R>(p, smem, b, uq, abort_flag, lane);
         } else {
-            aux_role<D, R>(p, smem, b, uq, abort_flag, lane);
+            scale_role<D, R>(p, smem, b, uq, abort_flag, lane);
         }
     }
     tc_fence_before();
@@ -1024,89 +1057,80 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
     }
 }
 
-// Four warps per output row (query token, head): where its unit was cut, its pieces by
+// The units that were cut, one CTA for each of their rows x % gridDim.y: piece by piece to its eight warps,
 //   m = max m_i,  l = sum l_i 2^(m_i - m),  O = sum 2^(m_i - m) O_i / l.
-constexpr int kMergeWarps = 4;
+// The pieces are one unit's last of CTA c0 and first of the CTAs up to c1.  Their (m, l) and O are asked for at once.
+constexpr int kMergeWarps = 8;
+constexpr int kMergeRows = 4;
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) paged8_merge_kernel(const __grid_constant__ Paged8Params p) {
     constexpr int PER = D / 32;
     using Vec = typename std::conditional<PER == 4, float4, float2>::type;
-    __shared__ float s_o[kMergeWarps][D];
-    const int tok = (int)(blockIdx.x / (unsigned)p.H), head = (int)(blockIdx.x - (unsigned)tok * (unsigned)p.H);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int r = tok;
-    if (p.cu_q != nullptr) {  // the last request whose first token is <= tok
-        int lo = 0, hi = p.B - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (__ldg(p.cu_q + mid) <= tok)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        r = lo;
-    }
-    const Extent e = extent(p, r);
-    const int t = tok - e.q_start;
-    if (t < 0 || t >= e.q_len) return;
-    const int kvh = head / p.G, x = t * p.G + head - kvh * p.G;
-    const int nb = key_tiles(e), qt = x / p.R;
-    const long long in_request = ((long long)kvh * row_tiles(p, e) + qt) * (nb + kUnitCost) + kUnitCost;
+    __shared__ float s_o[kMergeWarps][D], s_ml[kMergeWarps][2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.x;
     griddep_wait();
-    if (timeout_recorded(p.status)) return;
-    const long long share = __ldcg(p.plan), first = __ldcg(p.plan + 1 + r) + in_request;
-    const int c0 = (int)(first / share), c1 = (int)((first + nb - 1) / share);
-    if (c0 == c1) return;
-    auto record = [&](int c) { return ((size_t)(2 * c + (c == c0 && first != c * share ? 1 : 0))) * p.R + (x - qt * p.R); };
-    const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-    float m = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, __ldcg(ml + record(c)).x);
-    m = warp_max(m);
-    float l = 0.f, acc[PER];
+    const int4 cut = __ldcg(p.cuts + 2 * c0), unit = __ldcg(p.cuts + 2 * c0 + 1);
+    if (timeout_recorded(p.status) || cut.x < 0) return;
+    for (int r = blockIdx.y; r < cut.z; r += kMergeRows) {
+        float m = -INFINITY, l = 0.f, acc[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-    for (int base = c0; base <= c1; base += 32) {
-        float w = 0.f;
-        if (base + lane <= c1) {
-            const float2 y = __ldcg(ml + record(base + lane));
-            w = y.x == -INFINITY ? 0.f : ex2(y.x - m);  // a piece without a visible key has no O
-            if (w != 0.f) l += y.y * w;
-        }
-        const int n = min(32, c1 - base + 1);
-        for (int i = warp; i < n; i += 4 * kMergeWarps) {  // four pieces of the warp in flight
+        for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+        for (int c = c0 + warp; c <= cut.x; c += 4 * kMergeWarps) {  // four pieces in flight
             Vec v[4];
-            float wi[4];
+            float2 ml[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int c = i + k * kMergeWarps;
-                wi[k] = __shfl_sync(0xffffffffu, w, c & 31);
-                if (c >= n) wi[k] = 0.f;
-                if (wi[k] != 0.f) v[k] = __ldcg(reinterpret_cast<const Vec*>(p.part_o + record(base + c) * D) + lane);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (wi[k] != 0.f) {
-                    const float* f = reinterpret_cast<const float*>(&v[k]);
-#pragma unroll
-                    for (int q = 0; q < PER; ++q) acc[q] = fmaf(wi[k], f[q], acc[q]);
+                const int ck = c + k * kMergeWarps;
+                ml[k] = make_float2(-INFINITY, 0.f);
+                if (ck <= cut.x) {
+                    const size_t rec = (size_t)(ck == c0 ? cut.y : 2 * ck) * p.R + r;
+                    ml[k] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + rec);
+                    v[k] = __ldcg(reinterpret_cast<const Vec*>(p.part_o + rec * D) + lane);
                 }
+            }
+            float top = m;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top = fmaxf(top, ml[k].x);
+            const float old = m == -INFINITY ? 0.f : ex2(m - top);
+            m = top;
+            l *= old;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) acc[i] *= old;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (ml[k].x == -INFINITY) continue;  // no such piece, or one without a visible key: it has no O
+                const float w = ex2(ml[k].x - m);
+                const float* f = reinterpret_cast<const float*>(&v[k]);
+                l = fmaf(ml[k].y, w, l);
+#pragma unroll
+                for (int i = 0; i < PER; ++i) acc[i] = fmaf(f[i], w, acc[i]);
+            }
         }
-    }
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-#pragma unroll
-    for (int q = 0; q < PER; ++q) s_o[warp][lane * PER + q] = acc[q];
-    __syncthreads();
-    if (threadIdx.x < D / 2) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        float y[2] = {0.f, 0.f};
-#pragma unroll
-        for (int w = 0; w < kMergeWarps; ++w) {
-            y[0] += s_o[w][2 * threadIdx.x];
-            y[1] += s_o[w][2 * threadIdx.x + 1];
+        for (int i = 0; i < PER; ++i) s_o[warp][lane * PER + i] = acc[i];
+        if (lane == 0) {
+            s_ml[warp][0] = m;
+            s_ml[warp][1] = l;
         }
-        reinterpret_cast<uint32_t*>(p.o + (size_t)blockIdx.x * D)[threadIdx.x] = pack_bf16(y[0] * inv, y[1] * inv);
-        if (threadIdx.x == 0 && p.lse != nullptr) p.lse[blockIdx.x] = l == 0.f ? -INFINITY : (m + lg2(l)) * kLn2;
+        __syncthreads();
+        if (threadIdx.x < D / 2) {
+            float top = -INFINITY, sum = 0.f, y[2] = {0.f, 0.f};
+#pragma unroll
+            for (int w = 0; w < kMergeWarps; ++w) top = fmaxf(top, s_ml[w][0]);
+#pragma unroll
+            for (int w = 0; w < kMergeWarps; ++w) {
+                const float f = s_ml[w][0] == -INFINITY ? 0.f : ex2(s_ml[w][0] - top);
+                sum = fmaf(s_ml[w][1], f, sum);
+                y[0] = fmaf(s_o[w][2 * threadIdx.x], f, y[0]);
+                y[1] = fmaf(s_o[w][2 * threadIdx.x + 1], f, y[1]);
+            }
+            const int x = unit.y + r, tok = x / p.G;
+            const size_t row = (size_t)(unit.x + tok) * p.H + cut.w * p.G + (x - tok * p.G);
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            reinterpret_cast<uint32_t*>(p.o + row * D)[threadIdx.x] = pack_bf16(y[0] * inv, y[1] * inv);
+            if (threadIdx.x == 0 && p.lse != nullptr) p.lse[row] = sum == 0.f ? -INFINITY : (top + lg2(sum)) * kLn2;
+        }
+        __syncthreads();
     }
 }
 
@@ -1122,7 +1146,7 @@ cudaError_t launch(const Paged8Params& p, cudaStream_t stream) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.total_q * p.H));
+    cfg.gridDim = dim3((unsigned)p.n_ctas, kMergeRows);
     cfg.blockDim = dim3(kMergeWarps * 32);
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -1132,11 +1156,11 @@ cudaError_t launch(const Paged8Params& p, cudaStream_t stream) {
 
 }  // namespace
 
-Paged8Plan paged8_plan(int B, int max_q_len, int G, int d) {
+Paged8Plan paged8_plan(int max_q_len, int G, int d) {
     Paged8Plan pl;
     const long long rows = (long long)max_q_len * G;
     pl.R = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
-    pl.part_ml = (8 + (size_t)B * 8 + 255) / 256 * 256;
+    pl.part_ml = kPaged8Ctas * 2 * sizeof(int4);
     pl.part_o = pl.part_ml + (size_t)2 * kPaged8Ctas * pl.R * 2 * sizeof(float);
     pl.bytes = pl.part_o + (size_t)2 * kPaged8Ctas * pl.R * d * sizeof(float);
     return pl;
