@@ -8,14 +8,16 @@
 // subnormal.
 //
 // Work.  Tokens of one block follow one another in the call (a run).  A CTA owns
-// the runs that begin among its 32 tokens, for K or for V, and a share of the
-// heads; the last run may reach past them.  A thread holds 16 dims of one row (8
-// pairs of the rotation: their cosines and sines, computed once, serve all heads).
-// First pass: every head's rows are rotated and each run's largest magnitude found
-// (lanes of a row by shuffles, rows by an atomic maximum in shared memory, whose
-// order does not matter).  Then the scales; second pass: the rows, from L1 or L2,
-// rotated again and stored as codes.  Rows that a block held before are requantised
-// by the whole CTA where the scale grew.
+// the runs that begin among its 32 tokens, for K or for V, and up to four heads;
+// the last run may reach past them.  A thread holds 16 dims of one row (8 pairs of
+// the rotation: their cosines and sines, computed once, serve all heads) and has all
+// heads' loads in flight; those of the first 32 tokens leave before anything about
+// slots is known.  First pass: the rows are rotated and each run's largest magnitude
+// found (lanes of a row by shuffles, rows by an atomic maximum in shared memory, whose
+// order does not matter).  Then the scales; second pass: the rows, the last ones still
+// in registers, rotated again and stored as codes.  Rows that a block held before are
+// requantised by the whole CTA where the scale grew.  The same launch rotates q, in
+// CTAs of their own.
 #include <cmath>
 #include <cstring>
 
@@ -30,7 +32,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWindow = 32;  // tokens whose runs a CTA owns
-constexpr int kMaxHeads = 16;  // heads a CTA walks over
+constexpr int kHeads = 4;      // heads of a K or V CTA, and heads that a q CTA has in flight
+constexpr long long kStreamBytes = 128LL << 20;  // L2: a q_out above it is stored evict-first, as in rope.cu
 
 struct Append8Params {
     const char* in[2];       // k, v: bf16 through byte strides
@@ -45,6 +48,11 @@ struct Append8Params {
     int freq64, T, H_kv, d, rot;
     int page_shift, block_shift;
     int hpc, splits;         // heads per CTA, CTAs that share a window's heads
+    unsigned kv_ctas;        // CTAs of K, as many of V; those of q follow
+    const char* q;           // bf16 through byte strides, or nullptr
+    char* q_out;
+    long long qt, qh, qot, qoh;
+    int H, q_hpc, q_splits, q_stream;
     float amplitude;
 };
 
@@ -86,11 +94,6 @@ __device__ __forceinline__ int slot_of(const Append8Params& p, int t) {
     return s < 0 || s >= p.n_slots ? -1 : s;
 }
 
-// Whether token t, which has slot s, begins a run.
-__device__ __forceinline__ bool begins(const Append8Params& p, int t, int s) {
-    return t == 0 || (s & ((1 << p.block_shift) - 1)) == 0 || __ldg(p.slots + t - 1) != s - 1;
-}
-
 template <bool INTERLEAVED>
 struct Turn {  // 8 pairs of one row
     float cs[8], sn[8];
@@ -127,73 +130,22 @@ __device__ __forceinline__ float finite_abs(float x) {
     return a < INFINITY ? a : 0.f;
 }
 
+// What a thread knows of its place in a row: 16 dims in two pieces, that turn where the rotation reaches them.
 template <int D, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) append8_kernel(const __grid_constant__ Append8Params p) {
-    constexpr int UPR = D / 16;            // threads of a row
-    constexpr int ROWS = kThreads / UPR;   // rows side by side
-    __shared__ unsigned long long s_turn[D / 2];
-    __shared__ int s_amax[kMaxHeads][kWindow];     // by run, named by its first token's place in the window
-    __shared__ float s_scale[kMaxHeads][kWindow];
-    __shared__ float s_ratio[kMaxHeads][kWindow];  // before / now of the rows already there, 1: as they are
-    __shared__ unsigned s_lead;
-    __shared__ int s_end;
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int side = blockIdx.y;  // 0: K, 1: V
-    const int window = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
-    const int t0 = window * kWindow;
-    const int h0 = split * p.hpc, nh = min(p.hpc, p.H_kv - h0);
-    const int bmask = (1 << p.block_shift) - 1;
-
-    if (tid < 32) {  // which of the window's tokens begin runs
-        const int t = t0 + lane;
-        bool lead = false;
-        if (t < p.T) {
-            const int s = slot_of(p, t);
-            lead = s >= 0 && begins(p, t, s);
-            if (s < 0 && __ldg(p.slots + t) >= 0 && side == 0 && split == 0) atomicOr(p.status, 1u << kStatusDeviceData);
-        }
-        const unsigned m = __ballot_sync(0xffffffffu, lead);
-        if (lane == 0) {
-            s_lead = m;
-            s_end = p.T;
-        }
+struct Place {
+    static constexpr int UPR = D / 16;            // threads of a row
+    static constexpr int ROWS = kThreads / UPR;   // rows side by side
+    int j, row, off_a, off_b;                     // pieces in elements
+    bool turns;
+    __device__ __forceinline__ Place(int rot) {
+        j = threadIdx.x % UPR;
+        row = threadIdx.x / UPR;
+        turns = j * 16 < rot;
+        const bool split_halves = turns && !INTERLEAVED;
+        off_a = split_halves ? j * 8 : j * 16;
+        off_b = split_halves ? rot / 2 + j * 8 : j * 16 + 8;
     }
-    for (int i = tid; i < kMaxHeads * kWindow; i += kThreads) (&s_amax[0][0])[i] = 0;
-    const bool turning = side == 0 && p.rot > 0;
-    if (turning)
-        for (int i = tid; i < p.rot / 2; i += kThreads)
-            s_turn[i] = p.freq64 ? turn_fraction(static_cast<const double*>(p.freq)[i])
-                                 : turn_fraction(static_cast<const float*>(p.freq)[i]);
-    __syncthreads();
-    const unsigned lead = s_lead;
-    if (lead == 0u) return;  // the tokens here belong to a run that began before, or to none
-    const int first = t0 + __ffs(lead) - 1, last_lead = t0 + 31 - __clz(lead);
-    {  // the end of the last run: its first token that does not follow on
-        const int s0 = slot_of(p, last_lead);
-        const int room = bmask + 1 - (s0 & bmask);  // rows of the block from the run's first on
-        for (int i = 1 + tid; i <= room; i += kThreads) {
-            const int t = last_lead + i;
-            if (t >= p.T) break;
-            if (i == room || __ldg(p.slots + t) != s0 + i) {
-                atomicMin(&s_end, t);
-                break;
-            }
-        }
-    }
-    __syncthreads();
-    const int end = s_end;
-
-    const int j = tid % UPR, row = tid / UPR;
-    const bool turns = turning && j * 16 < p.rot;
-    const bool split_halves = turns && !INTERLEAVED;
-    const int off_a = split_halves ? j * 8 : j * 16;  // elements of the thread's two pieces
-    const int off_b = split_halves ? p.rot / 2 + j * 8 : j * 16 + 8;
-    // the run of token t: the last of the window's runs to begin at or before it
-    auto run_of = [&](int t) {
-        const int i = min(t - t0, 31);
-        return 31 - __clz(lead & (0xffffffffu >> (31 - i)));
-    };
-    auto turn_for = [&](int t, Turn<INTERLEAVED>& w) {
+    __device__ __forceinline__ void angles(const Append8Params& p, const unsigned long long* s_turn, int t, Turn<INTERLEAVED>& w) const {
         if (!turns) return;
         const int pos = __ldg(p.positions + t);
 #pragma unroll
@@ -203,94 +155,247 @@ __global__ void __launch_bounds__(kThreads) append8_kernel(const __grid_constant
             w.cs[e] = c * p.amplitude;
             w.sn[e] = s * p.amplitude;
         }
-    };
-    auto load = [&](int t, int h, const Turn<INTERLEAVED>& w, float* a, float* c) {
-        const char* src = p.in[side] + t * p.it[side] + (h0 + h) * p.ih[side];
-        unpack8(ld16(src + off_a * 2), a);
-        unpack8(ld16(src + off_b * 2), c);
-        if (turns) w.rotate(a, c);
-    };
+    }
+};
 
+__device__ __forceinline__ void load_turns(const Append8Params& p, unsigned long long* s_turn) {
+    for (int i = threadIdx.x; i < p.rot / 2; i += kThreads)
+        s_turn[i] = p.freq64 ? turn_fraction(static_cast<const double*>(p.freq)[i])
+                             : turn_fraction(static_cast<const float*>(p.freq)[i]);
+}
+
+__device__ __forceinline__ uint4 pack8(const float* x) {
+    return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+}
+__device__ __forceinline__ void st16(char* p, const uint4& v, bool stream) {
+    if (stream)
+        __stcs(reinterpret_cast<uint4*>(p), v);
+    else
+        *reinterpret_cast<uint4*>(p) = v;
+}
+
+// q of a CTA's tokens and heads, rotated into q_out.
+template <int D, bool INTERLEAVED>
+__device__ __forceinline__ void query_part(const Append8Params& p, int cta, unsigned long long* s_turn) {
+    const Place<D, INTERLEAVED> at(p.rot);
+    const int t = cta / p.q_splits * at.ROWS + at.row;
+    const int h0 = cta % p.q_splits * p.q_hpc, h1 = min(p.H, h0 + p.q_hpc);
+    load_turns(p, s_turn);
+    __syncthreads();
+    if (t >= p.T || slot_of(p, t) < 0) return;
     Turn<INTERLEAVED> w;
-    for (int base = first; base < end; base += ROWS) {  // the largest magnitudes
-        const int t = base + row;
-        const bool in = t < end && slot_of(p, min(t, p.T - 1)) >= 0;
-        if (in) turn_for(t, w);
-        for (int h = 0; h < nh; ++h) {
-            float top = 0.f;
-            if (in) {
-                float a[8], c[8];
-                load(t, h, w, a, c);
+    const char* src = p.q + t * p.qt;
+    char* dst = p.q_out + t * p.qot;
+    for (int h = h0; h < h1; h += kHeads) {
+        uint4 x[kHeads], y[kHeads];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) top = fmaxf(top, fmaxf(finite_abs(a[e]), finite_abs(c[e])));
+        for (int i = 0; i < kHeads; ++i)
+            if (h + i < h1) {
+                x[i] = ld16(src + (h + i) * p.qh + at.off_a * 2);
+                y[i] = ld16(src + (h + i) * p.qh + at.off_b * 2);
             }
+        if (h == h0) at.angles(p, s_turn, t, w);
 #pragma unroll
-            for (int o = UPR / 2; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            if (in && j == 0) atomicMax(&s_amax[h][run_of(t)], __float_as_int(top));
+        for (int i = 0; i < kHeads; ++i)
+            if (h + i < h1) {
+                if (at.turns) {
+                    float a[8], c[8];
+                    unpack8(x[i], a);
+                    unpack8(y[i], c);
+                    w.rotate(a, c);
+                    x[i] = pack8(a);
+                    y[i] = pack8(c);
+                }
+                st16(dst + (h + i) * p.qoh + at.off_a * 2, x[i], p.q_stream != 0);
+                st16(dst + (h + i) * p.qoh + at.off_b * 2, y[i], p.q_stream != 0);
+            }
+    }
+}
+
+template <int D, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads, 3) append8_kernel(const __grid_constant__ Append8Params p) {
+    using P = Place<D, INTERLEAVED>;
+    constexpr int UPR = P::UPR, ROWS = P::ROWS;
+    __shared__ unsigned long long s_turn[D / 2];
+    __shared__ int s_amax[kHeads][kWindow];     // by run, named by its first token's place in the window
+    __shared__ float s_scale[kHeads][kWindow];
+    __shared__ float s_ratio[kHeads][kWindow];  // before / now of the rows already there, 1: as they are
+    __shared__ int s_slot[kWindow];
+    __shared__ unsigned s_lead;
+    __shared__ int s_end;
+    if (blockIdx.x >= 2 * p.kv_ctas) {
+        query_part<D, INTERLEAVED>(p, (int)(blockIdx.x - 2 * p.kv_ctas), s_turn);
+        return;
+    }
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int side = blockIdx.x >= p.kv_ctas;  // 0: K, 1: V
+    const unsigned cta = blockIdx.x - (side ? p.kv_ctas : 0u);
+    const int window = (int)(cta / (unsigned)p.splits), split = (int)(cta % (unsigned)p.splits);
+    const int t0 = window * kWindow;
+    const int h0 = split * p.hpc, nh = min(p.hpc, p.H_kv - h0);
+    const int bmask = (1 << p.block_shift) - 1;
+    const P at(side == 0 ? p.rot : 0);
+
+    // rows t0 + base + row of all heads: the first ones asked for before their slots are known
+    uint4 x[kHeads], y[kHeads];
+    auto fetch = [&](int t) {
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h)
+            if (h < nh && t < p.T) {
+                const char* src = p.in[side] + t * p.it[side] + (h0 + h) * p.ih[side];
+                x[h] = ld16(src + at.off_a * 2);
+                y[h] = ld16(src + at.off_b * 2);
+            }
+    };
+    fetch(t0 + at.row);
+    if (tid < 32) {  // which of the window's tokens begin runs
+        const int t = t0 + lane;
+        bool lead = false;
+        int s = -1;
+        if (t < p.T) {
+            s = __ldg(p.slots + t);
+            const int before = t > 0 ? __ldg(p.slots + t - 1) : -2;
+            if (s >= p.n_slots) {
+                if (side == 0 && split == 0) atomicOr(p.status, 1u << kStatusDeviceData);
+                s = -1;
+            }
+            lead = s >= 0 && ((s & bmask) == 0 || before != s - 1 || t == 0);
+        }
+        s_slot[lane] = s;
+        const unsigned m = __ballot_sync(0xffffffffu, lead);
+        if (lane == 0) {
+            s_lead = m;
+            s_end = p.T;
         }
     }
+    for (int i = tid; i < kHeads * kWindow; i += kThreads) (&s_amax[0][0])[i] = 0;
+    if (side == 0 && p.rot > 0) load_turns(p, s_turn);
     __syncthreads();
-    for (int x = tid; x < nh * kWindow; x += kThreads) {  // the scales
-        const int h = x / kWindow, i = x % kWindow;
+    const unsigned lead = s_lead;
+    if (lead == 0u) return;  // the tokens here belong to a run that began before, or to none
+    const int first = t0 + __ffs(lead) - 1, last_lead = t0 + 31 - __clz(lead);
+    int end = last_lead + 1;
+    {  // the end of the last run: its first token that does not follow on
+        const int s0 = s_slot[last_lead - t0];
+        const int room = bmask + 1 - (s0 & bmask);  // rows of the block from the run's first on
+        if (room > 1) {
+            for (int i = 1 + tid; i <= room; i += kThreads) {
+                const int t = last_lead + i;
+                if (t >= p.T) break;
+                if (i == room || __ldg(p.slots + t) != s0 + i) {
+                    atomicMin(&s_end, t);
+                    break;
+                }
+            }
+            __syncthreads();
+            end = s_end;
+        }
+    }
+    // the run of token t: the last of the window's runs to begin at or before it
+    auto run_of = [&](int t) {
+        const int i = min(t - t0, 31);
+        return 31 - __clz(lead & (0xffffffffu >> (31 - i)));
+    };
+    // whether token t belongs to one of the window's runs
+    auto in_run = [&](int t) { return t >= first && t < end && (t - t0 >= kWindow || s_slot[t - t0] >= 0); };
+
+    Turn<INTERLEAVED> w;
+    const int passes = (end - t0 + ROWS - 1) / ROWS;
+    for (int pass = 0; pass < passes; ++pass) {  // the largest magnitudes
+        const int t = t0 + pass * ROWS + at.row;
+        const bool in = in_run(t);
+        if (pass > 0) fetch(t);
+        if (in) at.angles(p, s_turn, t, w);
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h)
+            if (h < nh) {
+                float top = 0.f;
+                if (in) {
+                    float a[8], c[8];
+                    unpack8(x[h], a);
+                    unpack8(y[h], c);
+                    if (at.turns) w.rotate(a, c);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) top = fmaxf(top, fmaxf(finite_abs(a[e]), finite_abs(c[e])));
+                }
+#pragma unroll
+                for (int o = UPR / 2; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                if (in && at.j == 0) atomicMax(&s_amax[h][run_of(t)], __float_as_int(top));
+            }
+    }
+    __syncthreads();
+    bool grew = false;
+    for (int k = tid; k < nh * kWindow; k += kThreads) {  // the scales
+        const int h = k / kWindow, i = k % kWindow;
         if (!(lead >> i & 1u)) continue;
-        const int s = slot_of(p, t0 + i);
+        const int s = s_slot[i];
         const int per_page = 1 << (p.page_shift - p.block_shift);
-        const long long at = ((long long)(s >> p.page_shift) * p.H_kv + h0 + h) * per_page +
-                             ((s & ((1 << p.page_shift) - 1)) >> p.block_shift);
+        float* scale = p.scale[side] + ((long long)(s >> p.page_shift) * p.H_kv + h0 + h) * per_page +
+                       ((s & ((1 << p.page_shift) - 1)) >> p.block_shift);
         const float need = scale_for(__int_as_float(s_amax[h][i]));
         float now = need, ratio = 1.f;
         if ((s & bmask) != 0) {
-            const float before = p.scale[side][at];
+            const float before = *scale;
             now = fmaxf(before, need);
-            if (!(before >= now)) ratio = before / now;
+            if (!(before >= now)) {
+                ratio = before / now;
+                grew = true;
+            }
         }
         s_scale[h][i] = now;
         s_ratio[h][i] = ratio;
-        p.scale[side][at] = now;
+        *scale = now;
     }
-    __syncthreads();
-    for (int base = first; base < end; base += ROWS) {  // the codes
-        const int t = base + row;
-        if (t >= end) break;
-        const int s = slot_of(p, t);
-        if (s < 0) continue;
-        if (base != first || end - first > ROWS) turn_for(t, w);
-        const int run = run_of(t);
-        for (int h = 0; h < nh; ++h) {
-            float a[8], c[8];
-            load(t, h, w, a, c);
-            const float now = s_scale[h][run];
-            uint2 x, y;
-            if (is_pow2(now)) {
-                const float inv = 1.f / now;
-                x = make_uint2(codes4(a[0], a[1], a[2], a[3], inv), codes4(a[4], a[5], a[6], a[7], inv));
-                y = make_uint2(codes4(c[0], c[1], c[2], c[3], inv), codes4(c[4], c[5], c[6], c[7], inv));
-            } else {  // a scale that another writer left
-                x = make_uint2(codes4_div(a[0], a[1], a[2], a[3], now), codes4_div(a[4], a[5], a[6], a[7], now));
-                y = make_uint2(codes4_div(c[0], c[1], c[2], c[3], now), codes4_div(c[4], c[5], c[6], c[7], now));
-            }
-            uint8_t* dst = p.codes[side] + ((long long)s * p.H_kv + h0 + h) * D;
-            *reinterpret_cast<uint2*>(dst + off_a) = x;
-            *reinterpret_cast<uint2*>(dst + off_b) = y;
+    const bool any_grew = __syncthreads_or(grew) != 0;
+    for (int pass = passes - 1; pass >= 0; --pass) {  // the codes; the last pass's rows and angles are at hand
+        const int t = t0 + pass * ROWS + at.row;
+        if (!in_run(t)) continue;
+        if (pass != passes - 1) {
+            fetch(t);
+            at.angles(p, s_turn, t, w);
         }
+        const int run = run_of(t);
+        const int s = s_slot[run] + (t - t0 - run);  // a run's slots follow one another
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h)
+            if (h < nh) {
+                float a[8], c[8];
+                unpack8(x[h], a);
+                unpack8(y[h], c);
+                if (at.turns) w.rotate(a, c);
+                const float now = s_scale[h][run];
+                uint2 ca, cc;
+                if (is_pow2(now)) {
+                    const float inv = 1.f / now;
+                    ca = make_uint2(codes4(a[0], a[1], a[2], a[3], inv), codes4(a[4], a[5], a[6], a[7], inv));
+                    cc = make_uint2(codes4(c[0], c[1], c[2], c[3], inv), codes4(c[4], c[5], c[6], c[7], inv));
+                } else {  // a scale that another writer left
+                    ca = make_uint2(codes4_div(a[0], a[1], a[2], a[3], now), codes4_div(a[4], a[5], a[6], a[7], now));
+                    cc = make_uint2(codes4_div(c[0], c[1], c[2], c[3], now), codes4_div(c[4], c[5], c[6], c[7], now));
+                }
+                uint8_t* dst = p.codes[side] + ((long long)s * p.H_kv + h0 + h) * D;
+                *reinterpret_cast<uint2*>(dst + at.off_a) = ca;
+                *reinterpret_cast<uint2*>(dst + at.off_b) = cc;
+            }
     }
+    if (!any_grew) return;
     for (unsigned left = lead; left != 0u; left &= left - 1) {  // rows that were there, under a larger scale now
         const int i = __ffs(left) - 1;
-        const int s = slot_of(p, t0 + i), held = s & bmask;
+        const int s = s_slot[i], held = s & bmask;
         if (held == 0) continue;
         for (int h = 0; h < nh; ++h) {
             const float ratio = s_ratio[h][i];
             if (ratio == 1.f) continue;
-            for (int r = row; r < held; r += ROWS) {
-                uint4* at = reinterpret_cast<uint4*>(p.codes[side] + ((long long)(s - held + r) * p.H_kv + h0 + h) * D + j * 16);
-                uint4 x = *at;
-                uint32_t* word = reinterpret_cast<uint32_t*>(&x);
+            for (int r = at.row; r < held; r += ROWS) {
+                uint4* word4 = reinterpret_cast<uint4*>(p.codes[side] + ((long long)(s - held + r) * p.H_kv + h0 + h) * D + at.j * 16);
+                uint4 old = *word4;
+                uint32_t* word = reinterpret_cast<uint32_t*>(&old);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float2 lo = values2((uint16_t)word[e]), hi = values2((uint16_t)(word[e] >> 16));
                     word[e] = pack_e4m3x4(lo.x * ratio, lo.y * ratio, hi.x * ratio, hi.y * ratio);
                 }
-                *at = x;
+                *word4 = old;
             }
         }
     }
@@ -423,7 +528,8 @@ attn_status_t attn_paged_append_fp8(const void* q, void* q_out, const void* k, c
     if (T > 0x7fffffff - 2048) return ATTN_ERR_INVALID_ARG;  // a run reaches at most 1024 tokens past its window
     if (!k_scale || !v_scale || !aligned(k_scale, 4) || !aligned(v_scale, 4)) return ATTN_ERR_INVALID_ARG;
     unsigned* status = nullptr;
-    st = status_word_address(&status);
+    int sm_count = 0;
+    st = status_word_address(&status, &sm_count);
     if (st != ATTN_OK) return st;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
 
@@ -452,12 +558,33 @@ attn_status_t attn_paged_append_fp8(const void* q, void* q_out, const void* k, c
     p.page_shift = shift_of(page_size);
     p.block_shift = shift_of(block);
     p.amplitude = amplitude;
-    p.hpc = H_kv < kMaxHeads ? H_kv : kMaxHeads;
+    // CTAs: as few heads to each as it takes to have two on every SM (q: its part of the bytes of them)
+    const int want = 2 * sm_count;
     const long long windows = ((long long)T + kWindow - 1) / kWindow;
-    while (p.hpc > 1 && windows * ((H_kv + p.hpc - 1) / p.hpc) < 304) p.hpc = (p.hpc + 1) / 2;
+    p.hpc = H_kv < kHeads ? H_kv : kHeads;
+    while (p.hpc > 1 && 2 * windows * ((H_kv + p.hpc - 1) / p.hpc) < want) p.hpc = (p.hpc + 1) / 2;
     p.splits = (H_kv + p.hpc - 1) / p.hpc;
-    if (windows * p.splits > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
-    const dim3 grid((unsigned)(windows * p.splits), 2);
+    long long ctas = 2 * windows * p.splits, q_ctas = 0;
+    if (ctas > 0x3fffffffLL) return ATTN_ERR_INVALID_ARG;
+    p.kv_ctas = (unsigned)(windows * p.splits);
+    if (q) {
+        const int rows = kThreads * 16 / d;
+        const long long tiles = ((long long)T + rows - 1) / rows;
+        p.q = static_cast<const char*>(q);
+        p.q_out = static_cast<char*>(q_out);
+        p.qt = strides[0] * 2;
+        p.qh = strides[1] * 2;
+        p.qot = strides[2] * 2;
+        p.qoh = strides[3] * 2;
+        p.H = H;
+        p.q_hpc = H < 16 ? H : 16;
+        while (p.q_hpc > 1 && tiles * ((H + p.q_hpc - 1) / p.q_hpc) < want) p.q_hpc = (p.q_hpc + 1) / 2;
+        p.q_splits = (H + p.q_hpc - 1) / p.q_hpc;
+        p.q_stream = (long long)T * H * d * 2 > kStreamBytes;
+        q_ctas = tiles * p.q_splits;
+    }
+    if (ctas + q_ctas > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+    const unsigned grid = (unsigned)(ctas + q_ctas);
     if (d == 128) {
         if (interleaved)
             append8_kernel<128, true><<<grid, kThreads, 0, cs>>>(p);
@@ -469,25 +596,7 @@ attn_status_t attn_paged_append_fp8(const void* q, void* q_out, const void* k, c
         else
             append8_kernel<64, false><<<grid, kThreads, 0, cs>>>(p);
     }
-    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
-    if (!q) return ATTN_OK;
-    AppendQ a;
-    a.q = q;
-    a.q_out = q_out;
-    a.strides = strides;
-    a.slots = slots;
-    a.positions = positions;
-    a.inv_freq = inv_freq;
-    a.status = status;
-    a.n_slots = p.n_slots;
-    a.freq_bits = freq_bits;
-    a.T = T;
-    a.H = H;
-    a.d = d;
-    a.rot = rot;
-    a.interleaved = interleaved;
-    a.amplitude = amplitude;
-    return launch_append_q(a, cs) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 attn_status_t attn_paged_read_fp8(const void* k_cache, const void* v_cache, const float* k_scale,

@@ -186,21 +186,6 @@ constexpr int sparse_chunk_keys(int d) { return d == 128 ? 16 : 32; }
 bool sparse_fused_ok(int d, int G, int max_pages, int budget);
 cudaError_t launch_sparse(int d, const SparseParams& p, int sm_count, cudaStream_t stream);
 
-// The q side of a cache append (rope.cu): q rotated for the tokens that have a slot.
-struct AppendQ {
-    const void* q;             // bf16 [T, H, d] through strides
-    void* q_out;
-    const long long* strides;  // (t, h) of q and of q_out, in elements
-    const int32_t* slots;
-    const int32_t* positions;
-    const void* inv_freq;
-    unsigned* status;
-    long long n_slots;
-    int freq_bits, T, H, d, rot, interleaved;
-    float amplitude;
-};
-cudaError_t launch_append_q(const AppendQ& a, cudaStream_t stream);
-
 // Attention over a cache of e4m3 codes with block scales (paged8.cu).  Query rows of a request
 // and KV head are numbered token * G + head of the group and cut into tiles of R.
 struct Paged8Params {

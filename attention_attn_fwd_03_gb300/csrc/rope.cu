@@ -344,29 +344,6 @@ attn_status_t append_args_ok(const void* q, const void* q_out, const void* k, co
     return ATTN_OK;
 }
 
-// The rotation of q on its way past the cache: tokens with a slot only.
-cudaError_t launch_append_q(const AppendQ& a, cudaStream_t stream) {
-    RopeParams p;
-    std::memset(&p, 0, sizeof p);
-    const long long i3[3] = {0, a.strides[1], a.strides[0]}, o3[3] = {0, a.strides[3], a.strides[2]};
-    set_side(p.q, a.q, a.q_out, i3, o3, 2);
-    p.positions = a.positions;
-    p.freq = a.inv_freq;
-    p.freq64 = a.freq_bits == 64;
-    p.slots = a.slots;
-    p.n_slots = a.n_slots;
-    p.status = a.status;
-    p.n_tokens = a.T;
-    p.N = a.T;
-    p.H = a.H;
-    p.n_heads = a.H;
-    p.d = a.d;
-    p.rot = a.rot;
-    p.amplitude = a.amplitude;
-    p.sign = 1.f;
-    return run(p, 2, a.interleaved != 0, true, stream);
-}
-
 }  // namespace attn
 
 using namespace attn;
