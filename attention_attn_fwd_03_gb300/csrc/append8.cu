@@ -8,16 +8,15 @@
 // subnormal.
 //
 // Work.  Tokens of one block follow one another in the call (a run).  A CTA owns
-// the runs that begin among its 32 tokens, for K or for V, and up to four heads;
-// the last run may reach past them.  A thread holds 16 dims of one row (8 pairs of
-// the rotation: their cosines and sines, computed once, serve all heads) and has all
-// heads' loads in flight; those of the first 32 tokens leave before anything about
-// slots is known.  First pass: the rows are rotated and each run's largest magnitude
-// found (lanes of a row by shuffles, rows by an atomic maximum in shared memory, whose
-// order does not matter).  Then the scales; second pass: the rows, the last ones still
-// in registers, rotated again and stored as codes.  Rows that a block held before are
-// requantised by the whole CTA where the scale grew.  The same launch rotates q, in
-// CTAs of their own.
+// the runs that begin among its 64 tokens, for K or for V, and up to eight heads; the
+// last run may reach past them.  A thread holds 16 dims of a row (8 pairs of the
+// rotation, whose cosines and sines serve all heads); 64 rows from the first run's
+// first token on go side by side, which is all of them unless blocks are larger.
+// First pass: the rows are rotated and each run's largest magnitude found (lanes of a
+// row by shuffles, rows by an atomic maximum in shared memory, whose order does not
+// matter).  Then the scales; second pass: the rows again, mostly from L1 and L2,
+// rotated and stored as codes.  Rows that a block held before are requantised by
+// the whole CTA where the scale grew.  The same launch rotates q, in CTAs of their own.
 #include <cmath>
 #include <cstring>
 
@@ -30,9 +29,10 @@ namespace attn {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWindow = 32;  // tokens whose runs a CTA owns
-constexpr int kHeads = 4;      // heads of a K or V CTA, and heads that a q CTA has in flight
+constexpr int kWindow = 64;    // tokens whose runs a K or V CTA owns, rows side by side in a CTA
+constexpr int kHeads = 2;      // heads whose loads a thread has in flight
+constexpr int kMaxHeads = 8;   // heads of a K or V CTA: their rows' angles are computed once
+constexpr int kReadThreads = 256;
 constexpr long long kStreamBytes = 128LL << 20;  // L2: a q_out above it is stored evict-first, as in rope.cu
 
 struct Append8Params {
@@ -56,14 +56,18 @@ struct Append8Params {
     float amplitude;
 };
 
-// Four fp32 -> four e4m3 bytes.  The magnitudes are at most 448 by the choice of the scale;
-// an infinity or NaN becomes the code of NaN (x - x is NaN for both, 0 otherwise).
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float inv) {
-    return pack_e4m3x4(fmaf(a, inv, a - a), fmaf(b, inv, b - b), fmaf(c, inv, c - c), fmaf(d, inv, d - d));
+// Eight fp32 -> eight e4m3 bytes.  The magnitudes are at most 448 by the choice of the scale.
+__device__ __forceinline__ uint2 codes8(const float* x, float inv) {
+    return make_uint2(pack_e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
+                      pack_e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
 }
-
-__device__ __forceinline__ uint32_t codes4_div(float a, float b, float c, float d, float s) {
-    return pack_e4m3x4(a / s + (a - a), b / s + (b - b), c / s + (c - c), d / s + (d - d));
+// The same by division, for a scale that is no power of two (another writer's), and with the code of NaN for an
+// infinity or NaN (x - x is NaN for both, 0 otherwise).
+__device__ uint2 codes8_careful(const float* x, float s) {
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = x[e] / s + (x[e] - x[e]);
+    return codes8(y, 1.f);
 }
 
 // Two e4m3 bytes -> two fp32 (exact).
@@ -84,7 +88,10 @@ __device__ __forceinline__ float scale_for(float amax) {
     return __uint_as_float((unsigned)max(e, 1) << 23);
 }
 
-__device__ __forceinline__ bool is_pow2(float s) { return (__float_as_uint(s) & 0x807fffffu) == 0u && s > 0.f; }
+// A power of two from 2^-126 to 2^126.
+__device__ __forceinline__ bool is_pow2(float s) {
+    return (__float_as_uint(s) & 0x807fffffu) == 0u && s > 0.f && s <= 0x1p126f;
+}
 
 __device__ __forceinline__ uint4 ld16(const char* p) { return *reinterpret_cast<const uint4*>(p); }
 
@@ -125,25 +132,27 @@ __device__ __forceinline__ void unpack8(const uint4& v, float* x) {
     x[6] = bf16lo_to_f32(v.w); x[7] = bf16hi_to_f32(v.w);
 }
 
-__device__ __forceinline__ float finite_abs(float x) {
-    const float a = fabsf(x);
-    return a < INFINITY ? a : 0.f;
-}
+__device__ __forceinline__ unsigned abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+constexpr unsigned kInfBits = 0x7f800000u;
 
 // What a thread knows of its place in a row: 16 dims in two pieces, that turn where the rotation reaches them.
 template <int D, bool INTERLEAVED>
 struct Place {
-    static constexpr int UPR = D / 16;            // threads of a row
-    static constexpr int ROWS = kThreads / UPR;   // rows side by side
+    static constexpr int UPR = D / 16;                 // threads of a row
+    static constexpr int THREADS = kWindow * UPR;
     int j, row, off_a, off_b;                     // pieces in elements
     bool turns;
     __device__ __forceinline__ Place(int rot) {
         j = threadIdx.x % UPR;
         row = threadIdx.x / UPR;
         turns = j * 16 < rot;
-        const bool split_halves = turns && !INTERLEAVED;
-        off_a = split_halves ? j * 8 : j * 16;
-        off_b = split_halves ? rot / 2 + j * 8 : j * 16 + 8;
+        if (turns) {
+            off_a = INTERLEAVED ? j * 16 : j * 8;
+            off_b = INTERLEAVED ? j * 16 + 8 : rot / 2 + j * 8;
+        } else {  // the dims that pass through, in two halves
+            off_a = rot + (j - rot / 16) * 8;
+            off_b = off_a + (D - rot) / 2;
+        }
     }
     __device__ __forceinline__ void angles(const Append8Params& p, const unsigned long long* s_turn, int t, Turn<INTERLEAVED>& w) const {
         if (!turns) return;
@@ -159,7 +168,8 @@ struct Place {
 };
 
 __device__ __forceinline__ void load_turns(const Append8Params& p, unsigned long long* s_turn) {
-    for (int i = threadIdx.x; i < p.rot / 2; i += kThreads)
+    const int i = threadIdx.x;
+    if (i < p.rot / 2)
         s_turn[i] = p.freq64 ? turn_fraction(static_cast<const double*>(p.freq)[i])
                              : turn_fraction(static_cast<const float*>(p.freq)[i]);
 }
@@ -178,7 +188,7 @@ __device__ __forceinline__ void st16(char* p, const uint4& v, bool stream) {
 template <int D, bool INTERLEAVED>
 __device__ __forceinline__ void query_part(const Append8Params& p, int cta, unsigned long long* s_turn) {
     const Place<D, INTERLEAVED> at(p.rot);
-    const int t = cta / p.q_splits * at.ROWS + at.row;
+    const int t = cta / p.q_splits * kWindow + at.row;
     const int h0 = cta % p.q_splits * p.q_hpc, h1 = min(p.H, h0 + p.q_hpc);
     load_turns(p, s_turn);
     __syncthreads();
@@ -213,21 +223,22 @@ __device__ __forceinline__ void query_part(const Append8Params& p, int cta, unsi
 }
 
 template <int D, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads, 3) append8_kernel(const __grid_constant__ Append8Params p) {
+__global__ void __launch_bounds__(4 * D, 1024 / (4 * D)) append8_kernel(const __grid_constant__ Append8Params p) {
     using P = Place<D, INTERLEAVED>;
-    constexpr int UPR = P::UPR, ROWS = P::ROWS;
+    constexpr int UPR = P::UPR, THREADS = P::THREADS;
+    static_assert(THREADS == 4 * D && THREADS >= 4 * kWindow, "a thread for each slot that is looked at first");
     __shared__ unsigned long long s_turn[D / 2];
-    __shared__ int s_amax[kHeads][kWindow];     // by run, named by its first token's place in the window
-    __shared__ float s_scale[kHeads][kWindow];
-    __shared__ float s_ratio[kHeads][kWindow];  // before / now of the rows already there, 1: as they are
-    __shared__ int s_slot[kWindow];
-    __shared__ unsigned s_lead;
+    __shared__ int s_amax[kMaxHeads][kWindow];     // by run, named by its first token's place in the window
+    __shared__ float s_scale[kMaxHeads][kWindow];
+    __shared__ float s_ratio[kMaxHeads][kWindow];  // before / now of the rows already there, 1: as they are
+    __shared__ int s_slot[2 * kWindow];         // of the window's tokens and as many behind it, -1: none
+    __shared__ unsigned s_lead[2];              // the window's tokens that begin runs
     __shared__ int s_end;
     if (blockIdx.x >= 2 * p.kv_ctas) {
         query_part<D, INTERLEAVED>(p, (int)(blockIdx.x - 2 * p.kv_ctas), s_turn);
         return;
     }
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int tid = threadIdx.x;
     const int side = blockIdx.x >= p.kv_ctas;  // 0: K, 1: V
     const unsigned cta = blockIdx.x - (side ? p.kv_ctas : 0u);
     const int window = (int)(cta / (unsigned)p.splits), split = (int)(cta % (unsigned)p.splits);
@@ -236,53 +247,53 @@ __global__ void __launch_bounds__(kThreads, 3) append8_kernel(const __grid_const
     const int bmask = (1 << p.block_shift) - 1;
     const P at(side == 0 ? p.rot : 0);
 
-    // rows t0 + base + row of all heads: the first ones asked for before their slots are known
-    uint4 x[kHeads], y[kHeads];
-    auto fetch = [&](int t) {
-#pragma unroll
-        for (int h = 0; h < kHeads; ++h)
-            if (h < nh && t < p.T) {
-                const char* src = p.in[side] + t * p.it[side] + (h0 + h) * p.ih[side];
-                x[h] = ld16(src + at.off_a * 2);
-                y[h] = ld16(src + at.off_b * 2);
-            }
-    };
-    fetch(t0 + at.row);
-    if (tid < 32) {  // which of the window's tokens begin runs
-        const int t = t0 + lane;
-        bool lead = false;
+    if (tid < 2 * kWindow) {
+        const int t = t0 + tid;
         int s = -1;
+        bool lead = false;
         if (t < p.T) {
             s = __ldg(p.slots + t);
             const int before = t > 0 ? __ldg(p.slots + t - 1) : -2;
             if (s >= p.n_slots) {
-                if (side == 0 && split == 0) atomicOr(p.status, 1u << kStatusDeviceData);
+                if (side == 0 && split == 0 && tid < kWindow) atomicOr(p.status, 1u << kStatusDeviceData);
                 s = -1;
             }
             lead = s >= 0 && ((s & bmask) == 0 || before != s - 1 || t == 0);
         }
-        s_slot[lane] = s;
+        s_slot[tid] = s;
         const unsigned m = __ballot_sync(0xffffffffu, lead);
-        if (lane == 0) {
-            s_lead = m;
-            s_end = p.T;
-        }
+        if ((tid & 31) == 0 && tid < kWindow) s_lead[tid / 32] = m;
     }
-    for (int i = tid; i < kHeads * kWindow; i += kThreads) (&s_amax[0][0])[i] = 0;
+    for (int i = tid; i < kMaxHeads * kWindow; i += THREADS) (&s_amax[0][0])[i] = 0;
+    if (tid == 0) s_end = p.T;
     if (side == 0 && p.rot > 0) load_turns(p, s_turn);
     __syncthreads();
-    const unsigned lead = s_lead;
-    if (lead == 0u) return;  // the tokens here belong to a run that began before, or to none
-    const int first = t0 + __ffs(lead) - 1, last_lead = t0 + 31 - __clz(lead);
+    const unsigned long long lead = s_lead[0] | (unsigned long long)s_lead[1] << 32;
+    if (lead == 0ull) return;  // the tokens here belong to a run that began before, or to none
+    const int first = t0 + __ffsll((long long)lead) - 1, last_lead = t0 + 63 - __clzll((long long)lead);
+
+    // token t's row of heads h, h + 1, ..
+    uint4 x[kHeads], y[kHeads];
+    auto fetch = [&](int t, int h) {
+        const char* src = p.in[side] + t * p.it[side] + (h0 + h) * p.ih[side];
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i)
+            if (h + i < nh && t < p.T) {
+                x[i] = ld16(src + i * p.ih[side] + at.off_a * 2);
+                y[i] = ld16(src + i * p.ih[side] + at.off_b * 2);
+            }
+    };
+    fetch(first + at.row, 0);
     int end = last_lead + 1;
     {  // the end of the last run: its first token that does not follow on
         const int s0 = s_slot[last_lead - t0];
         const int room = bmask + 1 - (s0 & bmask);  // rows of the block from the run's first on
         if (room > 1) {
-            for (int i = 1 + tid; i <= room; i += kThreads) {
+            for (int i = 1 + tid; i <= room; i += THREADS) {
                 const int t = last_lead + i;
                 if (t >= p.T) break;
-                if (i == room || __ldg(p.slots + t) != s0 + i) {
+                const int s = t - t0 < 2 * kWindow ? s_slot[t - t0] : __ldg(p.slots + t);
+                if (i == room || s != s0 + i) {
                     atomicMin(&s_end, t);
                     break;
                 }
@@ -293,41 +304,54 @@ __global__ void __launch_bounds__(kThreads, 3) append8_kernel(const __grid_const
     }
     // the run of token t: the last of the window's runs to begin at or before it
     auto run_of = [&](int t) {
-        const int i = min(t - t0, 31);
-        return 31 - __clz(lead & (0xffffffffu >> (31 - i)));
+        const int i = min(t - t0, 63);
+        return 63 - __clzll((long long)(lead & (~0ull >> (63 - i))));
     };
     // whether token t belongs to one of the window's runs
-    auto in_run = [&](int t) { return t >= first && t < end && (t - t0 >= kWindow || s_slot[t - t0] >= 0); };
+    auto in_run = [&](int t) { return t < end && (t - t0 >= kWindow || s_slot[t - t0] >= 0); };
 
     Turn<INTERLEAVED> w;
-    const int passes = (end - t0 + ROWS - 1) / ROWS;
+    bool bad = false;  // an infinity or NaN among the values
+    const int passes = (end - first + kWindow - 1) / kWindow;
     for (int pass = 0; pass < passes; ++pass) {  // the largest magnitudes
-        const int t = t0 + pass * ROWS + at.row;
+        const int t = first + pass * kWindow + at.row;
         const bool in = in_run(t);
-        if (pass > 0) fetch(t);
+        const int run = run_of(t);
         if (in) at.angles(p, s_turn, t, w);
+#pragma unroll 1
+        for (int h = 0; h < nh; h += kHeads) {
+            if (pass + h > 0) fetch(t, h);
 #pragma unroll
-        for (int h = 0; h < kHeads; ++h)
-            if (h < nh) {
-                float top = 0.f;
-                if (in) {
+            for (int i = 0; i < kHeads; ++i) {
+                unsigned top = 0u;  // of the bits: as numbers, in the same order
+                if (in && h + i < nh) {
                     float a[8], c[8];
-                    unpack8(x[h], a);
-                    unpack8(y[h], c);
+                    unpack8(x[i], a);
+                    unpack8(y[i], c);
                     if (at.turns) w.rotate(a, c);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) top = fmaxf(top, fmaxf(finite_abs(a[e]), finite_abs(c[e])));
+                    for (int e = 0; e < 8; ++e) top = max(top, max(abs_bits(a[e]), abs_bits(c[e])));
+                    if (top >= kInfBits) {
+                        bad = true;
+                        top = 0u;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            if (abs_bits(a[e]) < kInfBits) top = max(top, abs_bits(a[e]));
+                            if (abs_bits(c[e]) < kInfBits) top = max(top, abs_bits(c[e]));
+                        }
+                    }
                 }
 #pragma unroll
-                for (int o = UPR / 2; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                if (in && at.j == 0) atomicMax(&s_amax[h][run_of(t)], __float_as_int(top));
+                for (int o = UPR / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                if (in && at.j == 0 && h + i < nh) atomicMax(&s_amax[h + i][run], (int)top);
             }
+        }
     }
-    __syncthreads();
+    const bool any_bad = __syncthreads_or(bad) != 0;
     bool grew = false;
-    for (int k = tid; k < nh * kWindow; k += kThreads) {  // the scales
+    for (int k = tid; k < nh * kWindow; k += THREADS) {  // the scales
         const int h = k / kWindow, i = k % kWindow;
-        if (!(lead >> i & 1u)) continue;
+        if (!(lead >> i & 1ull)) continue;
         const int s = s_slot[i];
         const int per_page = 1 << (p.page_shift - p.block_shift);
         float* scale = p.scale[side] + ((long long)(s >> p.page_shift) * p.H_kv + h0 + h) * per_page +
@@ -347,46 +371,48 @@ __global__ void __launch_bounds__(kThreads, 3) append8_kernel(const __grid_const
         *scale = now;
     }
     const bool any_grew = __syncthreads_or(grew) != 0;
-    for (int pass = passes - 1; pass >= 0; --pass) {  // the codes; the last pass's rows and angles are at hand
-        const int t = t0 + pass * ROWS + at.row;
+    for (int pass = passes - 1; pass >= 0; --pass) {  // the codes; the last pass's angles and last heads are at hand
+        const int t = first + pass * kWindow + at.row;
         if (!in_run(t)) continue;
-        if (pass != passes - 1) {
-            fetch(t);
-            at.angles(p, s_turn, t, w);
-        }
+        if (pass != passes - 1) at.angles(p, s_turn, t, w);
         const int run = run_of(t);
         const int s = s_slot[run] + (t - t0 - run);  // a run's slots follow one another
+#pragma unroll 1
+        for (int h = (nh - 1) / kHeads * kHeads; h >= 0; h -= kHeads) {
+            if (pass != passes - 1 || h + kHeads < nh) fetch(t, h);
 #pragma unroll
-        for (int h = 0; h < kHeads; ++h)
-            if (h < nh) {
-                float a[8], c[8];
-                unpack8(x[h], a);
-                unpack8(y[h], c);
-                if (at.turns) w.rotate(a, c);
-                const float now = s_scale[h][run];
-                uint2 ca, cc;
-                if (is_pow2(now)) {
-                    const float inv = 1.f / now;
-                    ca = make_uint2(codes4(a[0], a[1], a[2], a[3], inv), codes4(a[4], a[5], a[6], a[7], inv));
-                    cc = make_uint2(codes4(c[0], c[1], c[2], c[3], inv), codes4(c[4], c[5], c[6], c[7], inv));
-                } else {  // a scale that another writer left
-                    ca = make_uint2(codes4_div(a[0], a[1], a[2], a[3], now), codes4_div(a[4], a[5], a[6], a[7], now));
-                    cc = make_uint2(codes4_div(c[0], c[1], c[2], c[3], now), codes4_div(c[4], c[5], c[6], c[7], now));
+            for (int i = 0; i < kHeads; ++i)
+                if (h + i < nh) {
+                    float a[8], c[8];
+                    unpack8(x[i], a);
+                    unpack8(y[i], c);
+                    if (at.turns) w.rotate(a, c);
+                    const float now = s_scale[h + i][run];
+                    uint2 ca, cc;
+                    if (!any_bad && is_pow2(now)) {
+                        // 1 / now: its exponent negated (now is 2^-126 to 2^126; above, the quotient would be subnormal)
+                        const float inv = __uint_as_float(0x7f000000u - __float_as_uint(now));
+                        ca = codes8(a, inv);
+                        cc = codes8(c, inv);
+                    } else {
+                        ca = codes8_careful(a, now);
+                        cc = codes8_careful(c, now);
+                    }
+                    uint8_t* dst = p.codes[side] + ((long long)s * p.H_kv + h0 + h + i) * D;
+                    *reinterpret_cast<uint2*>(dst + at.off_a) = ca;
+                    *reinterpret_cast<uint2*>(dst + at.off_b) = cc;
                 }
-                uint8_t* dst = p.codes[side] + ((long long)s * p.H_kv + h0 + h) * D;
-                *reinterpret_cast<uint2*>(dst + at.off_a) = ca;
-                *reinterpret_cast<uint2*>(dst + at.off_b) = cc;
-            }
+        }
     }
     if (!any_grew) return;
-    for (unsigned left = lead; left != 0u; left &= left - 1) {  // rows that were there, under a larger scale now
-        const int i = __ffs(left) - 1;
+    for (unsigned long long left = lead; left != 0ull; left &= left - 1) {  // rows that were there, under a larger scale now
+        const int i = __ffsll((long long)left) - 1;
         const int s = s_slot[i], held = s & bmask;
         if (held == 0) continue;
         for (int h = 0; h < nh; ++h) {
             const float ratio = s_ratio[h][i];
             if (ratio == 1.f) continue;
-            for (int r = at.row; r < held; r += ROWS) {
+            for (int r = at.row; r < held; r += kWindow) {
                 uint4* word4 = reinterpret_cast<uint4*>(p.codes[side] + ((long long)(s - held + r) * p.H_kv + h0 + h) * D + at.j * 16);
                 uint4 old = *word4;
                 uint32_t* word = reinterpret_cast<uint32_t*>(&old);
@@ -419,7 +445,7 @@ constexpr int kReadRows = 8;  // rows of a CTA
 // Bound by memory: a code is read, two bytes (or four) written.  A CTA takes 8 rows of K and V: their
 // requests and cache rows are looked up once, then each thread moves 16 codes at a time.
 template <int EB>
-__global__ void __launch_bounds__(kThreads) read8_kernel(const __grid_constant__ Read8Params p) {
+__global__ void __launch_bounds__(kReadThreads) read8_kernel(const __grid_constant__ Read8Params p) {
     __shared__ int s_row[kReadRows];  // cache row, -1: left as it is, -2: zeros
     const int tid = threadIdx.x;
     const int t0 = blockIdx.x * kReadRows;
@@ -454,7 +480,7 @@ __global__ void __launch_bounds__(kThreads) read8_kernel(const __grid_constant__
     __syncthreads();
     const int units = p.H_kv * (p.d / 16);  // pieces of 16 codes in a row
     const int per_page = 1 << (p.page_shift - p.block_shift);
-    for (int x = tid; x < kReadRows * units; x += kThreads) {
+    for (int x = tid; x < kReadRows * units; x += kReadThreads) {
         const int i = x / units, u = x - i * units;
         const int row = s_row[i];
         if (row == -1) continue;
@@ -558,18 +584,17 @@ attn_status_t attn_paged_append_fp8(const void* q, void* q_out, const void* k, c
     p.page_shift = shift_of(page_size);
     p.block_shift = shift_of(block);
     p.amplitude = amplitude;
-    // CTAs: as few heads to each as it takes to have two on every SM (q: its part of the bytes of them)
+    // CTAs: as many heads to each, up to 8 (q: 64), as leave one of K or V, and two of q, to every SM
     const int want = 2 * sm_count;
     const long long windows = ((long long)T + kWindow - 1) / kWindow;
-    p.hpc = H_kv < kHeads ? H_kv : kHeads;
-    while (p.hpc > 1 && 2 * windows * ((H_kv + p.hpc - 1) / p.hpc) < want) p.hpc = (p.hpc + 1) / 2;
+    p.hpc = H_kv < kMaxHeads ? H_kv : kMaxHeads;
+    while (p.hpc > 1 && 2 * windows * ((H_kv + p.hpc - 1) / p.hpc) < sm_count) p.hpc = (p.hpc + 1) / 2;
     p.splits = (H_kv + p.hpc - 1) / p.hpc;
     long long ctas = 2 * windows * p.splits, q_ctas = 0;
     if (ctas > 0x3fffffffLL) return ATTN_ERR_INVALID_ARG;
     p.kv_ctas = (unsigned)(windows * p.splits);
     if (q) {
-        const int rows = kThreads * 16 / d;
-        const long long tiles = ((long long)T + rows - 1) / rows;
+        const long long tiles = windows;
         p.q = static_cast<const char*>(q);
         p.q_out = static_cast<char*>(q_out);
         p.qt = strides[0] * 2;
@@ -577,7 +602,7 @@ attn_status_t attn_paged_append_fp8(const void* q, void* q_out, const void* k, c
         p.qot = strides[2] * 2;
         p.qoh = strides[3] * 2;
         p.H = H;
-        p.q_hpc = H < 16 ? H : 16;
+        p.q_hpc = H < 64 ? H : 64;
         while (p.q_hpc > 1 && tiles * ((H + p.q_hpc - 1) / p.q_hpc) < want) p.q_hpc = (p.q_hpc + 1) / 2;
         p.q_splits = (H + p.q_hpc - 1) / p.q_hpc;
         p.q_stream = (long long)T * H * d * 2 > kStreamBytes;
@@ -587,14 +612,14 @@ attn_status_t attn_paged_append_fp8(const void* q, void* q_out, const void* k, c
     const unsigned grid = (unsigned)(ctas + q_ctas);
     if (d == 128) {
         if (interleaved)
-            append8_kernel<128, true><<<grid, kThreads, 0, cs>>>(p);
+            append8_kernel<128, true><<<grid, 4 * d, 0, cs>>>(p);
         else
-            append8_kernel<128, false><<<grid, kThreads, 0, cs>>>(p);
+            append8_kernel<128, false><<<grid, 4 * d, 0, cs>>>(p);
     } else {
         if (interleaved)
-            append8_kernel<64, true><<<grid, kThreads, 0, cs>>>(p);
+            append8_kernel<64, true><<<grid, 4 * d, 0, cs>>>(p);
         else
-            append8_kernel<64, false><<<grid, kThreads, 0, cs>>>(p);
+            append8_kernel<64, false><<<grid, 4 * d, 0, cs>>>(p);
     }
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
@@ -641,9 +666,9 @@ attn_status_t attn_paged_read_fp8(const void* k_cache, const void* v_cache, cons
     const unsigned blocks = (unsigned)((total_k + kReadRows - 1) / kReadRows);
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (elem_bytes == 2)
-        read8_kernel<2><<<blocks, kThreads, 0, cs>>>(p);
+        read8_kernel<2><<<blocks, kReadThreads, 0, cs>>>(p);
     else
-        read8_kernel<4><<<blocks, kThreads, 0, cs>>>(p);
+        read8_kernel<4><<<blocks, kReadThreads, 0, cs>>>(p);
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
