@@ -29,7 +29,7 @@
 // A CTA, 384 threads:
 //   warp 0    TMA producer: the units, their pages, K and V tiles into a ring, in the order
 //             K of step n + 1, V of step n.
-//   warp 1    MMA issuer (one lane); the warp clears V rows past the request's keys.
+//   warp 1    MMA issuer (one lane); the warp clears rows past the request's keys.
 //   warps 2-9 softmax and epilogue: thread = key, then thread = channel.
 //   warp 10   query rows as e4m3 pairs.
 //   warp 11   the scales of the steps' keys.
@@ -83,7 +83,7 @@ struct Cfg {
     static constexpr int OFF_SUM = OFF_EXCH + 8 * R * 8;              // float [8][R]
     static constexpr int OFF_NAN = OFF_SUM + 8 * R * 4;               // int [D]: first row that sees a NaN in this channel
     static constexpr int OFF_BAR = OFF_NAN + D * 4;
-    static constexpr int N_BARS = 2 * NST + 14 + 2 * kQN;
+    static constexpr int N_BARS = 2 * NST + 15 + 2 * kQN;
     static constexpr int OFF_UQ = OFF_BAR + 8 * N_BARS;
     static constexpr int OFF_MISC = OFF_UQ + 4 * kQN * kUnitInts;
     static constexpr int SMEM_BYTES = OFF_MISC + 144 + 1024;
@@ -99,7 +99,7 @@ struct Bars {
     uint64_t* sc_full;   // [2] scales of a step
     uint64_t* sc_empty;  // [2] eight softmax warps
     uint64_t* s_full;    // [2]
-    uint64_t* p_full;    // 256 arrivals per step
+    uint64_t* p_full;    // [2] 256 arrivals per step
     uint64_t* o_full;    // [2] PV products of a step, and the issuing lane
     uint64_t* done;
     uint64_t* uq_full;   // [kQN]
@@ -153,8 +153,9 @@ __device__ __forceinline__ long long work_of(const Paged8Params& p, const Extent
 
 // a / b (both positive, the quotient an int), by a 32-bit division where that will do: the 64-bit one takes a noticeable
 // part of a short call.
+__device__ __noinline__ long long long_quotient(long long a, long long b) { return a / b; }
 __device__ __forceinline__ int quotient(long long a, long long b) {
-    return a < 0x7fffffffLL && b < 0x7fffffffLL ? (int)((unsigned)a / (unsigned)b) : (int)(a / b);
+    return a < 0x7fffffffLL && b < 0x7fffffffLL ? (int)((unsigned)a / (unsigned)b) : (int)long_quotient(a, b);
 }
 
 __device__ __forceinline__ void publish(volatile int* q, const Unit& u) {
@@ -174,9 +175,17 @@ __device__ __forceinline__ int last_key(const Paged8Params& p, const Unit& u, in
     return (int)min((long long)u.kv_len - 1, (long long)u.kv_len - u.q_len + x / p.G);
 }
 
+// wait_bar (ptx.cuh) with all but its first look out of line: this kernel waits in many places, and what is executed
+// has to fit the instruction cache.
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* status) {
+    return wait_bar(bar, parity, abort_flag, status);
+}
+__device__ __forceinline__ bool wait_short(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* status) {
+    return bar_try_wait(bar, parity) || wait_on(bar, parity, abort_flag, status);
+}
 // A whole warp's wait: every lane gets the same answer.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* status) {
-    return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, status));
+    return __all_sync(0xffffffffu, wait_short(bar, parity, abort_flag, status));
 }
 
 __device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
@@ -265,128 +274,123 @@ __device__ void producer_role(const Paged8Params& p, uint8_t* smem, const Bars& 
     // lane i: extent of request base + i (that of the first is known: the loads are not waited for)
     int base = r;
     Extent mine = extent(p, min(base + lane, p.B - 1));
-    int prev_rows[2] = {0, 0}, prev_nt = 0;
-
-    // tiles of one step into the ring: box x of the step in lane x % 32, register x / 32
-    auto load_tiles = [&](const CUtensorMap* map, const int* row_of, int nt, int kvh) {
-        for (int t = 0; ok && t < nt; ++t) {
+    int prev_rows[2] = {0, 0}, prev_nt = 0, prev_kvh = 0;  // the step whose V tiles are due
+    Unit u{};
+    int s = 0, id[2] = {-1, -1};
+    auto page_ids = [&](int from, int* ids) {  // of the boxes of a step (box x in lane x % 32, register x / 32)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int x = k * 32 + lane;
+            const long long key = (long long)(u.tile0 + from) * 128 + (long long)x * rows;
+            ids[k] = -1;
+            if (x < min(C::SB, u.nt - from) * per_tile && key < u.kv_len)
+                ids[k] = __ldg(p.block_table + (size_t)u.r * p.max_pages + (key >> p.page_shift));
+        }
+    };
+    while (ok) {
+        if (s >= u.nt) {  // the next unit of the cut
+            s = 0;
+            u.r = -1;
+            u.nt = 0;
+            while (w < w1) {
+                const long long work = work_of(p, e);
+                if (w - start >= work) {
+                    start += work;
+                    if (++r >= base + 32) {
+                        base = r;
+                        mine = extent(p, min(base + lane, p.B - 1));
+                    }
+                    e.q_start = __shfl_sync(0xffffffffu, mine.q_start, r - base);
+                    e.q_len = __shfl_sync(0xffffffffu, mine.q_len, r - base);
+                    e.kv_len = __shfl_sync(0xffffffffu, mine.kv_len, r - base);
+                    continue;
+                }
+                const int nb = key_tiles(e), nqt = row_tiles(p, e), size = nb + kUnitCost;
+                const long long off = w - start;
+                const int unit = quotient(off, size);
+                int at = (int)(off - (long long)unit * size);  // place in the unit: kUnitCost, then its tiles
+                if (at < kUnitCost) {
+                    w += kUnitCost - at;
+                    at = kUnitCost;
+                    if (w >= w1) break;
+                }
+                const int tile = at - kUnitCost;
+                const int n = (int)min((long long)(nb - tile), w1 - w);
+                u.r = r;
+                u.kvh = unit / nqt;
+                u.q_start = e.q_start;
+                u.q_len = e.q_len;
+                u.kv_len = e.kv_len;
+                u.row0 = (unit - u.kvh * nqt) * R;
+                u.nr = min(R, e.q_len * p.G - u.row0);
+                u.tile0 = tile;
+                const long long seen = (last_key(p, u, u.row0 + u.nr - 1) + 128LL) / 128;  // tiles that the last row sees
+                u.nt = (int)max(0LL, min((long long)n, seen - tile));
+                u.slot = n == nb ? -1 : 2 * (int)blockIdx.x + (w - tile <= w0 ? 0 : 1);
+                if (tile == 0 && n < nb && lane == 0) {  // for the merge: the unit goes on in the CTAs after this one
+                    int4* cut = p.cuts + 2 * blockIdx.x;
+                    cut[0] = make_int4(quotient(w + nb - 1, share), u.slot, u.nr, u.kvh);
+                    cut[1] = make_int4(u.q_start, u.row0, 0, 0);
+                }
+                w += n;
+                break;
+            }
+            page_ids(0, id);
+            if (lane == 0) {
+                const int slot = pub % kQN;
+                if (pub >= kQN) ok = wait_short(&b.uq_empty[slot], (uint32_t)((pub / kQN - 1) & 1), abort_flag, p.status);
+                if (ok) {
+                    publish(uq + slot * kUnitInts, u);
+                    bar_arrive(&b.uq_full[slot]);
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            ++pub;
+        }
+        const int nt = min(C::SB, u.nt - s);  // 0: a unit without visible keys, or the end: only V tiles may be due
+        int row_of[2], next_id[2];
+        page_ids(s + nt, next_id);            // loaded a step before they are used
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int x = k * 32 + lane;
+            const long long key = (long long)(u.tile0 + s) * 128 + (long long)x * rows;
+            row_of[k] = p.kv_rows;
+            if (id[k] >= 0 && id[k] < p.num_pages)
+                row_of[k] = (id[k] << p.page_shift) + (int)(key & ((1 << p.page_shift) - 1));
+            else if (x < nt * per_tile && key < u.kv_len)
+                atomicOr(p.status, 1u << kStatusDeviceData);
+            id[k] = next_id[k];
+        }
+        // K of this step, then V of the one before
+#pragma unroll 1
+        for (int t = 0; t < nt + prev_nt; ++t) {
+            const bool is_k = t < nt;
             const int slot = kv_idx % C::NST, round = kv_idx / C::NST;
             if (lane == 0) {
-                if (round > 0) ok = wait_bar(&b.kv_empty[slot], (uint32_t)((round - 1) & 1), abort_flag, p.status);
+                if (round > 0) ok = wait_short(&b.kv_empty[slot], (uint32_t)((round - 1) & 1), abort_flag, p.status);
                 if (ok) bar_arrive_expect_tx(&b.kv_full[slot], C::TILE);
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) break;
-            const int first = t * per_tile;  // per_tile divides 32: the tile's boxes lie in one register
+            const int first = (is_k ? t : t - nt) * per_tile;  // per_tile divides 32: the tile's boxes lie in one register
             const int i = lane - (first & 31);
+            const int* from = is_k ? row_of : prev_rows;
             if (i >= 0 && i < per_tile)
-                tma_load_3d(smem + C::OFF_KV + slot * C::TILE + i * rows * D, map, &b.kv_full[slot], 0, kvh,
-                            first < 32 ? row_of[0] : row_of[1]);
+                tma_load_3d(smem + C::OFF_KV + slot * C::TILE + i * rows * D, is_k ? &p.tm_k : &p.tm_v, &b.kv_full[slot], 0,
+                            is_k ? u.kvh : prev_kvh, first < 32 ? from[0] : from[1]);
             ++kv_idx;
         }
-    };
-    int prev_kvh = 0;
-    for (;;) {
-        Unit u;
-        u.r = -1;
-        u.nt = 0;
-        while (w < w1) {
-            const long long work = work_of(p, e);
-            if (w - start >= work) {
-                start += work;
-                if (++r >= base + 32) {
-                    base = r;
-                    mine = extent(p, min(base + lane, p.B - 1));
-                }
-                e.q_start = __shfl_sync(0xffffffffu, mine.q_start, r - base);
-                e.q_len = __shfl_sync(0xffffffffu, mine.q_len, r - base);
-                e.kv_len = __shfl_sync(0xffffffffu, mine.kv_len, r - base);
-                continue;
-            }
-            const int nb = key_tiles(e), nqt = row_tiles(p, e), size = nb + kUnitCost;
-            const long long off = w - start;
-            const int unit = quotient(off, size);
-            int at = (int)(off - (long long)unit * size);  // place in the unit: kUnitCost, then its tiles
-            if (at < kUnitCost) {
-                w += kUnitCost - at;
-                at = kUnitCost;
-                if (w >= w1) break;
-            }
-            const int tile = at - kUnitCost;
-            const int n = (int)min((long long)(nb - tile), w1 - w);
-            u.r = r;
-            u.kvh = unit / nqt;
-            u.q_start = e.q_start;
-            u.q_len = e.q_len;
-            u.kv_len = e.kv_len;
-            u.row0 = (unit - u.kvh * nqt) * R;
-            u.nr = min(R, e.q_len * p.G - u.row0);
-            u.tile0 = tile;
-            const long long seen = (last_key(p, u, u.row0 + u.nr - 1) + 128LL) / 128;  // tiles that the last row sees
-            u.nt = (int)max(0LL, min((long long)n, seen - tile));
-            u.slot = n == nb ? -1 : 2 * (int)blockIdx.x + (w - tile <= w0 ? 0 : 1);
-            if (tile == 0 && n < nb && lane == 0) {  // for the merge: the unit goes on in the CTAs after this one
-                int4* cut = p.cuts + 2 * blockIdx.x;
-                cut[0] = make_int4(quotient(w + nb - 1, share), u.slot, u.nr, u.kvh);
-                cut[1] = make_int4(u.q_start, u.row0, 0, 0);
-            }
-            w += n;
-            break;
-        }
-        if (lane == 0) {
-            const int slot = pub % kQN;
-            if (pub >= kQN) ok = wait_bar(&b.uq_empty[slot], (uint32_t)((pub / kQN - 1) & 1), abort_flag, p.status);
-            if (ok) {
-                publish(uq + slot * kUnitInts, u);
-                bar_arrive(&b.uq_full[slot]);
-            }
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok || u.r < 0) break;
-        ++pub;
-        if (u.nt == 0) {  // as in mma_role: no step follows that the pending values could come after
-            load_tiles(&p.tm_v, prev_rows, prev_nt, prev_kvh);
-            prev_nt = 0;
-        }
-        auto page_ids = [&](int s, int* id) {  // of the boxes of step s: loaded a step before they are used
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int x = k * 32 + lane;
-                const long long key = (long long)(u.tile0 + s) * 128 + (long long)x * rows;
-                id[k] = -1;
-                if (x < min(C::SB, u.nt - s) * per_tile && key < u.kv_len)
-                    id[k] = __ldg(p.block_table + (size_t)u.r * p.max_pages + (key >> p.page_shift));
-            }
-        };
-        int id[2], next_id[2];
-        if (u.nt > 0) page_ids(0, id);
-        for (int s = 0; ok && s < u.nt; s += C::SB) {
-            const int nt = min(C::SB, u.nt - s);
-            page_ids(s + C::SB, next_id);
-            int row_of[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int x = k * 32 + lane;
-                const long long key = (long long)(u.tile0 + s) * 128 + (long long)x * rows;
-                row_of[k] = p.kv_rows;
-                if (id[k] >= 0 && id[k] < p.num_pages)
-                    row_of[k] = (id[k] << p.page_shift) + (int)(key & ((1 << p.page_shift) - 1));
-                else if (x < nt * per_tile && key < u.kv_len)
-                    atomicOr(p.status, 1u << kStatusDeviceData);
-                id[k] = next_id[k];
-            }
-            load_tiles(&p.tm_k, row_of, nt, u.kvh);
-            load_tiles(&p.tm_v, prev_rows, prev_nt, prev_kvh);
-            prev_rows[0] = row_of[0];
-            prev_rows[1] = row_of[1];
-            prev_nt = nt;
-            prev_kvh = u.kvh;
-        }
-        if (!ok) break;
+        prev_rows[0] = row_of[0];
+        prev_rows[1] = row_of[1];
+        prev_nt = nt;
+        prev_kvh = u.kvh;
+        s += nt;
+        if (u.r < 0) break;
     }
-    load_tiles(&p.tm_v, prev_rows, prev_nt, prev_kvh);
     // every copy that this warp started must land before the CTA exits
     if (lane == 0)
+#pragma unroll 1
         for (int idx = kv_idx - C::NST > 0 ? kv_idx - C::NST : 0; idx < kv_idx; ++idx)
             drain_wait(&b.kv_full[idx % C::NST], (uint32_t)((idx / C::NST) & 1), p.status);
     __syncwarp();
@@ -394,45 +398,99 @@ __device__ void producer_role(const Paged8Params& p, uint8_t* smem, const Bars& 
 
 // ---------------------------------------------------------------- MMA issuer (whole warp, lane 0 issues)
 
+// Rows of a tile past the request's keys may hold anything: cleared, since a NaN there would reach every row of the
+// second product (as 0 * NaN), and the softmax masks scores by adding -inf to them.
+template <int D>
+__device__ __forceinline__ void clear_rows(uint32_t tile, int left, int lane) {
+#pragma unroll 1
+    for (int x = left * (D / 16) + lane; x < 128 * (D / 16); x += 32) st_zero16(tile + (uint32_t)x * 16u);
+    fence_async_smem();
+    __syncwarp();
+}
+
+// The scores of one tile.
+template <int D, int R>
+__device__ __forceinline__ void product_s(uint32_t d, uint64_t k, uint64_t q) {
+    constexpr uint32_t ID = idesc_make(128, 2 * R, 0u, false, false);
+    if (D == 128) {
+        mma4_ss<2, 4, 6, 2, 4, 6, true>(d, k, q, ID, 0u);
+    } else {
+        mma_f8_ss(d, k, q, ID, 0u);
+        mma_f8_ss(d, k + 2, q + 2, ID, 1u);
+    }
+}
+
+// One tile's part of O^T: four blocks of 32 keys.
+template <int D, int R>
+__device__ __forceinline__ void product_pv(uint32_t o, uint64_t v, uint64_t p, bool accumulate) {
+    constexpr uint32_t ID = idesc_make(D, Cfg<D, R>::NPV, 0u, true, false);
+    constexpr int VS = (32 * D) >> 4;  // 32 rows of V in descriptor units
+    mma4_ss<VS, 2 * VS, 3 * VS, 2, 4, 6, true>(o, v, p, ID, accumulate ? 1u : 0u);
+}
+
+// S^T of step n + 1, then O^T += V^T P^T of step n: the order of the ring.  (Two issuers, one for each product, were
+// slower: which tile of the ring is whose is known only in this order, and the waits for one another cost more than the
+// 300 to 500 cycles that a tile's few instructions, wait and commit take here.)
 template <int D, int R>
 __device__ void mma_role(const Paged8Params& p, uint8_t* smem, const Bars& b, volatile int* uq, volatile int* abort_flag,
                          uint32_t tmem, int lane) {
     using C = Cfg<D, R>;
-    constexpr uint32_t ID_S = idesc_make(128, C::NQ, 0u, false, false);
-    constexpr uint32_t ID_PV = idesc_make(D, C::NPV, 0u, true, false);
-    const uint32_t sbase = smem_u32(smem);
-    volatile int* s_nan = reinterpret_cast<volatile int*>(smem + C::OFF_NAN);
-    auto tile_addr = [&](int idx) { return sbase + C::OFF_KV + (uint32_t)((idx % C::NST) * C::TILE); };
-    int kv_idx = 0, units = 0;
+    const uint32_t sbase = smem_u32(smem), o = tmem + C::TM_O;
+    const uint64_t kv_desc = desc<D>(sbase + C::OFF_KV), p_desc = desc<128>(sbase + C::OFF_P);
+    int* s_nan = reinterpret_cast<int*>(smem + C::OFF_NAN);
+    int stage = 0, phase = 0, units = 0;
     uint32_t n = 0;  // steps issued
-    struct Step {
-        Unit u;
-        int s, nt;
-    } prev;
-    prev.nt = 0;
+    // the step whose second product is due: tiles, whether it is its unit's first, and what masks need of the unit
+    int prev_nt = 0, prev_first = 0, prev_tile0 = 0, prev_kv_len = 0, prev_q_len = 0, prev_row0 = 0, prev_last = 0;
 
-    // Rows of a tile past the request's keys may hold anything: cleared, since a NaN there would reach every row of the
-    // second product (as 0 * NaN), and the softmax masks scores by adding -inf to them.
-    auto clear_rows = [&](uint32_t tile, long long left) {
-        if (left >= 128) return;
-        for (int x = (int)left * (D / 16) + lane; x < 128 * (D / 16); x += 32) st_zero16(tile + (uint32_t)x * 16u);
-        fence_async_smem();
-        __syncwarp();
+    // Tiles [0, count) of the ring from here on, by one lane: issue(t, tile in descriptor units) for each.
+    auto tiles = [&](int count, auto issue) -> bool {
+        bool ok = true;
+        if (lane == 0) {
+            for (int t = 0; t < count; ++t) {
+                ok = wait_short(&b.kv_full[stage], (uint32_t)phase, abort_flag, p.status);
+                if (!ok) break;
+                tc_fence_after();
+                issue(t, (uint64_t)(stage * (C::TILE >> 4)));
+                tc_commit(&b.kv_empty[stage]);
+                if (++stage == C::NST) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        stage = __shfl_sync(0xffffffffu, stage, 0);
+        phase = __shfl_sync(0xffffffffu, phase, 0);
+        return __shfl_sync(0xffffffffu, ok, 0);
     };
-    auto product_pv = [&](uint32_t step) -> bool {  // of prev, step number `step`
-        const Unit& u = prev.u;
-        if (!warp_wait(b.p_full, step & 1u, abort_flag, p.status)) return false;
-        for (int t = 0; t < prev.nt; ++t, ++kv_idx) {
-            if (!warp_wait(&b.kv_full[kv_idx % C::NST], (uint32_t)((kv_idx / C::NST) & 1), abort_flag, p.status)) return false;
-            const int tile = u.tile0 + prev.s + t;
-            const int left = (int)min(128LL, (long long)u.kv_len - (long long)tile * 128);
-            const uint32_t v = tile_addr(kv_idx);
-            clear_rows(v, left);
-            if (p.causal && u.nr > 1 && tile * 128LL + left - 1 > last_key(p, u, u.row0)) {
+    auto next_stage = [&]() {
+        if (++stage == C::NST) {
+            stage = 0;
+            phase ^= 1;
+        }
+    };
+    auto second = [&](uint32_t step) -> bool {  // of the pending step, number `step`
+        const int nt = prev_nt;
+        const long long key0 = (long long)prev_tile0 * 128;
+        const int keys = (int)min((long long)nt * 128, prev_kv_len - key0);
+        // tiles without rows to clear (all but the request's last) and without keys that only some of the unit's rows see
+        const int whole = prev_last < prev_kv_len - 1 && key0 + keys - 1 > prev_last ? 0 : keys / 128;
+        const uint64_t p_step = p_desc + (uint64_t)((C::PBUF == 2 ? step & 1u : 0u) * (C::SB * C::PTILE >> 4));
+        if (!warp_wait(&b.p_full[step & 1u], (step >> 1) & 1u, abort_flag, p.status)) return false;
+        if (!tiles(whole, [&](int t, uint64_t tile) {
+                product_pv<D, R>(o, kv_desc + tile, p_step + (uint64_t)(t * (C::PTILE >> 4)), !prev_first || t > 0);
+            }))
+            return false;
+        for (int t = whole; t < nt; ++t) {
+            if (!warp_wait(&b.kv_full[stage], (uint32_t)phase, abort_flag, p.status)) return false;
+            const int left = min(128, keys - t * 128);
+            const uint32_t v = sbase + C::OFF_KV + (uint32_t)(stage * C::TILE);
+            if (left < 128) clear_rows<D>(v, left, lane);
+            if (key0 + t * 128 + left - 1 > prev_last) {
                 // Keys that only some of the rows see: a NaN among their values must not reach the others
                 // through 0 * NaN.  It is taken out and noted, by channel, for the rows from the first that sees it.
-                const long long pos0 = (long long)u.kv_len - u.q_len;
-                const int from = (int)max(0LL, min(128LL, last_key(p, u, u.row0) + 1LL - (long long)tile * 128));
+                const int from = (int)max(0LL, min(128LL, prev_last + 1LL - key0 - t * 128));
+#pragma unroll 1
                 for (int x = from * (D / 4) + lane; x < left * (D / 4); x += 32) {
                     const int key = x / (D / 4), word = x % (D / 4);  // stored word of the row, swizzled
                     const int chunk = (word >> 2) ^ (D == 128 ? key & 7 : (key >> 1) & 3);
@@ -445,9 +503,9 @@ __device__ void mma_role(const Paged8Params& p, uint8_t* smem, const Bars& b, vo
                         if (((c >> (8 * k)) & 0x7fu) == 0x7fu) {
                             keep &= ~(0xffu << (8 * k));
                             // token of the first row that sees the key
-                            const long long tok = (long long)tile * 128 + key - pos0;
-                            const int row = (int)max(0LL, tok * p.G - u.row0);
-                            atomicMin(const_cast<int*>(s_nan) + chunk * 16 + (word & 3) * 4 + k, row);
+                            const long long tok = key0 + t * 128 + key - ((long long)prev_kv_len - prev_q_len);
+                            const int row = (int)max(0LL, tok * p.G - prev_row0);
+                            atomicMin(s_nan + chunk * 16 + (word & 3) * 4 + k, row);
                         }
                     if (keep != c) st_u32(at, keep);
                 }
@@ -456,14 +514,10 @@ __device__ void mma_role(const Paged8Params& p, uint8_t* smem, const Bars& b, vo
             }
             if (lane == 0) {
                 tc_fence_after();
-                const uint32_t o = tmem + C::TM_O;
-                const uint64_t a = desc<D>(v), q = desc<128>(sbase + C::OFF_P + (uint32_t)(((C::PBUF == 2 ? step & 1u : 0u) * C::SB + t) * C::PTILE));
-                constexpr uint64_t VS = (32 * D) >> 4;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_f8_ss(o, a + k * VS, q + 2 * k, ID_PV, (prev.s > 0 || t > 0 || k > 0) ? 1u : 0u);
-                tc_commit(&b.kv_empty[kv_idx % C::NST]);
+                product_pv<D, R>(o, kv_desc + (uint64_t)(stage * (C::TILE >> 4)), p_step + (uint64_t)(t * (C::PTILE >> 4)), !prev_first || t > 0);
+                tc_commit(&b.kv_empty[stage]);
             }
+            next_stage();
         }
         __syncwarp();
         if (lane == 0) {
@@ -473,51 +527,70 @@ __device__ void mma_role(const Paged8Params& p, uint8_t* smem, const Bars& b, vo
         return true;
     };
 
-    for (int k = 0;; ++k) {
-        const int slot = k % kQN;
-        if (!warp_wait(&b.uq_full[slot], (uint32_t)((k / kQN) & 1), abort_flag, p.status)) return;
-        const Unit u = read_unit(uq + slot * kUnitInts);
-        __syncwarp();
-        if (lane == 0) bar_arrive(&b.uq_empty[slot]);
-        if (u.r < 0) break;
-        const int qb = units & 1;
-        if (!warp_wait(&b.q_full[qb], (uint32_t)((units >> 1) & 1), abort_flag, p.status)) return;
-        ++units;
-        const uint64_t q_desc = desc<D>(sbase + C::OFF_Q + (uint32_t)(qb * C::QBYTES));
-        if (u.nt == 0) {
-            // Nothing to compute.  The products of the step before must not wait for a later unit: its query rows
-            // would wait for the buffer that the unit of that step still holds.
-            if (prev.nt > 0 && !product_pv(n - 1u)) return;
-            prev.nt = 0;
-            if (lane == 0) bar_arrive(&b.q_empty[qb]);
+    Unit u{};
+    int s = 0, qb = 0, first_last = 0;  // next step of the unit; its query buffer; the last key that its first row sees
+    uint64_t q_desc = 0;
+    for (int k = 0;;) {
+        if (s >= u.nt) {
+            const int slot = k % kQN;
+            if (!warp_wait(&b.uq_full[slot], (uint32_t)((k / kQN) & 1), abort_flag, p.status)) return;
+            u = read_unit(uq + slot * kUnitInts);
+            __syncwarp();
+            if (lane == 0) bar_arrive(&b.uq_empty[slot]);
+            ++k;
+            s = 0;
+            qb = units & 1;
+            if (u.nt > 0) {
+                if (!warp_wait(&b.q_full[qb], (uint32_t)((units >> 1) & 1), abort_flag, p.status)) return;
+                ++units;
+                q_desc = desc<D>(sbase + C::OFF_Q + (uint32_t)(qb * C::QBYTES));
+                first_last = last_key(p, u, u.row0);
+            }
         }
-        for (int s = 0; s < u.nt; s += C::SB) {
-            const int nt = min(C::SB, u.nt - s);
-            for (int t = 0; t < nt; ++t, ++kv_idx) {
-                if (!warp_wait(&b.kv_full[kv_idx % C::NST], (uint32_t)((kv_idx / C::NST) & 1), abort_flag, p.status)) return;
-                clear_rows(tile_addr(kv_idx), (long long)u.kv_len - (long long)(u.tile0 + s + t) * 128);
+        const int nt = min(C::SB, u.nt - s);  // 0: a unit without visible keys, or the end
+        if (nt > 0) {
+            // (S's buffer is free: the softmax read step n - 2 before it let that step's second product go)
+            const uint32_t d = tmem + (n & 1u) * 64u;
+            const int keys = (int)min((long long)nt * 128, (long long)u.kv_len - (long long)(u.tile0 + s) * 128);
+            const int whole = keys / 128;  // tiles without rows to clear: all but the request's last
+            if (!tiles(whole, [&](int t, uint64_t tile) { product_s<D, R>(d + (uint32_t)(t * C::NQ), kv_desc + tile, q_desc); }))
+                return;
+            if (whole < nt) {
+                if (!warp_wait(&b.kv_full[stage], (uint32_t)phase, abort_flag, p.status)) return;
+                clear_rows<D>(sbase + C::OFF_KV + (uint32_t)(stage * C::TILE), keys - whole * 128, lane);
                 if (lane == 0) {
                     tc_fence_after();
-                    const uint32_t d = tmem + (n & 1u) * 64u + (uint32_t)(t * C::NQ);
-                    const uint64_t a = desc<D>(tile_addr(kv_idx));
-#pragma unroll
-                    for (int x = 0; x < D / 32; ++x) mma_f8_ss(d, a + 2 * x, q_desc + 2 * x, ID_S, x > 0 ? 1u : 0u);
-                    tc_commit(&b.kv_empty[kv_idx % C::NST]);
+                    product_s<D, R>(d + (uint32_t)(whole * C::NQ), kv_desc + (uint64_t)(stage * (C::TILE >> 4)), q_desc);
+                    tc_commit(&b.kv_empty[stage]);
                 }
+                next_stage();
             }
             if (lane == 0) {
                 tc_commit(&b.s_full[n & 1u]);
                 if (s + nt == u.nt) tc_commit(&b.q_empty[qb]);
             }
             __syncwarp();
-            if (prev.nt > 0 && !product_pv(n - 1u)) return;
-            prev.u = u;
-            prev.s = s;
-            prev.nt = nt;
+        }
+        if (prev_nt > 0 && !second(n - 1u)) return;
+        if (u.r < 0) return;
+        if (nt == 0) {
+            // (after the products of the step before, which must not wait for this unit: its query rows wait for the
+            // buffer that the unit of that step may still hold)
+            if (!warp_wait(&b.q_full[qb], (uint32_t)((units >> 1) & 1), abort_flag, p.status)) return;
+            ++units;
+            if (lane == 0) bar_arrive(&b.q_empty[qb]);
+        } else {
             ++n;
         }
+        prev_nt = nt;
+        prev_first = s == 0;
+        prev_tile0 = u.tile0 + s;
+        prev_kv_len = u.kv_len;
+        prev_q_len = u.q_len;
+        prev_row0 = u.row0;
+        prev_last = first_last;
+        s += nt;
     }
-    if (prev.nt > 0) product_pv(n - 1u);
 }
 
 // ---------------------------------------------------------------- query rows (one warp)
@@ -878,7 +951,7 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
             }
             fence_async_smem();
             tc_fence_before();
-            bar_arrive(b.p_full);
+            bar_arrive(&b.p_full[buf]);
             __syncwarp();
             if (lane == 0) bar_arrive(&b.sc_empty[buf]);
         }
@@ -945,7 +1018,7 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
     b.sc_empty = b.sc_full + 2;
     b.s_full = b.sc_empty + 2;
     b.p_full = b.s_full + 2;
-    b.o_full = b.p_full + 1;
+    b.o_full = b.p_full + 2;
     b.done = b.o_full + 2;
     b.uq_full = b.done + 1;
     b.uq_empty = b.uq_full + kQN;
@@ -962,7 +1035,7 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
     Extent e = extent(p, min(ra, p.B - 1));  // its load is under way during the set-up
     if (tid < C::N_BARS) {
         uint64_t* x = bars + tid;
-        bar_init(x, x >= b.uq_empty ? 11 : x >= b.o_full && x < b.done ? 2 : x == b.p_full ? 256 : x >= b.sc_empty && x < b.s_full ? 8
+        bar_init(x, x >= b.uq_empty ? 11 : x >= b.o_full && x < b.done ? 2 : x >= b.p_full && x < b.o_full ? 256 : x >= b.sc_empty && x < b.s_full ? 8
                     : x >= b.q_empty && x < b.sc_full ? 9 : 1);
         bar_init_fence();
     }
@@ -982,6 +1055,7 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
     fence_async_smem();
     long long sum = 0;
     bool bad = false;
+#pragma unroll 1
     for (int r = ra; r < rb; ++r) {
         if (r > ra) e = extent(p, r);
         bad |= e.bad;
@@ -1006,10 +1080,11 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
         total += wide[1 + w];
     }
     const long long share = total < 0x7fff0000LL ? max((unsigned)kMinShare, ((unsigned)total + gridDim.x - 1) / gridDim.x)
-                                                 : (total + gridDim.x - 1) / gridDim.x;
+                                                 : long_quotient(total + gridDim.x - 1, gridDim.x);
     const long long w0 = (long long)blockIdx.x * share, w1 = min(total, w0 + share);
     if (w0 >= before && w0 < before + sum) {  // this thread's requests hold the CTA's first tile
         long long at = before;
+#pragma unroll 1
         for (int r = ra; r < rb; ++r) {
             if (per > 1) e = extent(p, r);
             const long long work = work_of(p, e);
@@ -1031,7 +1106,15 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
     if (misc[2] == 0 && w0 < total) {
         if (warp >= 2 && warp < 10) {
             softmax_role<D, R>(p, smem, b, uq, abort_flag, tmem, warp - 2, warp & 3, lane);
-        } else if (warp == 1) {
+        } else if (warp == 0) {
+            const int* first = misc + kMiscFirst;
+            producer_role<D, R>(p, smem, b, uq, abort_flag, lane, misc[3], w0, w1, wide[0],
+                                Extent{first[0], first[1], first[2], false}, share);
+        } else if (warp == 10) {
+            query_role<D, R>(p, smem, b, uq, abort_flag, lane);
+        } else if (warp == 11) {
+            scale_role<D, R>(p, smem, b, uq, abort_flag, lane);
+        } else {
             mma_role<D, R>(p, smem, b, uq, abort_flag, tmem, lane);
             __syncwarp();
             if (lane == 0) {
@@ -1039,14 +1122,6 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
                 drain_wait(b.done, 0, p.status);
             }
             __syncwarp();
-        } else if (warp == 0) {
-            const int* first = misc + kMiscFirst;
-            producer_role<D, R>(p, smem, b, uq, abort_flag, lane, misc[3], w0, w1, wide[0],
-                                Extent{first[0], first[1], first[2], false}, share);
-        } else if (warp == 10) {
-            query_role<D, R>(p, smem, b, uq, abort_flag, lane);
-        } else {
-            scale_role<D, R>(p, smem, b, uq, abort_flag, lane);
         }
     }
     tc_fence_before();
