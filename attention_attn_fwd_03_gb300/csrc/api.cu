@@ -773,7 +773,7 @@ attn_status_t attn_varlen_fwd(const void* q, const void* k, const void* v, const
 size_t attn_paged_fwd_fp8_workspace_size(int B, int total_q, int max_q_len, int H, int H_kv, int d, int page_size,
                                          int max_pages) {
     if (paged_sizes_ok(B, total_q, max_q_len, H, H_kv, d, page_size, max_pages) != ATTN_OK) return 0;
-    return paged8_plan(max_q_len, H / H_kv, d).bytes;
+    return paged8_plan(B, max_q_len, H, H_kv, d, page_size, max_pages).bytes;
 }
 
 attn_status_t attn_paged_fwd_fp8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
@@ -793,7 +793,7 @@ attn_status_t attn_paged_fwd_fp8(const void* q, const void* k_cache, const void*
     auto a4 = [](const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 3u) == 0; };
     if (!a4(k_scale) || !a4(v_scale) || !a4(block_table) || !a4(seq_lens) || !a4(cu_seqlens_q) || !a4(lse))
         return ATTN_ERR_INVALID_ARG;
-    const Paged8Plan pl = paged8_plan(max_q_len, H / H_kv, d);
+    const Paged8Plan pl = paged8_plan(B, max_q_len, H, H_kv, d, page_size, max_pages);
     if (!workspace || workspace_bytes < pl.bytes || !aligned16(workspace)) return ATTN_ERR_WORKSPACE;
     DeviceState* ds = nullptr;
     st = device_state(&ds);
@@ -803,8 +803,11 @@ attn_status_t attn_paged_fwd_fp8(const void* q, const void* k_cache, const void*
     std::memset(&p, 0, sizeof p);
     const long long slots = (long long)num_pages * page_size;
     p.rows_per_box = page_size < 128 ? page_size : 128;
-    if (!make_codes_map(&p.tm_k, k_cache, d, H_kv, slots, p.rows_per_box) ||
-        !make_codes_map(&p.tm_v, v_cache, d, H_kv, slots, p.rows_per_box))
+    p.NH = pl.NH;
+    p.kv_units = H_kv / pl.NH;
+    const int wide = d == 64 ? pl.NH : 1;  // heads in a row of a tile
+    if (!make_codes_map(&p.tm_k, k_cache, wide * d, H_kv / wide, slots, p.rows_per_box) ||
+        !make_codes_map(&p.tm_v, v_cache, wide * d, H_kv / wide, slots, p.rows_per_box))
         return ATTN_ERR_CUDA;
     p.kv_rows = (int)slots;
     char* ws = static_cast<char*>(workspace);
@@ -812,6 +815,7 @@ attn_status_t attn_paged_fwd_fp8(const void* q, const void* k_cache, const void*
     p.part_ml = reinterpret_cast<float*>(ws + pl.part_ml);
     p.part_o = reinterpret_cast<float*>(ws + pl.part_o);
     p.R = pl.R;
+    p.RH = pl.R / pl.NH;
     p.n_ctas = 2 * ds->sm_count < kPaged8Ctas ? 2 * ds->sm_count : kPaged8Ctas;
     p.q = static_cast<const uint16_t*>(q);
     p.k_scale = k_scale;

@@ -189,7 +189,8 @@ cudaError_t launch_sparse(int d, const SparseParams& p, int sm_count, cudaStream
 // Attention over a cache of e4m3 codes with block scales (paged8.cu).  Query rows of a request
 // and KV head are numbered token * G + head of the group and cut into tiles of R.
 struct Paged8Params {
-    CUtensorMap tm_k;            // codes [slots, H_kv, d]: dims (d, H_kv, slots), box (d, 1, rows_per_box), swizzle d bytes
+    CUtensorMap tm_k;            // codes [slots, H_kv, d]: dims (d, H_kv, slots), box (d, 1, rows_per_box), swizzle d bytes;
+                                 // with NH = 2 and d = 64 two heads are one of d = 128
     CUtensorMap tm_v;
     const uint16_t* q;           // bf16 [total_q, H, d]
     const float* k_scale;        // [num_pages, H_kv, page_size / block]
@@ -200,11 +201,13 @@ struct Paged8Params {
     uint16_t* o;
     float* lse;                  // [total_q, H] or nullptr
     int4* cuts;                  // [n_ctas, 2] the unit that a CTA begins and others go on with, for the merge:
-                                 // (last of those CTAs or -1, record, rows, KV head), (first token, first row, -, -)
+                                 // (last of those CTAs or -1, record, rows of a head, first KV head / NH), (first token, first row, -, -)
     float* part_ml;              // [2 n_ctas, R, 2]: (m in log2 units, l) of a CTA's first and last piece
     float* part_o;               // [2 n_ctas, R, d]: unnormalised O
     unsigned* status;
-    int B, H, H_kv, G, R;
+    int B, H, H_kv, G;
+    int NH, kv_units;            // KV heads that a unit of work takes (1 or 2), H_kv / NH
+    int R, RH;                   // query rows of a unit, of each head
     int total_q, max_q_len;
     int page_shift, block_shift, max_pages, num_pages;
     int rows_per_box;            // min(page_size, 128)
@@ -215,11 +218,11 @@ struct Paged8Params {
 };
 // Workspace of the call: byte offsets of the plan's parts.
 struct Paged8Plan {
-    int R;                       // query rows of a tile
+    int NH, R;                   // KV heads and query rows of a unit
     size_t part_ml, part_o, bytes;
 };
 constexpr int kPaged8Ctas = 304;  // at most: two to each of the chip's 152 SMs
-Paged8Plan paged8_plan(int max_q_len, int G, int d);
+Paged8Plan paged8_plan(int B, int max_q_len, int H, int H_kv, int d, int page_size, int max_pages);
 cudaError_t launch_paged8(int d, const Paged8Params& p, cudaStream_t stream);
 
 // Failure-handling test: a bounded wait that nothing completes (selftest.cu).

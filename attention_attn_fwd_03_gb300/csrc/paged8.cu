@@ -17,13 +17,14 @@
 // Both products are transposed, so that keys (or channels) fill the 128 rows of the
 // matrix instruction and query rows its columns:
 //   S^T [128 keys, 2 R] = Kc [128, d] Q^T,    O^T [d, 3 R] += Vc^T [d, 128 keys] P^T,
-// R = 8, 16 or 32 query rows (tokens times the heads of a group).  A thread of the softmax
+// R = 8, 16 or 32 query rows (tokens times the heads of a group; those of two KV heads, if a
+// unit has two: each head's rows meet that head's codes only).  A thread of the softmax
 // then has one key and 8 rows: no thread is idle.  It takes 32 / R tiles of 128 keys (a step) at a time:
 // one test per step, over all threads, whether a row's maximum grew by more than kTau.
 //
-// Work split.  Requests, KV heads, row tiles and key tiles in a row, cut into equal shares,
+// Work split.  Requests, KV heads (or pairs of them: paged8_plan), row tiles and key tiles in a row, cut into equal shares,
 // one for each CTA (two to an SM, so that one's softmax runs during the other's loads).  Each
-// CTA computes the cut from the lengths.  A unit (request, head, row tile) that lies in one
+// CTA computes the cut from the lengths.  A unit (request, head or pair, row tile) that lies in one
 // CTA is finished there; pieces of others leave (m, l, O), merged by a second kernel.
 //
 // A CTA, 384 threads:
@@ -59,30 +60,36 @@ constexpr int kMiscFirst = 30;   // place in the misc words of the first request
 constexpr int kMinShare = 2;      // tiles
 constexpr int kUnitCost = 2;      // tiles
 
-template <int D, int R>
+template <int D, int R, int NH>
 struct Cfg {
     static constexpr int SB = 32 / R;                  // key tiles of a step
-    static constexpr int NQ = 2 * R;                   // columns of S^T per tile: hi, lo
-    static constexpr int NPV = R == 8 ? 32 : 3 * R;    // columns of O^T: hi, mid, lo (a multiple of 16)
-    static constexpr int TILE = 128 * D;               // bytes of a K or V tile
-    static constexpr int NST = (R == 8 ? 5 : 4) * 128 / D;  // ring stages
-    static constexpr int QBYTES = NQ * D;
-    static constexpr int PTILE = NPV * 128;
-    static constexpr int PBUF = R == 8 ? 1 : 2;        // steps' P held at once
+    static constexpr int RH = R / NH;                  // rows of a head
+    static constexpr bool WIDE = NH == 2 && D == 64;   // a tile holds the codes of two heads, side by side
+    static constexpr int TPK = NH == 2 && D == 128 ? 2 : 1;  // tiles to 128 keys: one for each head
+    static constexpr int W = WIDE ? 128 : D;           // bytes of a tile's row
+    static constexpr int PH = TPK == 2 ? RH : R;       // rows of a P operand
+    static constexpr int NPV = PH == 8 ? 32 : 3 * PH;  // columns of O^T: hi, mid, lo (a multiple of 16)
+    static constexpr int TILE = 128 * W;               // bytes of a K or V tile
+    static constexpr int NST = (SB * NH == 4 ? 5 : 4) * 128 / W;  // ring stages
+    static constexpr int QBYTES = 2 * R * D;
+    // A tile of P: hi, mid, lo; where those are 24 rows, the product's last 8 columns come from what follows and are not
+    // used.
+    static constexpr int PTILE = 3 * PH * 128;
+    static constexpr int PBUF = SB * NH == 4 || TPK == 2 ? 1 : 2;  // steps' P held at once
     static constexpr uint32_t TM_O = 128;              // S: two buffers of 64 columns
     static constexpr uint32_t TM_COLS = 256;
     static constexpr int OFF_KV = 0;
     static constexpr int OFF_P = OFF_KV + NST * TILE;
-    static constexpr int OFF_Q = OFF_P + PBUF * SB * PTILE;
-    static constexpr int OFF_SC = OFF_Q + 2 * QBYTES;                 // float2 [2][SB * 128]: ks, log2 vs of each key (or 2 .. 16 keys)
-    static constexpr int OFF_ROW = OFF_SC + 2 * SB * 128 * 8;         // int4 [2][R]: factor, last visible key, output row
+    static constexpr int OFF_Q = OFF_P + PBUF * SB * TPK * PTILE;
+    static constexpr int OFF_SC = OFF_Q + 2 * QBYTES;                 // float2 [2][NH][SB * 128]: ks, log2 vs of each key (or 2 .. 16 keys)
+    static constexpr int OFF_ROW = OFF_SC + 2 * NH * SB * 128 * 8;         // int4 [2][R]: factor, last visible key, output row
     static constexpr int OFF_STAT = OFF_ROW + 2 * R * 16;             // float2 [R]: running maxima of s and of s + log2 vs
     static constexpr int OFF_PAR = OFF_STAT + R * 8;                  // float2 [R]: the maximum, and P's factor
     static constexpr int OFF_ALPHA = OFF_PAR + R * 8;                 // float2 [R]
     static constexpr int OFF_EXCH = OFF_ALPHA + R * 8;                // float2 [8][R]
     static constexpr int OFF_SUM = OFF_EXCH + 8 * R * 8;              // float [8][R]
-    static constexpr int OFF_NAN = OFF_SUM + 8 * R * 4;               // int [D]: first row that sees a NaN in this channel
-    static constexpr int OFF_BAR = OFF_NAN + D * 4;
+    static constexpr int OFF_NAN = OFF_SUM + 8 * R * 4;               // int [NH * D]: first row that sees a NaN in this channel
+    static constexpr int OFF_BAR = OFF_NAN + NH * D * 4;
     static constexpr int N_BARS = 2 * NST + 15 + 2 * kQN;
     static constexpr int OFF_UQ = OFF_BAR + 8 * N_BARS;
     static constexpr int OFF_MISC = OFF_UQ + 4 * kQN * kUnitInts;
@@ -106,8 +113,8 @@ struct Bars {
     uint64_t* uq_empty;  // [kQN] eleven readers
 };
 
-// A piece of a unit: key tiles [tile0, tile0 + nt) for rows [row0, row0 + nr) of request r and KV head kvh.
-// Row x is query token x / G of the request, head x % G of the group.
+// A piece of a unit: key tiles [tile0, tile0 + nt) for rows [row0, row0 + nr) of request r and NH KV heads from
+// kvh * NH.  A head's row x is query token x / G of the request, head x % G of the group.
 struct Unit {
     int r;  // -1: no more
     int kvh, q_start, q_len, kv_len, row0, nr, tile0, nt;
@@ -146,9 +153,9 @@ __device__ __forceinline__ Extent extent(const Paged8Params& p, int r) {
 // Key tiles of every unit of a request (one at least, so that its rows are written), its row tiles, and its
 // size in the cut, where each unit counts kUnitCost tiles more: what its start and end take.
 __device__ __forceinline__ int key_tiles(const Extent& e) { return max(1, (int)(((long long)e.kv_len + 127) / 128)); }
-__device__ __forceinline__ int row_tiles(const Paged8Params& p, const Extent& e) { return (e.q_len * p.G + p.R - 1) / p.R; }
+__device__ __forceinline__ int row_tiles(const Paged8Params& p, const Extent& e) { return (e.q_len * p.G + p.RH - 1) / p.RH; }
 __device__ __forceinline__ long long work_of(const Paged8Params& p, const Extent& e) {
-    return (long long)p.H_kv * row_tiles(p, e) * (key_tiles(e) + kUnitCost);
+    return (long long)p.kv_units * row_tiles(p, e) * (key_tiles(e) + kUnitCost);
 }
 
 // a / b (both positive, the quotient an int), by a 32-bit division where that will do: the 64-bit one takes a noticeable
@@ -258,11 +265,11 @@ __device__ __forceinline__ float scale_for(float amax) {
 
 // ---------------------------------------------------------------- producer (whole warp)
 
-template <int D, int R>
+template <int D, int R, int NH>
 __device__ void producer_role(const Paged8Params& p, uint8_t* smem, const Bars& b, volatile int* uq, volatile int* abort_flag,
                               int lane, int r, long long w, long long w1, long long start, Extent e,
                               long long share) {
-    using C = Cfg<D, R>;
+    using C = Cfg<D, R, NH>;
     if (lane == 0) {
         tma_prefetch_map(&p.tm_k);
         tma_prefetch_map(&p.tm_v);
@@ -321,8 +328,8 @@ __device__ void producer_role(const Paged8Params& p, uint8_t* smem, const Bars& 
                 u.q_start = e.q_start;
                 u.q_len = e.q_len;
                 u.kv_len = e.kv_len;
-                u.row0 = (unit - u.kvh * nqt) * R;
-                u.nr = min(R, e.q_len * p.G - u.row0);
+                u.row0 = (unit - u.kvh * nqt) * C::RH;
+                u.nr = min(C::RH, e.q_len * p.G - u.row0);
                 u.tile0 = tile;
                 const long long seen = (last_key(p, u, u.row0 + u.nr - 1) + 128LL) / 128;  // tiles that the last row sees
                 u.nt = (int)max(0LL, min((long long)n, seen - tile));
@@ -364,8 +371,8 @@ __device__ void producer_role(const Paged8Params& p, uint8_t* smem, const Bars& 
         }
         // K of this step, then V of the one before
 #pragma unroll 1
-        for (int t = 0; t < nt + prev_nt; ++t) {
-            const bool is_k = t < nt;
+        for (int t = 0; t < (nt + prev_nt) * C::TPK; ++t) {
+            const bool is_k = t < nt * C::TPK;
             const int slot = kv_idx % C::NST, round = kv_idx / C::NST;
             if (lane == 0) {
                 if (round > 0) ok = wait_short(&b.kv_empty[slot], (uint32_t)((round - 1) & 1), abort_flag, p.status);
@@ -373,12 +380,13 @@ __device__ void producer_role(const Paged8Params& p, uint8_t* smem, const Bars& 
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) break;
-            const int first = (is_k ? t : t - nt) * per_tile;  // per_tile divides 32: the tile's boxes lie in one register
+            const int x = is_k ? t : t - nt * C::TPK;
+            const int first = x / C::TPK * per_tile;  // per_tile divides 32: the tile's boxes lie in one register
             const int i = lane - (first & 31);
             const int* from = is_k ? row_of : prev_rows;
             if (i >= 0 && i < per_tile)
-                tma_load_3d(smem + C::OFF_KV + slot * C::TILE + i * rows * D, is_k ? &p.tm_k : &p.tm_v, &b.kv_full[slot], 0,
-                            is_k ? u.kvh : prev_kvh, first < 32 ? from[0] : from[1]);
+                tma_load_3d(smem + C::OFF_KV + slot * C::TILE + i * rows * C::W, is_k ? &p.tm_k : &p.tm_v, &b.kv_full[slot], 0,
+                            (is_k ? u.kvh : prev_kvh) * C::TPK + x % C::TPK, first < 32 ? from[0] : from[1]);
             ++kv_idx;
         }
         prev_rows[0] = row_of[0];
@@ -409,10 +417,16 @@ __device__ __forceinline__ void clear_rows(uint32_t tile, int left, int lane) {
 }
 
 // The scores of one tile.
-template <int D, int R>
+template <int D, int R, int NH>
 __device__ __forceinline__ void product_s(uint32_t d, uint64_t k, uint64_t q) {
-    constexpr uint32_t ID = idesc_make(128, 2 * R, 0u, false, false);
-    if (D == 128) {
+    constexpr int N = 2 * Cfg<D, R, NH>::RH;
+    constexpr uint32_t ID = idesc_make(128, N, 0u, false, false);
+    if (Cfg<D, R, NH>::WIDE) {  // each head's half of the row
+        mma_f8_ss(d, k, q, ID, 0u);
+        mma_f8_ss(d, k + 2, q + 2, ID, 1u);
+        mma_f8_ss(d + N, k + 4, q + 4, ID, 0u);
+        mma_f8_ss(d + N, k + 6, q + 6, ID, 1u);
+    } else if (D == 128) {
         mma4_ss<2, 4, 6, 2, 4, 6, true>(d, k, q, ID, 0u);
     } else {
         mma_f8_ss(d, k, q, ID, 0u);
@@ -421,22 +435,23 @@ __device__ __forceinline__ void product_s(uint32_t d, uint64_t k, uint64_t q) {
 }
 
 // One tile's part of O^T: four blocks of 32 keys.
-template <int D, int R>
+template <int D, int R, int NH>
 __device__ __forceinline__ void product_pv(uint32_t o, uint64_t v, uint64_t p, bool accumulate) {
-    constexpr uint32_t ID = idesc_make(D, Cfg<D, R>::NPV, 0u, true, false);
-    constexpr int VS = (32 * D) >> 4;  // 32 rows of V in descriptor units
+    constexpr uint32_t ID = idesc_make(Cfg<D, R, NH>::W, Cfg<D, R, NH>::NPV, 0u, true, false);
+    constexpr int VS = (32 * Cfg<D, R, NH>::W) >> 4;  // 32 rows of V in descriptor units
     mma4_ss<VS, 2 * VS, 3 * VS, 2, 4, 6, true>(o, v, p, ID, accumulate ? 1u : 0u);
 }
 
 // S^T of step n + 1, then O^T += V^T P^T of step n: the order of the ring.  (Two issuers, one for each product, were
 // slower: which tile of the ring is whose is known only in this order, and the waits for one another cost more than the
 // 300 to 500 cycles that a tile's few instructions, wait and commit take here.)
-template <int D, int R>
+template <int D, int R, int NH>
 __device__ void mma_role(const Paged8Params& p, uint8_t* smem, const Bars& b, volatile int* uq, volatile int* abort_flag,
                          uint32_t tmem, int lane) {
-    using C = Cfg<D, R>;
+    using C = Cfg<D, R, NH>;
     const uint32_t sbase = smem_u32(smem), o = tmem + C::TM_O;
-    const uint64_t kv_desc = desc<D>(sbase + C::OFF_KV), p_desc = desc<128>(sbase + C::OFF_P);
+    constexpr int W = C::W, TPK = C::TPK;
+    const uint64_t kv_desc = desc<W>(sbase + C::OFF_KV), p_desc = desc<128>(sbase + C::OFF_P);
     int* s_nan = reinterpret_cast<int*>(smem + C::OFF_NAN);
     int stage = 0, phase = 0, units = 0;
     uint32_t n = 0;  // steps issued
@@ -475,26 +490,28 @@ __device__ void mma_role(const Paged8Params& p, uint8_t* smem, const Bars& b, vo
         const int keys = (int)min((long long)nt * 128, prev_kv_len - key0);
         // tiles without rows to clear (all but the request's last) and without keys that only some of the unit's rows see
         const int whole = prev_last < prev_kv_len - 1 && key0 + keys - 1 > prev_last ? 0 : keys / 128;
-        const uint64_t p_step = p_desc + (uint64_t)((C::PBUF == 2 ? step & 1u : 0u) * (C::SB * C::PTILE >> 4));
+        const uint64_t p_step = p_desc + (uint64_t)((C::PBUF == 2 ? step & 1u : 0u) * (C::SB * TPK * C::PTILE >> 4));
         if (!warp_wait(&b.p_full[step & 1u], (step >> 1) & 1u, abort_flag, p.status)) return false;
-        if (!tiles(whole, [&](int t, uint64_t tile) {
-                product_pv<D, R>(o, kv_desc + tile, p_step + (uint64_t)(t * (C::PTILE >> 4)), !prev_first || t > 0);
-            }))
-            return false;
-        for (int t = whole; t < nt; ++t) {
+        auto product = [&](int t, uint64_t tile) {
+            product_pv<D, R, NH>(o + (uint32_t)(t % TPK * C::NPV), kv_desc + tile, p_step + (uint64_t)(t * (C::PTILE >> 4)),
+                                 !prev_first || t >= TPK);
+        };
+        if (!tiles(whole * TPK, product)) return false;
+        for (int x = whole * TPK; x < nt * TPK; ++x) {
+            const int t = x / TPK;
             if (!warp_wait(&b.kv_full[stage], (uint32_t)phase, abort_flag, p.status)) return false;
             const int left = min(128, keys - t * 128);
             const uint32_t v = sbase + C::OFF_KV + (uint32_t)(stage * C::TILE);
-            if (left < 128) clear_rows<D>(v, left, lane);
+            if (left < 128) clear_rows<W>(v, left, lane);
             if (key0 + t * 128 + left - 1 > prev_last) {
                 // Keys that only some of the rows see: a NaN among their values must not reach the others
                 // through 0 * NaN.  It is taken out and noted, by channel, for the rows from the first that sees it.
                 const int from = (int)max(0LL, min(128LL, prev_last + 1LL - key0 - t * 128));
 #pragma unroll 1
-                for (int x = from * (D / 4) + lane; x < left * (D / 4); x += 32) {
-                    const int key = x / (D / 4), word = x % (D / 4);  // stored word of the row, swizzled
-                    const int chunk = (word >> 2) ^ (D == 128 ? key & 7 : (key >> 1) & 3);
-                    const uint32_t at = v + (uint32_t)(key * D + word * 4);
+                for (int i = from * (W / 4) + lane; i < left * (W / 4); i += 32) {
+                    const int key = i / (W / 4), word = i % (W / 4);  // stored word of the row, swizzled
+                    const int chunk = (word >> 2) ^ (W == 128 ? key & 7 : (key >> 1) & 3);
+                    const uint32_t at = v + (uint32_t)(key * W + word * 4);
                     uint32_t c;
                     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(c) : "r"(at) : "memory");
                     uint32_t keep = c;
@@ -505,7 +522,7 @@ __device__ void mma_role(const Paged8Params& p, uint8_t* smem, const Bars& b, vo
                             // token of the first row that sees the key
                             const long long tok = key0 + t * 128 + key - ((long long)prev_kv_len - prev_q_len);
                             const int row = (int)max(0LL, tok * p.G - prev_row0);
-                            atomicMin(s_nan + chunk * 16 + (word & 3) * 4 + k, row);
+                            atomicMin(s_nan + x % TPK * D + chunk * 16 + (word & 3) * 4 + k, row);
                         }
                     if (keep != c) st_u32(at, keep);
                 }
@@ -514,7 +531,7 @@ __device__ void mma_role(const Paged8Params& p, uint8_t* smem, const Bars& b, vo
             }
             if (lane == 0) {
                 tc_fence_after();
-                product_pv<D, R>(o, kv_desc + (uint64_t)(stage * (C::TILE >> 4)), p_step + (uint64_t)(t * (C::PTILE >> 4)), !prev_first || t > 0);
+                product(x, (uint64_t)(stage * (C::TILE >> 4)));
                 tc_commit(&b.kv_empty[stage]);
             }
             next_stage();
@@ -543,7 +560,7 @@ __device__ void mma_role(const Paged8Params& p, uint8_t* smem, const Bars& b, vo
             if (u.nt > 0) {
                 if (!warp_wait(&b.q_full[qb], (uint32_t)((units >> 1) & 1), abort_flag, p.status)) return;
                 ++units;
-                q_desc = desc<D>(sbase + C::OFF_Q + (uint32_t)(qb * C::QBYTES));
+                q_desc = desc<W>(sbase + C::OFF_Q + (uint32_t)(qb * C::QBYTES));
                 first_last = last_key(p, u, u.row0);
             }
         }
@@ -553,14 +570,16 @@ __device__ void mma_role(const Paged8Params& p, uint8_t* smem, const Bars& b, vo
             const uint32_t d = tmem + (n & 1u) * 64u;
             const int keys = (int)min((long long)nt * 128, (long long)u.kv_len - (long long)(u.tile0 + s) * 128);
             const int whole = keys / 128;  // tiles without rows to clear: all but the request's last
-            if (!tiles(whole, [&](int t, uint64_t tile) { product_s<D, R>(d + (uint32_t)(t * C::NQ), kv_desc + tile, q_desc); }))
-                return;
-            if (whole < nt) {
+            auto product = [&](int t, uint64_t tile) {
+                product_s<D, R, NH>(d + (uint32_t)(t * (2 * R / TPK)), kv_desc + tile, q_desc + (uint64_t)(t % TPK * (C::QBYTES / TPK >> 4)));
+            };
+            if (!tiles(whole * TPK, product)) return;
+            for (int t = whole * TPK; t < nt * TPK; ++t) {
                 if (!warp_wait(&b.kv_full[stage], (uint32_t)phase, abort_flag, p.status)) return;
-                clear_rows<D>(sbase + C::OFF_KV + (uint32_t)(stage * C::TILE), keys - whole * 128, lane);
+                clear_rows<W>(sbase + C::OFF_KV + (uint32_t)(stage * C::TILE), keys - whole * 128, lane);
                 if (lane == 0) {
                     tc_fence_after();
-                    product_s<D, R>(d + (uint32_t)(whole * C::NQ), kv_desc + (uint64_t)(stage * (C::TILE >> 4)), q_desc);
+                    product(t, (uint64_t)(stage * (C::TILE >> 4)));
                     tc_commit(&b.kv_empty[stage]);
                 }
                 next_stage();
@@ -595,12 +614,13 @@ __device__ void mma_role(const Paged8Params& p, uint8_t* smem, const Bars& b, vo
 
 // ---------------------------------------------------------------- query rows (one warp)
 
-template <int D, int R>
+template <int D, int R, int NH>
 __device__ void query_role(const Paged8Params& p, uint8_t* smem, const Bars& b, volatile int* uq, volatile int* abort_flag,
                          int lane) {
-    using C = Cfg<D, R>;
+    using C = Cfg<D, R, NH>;
     constexpr int LPR = D / 8;         // lanes of a query row, 8 elements each
-    constexpr int PASS = 8 * LPR / 32; // rounds for 8 rows
+    constexpr int GROUP = R < 16 || D == 128 ? 8 : 16;  // rows whose loads are in flight together
+    constexpr int PASS = GROUP * LPR / 32;
     const uint32_t sbase = smem_u32(smem);
     int units = 0;
     for (int k = 0;; ++k) {
@@ -616,19 +636,19 @@ __device__ void query_role(const Paged8Params& p, uint8_t* smem, const Bars& b, 
         const uint32_t q_at = sbase + C::OFF_Q + (uint32_t)(qb * C::QBYTES);
         int4* s_row = reinterpret_cast<int4*>(smem + C::OFF_ROW) + qb * R;
         if (lane < R) {
-            const int row = u.row0 + min(lane, u.nr - 1), tok = row / p.G;
+            const int row = u.row0 + min(lane % C::RH, u.nr - 1), tok = row / p.G;
             s_row[lane] = make_int4(0, max(last_key(p, u, row), -1),
-                                    (u.q_start + tok) * p.H + u.kvh * p.G + (row - tok * p.G), 0);
+                                    (u.q_start + tok) * p.H + (u.kvh * NH + lane / C::RH) * p.G + (row - tok * p.G), 0);
         }
         __syncwarp();
 #pragma unroll 1
-        for (int g0 = 0; g0 < R; g0 += 8) {
+        for (int g0 = 0; g0 < R; g0 += GROUP) {
             uint4 x[PASS];
 #pragma unroll
             for (int i = 0; i < PASS; ++i) {
                 const int r = g0 + (i * 32 + lane) / LPR;
                 x[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (r < u.nr)
+                if (r % C::RH < u.nr)
                     x[i] = *reinterpret_cast<const uint4*>(p.q + (size_t)(unsigned)s_row[r].z * D + lane % LPR * 8);
             }
 #pragma unroll
@@ -658,13 +678,14 @@ __device__ void query_role(const Paged8Params& p, uint8_t* smem, const Bars& b, 
                     hi[c / 4] = c & 2 ? hi[c / 4] | (uint32_t)e << 16 : (uint32_t)e;
                     lo[c / 4] = c & 2 ? lo[c / 4] | (uint32_t)e2 << 16 : (uint32_t)e2;
                 }
-                const int byte = lane % LPR * 8;
+                // a head's rows: hi, lo; its operand is a tile of its own, or its half of the rows of the common one
+                const int byte = lane % LPR * 8 + (C::WIDE ? r / C::RH * D : 0), head = C::WIDE ? 0 : r / C::RH;
                 auto at = [&](int row) {
-                    const int chunk = (byte >> 4) ^ (D == 128 ? row & 7 : (row >> 1) & 3);
-                    return q_at + (uint32_t)(row * D + chunk * 16 + (byte & 15));
+                    const int chunk = (byte >> 4) ^ (C::W == 128 ? row & 7 : (row >> 1) & 3);
+                    return q_at + (uint32_t)((head * 2 * C::RH + row) * C::W + chunk * 16 + (byte & 15));
                 };
-                st_v2(at(r), hi[0], hi[1]);
-                st_v2(at(R + r), lo[0], lo[1]);
+                st_v2(at(r % C::RH), hi[0], hi[1]);
+                st_v2(at(C::RH + r % C::RH), lo[0], lo[1]);
                 if (lane % LPR == 0) s_row[r].x = __float_as_int(qs * p.c_scale);
             }
         }
@@ -676,10 +697,10 @@ __device__ void query_role(const Paged8Params& p, uint8_t* smem, const Bars& b, 
 
 // ---------------------------------------------------------------- scales of the steps' keys (one warp)
 
-template <int D, int R>
+template <int D, int R, int NH>
 __device__ void scale_role(const Paged8Params& p, uint8_t* smem, const Bars& b, volatile int* uq, volatile int* abort_flag,
                            int lane) {
-    using C = Cfg<D, R>;
+    using C = Cfg<D, R, NH>;
     const int per_page = p.page_shift - p.block_shift;
     const int gshift = min(p.block_shift, 4);  // keys that share an entry of s_scale: 1 to 16
     uint32_t n = 0;
@@ -693,20 +714,20 @@ __device__ void scale_role(const Paged8Params& p, uint8_t* smem, const Bars& b, 
         for (int s = 0; s < u.nt; s += C::SB, ++n) {
             const uint32_t buf = n & 1u;
             const int groups = (min(C::SB, u.nt - s) * 128) >> gshift;
-            float2* dst = reinterpret_cast<float2*>(smem + C::OFF_SC) + buf * C::SB * 128;
+            float2* dst = reinterpret_cast<float2*>(smem + C::OFF_SC) + buf * NH * C::SB * 128;
             bool free = n < 2;
 #pragma unroll 1
-            for (int g0 = 0; g0 < groups; g0 += 128) {
+            for (int g0 = 0; g0 < NH * groups; g0 += 128) {
                 float2 v[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {  // four groups' loads in flight
-                    const int g = g0 + i * 32 + lane;
+                    const int x = g0 + i * 32 + lane, head = NH == 2 && x >= groups, g = x - head * groups;
                     const long long key = (long long)(u.tile0 + s) * 128 + ((long long)g << gshift);
                     v[i] = make_float2(0.f, 0.f);
                     if (g < groups && key < u.kv_len) {
                         const int id = __ldg(p.block_table + (size_t)u.r * p.max_pages + (key >> p.page_shift));
                         if (id >= 0 && id < p.num_pages) {
-                            const size_t at = (((size_t)(unsigned)id * p.H_kv + u.kvh) << per_page) +
+                            const size_t at = (((size_t)(unsigned)id * p.H_kv + u.kvh * NH + head) << per_page) +
                                               (((int)key & ((1 << p.page_shift) - 1)) >> p.block_shift);
                             v[i] = make_float2(__ldg(p.k_scale + at), __ldg(p.v_scale + at));
                         }
@@ -717,8 +738,10 @@ __device__ void scale_role(const Paged8Params& p, uint8_t* smem, const Bars& b, 
                     free = true;
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (g0 + i * 32 + lane < groups) dst[g0 + i * 32 + lane] = make_float2(v[i].x, lg2(v[i].y));
+                for (int i = 0; i < 4; ++i) {
+                    const int x = g0 + i * 32 + lane, head = NH == 2 && x >= groups;
+                    if (x < NH * groups) dst[head * C::SB * 128 + x - head * groups] = make_float2(v[i].x, lg2(v[i].y));
+                }
             }
             __syncwarp();
             if (lane == 0) bar_arrive(&b.sc_full[buf]);
@@ -755,11 +778,11 @@ __device__ __forceinline__ float warp_sum8(const float* v, int lane) {
 // A step's 32 / R x R / 8 blocks of 128 keys x 8 rows go to two groups of four warps: two blocks to a thread, whose 16
 // scores stay in registers.  Few instructions, each used often: with 32 scores a thread, everything unrolled, warps
 // waited for instructions more than for data.
-template <int D, int R>
+template <int D, int R, int NH>
 __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b, volatile int* uq, volatile int* abort_flag,
                              uint32_t tmem, int warp8, int wq, int lane) {
-    using C = Cfg<D, R>;
-    constexpr int SB = C::SB;
+    using C = Cfg<D, R, NH>;
+    constexpr int SB = C::SB, RH = C::RH, PH = C::PH;
     constexpr int SETS = R == 32 ? 2 : 1;        // sets of 8 rows that a thread sees
     const int grp = warp8 >> 2;
     const int tid = wq * 32 + lane;              // key within a tile, TMEM lane
@@ -814,11 +837,12 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int t = tile_of(j), rb = row_of(j);
-                if (t < nt && rb < u.nr) {
+                if (t < nt && rb % RH < u.nr) {
                     uint32_t x[16];
-                    tmem_ld8(tS + buf * 64u + (uint32_t)(t * C::NQ + rb), x);
-                    tmem_ld8(tS + buf * 64u + (uint32_t)(t * C::NQ + R + rb), x + 8);
-                    const float2 sc = s_scale[buf * SB * 128 + ((t * 128 + tid) >> gshift)];
+                    const uint32_t col = buf * 64u + (uint32_t)(t * 2 * R + rb / RH * 2 * RH + rb % RH);
+                    tmem_ld8(tS + col, x);
+                    tmem_ld8(tS + col + (uint32_t)RH, x + 8);
+                    const float2 sc = s_scale[(buf * NH + rb / RH) * SB * 128 + ((t * 128 + tid) >> gshift)];
                     // the rows of keys past the request's end are zeros
                     const float mask = (unsigned)key0 + (unsigned)(t * 128 + tid) < (unsigned)u.kv_len ? 0.f : -INFINITY;
                     lv[j] = sc.y;
@@ -888,12 +912,14 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
 #pragma unroll 1
                     for (int c = 8 * grp; c < 3 * R; c += 16) {  // hi, mid, lo
                         uint32_t x[8];
-                        tmem_ld8(tO + (uint32_t)c, x);
+                        const uint32_t col = tO + (uint32_t)(c / (3 * PH) * C::NPV + c % (3 * PH));
+                        const int r = c / (3 * PH) * PH + c % PH;
+                        tmem_ld8(col, x);
                         tmem_ld_wait();
                         reg_after_wait<8>(x);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * s_alpha[c % R + i].y);
-                        tmem_st8(tO + (uint32_t)c, x);
+                        for (int i = 0; i < 8; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * s_alpha[r + i].y);
+                        tmem_st8(col, x);
                     }
                     tmem_st_wait();
                 }
@@ -909,7 +935,7 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
 #pragma unroll
                     for (int i = 0; i < 8; ++i) l[i] = 0.f;
                 }
-                if (t < nt && rb < u.nr) {
+                if (t < nt && rb % RH < u.nr) {
                     const float vk = ex2(lv[j]);
                     uint32_t h[4], hi[4], mid[4], lo[4];
 #pragma unroll
@@ -930,17 +956,17 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
                     for (int i = 0; i < 4; ++i) h[i] = h2_mul32(h2_sub(h[i], half2_of(mid[i])));
 #pragma unroll
                     for (int i = 0; i < 4; ++i) lo[i] = e4m3_of(h[i]);
-                    const uint32_t at = p_at + (uint32_t)(((C::PBUF == 2 ? buf : 0u) * SB + t) * C::PTILE + rb * 128);
+                    const uint32_t at = p_at + (uint32_t)((((C::PBUF == 2 ? buf : 0u) * SB + t) * C::TPK + rb / PH) * C::PTILE + rb % PH * 128);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint32_t a0 = (at ^ (uint32_t)(2 * i << 4)) + (uint32_t)(2 * i * 128);
                         const uint32_t a1 = (at ^ (uint32_t)((2 * i + 1) << 4)) + (uint32_t)((2 * i + 1) * 128);
                         st_u8(a0, hi[i]);
                         st_u8(a1, hi[i] >> 8);
-                        st_u8(a0 + R * 128, mid[i]);
-                        st_u8(a1 + R * 128, mid[i] >> 8);
-                        st_u8(a0 + 2 * R * 128, lo[i]);
-                        st_u8(a1 + 2 * R * 128, lo[i] >> 8);
+                        st_u8(a0 + PH * 128, mid[i]);
+                        st_u8(a1 + PH * 128, mid[i] >> 8);
+                        st_u8(a0 + 2 * PH * 128, lo[i]);
+                        st_u8(a1 + 2 * PH * 128, lo[i] >> 8);
                     }
                 }
                 if (SETS == 2 || j == 1) {  // the rows' sums, one lane each
@@ -959,18 +985,19 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
         // ---- the unit's end: O by channel, every other row by each group
         softmax_sync();  // every warp's sums
         if (u.nt > 0) wait_products(n - 1u);
-        const int chan = D == 128 ? tid : wq * 16 + (lane & 15);
-        const bool mine = !fail && (D == 128 || lane < 16);
-        const int nan_from = s_nan[chan];
+        const int lane_chan = C::W == 128 ? tid : wq * 16 + (lane & 15), chan = lane_chan % D;
+        const bool mine = !fail && (C::W == 128 || lane < 16);
         tc_fence_after();
 #pragma unroll 1
-        for (int r = grp; r < u.nr; r += 2) {
+        for (int x = grp; x < u.nr * C::TPK; x += 2) {  // (a wide tile's heads: half of the channels each)
+            const int head = C::WIDE ? tid / D : x >= u.nr, y = C::WIDE ? x : x - head * u.nr, r = head * RH + y;
             float v = 0.f, m = 0.f, sum = 0.f;
             if (u.nt > 0) {
                 uint32_t x[3];
-                tmem_ld1(tO + (uint32_t)r, x);
-                tmem_ld1(tO + (uint32_t)(R + r), x + 1);
-                tmem_ld1(tO + (uint32_t)(2 * R + r), x + 2);
+                const uint32_t col = tO + (uint32_t)(r / PH * C::NPV + r % PH);
+                tmem_ld1(col, x);
+                tmem_ld1(col + (uint32_t)PH, x + 1);
+                tmem_ld1(col + (uint32_t)(2 * PH), x + 2);
                 const int from = R == 8 ? 0 : (r >> 3 & 1) * 4;
 #pragma unroll
                 for (int w = 0; w < (R == 8 ? 8 : 4); ++w) sum += s_sum[(from + w) * R + r];
@@ -980,31 +1007,31 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
                 tmem_ld_wait();
                 reg_after_wait<3>(x);
                 v = fmaf(__uint_as_float(x[2]), 0x1p-10f, fmaf(__uint_as_float(x[1]), 0x1p-5f, __uint_as_float(x[0]))) * f;
-                if (r >= nan_from) v = __int_as_float(0x7fffffff);
+                if (y >= s_nan[head * D + chan]) v = __int_as_float(0x7fffffff);
             }
             if (u.slot < 0) {
                 const size_t out = (size_t)(unsigned)s_row[r].z;
-                const float y = sum == 0.f ? 0.f : v * (1.f / sum);
-                if (mine) p.o[out * D + chan] = (uint16_t)pack_bf16(y, y);
-                if (!fail && tid == r && p.lse != nullptr) p.lse[out] = sum == 0.f ? -INFINITY : (m + lg2(sum)) * kLn2;
+                const float o = sum == 0.f ? 0.f : v * (1.f / sum);
+                if (mine) p.o[out * D + chan] = (uint16_t)pack_bf16(o, o);
+                if (!fail && chan == y && p.lse != nullptr) p.lse[out] = sum == 0.f ? -INFINITY : (m + lg2(sum)) * kLn2;
             } else {
                 const size_t rec = (size_t)u.slot * R + r;
                 if (mine) p.part_o[rec * D + chan] = v;
-                if (!fail && tid == r) *reinterpret_cast<float2*>(p.part_ml + rec * 2) = make_float2(sum == 0.f ? -INFINITY : m, sum);
+                if (!fail && chan == y) *reinterpret_cast<float2*>(p.part_ml + rec * 2) = make_float2(sum == 0.f ? -INFINITY : m, sum);
             }
         }
         tc_fence_before();
         softmax_sync();  // s_stat, s_sum, s_nan and the rows have been read
-        if (mine && grp == 0) s_nan[chan] = 0x7fffffff;
+        if (gtid < NH * D) s_nan[gtid] = 0x7fffffff;
         if (lane == 0) bar_arrive(&b.q_empty[qb]);
     }
 }
 
 // ---------------------------------------------------------------- kernels
 
-template <int D, int R>
+template <int D, int R, int NH>
 __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_constant__ Paged8Params p) {
-    using C = Cfg<D, R>;
+    using C = Cfg<D, R, NH>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
@@ -1047,12 +1074,7 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
         tmem_alloc(tmem_holder, C::TM_COLS);
         tmem_relinquish();
     }
-    for (int i = tid; i < D; i += kThreads8) reinterpret_cast<int*>(smem + C::OFF_NAN)[i] = 0x7fffffff;
-    // columns of O^T that pad 3 R to 32: their rows of P read as zeros
-    if (R == 8)
-        for (int i = tid; i < C::SB * 8 * 8; i += kThreads8)
-            st_zero16(smem_u32(smem + C::OFF_P) + (uint32_t)((i / 64) * C::PTILE + 24 * 128 + (i % 64) * 16));
-    fence_async_smem();
+    for (int i = tid; i < NH * D; i += kThreads8) reinterpret_cast<int*>(smem + C::OFF_NAN)[i] = 0x7fffffff;
     long long sum = 0;
     bool bad = false;
 #pragma unroll 1
@@ -1105,17 +1127,17 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
     const uint32_t tmem = *tmem_holder;
     if (misc[2] == 0 && w0 < total) {
         if (warp >= 2 && warp < 10) {
-            softmax_role<D, R>(p, smem, b, uq, abort_flag, tmem, warp - 2, warp & 3, lane);
+            softmax_role<D, R, NH>(p, smem, b, uq, abort_flag, tmem, warp - 2, warp & 3, lane);
         } else if (warp == 0) {
             const int* first = misc + kMiscFirst;
-            producer_role<D, R>(p, smem, b, uq, abort_flag, lane, misc[3], w0, w1, wide[0],
+            producer_role<D, R, NH>(p, smem, b, uq, abort_flag, lane, misc[3], w0, w1, wide[0],
                                 Extent{first[0], first[1], first[2], false}, share);
         } else if (warp == 10) {
-            query_role<D, R>(p, smem, b, uq, abort_flag, lane);
+            query_role<D, R, NH>(p, smem, b, uq, abort_flag, lane);
         } else if (warp == 11) {
-            scale_role<D, R>(p, smem, b, uq, abort_flag, lane);
+            scale_role<D, R, NH>(p, smem, b, uq, abort_flag, lane);
         } else {
-            mma_role<D, R>(p, smem, b, uq, abort_flag, tmem, lane);
+            mma_role<D, R, NH>(p, smem, b, uq, abort_flag, tmem, lane);
             __syncwarp();
             if (lane == 0) {
                 tc_commit(b.done);  // every issued MMA finishes before tensor memory is released
@@ -1132,21 +1154,25 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
     }
 }
 
-// The units that were cut, one CTA for each of their rows x % gridDim.y: piece by piece to its eight warps,
+// The units that were cut, a CTA for every fourth pair of their rows: a row's pieces to kMergeWarps warps in turn,
 //   m = max m_i,  l = sum l_i 2^(m_i - m),  O = sum 2^(m_i - m) O_i / l.
 // The pieces are one unit's last of CTA c0 and first of the CTAs up to c1.  Their (m, l) and O are asked for at once.
-constexpr int kMergeWarps = 8;
-constexpr int kMergeRows = 4;
+constexpr int kMergeWarps = 4;
+constexpr int kMergeRows = 2;   // of a CTA
+constexpr int kMergeCtas = 4;
 template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32) paged8_merge_kernel(const __grid_constant__ Paged8Params p) {
+__global__ void __launch_bounds__(kMergeRows * kMergeWarps * 32) paged8_merge_kernel(const __grid_constant__ Paged8Params p) {
     constexpr int PER = D / 32;
     using Vec = typename std::conditional<PER == 4, float4, float2>::type;
-    __shared__ float s_o[kMergeWarps][D], s_ml[kMergeWarps][2];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.x;
+    __shared__ float s_o[kMergeRows][kMergeWarps][D], s_ml[kMergeRows][kMergeWarps][2];
+    const int lane = threadIdx.x & 31, c0 = blockIdx.x;
+    const int sub = threadIdx.x / (kMergeWarps * 32), tid = threadIdx.x % (kMergeWarps * 32), warp = tid >> 5;
     griddep_wait();
     const int4 cut = __ldcg(p.cuts + 2 * c0), unit = __ldcg(p.cuts + 2 * c0 + 1);
     if (timeout_recorded(p.status) || cut.x < 0) return;
-    for (int r = blockIdx.y; r < cut.z; r += kMergeRows) {
+    for (int x0 = blockIdx.y * kMergeRows; x0 < cut.z * p.NH; x0 += kMergeCtas * kMergeRows) {
+        const int x = min(x0 + sub, cut.z * p.NH - 1);  // (the last row twice, if they are odd)
+        const int head = x / cut.z, y = x - head * cut.z, r = head * p.RH + y;
         float m = -INFINITY, l = 0.f, acc[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) acc[i] = 0.f;
@@ -1182,47 +1208,47 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged8_merge_kernel(const __
             }
         }
 #pragma unroll
-        for (int i = 0; i < PER; ++i) s_o[warp][lane * PER + i] = acc[i];
+        for (int i = 0; i < PER; ++i) s_o[sub][warp][lane * PER + i] = acc[i];
         if (lane == 0) {
-            s_ml[warp][0] = m;
-            s_ml[warp][1] = l;
+            s_ml[sub][warp][0] = m;
+            s_ml[sub][warp][1] = l;
         }
         __syncthreads();
-        if (threadIdx.x < D / 2) {
-            float top = -INFINITY, sum = 0.f, y[2] = {0.f, 0.f};
+        if (tid < D / 2) {
+            float top = -INFINITY, sum = 0.f, f2[2] = {0.f, 0.f};
 #pragma unroll
-            for (int w = 0; w < kMergeWarps; ++w) top = fmaxf(top, s_ml[w][0]);
+            for (int w = 0; w < kMergeWarps; ++w) top = fmaxf(top, s_ml[sub][w][0]);
 #pragma unroll
             for (int w = 0; w < kMergeWarps; ++w) {
-                const float f = s_ml[w][0] == -INFINITY ? 0.f : ex2(s_ml[w][0] - top);
-                sum = fmaf(s_ml[w][1], f, sum);
-                y[0] = fmaf(s_o[w][2 * threadIdx.x], f, y[0]);
-                y[1] = fmaf(s_o[w][2 * threadIdx.x + 1], f, y[1]);
+                const float f = s_ml[sub][w][0] == -INFINITY ? 0.f : ex2(s_ml[sub][w][0] - top);
+                sum = fmaf(s_ml[sub][w][1], f, sum);
+                f2[0] = fmaf(s_o[sub][w][2 * tid], f, f2[0]);
+                f2[1] = fmaf(s_o[sub][w][2 * tid + 1], f, f2[1]);
             }
-            const int x = unit.y + r, tok = x / p.G;
-            const size_t row = (size_t)(unit.x + tok) * p.H + cut.w * p.G + (x - tok * p.G);
+            const int at = unit.y + y, tok = at / p.G;
+            const size_t row = (size_t)(unit.x + tok) * p.H + (cut.w * p.NH + head) * p.G + (at - tok * p.G);
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            reinterpret_cast<uint32_t*>(p.o + row * D)[threadIdx.x] = pack_bf16(y[0] * inv, y[1] * inv);
-            if (threadIdx.x == 0 && p.lse != nullptr) p.lse[row] = sum == 0.f ? -INFINITY : (top + lg2(sum)) * kLn2;
+            reinterpret_cast<uint32_t*>(p.o + row * D)[tid] = pack_bf16(f2[0] * inv, f2[1] * inv);
+            if (tid == 0 && p.lse != nullptr) p.lse[row] = sum == 0.f ? -INFINITY : (top + lg2(sum)) * kLn2;
         }
         __syncthreads();
     }
 }
 
-template <int D, int R>
+template <int D, int R, int NH>
 cudaError_t launch(const Paged8Params& p, cudaStream_t stream) {
     static std::atomic<unsigned long long> opted{0};
-    cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(paged8_kernel<D, R>), Cfg<D, R>::SMEM_BYTES, opted);
+    cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(paged8_kernel<D, R, NH>), Cfg<D, R, NH>::SMEM_BYTES, opted);
     if (e != cudaSuccess) return e;
-    paged8_kernel<D, R><<<p.n_ctas, kThreads8, Cfg<D, R>::SMEM_BYTES, stream>>>(p);
+    paged8_kernel<D, R, NH><<<p.n_ctas, kThreads8, Cfg<D, R, NH>::SMEM_BYTES, stream>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.n_ctas, kMergeRows);
-    cfg.blockDim = dim3(kMergeWarps * 32);
+    cfg.gridDim = dim3((unsigned)p.n_ctas, kMergeCtas);
+    cfg.blockDim = dim3(kMergeRows * kMergeWarps * 32);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -1231,10 +1257,20 @@ cudaError_t launch(const Paged8Params& p, cudaStream_t stream) {
 
 }  // namespace
 
-Paged8Plan paged8_plan(int max_q_len, int G, int d) {
+// Two KV heads to a unit halve the number of units, and read rows of the cache that lie side by side together: 128 bytes
+// for two heads of d = 64, where rows of 64 bytes come at 3.2 TB/s, those of 128 at 6.2; tiles in turn with d = 128 (4
+// requests of 200 to 262 thousand keys, 8 heads: 313 instead of 343 us; 64 requests of 512 to 8192: 109 instead of 113;
+// 64 of 256: 18 instead of 21).  One unit takes longer, though: what does not fill the CTAs, or leaves each a few tiles
+// only, is faster by single heads (one request of 1024 keys: 13.6 instead of 17.2 us with d = 128, 12.6 instead of 14.1
+// with d = 64; of 131 thousand: 53 instead of 57, 44 instead of 39).  The lengths are not known here, but how long they
+// can be.  More rows than 16 to a head share their tiles well enough with d = 128.
+Paged8Plan paged8_plan(int B, int max_q_len, int H, int H_kv, int d, int page_size, int max_pages) {
     Paged8Plan pl;
-    const long long rows = (long long)max_q_len * G;
-    pl.R = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+    const long long rows = (long long)max_q_len * (H / H_kv);
+    const long long units = (long long)B * H_kv, tiles = units * (((long long)page_size * max_pages + 127) / 128);
+    const bool large = units > kPaged8Ctas || tiles > kPaged8Ctas * (d == 128 ? 32LL : 2LL);
+    pl.NH = H_kv % 2 == 0 && large && (d == 64 || rows <= 16) ? 2 : 1;
+    pl.R = rows <= 8 ? 8 * pl.NH : rows * pl.NH <= 16 ? 16 : 32;
     pl.part_ml = kPaged8Ctas * 2 * sizeof(int4);
     pl.part_o = pl.part_ml + (size_t)2 * kPaged8Ctas * pl.R * 2 * sizeof(float);
     pl.bytes = pl.part_o + (size_t)2 * kPaged8Ctas * pl.R * d * sizeof(float);
@@ -1242,8 +1278,12 @@ Paged8Plan paged8_plan(int max_q_len, int G, int d) {
 }
 
 cudaError_t launch_paged8(int d, const Paged8Params& p, cudaStream_t stream) {
-    if (d == 128) return p.R == 8 ? launch<128, 8>(p, stream) : p.R == 16 ? launch<128, 16>(p, stream) : launch<128, 32>(p, stream);
-    return p.R == 8 ? launch<64, 8>(p, stream) : p.R == 16 ? launch<64, 16>(p, stream) : launch<64, 32>(p, stream);
+    if (d == 128) {
+        if (p.NH == 2) return p.R == 16 ? launch<128, 16, 2>(p, stream) : launch<128, 32, 2>(p, stream);
+        return p.R == 8 ? launch<128, 8, 1>(p, stream) : p.R == 16 ? launch<128, 16, 1>(p, stream) : launch<128, 32, 1>(p, stream);
+    }
+    if (p.NH == 2) return p.R == 16 ? launch<64, 16, 2>(p, stream) : launch<64, 32, 2>(p, stream);
+    return p.R == 8 ? launch<64, 8, 1>(p, stream) : p.R == 16 ? launch<64, 16, 1>(p, stream) : launch<64, 32, 1>(p, stream);
 }
 
 }  // namespace attn
