@@ -296,6 +296,7 @@ __device__ void producer_role(const Paged8Params& p, uint8_t* smem, const Bars& 
     };
     while (ok) {
         if (s >= u.nt) {  // the next unit of the cut
+            long long past = -1;  // its last place, if it begins here and goes on in the CTAs after this one
             s = 0;
             u.r = -1;
             u.nt = 0;
@@ -334,11 +335,7 @@ __device__ void producer_role(const Paged8Params& p, uint8_t* smem, const Bars& 
                 const long long seen = (last_key(p, u, u.row0 + u.nr - 1) + 128LL) / 128;  // tiles that the last row sees
                 u.nt = (int)max(0LL, min((long long)n, seen - tile));
                 u.slot = n == nb ? -1 : 2 * (int)blockIdx.x + (w - tile <= w0 ? 0 : 1);
-                if (tile == 0 && n < nb && lane == 0) {  // for the merge: the unit goes on in the CTAs after this one
-                    int4* cut = p.cuts + 2 * blockIdx.x;
-                    cut[0] = make_int4(quotient(w + nb - 1, share), u.slot, u.nr, u.kvh);
-                    cut[1] = make_int4(u.q_start, u.row0, 0, 0);
-                }
+                if (tile == 0 && n < nb) past = w + nb - 1;
                 w += n;
                 break;
             }
@@ -349,6 +346,11 @@ __device__ void producer_role(const Paged8Params& p, uint8_t* smem, const Bars& 
                 if (ok) {
                     publish(uq + slot * kUnitInts, u);
                     bar_arrive(&b.uq_full[slot]);
+                    if (past >= 0) {  // for the merge
+                        int4* cut = p.cuts + 2 * blockIdx.x;
+                        cut[0] = make_int4(quotient(past, share), u.slot, u.nr, u.kvh);
+                        cut[1] = make_int4(u.q_start, u.row0, 0, 0);
+                    }
                 }
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -1056,12 +1058,22 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
     long long* wide = reinterpret_cast<long long*>(misc + 4);  // [0] start of request r0, [1 .. 12] sums of the warps
 
     griddep_launch_dependents();  // the merge may be scheduled; it waits for this grid
-    // ---- the cut: tiles of all requests, in order, in shares of equal size
-    const int per = (p.B + kThreads8 - 1) / kThreads8;
+    // ---- the cut: tiles of all requests, in order, in shares of equal size.  Warp 0, which needs it, makes it for up to 64
+    // requests, without a barrier; all threads do for more.
+    const bool few = p.B <= 64, cutter = !few || warp == 0;
+    const int per = few ? (p.B + 31) >> 5 : (p.B + kThreads8 - 1) / kThreads8;
     const int ra = min(p.B, tid * per), rb = min(p.B, ra + per);
-    Extent e = extent(p, min(ra, p.B - 1));  // its load is under way during the set-up
-    if (tid < C::N_BARS) {
-        uint64_t* x = bars + tid;
+    Extent e{}, e2{};
+    if (cutter) {  // the loads are under way during the set-up
+        e = extent(p, min(ra, p.B - 1));
+        if (few) e2 = extent(p, min(ra + 1, p.B - 1));
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_holder, C::TM_COLS);
+        tmem_relinquish();
+    }
+    if (tid >= 64 && tid - 64 < C::N_BARS) {
+        uint64_t* x = bars + tid - 64;
         bar_init(x, x >= b.uq_empty ? 11 : x >= b.o_full && x < b.done ? 2 : x >= b.p_full && x < b.o_full ? 256 : x >= b.sc_empty && x < b.s_full ? 8
                     : x >= b.q_empty && x < b.sc_full ? 9 : 1);
         bar_init_fence();
@@ -1070,68 +1082,72 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
         *abort_flag = 0;
         misc[2] = timeout_recorded(p.status) ? 1 : 0;  // an earlier launch gave up
     }
-    if (warp == 0) {
-        tmem_alloc(tmem_holder, C::TM_COLS);
-        tmem_relinquish();
-    }
-    for (int i = tid; i < NH * D; i += kThreads8) reinterpret_cast<int*>(smem + C::OFF_NAN)[i] = 0x7fffffff;
-    long long sum = 0;
-    bool bad = false;
+    for (int i = kThreads8 - 1 - tid; i < NH * D; i += kThreads8) reinterpret_cast<int*>(smem + C::OFF_NAN)[i] = 0x7fffffff;
+    long long share = 0, w0 = 0, w1 = 0;
+    if (cutter) {
+        long long sum = 0, total;
+        bool bad = false;
 #pragma unroll 1
-    for (int r = ra; r < rb; ++r) {
-        if (r > ra) e = extent(p, r);
-        bad |= e.bad;
-        sum += work_of(p, e);
-    }
-    if (bad && blockIdx.x == 0) atomicOr(p.status, 1u << kStatusDeviceData);
-    long long before = sum;
+        for (int r = ra; r < rb; ++r) {
+            const Extent x = r == ra ? e : few ? e2 : extent(p, r);
+            bad |= x.bad;
+            sum += work_of(p, x);
+        }
+        if (bad && blockIdx.x == 0) atomicOr(p.status, 1u << kStatusDeviceData);
+        long long before = sum;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += y;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += y;
+        }
+        total = __shfl_sync(0xffffffffu, before, 31);
+        before -= sum;
+        if (!few) {
+            if (lane == 31) wide[1 + warp] = total;
+            __syncthreads();
+            total = 0;
+#pragma unroll 1
+            for (int w = 0; w < kThreads8 / 32; ++w) {
+                if (w < warp) before += wide[1 + w];
+                total += wide[1 + w];
+            }
+        }
+        share = total < 0x7fff0000LL ? max((unsigned)kMinShare, ((unsigned)total + gridDim.x - 1) / gridDim.x)
+                                     : long_quotient(total + gridDim.x - 1, gridDim.x);
+        w0 = (long long)blockIdx.x * share;
+        w1 = min(total, w0 + share);
+        if (w0 >= before && w0 < before + sum) {  // this thread's requests hold the CTA's first tile
+            long long at = before;
+#pragma unroll 1
+            for (int r = ra; r < rb; ++r) {
+                const Extent x = r == ra ? e : few ? e2 : extent(p, r);
+                const long long work = work_of(p, x);
+                if (w0 < at + work) {
+                    misc[3] = r;
+                    wide[0] = at;
+                    int* first = misc + kMiscFirst;
+                    first[0] = x.q_start;
+                    first[1] = x.q_len;
+                    first[2] = x.kv_len;
+                    break;
+                }
+                at += work;
+            }
+        }
+        if (tid == 0) p.cuts[2 * blockIdx.x].x = -1;  // the producer (this thread) may put a cut in its place
     }
-    if (lane == 31) wide[1 + warp] = before;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    long long total = 0;
-    before -= sum;
-#pragma unroll
-    for (int w = 0; w < kThreads8 / 32; ++w) {
-        if (w < warp) before += wide[1 + w];
-        total += wide[1 + w];
-    }
-    const long long share = total < 0x7fff0000LL ? max((unsigned)kMinShare, ((unsigned)total + gridDim.x - 1) / gridDim.x)
-                                                 : long_quotient(total + gridDim.x - 1, gridDim.x);
-    const long long w0 = (long long)blockIdx.x * share, w1 = min(total, w0 + share);
-    if (w0 >= before && w0 < before + sum) {  // this thread's requests hold the CTA's first tile
-        long long at = before;
-#pragma unroll 1
-        for (int r = ra; r < rb; ++r) {
-            if (per > 1) e = extent(p, r);
-            const long long work = work_of(p, e);
-            if (w0 < at + work) {
-                misc[3] = r;
-                wide[0] = at;
-                int* first = misc + kMiscFirst;
-                first[0] = e.q_start;
-                first[1] = e.q_len;
-                first[2] = e.kv_len;
-                break;
-            }
-            at += work;
-        }
-    }
-    if (tid == 0) p.cuts[2 * blockIdx.x].x = -1;  // the producer (this thread) may put a cut in its place
-    __syncthreads();
     const uint32_t tmem = *tmem_holder;
-    if (misc[2] == 0 && w0 < total) {
+    if (misc[2] == 0) {
         if (warp >= 2 && warp < 10) {
             softmax_role<D, R, NH>(p, smem, b, uq, abort_flag, tmem, warp - 2, warp & 3, lane);
         } else if (warp == 0) {
+            const bool any = w0 < w1;  // otherwise its first unit is the end
             const int* first = misc + kMiscFirst;
-            producer_role<D, R, NH>(p, smem, b, uq, abort_flag, lane, misc[3], w0, w1, wide[0],
-                                Extent{first[0], first[1], first[2], false}, share);
+            producer_role<D, R, NH>(p, smem, b, uq, abort_flag, lane, any ? misc[3] : 0, w0, w1, any ? wide[0] : 0,
+                                    Extent{first[0], first[1], first[2], false}, share);
         } else if (warp == 10) {
             query_role<D, R, NH>(p, smem, b, uq, abort_flag, lane);
         } else if (warp == 11) {
@@ -1148,7 +1164,7 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) {
+    if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, C::TM_COLS);
     }

@@ -9,6 +9,7 @@ Argument marshalling only, as in the package itself, which re-exports every name
     their shapes say how many rows share a scale.
 """
 import ctypes
+import functools
 import math
 
 import torch
@@ -59,6 +60,13 @@ def attn_paged_fwd_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_se
 
 # ---------------------------------------------------------------- torch helpers
 
+_Strides = ctypes.c_longlong * 8
+_bf16, _f8, _f32, _i32 = torch.bfloat16, torch.float8_e4m3fn, torch.float32, torch.int32
+
+# Decode steps ask for the same few sizes again and again, and the answer is a function of them.
+_workspace_bytes = functools.lru_cache(maxsize=1024)(attn_paged_fwd_fp8_workspace_size)
+
+
 def _cache(k_cache, v_cache, k_scale, v_scale, dev):
     """Checked addresses of a cache's codes and scales, and (num_pages, page_size, block, H_kv, d)."""
     _dims(k_cache, "k_cache", 4)
@@ -67,9 +75,9 @@ def _cache(k_cache, v_cache, k_scale, v_scale, dev):
     per_page = k_scale.shape[2]
     if per_page < 1 or page_size % per_page:
         raise ValueError("k_scale has %d scales for the %d rows of a page" % (per_page, page_size))
-    f8, f32, scales = torch.float8_e4m3fn, torch.float32, (num_pages, H_kv, per_page)
-    return ((_check(k_cache, "k_cache", f8, dev, shape), _check(v_cache, "v_cache", f8, dev, shape),
-             _check(k_scale, "k_scale", f32, dev, scales), _check(v_scale, "v_scale", f32, dev, scales)),
+    scales = (num_pages, H_kv, per_page)
+    return ((_check(k_cache, "k_cache", _f8, dev, shape), _check(v_cache, "v_cache", _f8, dev, shape),
+             _check(k_scale, "k_scale", _f32, dev, scales), _check(v_scale, "v_scale", _f32, dev, scales)),
             (num_pages, page_size, page_size // per_page, H_kv, d))
 
 
@@ -83,7 +91,7 @@ def paged_append_fp8(q, k, v, k_cache, v_cache, k_scale, v_scale, slots, positio
     negative: the token is skipped, its row of q_out left as it was.  positions int32 [T] and inv_freq as for
     ``rope``; both None: nothing rotates.  q_out may be q.  Returns q_out."""
     dev = _device(k, "k")
-    bf = torch.bfloat16
+    bf = _bf16
     _dims(k, "k", 3)
     if (positions is None) != (inv_freq is None):
         raise ValueError("positions and inv_freq go together")
@@ -110,7 +118,7 @@ def paged_append_fp8(q, k, v, k_cache, v_cache, k_scale, v_scale, slots, positio
         pp = _check(positions, "positions", torch.int32, dev, (T,))
     st = lib().attn_paged_append_fp8(qp, qop, kp, vp, *cache, _check(slots, "slots", torch.int32, dev, (T,)), pp, fp, bits,
                                      T, H, H_kv, d, rot, page_size, block, num_pages,
-                                     (ctypes.c_longlong * 8)(*qs, *qos, *ks, *vs), int(bool(interleaved)),
+                                     _Strides(*qs, *qos, *ks, *vs), int(bool(interleaved)),
                                      float(amplitude), _handle(stream, dev))
     _raise(st, "attn_paged_append_fp8")
     return q_out
@@ -164,7 +172,7 @@ def paged_fwd_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, 
     if cd != d:
         raise ValueError("q has head dim %d, the cache %d" % (d, cd))
     B, max_pages = block_table.shape
-    i32 = torch.int32
+    i32 = _i32
     cp = None
     if cu_seqlens_q is not None:
         cp = _check(cu_seqlens_q, "cu_seqlens_q", i32, dev, (B + 1,))
@@ -179,7 +187,7 @@ def paged_fwd_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, 
         if lse is None and return_lse:
             lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
         if workspace is None:
-            need = lib().attn_paged_fwd_fp8_workspace_size(B, T, max_q_len, H, H_kv, d, page_size, max_pages)
+            need = _workspace_bytes(B, T, max_q_len, H, H_kv, d, page_size, max_pages)
             if need == 0:
                 raise AttnError(ATTN_ERR_UNSUPPORTED, "attn_paged_fwd_fp8_workspace_size")
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
