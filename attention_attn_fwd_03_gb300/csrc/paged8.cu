@@ -126,13 +126,28 @@ struct Extent {
     bool bad;
 };
 
-__device__ __forceinline__ Extent extent(const Paged8Params& p, int r) {
+// A request's numbers as they are in memory, and what they say.
+struct Raw {
+    int q0, q1, len;
+};
+__device__ __forceinline__ Raw raw_extent(const Paged8Params& p, int r) {
+    Raw x;
+    x.q0 = r;
+    x.q1 = r + 1;
+    if (p.cu_q != nullptr) {
+        x.q0 = __ldg(p.cu_q + r);
+        x.q1 = __ldg(p.cu_q + r + 1);
+    }
+    x.len = __ldg(p.seq_lens + r);
+    return x;
+}
+__device__ __forceinline__ Extent extent_of(const Paged8Params& p, const Raw& x) {
     Extent e;
     e.bad = false;
-    e.q_start = r;
+    e.q_start = x.q0;
     e.q_len = 1;
     if (p.cu_q != nullptr) {
-        const int a = __ldg(p.cu_q + r), b = __ldg(p.cu_q + r + 1);
+        const int a = x.q0, b = x.q1;
         e.q_start = a;
         e.q_len = b - a;
         if (a < 0 || b < a || b > p.total_q || e.q_len > p.max_q_len) {
@@ -141,7 +156,7 @@ __device__ __forceinline__ Extent extent(const Paged8Params& p, int r) {
             e.q_len = 0;
         }
     }
-    e.kv_len = __ldg(p.seq_lens + r);
+    e.kv_len = x.len;
     const int cap = p.max_pages << p.page_shift;
     if (e.kv_len < 0 || e.kv_len > cap) {
         e.bad = true;
@@ -149,6 +164,8 @@ __device__ __forceinline__ Extent extent(const Paged8Params& p, int r) {
     }
     return e;
 }
+
+__device__ __forceinline__ Extent extent(const Paged8Params& p, int r) { return extent_of(p, raw_extent(p, r)); }
 
 // Key tiles of every unit of a request (one at least, so that its rows are written), its row tiles, and its
 // size in the cut, where each unit counts kUnitCost tiles more: what its start and end take.
@@ -218,6 +235,12 @@ __device__ __forceinline__ void st_zero16(uint32_t addr) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
 }
 
+// 16 bytes from global to shared memory, or zeros; and the wait for a thread's own.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // Two fp16 numbers <-> two e4m3 numbers (nearest, saturating; NaN stays NaN).
 __device__ __forceinline__ uint32_t e4m3_of(uint32_t h2) {
     uint16_t r;
@@ -278,9 +301,9 @@ __device__ void producer_role(const Paged8Params& p, uint8_t* smem, const Bars& 
     const long long w0 = w;
     int kv_idx = 0, pub = 0;
     bool ok = true;
-    // lane i: extent of request base + i (that of the first is known: the loads are not waited for)
+    // lane i: request base + i (the first one's extent is known: the loads are not waited for)
     int base = r;
-    Extent mine = extent(p, min(base + lane, p.B - 1));
+    Raw mine = raw_extent(p, min(base + lane, p.B - 1));
     int prev_rows[2] = {0, 0}, prev_nt = 0, prev_kvh = 0;  // the step whose V tiles are due
     Unit u{};
     int s = 0, id[2] = {-1, -1};
@@ -306,11 +329,10 @@ __device__ void producer_role(const Paged8Params& p, uint8_t* smem, const Bars& 
                     start += work;
                     if (++r >= base + 32) {
                         base = r;
-                        mine = extent(p, min(base + lane, p.B - 1));
+                        mine = raw_extent(p, min(base + lane, p.B - 1));
                     }
-                    e.q_start = __shfl_sync(0xffffffffu, mine.q_start, r - base);
-                    e.q_len = __shfl_sync(0xffffffffu, mine.q_len, r - base);
-                    e.kv_len = __shfl_sync(0xffffffffu, mine.kv_len, r - base);
+                    e = extent_of(p, Raw{__shfl_sync(0xffffffffu, mine.q0, r - base), __shfl_sync(0xffffffffu, mine.q1, r - base),
+                                         __shfl_sync(0xffffffffu, mine.len, r - base)});
                     continue;
                 }
                 const int nb = key_tiles(e), nqt = row_tiles(p, e), size = nb + kUnitCost;
@@ -621,8 +643,7 @@ __device__ void query_role(const Paged8Params& p, uint8_t* smem, const Bars& b, 
                          int lane) {
     using C = Cfg<D, R, NH>;
     constexpr int LPR = D / 8;         // lanes of a query row, 8 elements each
-    constexpr int GROUP = R < 16 || D == 128 ? 8 : 16;  // rows whose loads are in flight together
-    constexpr int PASS = GROUP * LPR / 32;
+    constexpr int PASS = R * LPR / 32;
     const uint32_t sbase = smem_u32(smem);
     int units = 0;
     for (int k = 0;; ++k) {
@@ -643,53 +664,65 @@ __device__ void query_role(const Paged8Params& p, uint8_t* smem, const Bars& b, 
                                     (u.q_start + tok) * p.H + (u.kvh * NH + lane / C::RH) * p.G + (row - tok * p.G), 0);
         }
         __syncwarp();
+        // A row goes as it is to the place of its codes, the first half where hi will be, the second where lo will be, and
+        // is taken from there: a rolled loop without loads' latency in it.  (Unrolled over registers, its first run waits
+        // for instructions.)  A lane's row in pass i and its 8 elements; two heads that share operand rows go together.
+        auto row_at = [&](int i) {
+            const int x = (i * 32 + lane) / LPR;
+            return C::WIDE ? (x & 1) * C::RH + (x >> 1) : x;
+        };
+        auto place = [&](int r, int half) {  // of a row's hi (0) or lo (1)
+            return q_at + (uint32_t)(((C::WIDE ? 0 : r / C::RH * 2 * C::RH) + half * C::RH + r % C::RH) * C::W + (C::WIDE ? r / C::RH * D : 0));
+        };
+        const int part = lane % LPR;
+#pragma unroll
+        for (int i = 0; i < PASS; ++i) {
+            const int r = row_at(i);
+            const bool there = r % C::RH < u.nr;
+            copy16(place(r, part / (LPR / 2)) + (uint32_t)(part % (LPR / 2) * 16),
+                   p.q + (there ? (size_t)(unsigned)s_row[r].z * D + part * 8 : 0), there);
+        }
+        copies_wait();
+        __syncwarp();
 #pragma unroll 1
-        for (int g0 = 0; g0 < R; g0 += GROUP) {
-            uint4 x[PASS];
+        for (int i = 0; i < PASS; ++i) {
+            const int r = row_at(i);
+            uint32_t word[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(word[0]), "=r"(word[1]), "=r"(word[2]), "=r"(word[3])
+                         : "r"(place(r, part / (LPR / 2)) + (uint32_t)(part % (LPR / 2) * 16)) : "memory");
+            __syncwarp();  // the pass's rows have been read
+            float f[8], top = 0.f;
 #pragma unroll
-            for (int i = 0; i < PASS; ++i) {
-                const int r = g0 + (i * 32 + lane) / LPR;
-                x[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (r % C::RH < u.nr)
-                    x[i] = *reinterpret_cast<const uint4*>(p.q + (size_t)(unsigned)s_row[r].z * D + lane % LPR * 8);
+            for (int c = 0; c < 8; ++c) {
+                f[c] = c & 1 ? bf16hi_to_f32(word[c / 2]) : bf16lo_to_f32(word[c / 2]);
+                const float a = fabsf(f[c]);
+                top = fmaxf(top, a < INFINITY ? a : 0.f);
             }
 #pragma unroll
-            for (int i = 0; i < PASS; ++i) {
-                const int r = g0 + (i * 32 + lane) / LPR;
-                const uint32_t* word = reinterpret_cast<const uint32_t*>(&x[i]);
-                float f[8], top = 0.f;
+            for (int o = LPR / 2; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float qs = scale_for(top), inv = 1.f / qs;
+            uint32_t hi[2], lo[2];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    f[c] = c & 1 ? bf16hi_to_f32(word[c / 2]) : bf16lo_to_f32(word[c / 2]);
-                    const float a = fabsf(f[c]);
-                    top = fmaxf(top, a < INFINITY ? a : 0.f);
-                }
-#pragma unroll
-                for (int o = LPR / 2; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                const float qs = scale_for(top), inv = 1.f / qs;
-                uint32_t hi[2], lo[2];
-#pragma unroll
-                for (int c = 0; c < 8; c += 2) {
-                    // an infinity or NaN: x - x makes a NaN of it
-                    const float a = fmaf(f[c], inv, f[c] - f[c]), d = fmaf(f[c + 1], inv, f[c + 1] - f[c + 1]);
-                    uint16_t e, e2;
-                    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e) : "f"(d), "f"(a));
-                    const uint32_t back = half2_of(e);
-                    const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&back));
-                    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e2) : "f"((d - w.y) * 16.f), "f"((a - w.x) * 16.f));
-                    hi[c / 4] = c & 2 ? hi[c / 4] | (uint32_t)e << 16 : (uint32_t)e;
-                    lo[c / 4] = c & 2 ? lo[c / 4] | (uint32_t)e2 << 16 : (uint32_t)e2;
-                }
-                // a head's rows: hi, lo; its operand is a tile of its own, or its half of the rows of the common one
-                const int byte = lane % LPR * 8 + (C::WIDE ? r / C::RH * D : 0), head = C::WIDE ? 0 : r / C::RH;
-                auto at = [&](int row) {
-                    const int chunk = (byte >> 4) ^ (C::W == 128 ? row & 7 : (row >> 1) & 3);
-                    return q_at + (uint32_t)((head * 2 * C::RH + row) * C::W + chunk * 16 + (byte & 15));
-                };
-                st_v2(at(r % C::RH), hi[0], hi[1]);
-                st_v2(at(C::RH + r % C::RH), lo[0], lo[1]);
-                if (lane % LPR == 0) s_row[r].x = __float_as_int(qs * p.c_scale);
+            for (int c = 0; c < 8; c += 2) {
+                // an infinity or NaN: x - x makes a NaN of it
+                const float a = fmaf(f[c], inv, f[c] - f[c]), d = fmaf(f[c + 1], inv, f[c + 1] - f[c + 1]);
+                uint16_t e, e2;
+                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e) : "f"(d), "f"(a));
+                const uint32_t back = half2_of(e);
+                const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&back));
+                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e2) : "f"((d - w.y) * 16.f), "f"((a - w.x) * 16.f));
+                hi[c / 4] = c & 2 ? hi[c / 4] | (uint32_t)e << 16 : (uint32_t)e;
+                lo[c / 4] = c & 2 ? lo[c / 4] | (uint32_t)e2 << 16 : (uint32_t)e2;
             }
+            // a head's rows: hi, lo; its operand is a tile of its own, or its half of the rows of the common one
+            const int byte = lane % LPR * 8 + (C::WIDE ? r / C::RH * D : 0), head = C::WIDE ? 0 : r / C::RH;
+            auto at = [&](int row) {
+                const int chunk = (byte >> 4) ^ (C::W == 128 ? row & 7 : (row >> 1) & 3);
+                return q_at + (uint32_t)((head * 2 * C::RH + row) * C::W + chunk * 16 + (byte & 15));
+            };
+            st_v2(at(r % C::RH), hi[0], hi[1]);
+            st_v2(at(C::RH + r % C::RH), lo[0], lo[1]);
+            if (lane % LPR == 0) s_row[r].x = __float_as_int(qs * p.c_scale);
         }
         fence_async_smem();
         __syncwarp();
