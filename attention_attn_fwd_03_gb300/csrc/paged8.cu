@@ -170,9 +170,11 @@ __device__ __forceinline__ Extent extent(const Paged8Params& p, int r) { return 
 // Key tiles of every unit of a request (one at least, so that its rows are written), its row tiles, and its
 // size in the cut, where each unit counts kUnitCost tiles more: what its start and end take.
 __device__ __forceinline__ int key_tiles(const Extent& e) { return max(1, (int)(((long long)e.kv_len + 127) / 128)); }
-__device__ __forceinline__ int row_tiles(const Paged8Params& p, const Extent& e) { return (e.q_len * p.G + p.RH - 1) / p.RH; }
+template <int RH>
+__device__ __forceinline__ int row_tiles(const Paged8Params& p, const Extent& e) { return (e.q_len * p.G + RH - 1) / RH; }
+template <int RH>
 __device__ __forceinline__ long long work_of(const Paged8Params& p, const Extent& e) {
-    return (long long)p.kv_units * row_tiles(p, e) * (key_tiles(e) + kUnitCost);
+    return (long long)p.kv_units * row_tiles<RH>(p, e) * (key_tiles(e) + kUnitCost);
 }
 
 // a / b (both positive, the quotient an int), by a 32-bit division where that will do: the 64-bit one takes a noticeable
@@ -195,7 +197,7 @@ __device__ __forceinline__ Unit read_unit(const volatile int* q) {
 
 // Position of row x of a unit's request in the request, and with the causal mask its last visible key.
 __device__ __forceinline__ int last_key(const Paged8Params& p, const Unit& u, int x) {
-    if (!p.causal) return u.kv_len - 1;
+    if (!p.causal || u.q_len == 1) return u.kv_len - 1;
     return (int)min((long long)u.kv_len - 1, (long long)u.kv_len - u.q_len + x / p.G);
 }
 
@@ -324,7 +326,7 @@ __device__ void producer_role(const Paged8Params& p, uint8_t* smem, const Bars& 
             u.r = -1;
             u.nt = 0;
             while (w < w1) {
-                const long long work = work_of(p, e);
+                const long long work = work_of<C::RH>(p, e);
                 if (w - start >= work) {
                     start += work;
                     if (++r >= base + 32) {
@@ -335,7 +337,7 @@ __device__ void producer_role(const Paged8Params& p, uint8_t* smem, const Bars& 
                                          __shfl_sync(0xffffffffu, mine.len, r - base)});
                     continue;
                 }
-                const int nb = key_tiles(e), nqt = row_tiles(p, e), size = nb + kUnitCost;
+                const int nb = key_tiles(e), nqt = row_tiles<C::RH>(p, e), size = nb + kUnitCost;
                 const long long off = w - start;
                 const int unit = quotient(off, size);
                 int at = (int)(off - (long long)unit * size);  // place in the unit: kUnitCost, then its tiles
@@ -347,7 +349,7 @@ __device__ void producer_role(const Paged8Params& p, uint8_t* smem, const Bars& 
                 const int tile = at - kUnitCost;
                 const int n = (int)min((long long)(nb - tile), w1 - w);
                 u.r = r;
-                u.kvh = unit / nqt;
+                u.kvh = nqt == 1 ? unit : unit / nqt;
                 u.q_start = e.q_start;
                 u.q_len = e.q_len;
                 u.kv_len = e.kv_len;
@@ -1124,7 +1126,7 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
         for (int r = ra; r < rb; ++r) {
             const Extent x = r == ra ? e : few ? e2 : extent(p, r);
             bad |= x.bad;
-            sum += work_of(p, x);
+            sum += work_of<C::RH>(p, x);
         }
         if (bad && blockIdx.x == 0) atomicOr(p.status, 1u << kStatusDeviceData);
         long long before = sum;
@@ -1154,7 +1156,7 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
 #pragma unroll 1
             for (int r = ra; r < rb; ++r) {
                 const Extent x = r == ra ? e : few ? e2 : extent(p, r);
-                const long long work = work_of(p, x);
+                const long long work = work_of<C::RH>(p, x);
                 if (w0 < at + work) {
                     misc[3] = r;
                     wide[0] = at;
