@@ -932,8 +932,9 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
                         now.x = fmaxf(now.x, x.x);
                         now.y = fmaxf(now.y, x.y);
                     }
-                    // (a bound on the factor below: values 2^-110 of the scores' weight are as good as zero)
-                    now.y = fmaxf(now.y, now.x - 110.f);
+                    // (so that P's factor, and its inverse at the unit's end, stay normal numbers: scales of V are 2^-126 at least;
+                    // P of a row whose own are all below 2^-120 is smaller than it might be, by up to 2^6)
+                    now.y = fmaxf(now.y, now.x - 120.f);
                     const float m = now.x == -INFINITY ? 0.f : now.x;
                     s_stat[gtid] = now;
                     s_par[gtid] = make_float2(m, now.y == -INFINITY ? 0.f : ex2(m - now.y + kBase));
