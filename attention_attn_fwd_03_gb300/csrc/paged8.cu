@@ -81,7 +81,7 @@ struct Cfg {
     static constexpr int OFF_KV = 0;
     static constexpr int OFF_P = OFF_KV + NST * TILE;
     static constexpr int OFF_Q = OFF_P + PBUF * SB * TPK * PTILE;
-    static constexpr int OFF_SC = OFF_Q + 2 * QBYTES;                 // float2 [2][NH][SB * 128]: ks, log2 vs of each key (or 2 .. 16 keys)
+    static constexpr int OFF_SC = OFF_Q + 2 * QBYTES;                 // float2 [2][NH][SB * 128]: ks, vs of each key (or 2 .. 16 keys)
     static constexpr int OFF_ROW = OFF_SC + 2 * NH * SB * 128 * 8;         // int4 [2][R]: factor, last visible key, output row
     static constexpr int OFF_STAT = OFF_ROW + 2 * R * 16;             // float2 [R]: running maxima of s and of s + log2 vs
     static constexpr int OFF_PAR = OFF_STAT + R * 8;                  // float2 [R]: the maximum, and P's factor
@@ -103,7 +103,7 @@ struct Bars {
     uint64_t* kv_empty;  // [NST]
     uint64_t* q_full;    // [2] query rows prepared
     uint64_t* q_empty;   // [2] the unit's last S product, and the eight softmax warps
-    uint64_t* sc_full;   // [2] scales of a step
+    uint64_t* sc_full;   // [2] scales of a step: 32 lanes' copies
     uint64_t* sc_empty;  // [2] eight softmax warps
     uint64_t* s_full;    // [2]
     uint64_t* p_full;    // [2] 256 arrivals per step
@@ -237,9 +237,15 @@ __device__ __forceinline__ void st_zero16(uint32_t addr) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
 }
 
-// 16 bytes from global to shared memory, or zeros; and the wait for a thread's own.
+// 16 or 4 bytes from global to shared memory, or zeros; and the wait for a thread's own.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {  // this thread's arrival, once its copies are there
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
@@ -488,6 +494,7 @@ __device__ void mma_role(const Paged8Params& p, uint8_t* smem, const Bars& b, vo
     auto tiles = [&](int count, auto issue) -> bool {
         bool ok = true;
         if (lane == 0) {
+#pragma unroll 1
             for (int t = 0; t < count; ++t) {
                 ok = wait_short(&b.kv_full[stage], (uint32_t)phase, abort_flag, p.status);
                 if (!ok) break;
@@ -523,6 +530,7 @@ __device__ void mma_role(const Paged8Params& p, uint8_t* smem, const Bars& b, vo
                                  !prev_first || t >= TPK);
         };
         if (!tiles(whole * TPK, product)) return false;
+#pragma unroll 1
         for (int x = whole * TPK; x < nt * TPK; ++x) {
             const int t = x / TPK;
             if (!warp_wait(&b.kv_full[stage], (uint32_t)phase, abort_flag, p.status)) return false;
@@ -600,6 +608,7 @@ __device__ void mma_role(const Paged8Params& p, uint8_t* smem, const Bars& b, vo
                 product_s<D, R, NH>(d + (uint32_t)(t * (2 * R / TPK)), kv_desc + tile, q_desc + (uint64_t)(t % TPK * (C::QBYTES / TPK >> 4)));
             };
             if (!tiles(whole * TPK, product)) return;
+#pragma unroll 1
             for (int t = whole * TPK; t < nt * TPK; ++t) {
                 if (!warp_wait(&b.kv_full[stage], (uint32_t)phase, abort_flag, p.status)) return;
                 clear_rows<W>(sbase + C::OFF_KV + (uint32_t)(stage * C::TILE), keys - whole * 128, lane);
@@ -677,7 +686,7 @@ __device__ void query_role(const Paged8Params& p, uint8_t* smem, const Bars& b, 
             return q_at + (uint32_t)(((C::WIDE ? 0 : r / C::RH * 2 * C::RH) + half * C::RH + r % C::RH) * C::W + (C::WIDE ? r / C::RH * D : 0));
         };
         const int part = lane % LPR;
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < PASS; ++i) {
             const int r = row_at(i);
             const bool there = r % C::RH < u.nr;
@@ -740,50 +749,52 @@ __device__ void scale_role(const Paged8Params& p, uint8_t* smem, const Bars& b, 
     using C = Cfg<D, R, NH>;
     const int per_page = p.page_shift - p.block_shift;
     const int gshift = min(p.block_shift, 4);  // keys that share an entry of s_scale: 1 to 16
+    const uint32_t at0 = smem_u32(smem + C::OFF_SC);
     uint32_t n = 0;
-    for (int k = 0;; ++k) {
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
         const int slot = k % kQN;
-        if (!warp_wait(&b.uq_full[slot], (uint32_t)((k / kQN) & 1), abort_flag, p.status)) return;
+        if (!warp_wait(&b.uq_full[slot], (uint32_t)((k / kQN) & 1), abort_flag, p.status)) break;
         const Unit u = read_unit(uq + slot * kUnitInts);
         __syncwarp();
         if (lane == 0) bar_arrive(&b.uq_empty[slot]);
-        if (u.r < 0) return;
+        if (u.r < 0) break;
+#pragma unroll 1
         for (int s = 0; s < u.nt; s += C::SB, ++n) {
             const uint32_t buf = n & 1u;
             const int groups = (min(C::SB, u.nt - s) * 128) >> gshift;
-            float2* dst = reinterpret_cast<float2*>(smem + C::OFF_SC) + buf * NH * C::SB * 128;
-            bool free = n < 2;
+            const long long key0 = (long long)(u.tile0 + s) * 128;
+            // pages of the step (64 at most): x in lane x % 32, register x / 32
+            const long long page0 = key0 >> p.page_shift;
+            int id[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const long long page = page0 + i * 32 + lane, key = page << p.page_shift;
+                id[i] = -1;
+                if (key < key0 + C::SB * 128 && key < u.kv_len) id[i] = __ldg(p.block_table + (size_t)u.r * p.max_pages + page);
+            }
+            if (n >= 2 && !(ok = warp_wait(&b.sc_empty[buf], ((n >> 1) - 1u) & 1u, abort_flag, p.status))) break;
 #pragma unroll 1
-            for (int g0 = 0; g0 < NH * groups; g0 += 128) {
-                float2 v[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {  // four groups' loads in flight
-                    const int x = g0 + i * 32 + lane, head = NH == 2 && x >= groups, g = x - head * groups;
-                    const long long key = (long long)(u.tile0 + s) * 128 + ((long long)g << gshift);
-                    v[i] = make_float2(0.f, 0.f);
-                    if (g < groups && key < u.kv_len) {
-                        const int id = __ldg(p.block_table + (size_t)u.r * p.max_pages + (key >> p.page_shift));
-                        if (id >= 0 && id < p.num_pages) {
-                            const size_t at = (((size_t)(unsigned)id * p.H_kv + u.kvh * NH + head) << per_page) +
-                                              (((int)key & ((1 << p.page_shift) - 1)) >> p.block_shift);
-                            v[i] = make_float2(__ldg(p.k_scale + at), __ldg(p.v_scale + at));
-                        }
-                    }
-                }
-                if (!free) {
-                    if (!warp_wait(&b.sc_empty[buf], ((n >> 1) - 1u) & 1u, abort_flag, p.status)) return;
-                    free = true;
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int x = g0 + i * 32 + lane, head = NH == 2 && x >= groups;
-                    if (x < NH * groups) dst[head * C::SB * 128 + x - head * groups] = make_float2(v[i].x, lg2(v[i].y));
+            for (int x0 = 0; x0 < NH * groups; x0 += 32) {
+                const int x = x0 + lane, head = NH == 2 && x >= groups, g = x - head * groups;
+                const long long key = key0 + ((long long)g << gshift);
+                const int page = (int)((key >> p.page_shift) - page0);
+                const int id0 = __shfl_sync(0xffffffffu, id[0], page & 31), id1 = __shfl_sync(0xffffffffu, id[1], page & 31);
+                const int of = page < 32 ? id0 : id1;
+                const bool there = key < u.kv_len && of >= 0 && of < p.num_pages;
+                const size_t at = there ? (((size_t)(unsigned)of * p.H_kv + u.kvh * NH + head) << per_page) +
+                                              (((int)key & ((1 << p.page_shift) - 1)) >> p.block_shift)
+                                        : 0;
+                const uint32_t to = at0 + (uint32_t)(((buf * NH + head) * C::SB * 128 + g) * 8);
+                if (x < NH * groups) {
+                    copy4(to, p.k_scale + at, there);
+                    copy4(to + 4, p.v_scale + at, there);
                 }
             }
-            __syncwarp();
-            if (lane == 0) bar_arrive(&b.sc_full[buf]);
+            copies_arrive(&b.sc_full[buf]);
         }
     }
+    copies_wait();
 }
 
 // ---------------------------------------------------------------- softmax + epilogue (eight warps)
@@ -813,8 +824,8 @@ __device__ __forceinline__ float warp_sum8(const float* v, int lane) {
 }
 
 // A step's 32 / R x R / 8 blocks of 128 keys x 8 rows go to two groups of four warps: two blocks to a thread, whose 16
-// scores stay in registers.  Few instructions, each used often: with 32 scores a thread, everything unrolled, warps
-// waited for instructions more than for data.
+// scores stay in registers.  Few instructions, each used often: the two blocks are two turns of a rolled loop that shifts
+// their scores along.  Warps wait for instructions before they wait for data, once the loop does not fit the cache.
 template <int D, int R, int NH>
 __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b, volatile int* uq, volatile int* abort_flag,
                              uint32_t tmem, int warp8, int wq, int lane) {
@@ -869,11 +880,14 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
             wait(&b.s_full[buf], (n >> 1) & 1u);
             tc_fence_after();
             // ---- scores in log2 units, -inf where masked; the rows' maxima over the warp
-            float e[2][8], lv[2];
+            float e0[8], e1[8], vk0 = 0.f, vk1 = 0.f;  // of the thread's two blocks; their values' scales
             bool grew = s == 0;
-#pragma unroll
+#pragma unroll 1
             for (int j = 0; j < 2; ++j) {
                 const int t = tile_of(j), rb = row_of(j);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) e0[i] = e1[i];
+                vk0 = vk1;
                 if (t < nt && rb % RH < u.nr) {
                     uint32_t x[16];
                     const uint32_t col = buf * 64u + (uint32_t)(t * 2 * R + rb / RH * 2 * RH + rb % RH);
@@ -882,7 +896,7 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
                     const float2 sc = s_scale[(buf * NH + rb / RH) * SB * 128 + ((t * 128 + tid) >> gshift)];
                     // the rows of keys past the request's end are zeros
                     const float mask = (unsigned)key0 + (unsigned)(t * 128 + tid) < (unsigned)u.kv_len ? 0.f : -INFINITY;
-                    lv[j] = sc.y;
+                    vk1 = sc.y;
                     float f[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) f[i] = __int_as_float(s_row[rb + i].x) * sc.x;
@@ -890,23 +904,24 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
                     reg_after_wait<16>(x);
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        e[j][i] = fmaf(fmaf(__uint_as_float(x[8 + i]), 0.0625f, __uint_as_float(x[i])), f[i], mask);
+                        e1[i] = fmaf(fmaf(__uint_as_float(x[8 + i]), 0.0625f, __uint_as_float(x[i])), f[i], mask);
                     if (diagonal) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            if ((long long)key0 + t * 128 + tid > s_row[rb + i].y) e[j][i] = -INFINITY;
+                            if ((long long)key0 + t * 128 + tid > s_row[rb + i].y) e1[i] = -INFINITY;
                     }
                 } else {
-                    lv[j] = -INFINITY;
+                    vk1 = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) e[j][i] = -INFINITY;
+                    for (int i = 0; i < 8; ++i) e1[i] = -INFINITY;
                 }
                 if (SETS == 2 || j == 1) {
                     float a = 0.f, c = 0.f;
+                    const float lv0 = lg2(vk0), lv1 = lg2(vk1);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float top = warp_max(SETS == 2 ? e[j][i] : fmaxf(e[0][i], e[j][i]));
-                        const float top_v = warp_max(SETS == 2 ? e[j][i] + lv[j] : fmaxf(e[0][i] + lv[0], e[j][i] + lv[j]));
+                        const float top = warp_max(SETS == 2 ? e1[i] : fmaxf(e0[i], e1[i]));
+                        const float top_v = warp_max(SETS == 2 ? e1[i] + lv1 : fmaxf(e0[i] + lv0, e1[i] + lv1));
                         if (lane == i) {
                             a = top;
                             c = top_v;
@@ -967,22 +982,19 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
             // ---- probabilities
             float l[8];
 #pragma unroll
+            for (int i = 0; i < 8; ++i) l[i] = 0.f;
+#pragma unroll 1
             for (int j = 0; j < 2; ++j) {
                 const int t = tile_of(j), rb = row_of(j);
-                if (SETS == 2 || j == 0) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) l[i] = 0.f;
-                }
                 if (t < nt && rb % RH < u.nr) {
-                    const float vk = ex2(lv[j]);
                     uint32_t h[4], hi[4], mid[4], lo[4];
 #pragma unroll
                     for (int i = 0; i < 8; i += 2) {  // two rows share the conversions
                         const float2 par0 = s_par[rb + i], par1 = s_par[rb + i + 1];
-                        const float p0 = ex2(e[j][i] - par0.x), p1 = ex2(e[j][i + 1] - par1.x);
+                        const float p0 = ex2(e0[i] - par0.x), p1 = ex2(e0[i + 1] - par1.x);
                         l[i] += p0;
                         l[i + 1] += p1;
-                        h[i / 2] = pack_half(p0 * fminf(vk * par0.y, kHuge), p1 * fminf(vk * par1.y, kHuge));
+                        h[i / 2] = pack_half(p0 * fminf(vk0 * par0.y, kHuge), p1 * fminf(vk0 * par1.y, kHuge));
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) hi[i] = e4m3_of(h[i]);
@@ -1011,7 +1023,14 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
                     const float x = warp_sum8(l, lane);
                     float* sum = s_sum + warp8 * R + rb + (lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1);
                     if ((lane & 3) == 0) *sum = x + (s > 0 ? *sum : 0.f);
+                    if (SETS == 2) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) l[i] = 0.f;
+                    }
                 }
+                vk0 = vk1;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) e0[i] = e1[i];
             }
             fence_async_smem();
             tc_fence_before();
@@ -1110,7 +1129,7 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
     }
     if (tid >= 64 && tid - 64 < C::N_BARS) {
         uint64_t* x = bars + tid - 64;
-        bar_init(x, x >= b.uq_empty ? 11 : x >= b.o_full && x < b.done ? 2 : x >= b.p_full && x < b.o_full ? 256 : x >= b.sc_empty && x < b.s_full ? 8
+        bar_init(x, x >= b.uq_empty ? 11 : x >= b.o_full && x < b.done ? 2 : x >= b.p_full && x < b.o_full ? 256 : x >= b.sc_empty && x < b.s_full ? 8 : x >= b.sc_full && x < b.sc_empty ? 32
                     : x >= b.q_empty && x < b.sc_full ? 9 : 1);
         bar_init_fence();
     }
