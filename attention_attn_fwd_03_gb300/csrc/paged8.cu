@@ -57,7 +57,7 @@ constexpr float kHuge = 3e38f;
 constexpr int kQN = 4;            // unit queue between the producer and the other warps
 constexpr int kUnitInts = 10;
 constexpr int kMiscFirst = 30;   // place in the misc words of the first request's extent
-constexpr int kMinShare = 2;      // tiles
+constexpr int kMinShare = 1;      // tiles
 constexpr int kUnitCost = 2;      // tiles
 
 template <int D, int R, int NH>
@@ -1225,12 +1225,14 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
     }
 }
 
-// The units that were cut, a CTA for every fourth pair of their rows: a row's pieces to kMergeWarps warps in turn,
+// The units that were cut, gridDim.y CTAs to each, which take two of its rows at a time: a row's pieces to kMergeWarps
+// warps in turn,
 //   m = max m_i,  l = sum l_i 2^(m_i - m),  O = sum 2^(m_i - m) O_i / l.
-// The pieces are one unit's last of CTA c0 and first of the CTAs up to c1.  Their (m, l) and O are asked for at once.
+// The pieces are one unit's last of CTA c0 and first of the CTAs up to c1.  Their (m, l) and O are asked for at once.  (More
+// CTAs to a unit cost more, since most have nothing to do, than they save: 32 thousand keys of one request 21.9 us with 2,
+// 22.4 with 4; with 32 rows 58 and 55.)
 constexpr int kMergeWarps = 4;
 constexpr int kMergeRows = 2;   // of a CTA
-constexpr int kMergeCtas = 4;
 template <int D>
 __global__ void __launch_bounds__(kMergeRows * kMergeWarps * 32) paged8_merge_kernel(const __grid_constant__ Paged8Params p) {
     constexpr int PER = D / 32;
@@ -1241,7 +1243,7 @@ __global__ void __launch_bounds__(kMergeRows * kMergeWarps * 32) paged8_merge_ke
     griddep_wait();
     const int4 cut = __ldcg(p.cuts + 2 * c0), unit = __ldcg(p.cuts + 2 * c0 + 1);
     if (timeout_recorded(p.status) || cut.x < 0) return;
-    for (int x0 = blockIdx.y * kMergeRows; x0 < cut.z * p.NH; x0 += kMergeCtas * kMergeRows) {
+    for (int x0 = blockIdx.y * kMergeRows; x0 < cut.z * p.NH; x0 += gridDim.y * kMergeRows) {
         const int x = min(x0 + sub, cut.z * p.NH - 1);  // (the last row twice, if they are odd)
         const int head = x / cut.z, y = x - head * cut.z, r = head * p.RH + y;
         float m = -INFINITY, l = 0.f, acc[PER];
@@ -1318,7 +1320,7 @@ cudaError_t launch(const Paged8Params& p, cudaStream_t stream) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.n_ctas, kMergeCtas);
+    cfg.gridDim = dim3((unsigned)p.n_ctas, p.R > 16 ? 4u : 2u);
     cfg.blockDim = dim3(kMergeRows * kMergeWarps * 32);
     cfg.stream = stream;
     cfg.attrs = attr;
