@@ -20,7 +20,8 @@ Two levels:
   * ``fwd_host``: the same for host (CPU) tensors through ``attn_fwd_host``.
 
 The operators around the cache (include/attn_kv.h: rotary positions, page plans, cache appends, page
-sketches, page-sparse attention) are in ``kv``, both levels, and re-exported here.
+sketches, page-sparse attention) are in ``kv``, those on a cache held in 8 bits (include/attn_kv8.h: appends
+that quantise, reading back, attention) in ``kv8``, both levels, and re-exported here.
 """
 import ctypes
 import math

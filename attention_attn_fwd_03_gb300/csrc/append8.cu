@@ -17,6 +17,10 @@
 // matter).  Then the scales; second pass: the rows again, mostly from L1 and L2,
 // rotated and stored as codes.  Rows that a block held before are requantised by
 // the whole CTA where the scale grew.  The same launch rotates q, in CTAs of their own.
+//
+// Measured.  16,300 tokens of 8 requests, 32 + 8 heads, d = 128, blocks of 64 rows: 71 us, 5.2 TB/s of what has to move (a
+// copy: 6.8); loads are waited for more than anything, and 64 registers a thread leave 0.43 of the warps.  64
+// tokens: 5.4 us, 16 x 1 .. 8 tokens with d = 64: 4.3 us: latency (slot, rows, angles, then the block's scale).
 #include <cmath>
 #include <cstring>
 
@@ -443,7 +447,8 @@ struct Read8Params {
 constexpr int kReadRows = 8;  // rows of a CTA
 
 // Bound by memory: a code is read, two bytes (or four) written.  A CTA takes 8 rows of K and V: their
-// requests and cache rows are looked up once, then each thread moves 16 codes at a time.
+// requests and cache rows are looked up once, then each thread moves 16 codes at a time.  Measured: 57 thousand keys of 8
+// heads, d = 128, 57 us, 0.91 of a copy; 777 keys of 2 heads 2.4 us.
 template <int EB>
 __global__ void __launch_bounds__(kReadThreads) read8_kernel(const __grid_constant__ Read8Params p) {
     __shared__ int s_row[kReadRows];  // cache row, -1: left as it is, -2: zeros
