@@ -38,7 +38,7 @@
 // Measured (inputs from HBM, d = 128, 32 heads over 8 unless said).  4 requests of 200 to 262 thousand keys: 287 to 319 us
 // on different GPUs, 5.9 to 6.6 TB/s (a copy: 6.8); 64 of 512 to 8192: 99 to 108 us, 5.3 to 5.8 TB/s; 33 of 0 to 4096 with
 // 16 heads over 16: 56 us; one of 32 thousand (which stays in L2): 22 us; 8 tokens of 16 requests, d = 64, 16 heads over 2,
-// a scale to every token: 55 us, 0.9 of it in the softmax.  A call of one tile takes 11 us: 4 until the first page is asked
+// a scale to every token: 53 us, 0.9 of it in the softmax.  A call of one tile takes 11 us: 4 until the first page is asked
 // for, 4 for the tile, 2 to 3 for the merge; a unit's start and end, and the last CTAs' lead over the mean, take most of what
 // is not streaming in the others.
 #include <cuda_fp16.h>
@@ -81,10 +81,13 @@ struct Cfg {
     static constexpr int TILE = 128 * W;               // bytes of a K or V tile
     static constexpr int NST = (SB * NH == 4 ? 5 : 4) * 128 / W;  // ring stages
     static constexpr int QBYTES = 2 * R * D;
-    // A tile of P: hi, mid, lo; where those are 24 rows, the product's last 8 columns come from what follows and are not
-    // used.
-    static constexpr int PTILE = 3 * PH * 128;
-    static constexpr int PBUF = SB * NH == 4 || TPK == 2 ? 1 : 2;  // steps' P held at once
+    // A tile of P: keys as its rows and hi, mid, lo of the query rows side by side in each (a thread's eight rows are then
+    // eight bytes: 53.5 us instead of 55.4 for 8 tokens of 16 requests); for 8 rows, whose 24 bytes would take 32, hi, mid and lo as its rows.  The product's last 8 columns come
+    // from what follows then, and are not used.
+    static constexpr bool KEYS = PH >= 16;
+    static constexpr int WP = PH == 32 ? 128 : PH == 16 ? 64 : 128;  // bytes of a row of P, and its swizzle
+    static constexpr int PTILE = KEYS ? 128 * WP : 3 * PH * 128;
+    static constexpr int PBUF = SB * NH == 4 || TPK == 2 || R == 32 ? 1 : 2;  // steps' P held at once
     static constexpr uint32_t TM_O = 128;              // S: two buffers of 64 columns
     static constexpr uint32_t TM_COLS = 256;
     static constexpr int OFF_KV = 0;
@@ -478,9 +481,10 @@ __device__ __forceinline__ void product_s(uint32_t d, uint64_t k, uint64_t q) {
 // One tile's part of O^T: four blocks of 32 keys.
 template <int D, int R, int NH>
 __device__ __forceinline__ void product_pv(uint32_t o, uint64_t v, uint64_t p, bool accumulate) {
-    constexpr uint32_t ID = idesc_make(Cfg<D, R, NH>::W, Cfg<D, R, NH>::NPV, 0u, true, false);
+    constexpr uint32_t ID = idesc_make(Cfg<D, R, NH>::W, Cfg<D, R, NH>::NPV, 0u, true, Cfg<D, R, NH>::KEYS);
     constexpr int VS = (32 * Cfg<D, R, NH>::W) >> 4;  // 32 rows of V in descriptor units
-    mma4_ss<VS, 2 * VS, 3 * VS, 2, 4, 6, true>(o, v, p, ID, accumulate ? 1u : 0u);
+    constexpr int PS = Cfg<D, R, NH>::KEYS ? (32 * Cfg<D, R, NH>::WP) >> 4 : 2;
+    mma4_ss<VS, 2 * VS, 3 * VS, PS, 2 * PS, 3 * PS, true>(o, v, p, ID, accumulate ? 1u : 0u);
 }
 
 // S^T of step n + 1, then O^T += V^T P^T of step n: the order of the ring.  (Two issuers, one for each product, were
@@ -492,7 +496,7 @@ __device__ void mma_role(const Paged8Params& p, uint8_t* smem, const Bars& b, vo
     using C = Cfg<D, R, NH>;
     const uint32_t sbase = smem_u32(smem), o = tmem + C::TM_O;
     constexpr int W = C::W, TPK = C::TPK;
-    const uint64_t kv_desc = desc<W>(sbase + C::OFF_KV), p_desc = desc<128>(sbase + C::OFF_P);
+    const uint64_t kv_desc = desc<W>(sbase + C::OFF_KV), p_desc = desc<C::WP>(sbase + C::OFF_P);
     int* s_nan = reinterpret_cast<int*>(smem + C::OFF_NAN);
     int stage = 0, phase = 0, units = 0;
     uint32_t n = 0;  // steps issued
@@ -849,7 +853,8 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
     auto row_of = [&](int k) { return R == 8 ? 0 : R == 16 ? 8 * grp : 8 * grp + 16 * k; };
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t tS = tmem + lane_off, tO = tmem + lane_off + C::TM_O;
-    const uint32_t p_at = smem_u32(smem + C::OFF_P) + (uint32_t)tid;  // this key's byte of P's row 0, before the swizzle
+    // this key's row of P, or its byte of row 0 before the swizzle
+    const uint32_t p_at = smem_u32(smem + C::OFF_P) + (uint32_t)(C::KEYS ? tid * C::WP : tid);
     const float2* s_scale = reinterpret_cast<const float2*>(smem + C::OFF_SC);
     float2* s_stat = reinterpret_cast<float2*>(smem + C::OFF_STAT);
     float2* s_par = reinterpret_cast<float2*>(smem + C::OFF_PAR);
@@ -1015,17 +1020,28 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
                     for (int i = 0; i < 4; ++i) h[i] = h2_mul32(h2_sub(h[i], half2_of(mid[i])));
 #pragma unroll
                     for (int i = 0; i < 4; ++i) lo[i] = e4m3_of(h[i]);
-                    const uint32_t at = p_at + (uint32_t)((((C::PBUF == 2 ? buf : 0u) * SB + t) * C::TPK + rb / PH) * C::PTILE + rb % PH * 128);
+                    const uint32_t tile = p_at + (uint32_t)((((C::PBUF == 2 ? buf : 0u) * SB + t) * C::TPK + rb / PH) * C::PTILE);
+                    if (C::KEYS) {
+                        const uint32_t turn = (uint32_t)(C::WP == 128 ? tid & 7 : (tid >> 1) & 3) << 4;
+                        auto put = [&](int col, const uint32_t* x) {
+                            st_v2(tile + ((uint32_t)col ^ turn), x[0] | x[1] << 16, x[2] | x[3] << 16);
+                        };
+                        put(rb % PH, hi);
+                        put(PH + rb % PH, mid);
+                        put(2 * PH + rb % PH, lo);
+                    } else {
+                        const uint32_t at = tile + (uint32_t)(rb % PH * 128);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t a0 = (at ^ (uint32_t)(2 * i << 4)) + (uint32_t)(2 * i * 128);
-                        const uint32_t a1 = (at ^ (uint32_t)((2 * i + 1) << 4)) + (uint32_t)((2 * i + 1) * 128);
-                        st_u8(a0, hi[i]);
-                        st_u8(a1, hi[i] >> 8);
-                        st_u8(a0 + PH * 128, mid[i]);
-                        st_u8(a1 + PH * 128, mid[i] >> 8);
-                        st_u8(a0 + 2 * PH * 128, lo[i]);
-                        st_u8(a1 + 2 * PH * 128, lo[i] >> 8);
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t a0 = (at ^ (uint32_t)(2 * i << 4)) + (uint32_t)(2 * i * 128);
+                            const uint32_t a1 = (at ^ (uint32_t)((2 * i + 1) << 4)) + (uint32_t)((2 * i + 1) * 128);
+                            st_u8(a0, hi[i]);
+                            st_u8(a1, hi[i] >> 8);
+                            st_u8(a0 + PH * 128, mid[i]);
+                            st_u8(a1 + PH * 128, mid[i] >> 8);
+                            st_u8(a0 + 2 * PH * 128, lo[i]);
+                            st_u8(a1 + 2 * PH * 128, lo[i] >> 8);
+                        }
                     }
                 }
                 if (SETS == 2 || j == 1) {  // the rows' sums, one lane each
