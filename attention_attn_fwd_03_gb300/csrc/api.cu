@@ -772,7 +772,7 @@ attn_status_t attn_varlen_fwd(const void* q, const void* k, const void* v, const
 
 size_t attn_paged_fwd_fp8_workspace_size(int B, int total_q, int max_q_len, int H, int H_kv, int d, int page_size,
                                          int max_pages) {
-    if (paged_sizes_ok(B, total_q, max_q_len, H, H_kv, d, page_size, max_pages) != ATTN_OK) return 0;
+    if (paged_sizes_ok(B, total_q, max_q_len, H, H_kv, d, page_size, max_pages) != ATTN_OK || B > kPaged8MaxB) return 0;
     return paged8_plan(B, max_q_len, H, H_kv, d, page_size, max_pages).bytes;
 }
 
@@ -787,7 +787,7 @@ attn_status_t attn_paged_fwd_fp8(const void* q, const void* k_cache, const void*
     if (st != ATTN_OK) return st;
     st = blocks_ok(page_size, block, num_pages);
     if (st != ATTN_OK) return st;
-    if (!(std::isfinite(scale) && scale > 0.f)) return ATTN_ERR_INVALID_ARG;
+    if (B > kPaged8MaxB || !(std::isfinite(scale) && scale > 0.f)) return ATTN_ERR_INVALID_ARG;
     if (causal != 0 && causal != 1) return ATTN_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o)) return ATTN_ERR_INVALID_ARG;
     auto a4 = [](const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 3u) == 0; };

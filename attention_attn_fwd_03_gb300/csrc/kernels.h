@@ -222,6 +222,7 @@ struct Paged8Plan {
     size_t part_ml, part_o, bytes;
 };
 constexpr int kPaged8Ctas = 304;  // at most: two to each of the chip's 152 SMs
+constexpr int kPaged8MaxB = 1 << 30;  // requests are counted in ints, some hundreds past the last
 Paged8Plan paged8_plan(int B, int max_q_len, int H, int H_kv, int d, int page_size, int max_pages);
 cudaError_t launch_paged8(int d, const Paged8Params& p, cudaStream_t stream);
 

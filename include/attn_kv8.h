@@ -92,7 +92,7 @@ attn_status_t attn_paged_read_fp8(const void* k_cache, const void* v_cache, cons
  *   q, o: bf16 [total_q, H, d]; lse: fp32 [total_q, H] or NULL; block_table,
  *   cu_seqlens_q (NULL: one token per request, total_q = B and max_q_len = 1),
  *   seq_lens, max_q_len, scale, causal: as for attn_paged_fwd.  H a multiple
- *   of H_kv, H / H_kv at most 128.
+ *   of H_kv, H / H_kv at most 128; B at most 2^30.
  * Precision: the matrix units take the codes as they are, e4m3 by e4m3 with
  * fp32 sums.  q enters as two e4m3 numbers for each element over a power of two of its
  * head vector: exact where it is above 2^-12 of the vector's largest, off by less than 2^-22

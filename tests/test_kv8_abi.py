@@ -95,7 +95,7 @@ def _fwd(**kw):
     (dict(v_cache=FAKE + 8), BAD), (dict(k_scale=FAKE + 2), BAD), (dict(lse=FAKE + 2), BAD), (dict(seq_lens=FAKE + 1), BAD),
     (dict(cu_seqlens_q=FAKE + 2), BAD), (dict(d=32), UNS), (dict(H=258, H_kv=2), UNS), (dict(page_size=40, block=8), UNS),
     (dict(block=0), BAD), (dict(block=24), UNS), (dict(block=128), BAD), (dict(workspace=None), WS), (dict(workspace=FAKE + 8), WS),
-    (dict(workspace_bytes=4000), WS)])
+    (dict(workspace_bytes=4000), WS), (dict(B=(1 << 30) + 1, total_q=(1 << 30) + 1, H=1, H_kv=1, max_pages=1), BAD)])
 def test_fwd_refusals(kw, code):
     assert _fwd(**kw) == code
 
