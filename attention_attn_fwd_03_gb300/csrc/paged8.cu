@@ -1363,17 +1363,18 @@ cudaError_t launch(const Paged8Params& p, cudaStream_t stream) {
 }  // namespace
 
 // Two KV heads to a unit halve the number of units, and read rows of the cache that lie side by side together: 128 bytes
-// for two heads of d = 64, where rows of 64 bytes come at 3.2 TB/s, those of 128 at 6.2; tiles in turn with d = 128 (4
-// requests of 200 to 262 thousand keys, 8 heads: 313 instead of 343 us; 64 requests of 512 to 8192: 109 instead of 113;
-// 64 of 256: 18 instead of 21).  One unit takes longer, though: what does not fill the CTAs, or leaves each a few tiles
-// only, is faster by single heads (one request of 1024 keys: 13.6 instead of 17.2 us with d = 128, 12.6 instead of 14.1
-// with d = 64; of 131 thousand: 53 instead of 57, 44 instead of 39).  The lengths are not known here, but how long they
-// can be.  More rows than 16 to a head share their tiles well enough with d = 128.
+// for two heads of d = 64, where rows of 64 bytes come at 3.2 TB/s, those of 128 at 6.2; tiles in turn with d = 128.  Single
+// heads and pairs, d = 128: 33 requests of 0 to 4096 keys, 16 heads 64 and 56 us; 64 of 256, 8 heads 18.0 and 16.4, of 512 to
+// 8192 98 and 100 (on a GPU with slower memory 113 and 109); 4 of 200 to 262 thousand 298 and 289 (343 and 313).  d = 64: 64
+// of 256 17.1 and 12.9, 8 of 32 thousand 71 and 54.  One unit takes longer, though: what does not fill the CTAs, or leaves
+// each a few tiles only, is faster by single heads (one request of 1024 keys 11.6 and 14.9 us with d = 128, 11.3 and 12.2
+// with d = 64; of 32 thousand 20 and 25, 19 and 20; of 131 thousand 50 and 55, 41 and 39).  The lengths are not known here,
+// but how long they can be.  More rows than 16 to a head share their tiles well enough with d = 128.
 Paged8Plan paged8_plan(int B, int max_q_len, int H, int H_kv, int d, int page_size, int max_pages) {
     Paged8Plan pl;
     const long long rows = (long long)max_q_len * (H / H_kv);
     const long long units = (long long)B * H_kv, tiles = units * (((long long)page_size * max_pages + 127) / 128);
-    const bool large = units > kPaged8Ctas || tiles > kPaged8Ctas * (d == 128 ? 32LL : 2LL);
+    const bool large = units > kPaged8Ctas || tiles > kPaged8Ctas * (d == 128 ? 32LL : 8LL);
     pl.NH = H_kv % 2 == 0 && large && (d == 64 || rows <= 16) ? 2 : 1;
     pl.R = rows <= 8 ? 8 * pl.NH : rows * pl.NH <= 16 ? 16 : 32;
     pl.part_ml = kPaged8Ctas * 2 * sizeof(int4);
