@@ -191,13 +191,15 @@ def paged_fwd_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, 
             if need == 0:
                 raise AttnError(ATTN_ERR_UNSUPPORTED, "attn_paged_fwd_fp8_workspace_size")
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    wp = _check(workspace, "workspace", torch.uint8, dev, (workspace.numel(),))
+        else:
+            need = workspace.numel()
+            _check(workspace, "workspace", torch.uint8, dev, (need,))
     st = lib().attn_paged_fwd_fp8(_check(q, "q", torch.bfloat16, dev, (T, H, d)), *cache,
                                   _check(block_table, "block_table", i32, dev, (B, max_pages)), cp,
                                   _check(seq_lens, "seq_lens", i32, dev, (B,)), B, T, max_q_len, H, H_kv, d, page_size,
                                   block, max_pages, num_pages, float(scale) if scale is not None else 1.0 / math.sqrt(d),
                                   int(bool(causal)), _check(out, "out", torch.bfloat16, dev, (T, H, d)),
-                                  None if lse is None else _check(lse, "lse", torch.float32, dev, (T, H)), wp,
-                                  workspace.numel(), _handle(stream, dev))
+                                  None if lse is None else _check(lse, "lse", torch.float32, dev, (T, H)),
+                                  workspace.data_ptr(), need, _handle(stream, dev))
     _raise(st, "attn_paged_fwd_fp8")
     return out, lse

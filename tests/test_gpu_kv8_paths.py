@@ -488,3 +488,33 @@ def test_drawn_appends(seed):
     inter, amp = r.random() < 0.5, r.choice((1.0, 0.75))
     kw = dict(interleaved=inter, amplitude=amp) if rot else {}
     _check_append(c, _append(c, **kw), **kw)
+
+
+@pytest.mark.parametrize("H,H_kv,d,max_q", [(8, 2, 128, 2), (8, 2, 128, 9), (4, 1, 64, 3), (16, 2, 64, 9)])
+def test_max_q_len_above_the_longest(H, H_kv, d, max_q):
+    """Tiles for more rows than any request has: the same results, within their bounds."""
+    c = _fwd_case(47, [300, 9, 0, 2000, 64, 1, 700, 128, 5], [1] * 9, H, H_kv, d, 16, 4)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    for long in (False, True):
+        if long:
+            _long_table(c, H_kv)
+        o, lse = torch.full(c["q"].shape, 9.0, dtype=BF, device=DEV), torch.full(c["q"].shape[:2], 9.0, device=DEV)
+        attn.paged_fwd_fp8(c["q"].to(DEV), *_gpu_cache(c), c["table"].to(DEV), i32(c["lens"]), cu_seqlens_q=i32(c["cu"]), max_q_len=max_q,
+                           causal=True, out=o, lse=lse)
+        attn.device_status()
+        _check_fwd(c, True, (o.cpu(), lse.cpu()))
+
+
+@pytest.mark.parametrize("page", [8, 128, 1024])
+def test_tables_filled_to_the_last_page(page):
+    """Requests whose keys are all that the table can hold, in the last place of the cache and of the table."""
+    n = max(page, 256) * 2
+    c = _fwd_case(48 + page, [n, n - 1, n], None, 4, 2, 64, page, 8)
+    c["table"] = c["table"][:, :n // page].contiguous()
+    _check_fwd(c, True, _fwd(c, True))
+    cu = torch.tensor([0, n, 2 * n - 1, 3 * n - 1], dtype=torch.int32, device=DEV)
+    k, v = attn.paged_read_fp8(*_gpu_cache(c), c["table"].to(DEV), cu, 3 * n - 1, dtype=torch.float32)
+    attn.device_status()
+    for got, name in ((k, "k"), (v, "v")):
+        want = torch.cat([ref.values(c[name + "_cache"], c[name + "_scale"], c["table"][r], m) for r, m in enumerate(c["lens"])])
+        assert torch.equal(got.cpu().double(), want.float().double())
