@@ -81,6 +81,18 @@ def _cache(k_cache, v_cache, k_scale, v_scale, dev):
             (num_pages, page_size, page_size // per_page, H_kv, d))
 
 
+def _rows(t, name, dev, shape):
+    """Address of bf16 rows of heads of this shape, and their strides: of tokens, of heads, the head dim dense."""
+    try:
+        if t.dtype is _bf16 and t.get_device() == dev and t.shape == shape:
+            token, head, dim = t.stride()
+            if dim == 1:
+                return t.data_ptr(), token, head
+    except AttributeError:
+        pass
+    return (_check(t, name, _bf16, dev, shape, dense=False),) + _dense_heads(t, name)
+
+
 def paged_append_fp8(q, k, v, k_cache, v_cache, k_scale, v_scale, slots, positions=None, inv_freq=None,
                      interleaved=False, amplitude=1.0, q_out=None, stream=None):
     """Rotates q and k and writes k and v to their cache slots as e4m3 codes, updating the scales of the blocks
@@ -91,7 +103,6 @@ def paged_append_fp8(q, k, v, k_cache, v_cache, k_scale, v_scale, slots, positio
     negative: the token is skipped, its row of q_out left as it was.  positions int32 [T] and inv_freq as for
     ``rope``; both None: nothing rotates.  q_out may be q.  Returns q_out."""
     dev = _device(k, "k")
-    bf = _bf16
     _dims(k, "k", 3)
     if (positions is None) != (inv_freq is None):
         raise ValueError("positions and inv_freq go together")
@@ -99,26 +110,26 @@ def paged_append_fp8(q, k, v, k_cache, v_cache, k_scale, v_scale, slots, positio
     T = _size(k.shape[0], "the number of tokens")
     H = 0
     qp = qop = None
-    qs = qos = (0, 0)
+    qt = qh = qot = qoh = 0
     if q is not None:
         _dims(q, "q", 3)
         H = q.shape[1]
         if q_out is None:
             with _on(stream):
-                q_out = torch.empty((T, H, d), dtype=bf, device=q.device)
-        qp, qs = _check(q, "q", bf, dev, (T, H, d), dense=False), _dense_heads(q, "q")
-        qop, qos = _check(q_out, "q_out", bf, dev, (T, H, d), dense=False), _dense_heads(q_out, "q_out")
+                q_out = torch.empty((T, H, d), dtype=_bf16, device=q.device)
+        qp, qt, qh = _rows(q, "q", dev, (T, H, d))
+        qop, qot, qoh = _rows(q_out, "q_out", dev, (T, H, d))
     elif q_out is not None:
         raise ValueError("q_out without q")
-    kp, ks = _check(k, "k", bf, dev, (T, H_kv, d), dense=False), _dense_heads(k, "k")
-    vp, vs = _check(v, "v", bf, dev, (T, H_kv, d), dense=False), _dense_heads(v, "v")
+    kp, kt, kh = _rows(k, "k", dev, (T, H_kv, d))
+    vp, vt, vh = _rows(v, "v", dev, (T, H_kv, d))
     fp, bits, rot, pp = None, 64, 0, None
     if inv_freq is not None:
         fp, bits, rot = _freqs(inv_freq, dev)
         pp = _check(positions, "positions", torch.int32, dev, (T,))
     st = lib().attn_paged_append_fp8(qp, qop, kp, vp, *cache, _check(slots, "slots", torch.int32, dev, (T,)), pp, fp, bits,
                                      T, H, H_kv, d, rot, page_size, block, num_pages,
-                                     _Strides(*qs, *qos, *ks, *vs), int(bool(interleaved)),
+                                     _Strides(qt, qh, qot, qoh, kt, kh, vt, vh), int(bool(interleaved)),
                                      float(amplitude), _handle(stream, dev))
     _raise(st, "attn_paged_append_fp8")
     return q_out
