@@ -804,7 +804,7 @@ attn_status_t attn_paged_fwd_fp8(const void* q, const void* k_cache, const void*
     const long long slots = (long long)num_pages * page_size;
     p.rows_per_box = page_size < 128 ? page_size : 128;
     p.NH = pl.NH;
-    p.any = pl.any;
+    p.kv_units = H_kv / pl.NH;
     const int wide = d == 64 ? pl.NH : 1;  // heads in a row of a tile
     if (!make_codes_map(&p.tm_k, k_cache, wide * d, H_kv / wide, slots, p.rows_per_box) ||
         !make_codes_map(&p.tm_v, v_cache, wide * d, H_kv / wide, slots, p.rows_per_box))
@@ -815,6 +815,7 @@ attn_status_t attn_paged_fwd_fp8(const void* q, const void* k_cache, const void*
     p.part_ml = reinterpret_cast<float*>(ws + pl.part_ml);
     p.part_o = reinterpret_cast<float*>(ws + pl.part_o);
     p.R = pl.R;
+    p.RH = pl.R / pl.NH;
     p.n_ctas = 2 * ds->sm_count < kPaged8Ctas ? 2 * ds->sm_count : kPaged8Ctas;
     p.q = static_cast<const uint16_t*>(q);
     p.k_scale = k_scale;

@@ -201,14 +201,13 @@ struct Paged8Params {
     uint16_t* o;
     float* lse;                  // [total_q, H] or nullptr
     int4* cuts;                  // [n_ctas, 2] the unit that a CTA begins and others go on with, for the merge:
-                                 // (last of those CTAs or -1, record, rows of a head, first KV head / NH), (first token, first row, NH, R)
+                                 // (last of those CTAs or -1, record, rows of a head, first KV head / NH), (first token, first row, -, -)
     float* part_ml;              // [2 n_ctas, R, 2]: (m in log2 units, l) of a CTA's first and last piece
     float* part_o;               // [2 n_ctas, R, d]: unnormalised O
     unsigned* status;
     int B, H, H_kv, G;
-    int NH;                      // KV heads that a unit of work takes (any: at most)
-    int R;                       // query rows of a unit (any: at most)
-    int any;                     // the kernel chooses one, two or four heads to a unit
+    int NH, kv_units;            // KV heads that a unit of work takes (1 or 2), H_kv / NH
+    int R, RH;                   // query rows of a unit, of each head
     int total_q, max_q_len;
     int page_shift, block_shift, max_pages, num_pages;
     int rows_per_box;            // min(page_size, 128)
@@ -219,8 +218,7 @@ struct Paged8Params {
 };
 // Workspace of the call: byte offsets of the plan's parts.
 struct Paged8Plan {
-    int NH, R;                   // KV heads and query rows of a unit (any: at most)
-    bool any;
+    int NH, R;                   // KV heads and query rows of a unit
     size_t part_ml, part_o, bytes;
 };
 constexpr int kPaged8Ctas = 304;  // at most: two to each of the chip's 152 SMs

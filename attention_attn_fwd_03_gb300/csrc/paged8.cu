@@ -17,14 +17,14 @@
 // Both products are transposed, so that keys (or channels) fill the 128 rows of the
 // matrix instruction and query rows its columns:
 //   S^T [128 keys, 2 R] = Kc [128, d] Q^T,    O^T [d, 3 R] += Vc^T [d, 128 keys] P^T,
-// R = 8, 16 or 32 query rows (tokens times the heads of a group; those of two or four KV heads,
-// if a unit has as many: each head's rows meet that head's codes only).  A thread of the softmax
+// R = 8, 16 or 32 query rows (tokens times the heads of a group; those of two KV heads, if a
+// unit has two: each head's rows meet that head's codes only).  A thread of the softmax
 // then has one key and 8 rows: no thread is idle.  It takes 32 / R tiles of 128 keys (a step) at a time:
 // one test per step, over all threads, whether a row's maximum grew by more than kTau.
 //
-// Work split.  Requests, KV heads (or two, four together: paged8_plan), row tiles and key tiles in a row, cut into equal shares,
+// Work split.  Requests, KV heads (or pairs of them: paged8_plan), row tiles and key tiles in a row, cut into equal shares,
 // one for each CTA (two to an SM, so that one's softmax runs during the other's loads).  Each
-// CTA computes the cut from the lengths.  A unit (request, heads, row tile) that lies in one
+// CTA computes the cut from the lengths.  A unit (request, head or pair, row tile) that lies in one
 // CTA is finished there; pieces of others leave (m, l, O), merged by a second kernel.
 //
 // A CTA, 384 threads:
@@ -35,10 +35,10 @@
 //   warp 10   query rows as e4m3 pairs.
 //   warp 11   the scales of the steps' keys.
 //
-// Measured (inputs from HBM, d = 128, 32 heads over 8 unless said).  4 requests of 200 to 262 thousand keys: 286 to 301 us
-// on different GPUs, 6.3 to 6.6 TB/s (a copy: 6.8); 64 of 512 to 8192: 99 to 108 us, 5.3 to 5.8 TB/s; 33 of 0 to 4096 with
-// 16 heads over 16: 56 to 60 us; one of 32 thousand (which stays in L2): 22 us; 8 tokens of 16 requests, d = 64, 16 heads over 2,
-// a scale to every token: 51 to 53 us, 0.9 of it in the softmax.  A call of one tile takes 11 us: 4 until the first page is asked
+// Measured (inputs from HBM, d = 128, 32 heads over 8 unless said).  4 requests of 200 to 262 thousand keys: 287 to 319 us
+// on different GPUs, 5.9 to 6.6 TB/s (a copy: 6.8); 64 of 512 to 8192: 99 to 108 us, 5.3 to 5.8 TB/s; 33 of 0 to 4096 with
+// 16 heads over 16: 56 us; one of 32 thousand (which stays in L2): 22 us; 8 tokens of 16 requests, d = 64, 16 heads over 2,
+// a scale to every token: 53 us, 0.9 of it in the softmax.  A call of one tile takes 11 us: 4 until the first page is asked
 // for, 4 for the tile, 2 to 3 for the merge; a unit's start and end, and the last CTAs' lead over the mean, take most of what
 // is not streaming in the others.
 #include <cuda_fp16.h>
@@ -63,7 +63,7 @@ constexpr int kThreads8 = 384;
 constexpr float kHuge = 3e38f;
 constexpr int kQN = 4;            // unit queue between the producer and the other warps
 constexpr int kUnitInts = 10;
-constexpr int kMiscFirst = 30;   // place in the misc words of the first request's extent; after it the heads of a unit
+constexpr int kMiscFirst = 30;   // place in the misc words of the first request's extent
 constexpr int kMinShare = 1;      // tiles
 // What a unit's start and end take, in tiles of 128 keys (33 requests of up to 4096 keys, 16 heads: 63 us with 1, 57 with
 // 2, 59 with 3).
@@ -74,12 +74,12 @@ struct Cfg {
     static constexpr int SB = 32 / R;                  // key tiles of a step
     static constexpr int RH = R / NH;                  // rows of a head
     static constexpr bool WIDE = NH == 2 && D == 64;   // a tile holds the codes of two heads, side by side
-    static constexpr int TPK = D == 128 ? NH : 1;  // tiles to 128 keys: one for each head
+    static constexpr int TPK = NH == 2 && D == 128 ? 2 : 1;  // tiles to 128 keys: one for each head
     static constexpr int W = WIDE ? 128 : D;           // bytes of a tile's row
-    static constexpr int PH = TPK > 1 ? RH : R;       // rows of a P operand
+    static constexpr int PH = TPK == 2 ? RH : R;       // rows of a P operand
     static constexpr int NPV = PH == 8 ? 32 : 3 * PH;  // columns of O^T: hi, mid, lo (a multiple of 16)
     static constexpr int TILE = 128 * W;               // bytes of a K or V tile
-    static constexpr int NST = (SB * NH == 4 && NH < 4 ? 5 : 4) * 128 / W;  // ring stages
+    static constexpr int NST = (SB * NH == 4 ? 5 : 4) * 128 / W;  // ring stages
     static constexpr int QBYTES = 2 * R * D;
     // A tile of P: keys as its rows and hi, mid, lo of the query rows side by side in each (a thread's eight rows are then
     // eight bytes: 53.5 us instead of 55.4 for 8 tokens of 16 requests); for 8 rows, whose 24 bytes would take 32, hi, mid and lo as its rows.  The product's last 8 columns come
@@ -87,29 +87,25 @@ struct Cfg {
     static constexpr bool KEYS = PH >= 16;
     static constexpr int WP = PH == 32 ? 128 : PH == 16 ? 64 : 128;  // bytes of a row of P, and its swizzle
     static constexpr int PTILE = KEYS ? 128 * WP : 3 * PH * 128;
-    static constexpr int PBUF = SB * NH == 4 || TPK > 1 || R == 32 ? 1 : 2;  // steps' P held at once
+    static constexpr int PBUF = SB * NH == 4 || TPK == 2 || R == 32 ? 1 : 2;  // steps' P held at once
     static constexpr uint32_t TM_O = 128;              // S: two buffers of 64 columns
     static constexpr uint32_t TM_COLS = 256;
-    // Barriers, unit queue and misc words lie in the same place for every form of a kernel.
-    static constexpr int BST = 5 * 128 / W;            // places for the stages' barriers
-    static constexpr int N_BARS = 2 * BST + 15 + 2 * kQN;
-    static constexpr int OFF_BAR = 0;
-    static constexpr int OFF_UQ = OFF_BAR + 8 * N_BARS;
-    static constexpr int OFF_MISC = OFF_UQ + 4 * kQN * kUnitInts;
-    static constexpr bool FRONT = OFF_MISC + 144 + 3 * R * 8 <= 1024;  // room for the rows' words before the tiles
-    static constexpr int OFF_KV = 1024;
+    static constexpr int OFF_KV = 0;
     static constexpr int OFF_P = OFF_KV + NST * TILE;
     static constexpr int OFF_Q = OFF_P + PBUF * SB * TPK * PTILE;
     static constexpr int OFF_SC = OFF_Q + 2 * QBYTES;                 // float2 [2][NH][SB * 128]: ks, vs of 1 .. 16 keys
     static constexpr int OFF_ROW = OFF_SC + 2 * NH * SB * 128 * 8;    // int4 [2][R]: factor, last visible key, output row
-    static constexpr int OFF_EXCH = OFF_ROW + 2 * R * 16;             // float2 [8][R]
-    static constexpr int OFF_SUM = OFF_EXCH + 8 * R * 8;              // float [8][R]
-    static constexpr int OFF_NAN = OFF_SUM + 8 * R * 4;               // int [NH * D]: first row that sees a NaN in this channel
-    static constexpr int OFF_END = OFF_NAN + NH * D * 4;
-    static constexpr int OFF_STAT = FRONT ? OFF_MISC + 144 : OFF_END; // float2 [R]: running maxima of s and of s + log2 vs
+    static constexpr int OFF_STAT = OFF_ROW + 2 * R * 16;             // float2 [R]: running maxima of s and of s + log2 vs
     static constexpr int OFF_PAR = OFF_STAT + R * 8;                  // float2 [R]: the maximum, and P's factor
     static constexpr int OFF_ALPHA = OFF_PAR + R * 8;                 // float2 [R]
-    static constexpr int SMEM_BYTES = OFF_END + (FRONT ? 0 : 3 * R * 8) + 1024;
+    static constexpr int OFF_EXCH = OFF_ALPHA + R * 8;                // float2 [8][R]
+    static constexpr int OFF_SUM = OFF_EXCH + 8 * R * 8;              // float [8][R]
+    static constexpr int OFF_NAN = OFF_SUM + 8 * R * 4;               // int [NH * D]: first row that sees a NaN in this channel
+    static constexpr int OFF_BAR = OFF_NAN + NH * D * 4;
+    static constexpr int N_BARS = 2 * NST + 15 + 2 * kQN;
+    static constexpr int OFF_UQ = OFF_BAR + 8 * N_BARS;
+    static constexpr int OFF_MISC = OFF_UQ + 4 * kQN * kUnitInts;
+    static constexpr int SMEM_BYTES = OFF_MISC + 144 + 1024;
     static_assert(SMEM_BYTES <= 115712, "two CTAs to an SM");
     static_assert(OFF_P % 1024 == 0 && PTILE % 1024 == 0 && OFF_Q % 1024 == 0 && QBYTES % 1024 == 0, "swizzle atoms");
 };
@@ -189,8 +185,8 @@ __device__ __forceinline__ int key_tiles(const Extent& e) { return max(1, (int)(
 template <int RH>
 __device__ __forceinline__ int row_tiles(const Paged8Params& p, const Extent& e) { return (e.q_len * p.G + RH - 1) / RH; }
 template <int RH>
-__device__ __forceinline__ long long head_work(const Paged8Params& p, const Extent& e) {  // of one KV head, or NH together
-    return (long long)row_tiles<RH>(p, e) * (key_tiles(e) + kUnitCost);
+__device__ __forceinline__ long long work_of(const Paged8Params& p, const Extent& e) {
+    return (long long)p.kv_units * row_tiles<RH>(p, e) * (key_tiles(e) + kUnitCost);
 }
 
 // a / b (both positive, the quotient an int), by a 32-bit division where that will do: the 64-bit one takes a noticeable
@@ -348,7 +344,7 @@ __device__ void producer_role(const Paged8Params& p, uint8_t* smem, const Bars& 
             u.r = -1;
             u.nt = 0;
             while (w < w1) {
-                const long long work = p.H_kv / NH * head_work<C::RH>(p, e);
+                const long long work = work_of<C::RH>(p, e);
                 if (w - start >= work) {
                     start += work;
                     if (++r >= base + 32) {
@@ -395,7 +391,7 @@ __device__ void producer_role(const Paged8Params& p, uint8_t* smem, const Bars& 
                     if (past >= 0) {  // for the merge
                         int4* cut = p.cuts + 2 * blockIdx.x;
                         cut[0] = make_int4(quotient(past, share), u.slot, u.nr, u.kvh);
-                        cut[1] = make_int4(u.q_start, u.row0, NH, R);
+                        cut[1] = make_int4(u.q_start, u.row0, 0, 0);
                     }
                 }
             }
@@ -793,7 +789,7 @@ __device__ void scale_role(const Paged8Params& p, uint8_t* smem, const Bars& b, 
             if (n >= 2 && !(ok = warp_wait(&b.sc_empty[buf], ((n >> 1) - 1u) & 1u, abort_flag, p.status))) break;
 #pragma unroll 1
             for (int x0 = 0; x0 < NH * groups; x0 += 32) {
-                const int x = x0 + lane, head = NH == 1 ? 0 : NH == 2 ? x >= groups : x / groups, g = x - head * groups;
+                const int x = x0 + lane, head = NH == 2 && x >= groups, g = x - head * groups;
                 const long long key = key0 + ((long long)g << gshift);
                 const int page = (int)((key >> p.page_shift) - page0);
                 const int id0 = __shfl_sync(0xffffffffu, id[0], page & 31), id1 = __shfl_sync(0xffffffffu, id[1], page & 31);
@@ -867,7 +863,6 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
     float* s_sum = reinterpret_cast<float*>(smem + C::OFF_SUM);
     int* s_nan = reinterpret_cast<int*>(smem + C::OFF_NAN);
     const int gshift = min(p.block_shift, 4);
-    for (int i = gtid; i < NH * D; i += 256) s_nan[i] = 0x7fffffff;  // (seen by the issuer's warp with the first P)
     uint32_t n = 0;  // step
     // A failed wait leaves this warp on the common path, so that no barrier lacks a warp; all leave together where
     // they next agree on it.
@@ -1077,7 +1072,7 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
         tc_fence_after();
 #pragma unroll 1
         for (int x = grp; x < u.nr * C::TPK; x += 2) {  // (a wide tile's heads: half of the channels each)
-            const int head = C::WIDE ? tid / D : C::TPK <= 2 ? x >= u.nr : x / u.nr, y = C::WIDE ? x : x - head * u.nr, r = head * RH + y;
+            const int head = C::WIDE ? tid / D : x >= u.nr, y = C::WIDE ? x : x - head * u.nr, r = head * RH + y;
             float v = 0.f, m = 0.f, sum = 0.f;
             if (u.nt > 0) {
                 uint32_t x[3];
@@ -1109,48 +1104,14 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
         }
         tc_fence_before();
         softmax_sync();  // s_stat, s_sum, s_nan and the rows have been read
-        for (int i = gtid; i < NH * D; i += 256) s_nan[i] = 0x7fffffff;
+        if (gtid < NH * D) s_nan[gtid] = 0x7fffffff;
         if (lane == 0) bar_arrive(&b.q_empty[qb]);
     }
 }
 
 // ---------------------------------------------------------------- kernels
 
-// Where a CTA's share of the cut begins.
-struct Start {
-    int r;              // its first request
-    long long w0, w1;   // the share
-    long long before;   // of the requests before the first
-    long long share;
-};
-
 template <int D, int R, int NH>
-__device__ __forceinline__ void roles(const Paged8Params& p, uint8_t* smem, const Bars& b, volatile int* uq, volatile int* abort_flag,
-                                      uint32_t tmem, const Start& at, const Extent& first, int warp, int lane) {
-    if (warp >= 2 && warp < 10) {
-        softmax_role<D, R, NH>(p, smem, b, uq, abort_flag, tmem, warp - 2, warp & 3, lane);
-    } else if (warp == 0) {
-        producer_role<D, R, NH>(p, smem, b, uq, abort_flag, lane, at.r, at.w0, at.w1, at.before, first, at.share);
-    } else if (warp == 10) {
-        query_role<D, R, NH>(p, smem, b, uq, abort_flag, lane);
-    } else if (warp == 11) {
-        scale_role<D, R, NH>(p, smem, b, uq, abort_flag, lane);
-    } else {
-        mma_role<D, R, NH>(p, smem, b, uq, abort_flag, tmem, lane);
-        __syncwarp();
-        if (lane == 0) {
-            tc_commit(b.done);  // every issued MMA finishes before tensor memory is released
-            drain_wait(b.done, 0, p.status);
-        }
-        __syncwarp();
-    }
-}
-
-// Tiles of 128 keys, all heads', to a CTA: from here on two heads to a unit, four.
-constexpr int kPairTiles = 40, kFourTiles = 96;
-
-// ANY (d = 128, up to 8 rows to a head): one, two or four KV heads to a unit, by the lengths; R and NH are those of one.
-template <int D, int R, int NH, bool ANY>
 __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_constant__ Paged8Params p) {
     using C = Cfg<D, R, NH>;
     extern __shared__ uint8_t smem_raw[];
@@ -1159,8 +1120,8 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     Bars b;
     b.kv_full = bars;
-    b.kv_empty = b.kv_full + C::BST;
-    b.q_full = b.kv_empty + C::BST;
+    b.kv_empty = b.kv_full + C::NST;
+    b.q_full = b.kv_empty + C::NST;
     b.q_empty = b.q_full + 2;
     b.sc_full = b.q_empty + 2;
     b.sc_empty = b.sc_full + 2;
@@ -1208,6 +1169,7 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
         *abort_flag = 0;
         misc[2] = timeout_recorded(p.status) ? 1 : 0;  // an earlier launch gave up
     }
+    for (int i = kThreads8 - 1 - tid; i < NH * D; i += kThreads8) reinterpret_cast<int*>(smem + C::OFF_NAN)[i] = 0x7fffffff;
     long long share = 0, w0 = 0, w1 = 0;
     if (cutter) {
         long long sum = 0, total;
@@ -1216,7 +1178,7 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
         for (int r = ra; r < rb; ++r) {
             const Extent x = r == ra ? e : few ? e2 : extent(p, r);
             bad |= x.bad;
-            sum += head_work<C::RH>(p, x);
+            sum += work_of<C::RH>(p, x);
         }
         if (bad && blockIdx.x == 0) atomicOr(p.status, 1u << kStatusDeviceData);
         long long before = sum;
@@ -1237,16 +1199,6 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
                 total += wide[1 + w];
             }
         }
-        int heads = NH;
-        if (ANY) {
-            const long long all = total * p.H_kv;
-            if (all > (long long)gridDim.x * kFourTiles) heads = p.NH;
-            else if (all > (long long)gridDim.x * kPairTiles || (long long)p.B * p.H_kv > gridDim.x) heads = 2;
-        }
-        const int kv_units = p.H_kv / heads;
-        before *= kv_units;
-        sum *= kv_units;
-        total *= kv_units;
         share = total < 0x7fff0000LL ? max((unsigned)kMinShare, ((unsigned)total + gridDim.x - 1) / gridDim.x)
                                      : long_quotient(total + gridDim.x - 1, gridDim.x);
         w0 = (long long)blockIdx.x * share;
@@ -1256,7 +1208,7 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
 #pragma unroll 1
             for (int r = ra; r < rb; ++r) {
                 const Extent x = r == ra ? e : few ? e2 : extent(p, r);
-                const long long work = kv_units * head_work<C::RH>(p, x);
+                const long long work = work_of<C::RH>(p, x);
                 if (w0 < at + work) {
                     misc[3] = r;
                     wide[0] = at;
@@ -1269,26 +1221,33 @@ __global__ void __launch_bounds__(kThreads8, 2) paged8_kernel(const __grid_const
                 at += work;
             }
         }
-        if (tid == 0) {
-            p.cuts[2 * blockIdx.x].x = -1;  // the producer (this thread) may put a cut in its place
-            misc[kMiscFirst + 3] = heads;
-        }
+        if (tid == 0) p.cuts[2 * blockIdx.x].x = -1;  // the producer (this thread) may put a cut in its place
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
     if (misc[2] == 0) {
-        const bool any = w0 < w1;  // otherwise its first unit is the end
-        const int* x = misc + kMiscFirst;
-        const Start at{any ? misc[3] : 0, w0, w1, any ? wide[0] : 0, share};
-        const Extent first{x[0], x[1], x[2], false};
-        if (!ANY || x[3] == 1)
-            roles<D, R, NH>(p, smem, b, uq, abort_flag, tmem, at, first, warp, lane);
-        else if (x[3] == 2)
-            roles<D, ANY ? 2 * R : R, ANY ? 2 : NH>(p, smem, b, uq, abort_flag, tmem, at, first, warp, lane);
-        else
-            roles<D, ANY ? 4 * R : R, ANY ? 4 : NH>(p, smem, b, uq, abort_flag, tmem, at, first, warp, lane);
+        if (warp >= 2 && warp < 10) {
+            softmax_role<D, R, NH>(p, smem, b, uq, abort_flag, tmem, warp - 2, warp & 3, lane);
+        } else if (warp == 0) {
+            const bool any = w0 < w1;  // otherwise its first unit is the end
+            const int* first = misc + kMiscFirst;
+            producer_role<D, R, NH>(p, smem, b, uq, abort_flag, lane, any ? misc[3] : 0, w0, w1, any ? wide[0] : 0,
+                                    Extent{first[0], first[1], first[2], false}, share);
+        } else if (warp == 10) {
+            query_role<D, R, NH>(p, smem, b, uq, abort_flag, lane);
+        } else if (warp == 11) {
+            scale_role<D, R, NH>(p, smem, b, uq, abort_flag, lane);
+        } else {
+            mma_role<D, R, NH>(p, smem, b, uq, abort_flag, tmem, lane);
+            __syncwarp();
+            if (lane == 0) {
+                tc_commit(b.done);  // every issued MMA finishes before tensor memory is released
+                drain_wait(b.done, 0, p.status);
+            }
+            __syncwarp();
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -1316,10 +1275,9 @@ __global__ void __launch_bounds__(kMergeRows * kMergeWarps * 32) paged8_merge_ke
     griddep_wait();
     const int4 cut = __ldcg(p.cuts + 2 * c0), unit = __ldcg(p.cuts + 2 * c0 + 1);
     if (timeout_recorded(p.status) || cut.x < 0) return;
-    const int NH = unit.z, R = unit.w, rows = cut.z * NH;
-    for (int x0 = blockIdx.y * kMergeRows; x0 < rows; x0 += gridDim.y * kMergeRows) {
-        const int x = min(x0 + sub, rows - 1);  // (the last row twice, if they are odd)
-        const int head = x / cut.z, y = x - head * cut.z, r = head * (R / NH) + y;
+    for (int x0 = blockIdx.y * kMergeRows; x0 < cut.z * p.NH; x0 += gridDim.y * kMergeRows) {
+        const int x = min(x0 + sub, cut.z * p.NH - 1);  // (the last row twice, if they are odd)
+        const int head = x / cut.z, y = x - head * cut.z, r = head * p.RH + y;
         float m = -INFINITY, l = 0.f, acc[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) acc[i] = 0.f;
@@ -1331,7 +1289,7 @@ __global__ void __launch_bounds__(kMergeRows * kMergeWarps * 32) paged8_merge_ke
                 const int ck = c + k * kMergeWarps;
                 ml[k] = make_float2(-INFINITY, 0.f);
                 if (ck <= cut.x) {
-                    const size_t rec = (size_t)(ck == c0 ? cut.y : 2 * ck) * R + r;
+                    const size_t rec = (size_t)(ck == c0 ? cut.y : 2 * ck) * p.R + r;
                     ml[k] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + rec);
                     v[k] = __ldcg(reinterpret_cast<const Vec*>(p.part_o + rec * D) + lane);
                 }
@@ -1373,7 +1331,7 @@ __global__ void __launch_bounds__(kMergeRows * kMergeWarps * 32) paged8_merge_ke
                 f2[1] = fmaf(s_o[sub][w][2 * tid + 1], f, f2[1]);
             }
             const int at = unit.y + y, tok = at / p.G;
-            const size_t row = (size_t)(unit.x + tok) * p.H + (cut.w * NH + head) * p.G + (at - tok * p.G);
+            const size_t row = (size_t)(unit.x + tok) * p.H + (cut.w * p.NH + head) * p.G + (at - tok * p.G);
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             reinterpret_cast<uint32_t*>(p.o + row * D)[tid] = pack_bf16(f2[0] * inv, f2[1] * inv);
             if (tid == 0 && p.lse != nullptr) p.lse[row] = sum == 0.f ? -INFINITY : (top + lg2(sum)) * kLn2;
@@ -1382,23 +1340,19 @@ __global__ void __launch_bounds__(kMergeRows * kMergeWarps * 32) paged8_merge_ke
     }
 }
 
-template <int D, int R, int NH, bool ANY = false>
+template <int D, int R, int NH>
 cudaError_t launch(const Paged8Params& p, cudaStream_t stream) {
     static std::atomic<unsigned long long> opted{0};
-    constexpr int one = Cfg<D, R, NH>::SMEM_BYTES, two = Cfg<D, ANY ? 2 * R : R, ANY ? 2 : NH>::SMEM_BYTES,
-                  four = Cfg<D, ANY ? 4 * R : R, ANY ? 4 : NH>::SMEM_BYTES;
-    constexpr int smem = one > two ? (one > four ? one : four) : two > four ? two : four;
-    const auto kernel = paged8_kernel<D, R, NH, ANY>;
-    cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(kernel), smem, opted);
+    cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(paged8_kernel<D, R, NH>), Cfg<D, R, NH>::SMEM_BYTES, opted);
     if (e != cudaSuccess) return e;
-    kernel<<<p.n_ctas, kThreads8, smem, stream>>>(p);
+    paged8_kernel<D, R, NH><<<p.n_ctas, kThreads8, Cfg<D, R, NH>::SMEM_BYTES, stream>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.n_ctas, p.R > 16 && !ANY ? 4u : 2u);
+    cfg.gridDim = dim3((unsigned)p.n_ctas, p.R > 16 ? 4u : 2u);
     cfg.blockDim = dim3(kMergeRows * kMergeWarps * 32);
     cfg.stream = stream;
     cfg.attrs = attr;
@@ -1409,29 +1363,20 @@ cudaError_t launch(const Paged8Params& p, cudaStream_t stream) {
 }  // namespace
 
 // Two KV heads to a unit halve the number of units, and read rows of the cache that lie side by side together: 128 bytes
-// for two heads of d = 64, where rows of 64 bytes come at 3.2 TB/s, those of 128 at 6.2; tiles in turn with d = 128, four heads'
-// for still larger pieces.  One unit takes longer, though: what does not fill the CTAs, or leaves each a few tiles only, is
-// faster by single heads.
-//   d = 128, up to 8 rows to a head (decode): the kernel decides, by the lengths.  Single heads and pairs: 33 requests of 0
-// to 4096 keys, 16 heads 64 and 56 us; 64 of 256, 8 heads 18.0 and 16.4; one of 1024 11.6 and 14.9, of 131 thousand 50 and 55; 8
-// of 32 thousand 87 and 87.  Pairs and fours: 4 of 65 thousand 94 and 98, of 131 thousand 176 and 171, of 262 thousand
-// 338 and 319; 64 of 4096 96 and 100, of 8192 180 and 174, of 16 thousand 340 and 321.
-//   d = 64: decided here, as the tiles' rows differ, by how long the requests can be.  Single heads and pairs: 64 of 256
-// 17.1 and 12.9, 8 of 32 thousand 71 and 54; one of 1024 11.3 and 12.2, of 32 thousand 19 and 20, of 131 thousand 41 and 39.
-//   More rows than 16 to a head share their tiles well enough with d = 128.
+// for two heads of d = 64, where rows of 64 bytes come at 3.2 TB/s, those of 128 at 6.2; tiles in turn with d = 128.  Single
+// heads and pairs, d = 128: 33 requests of 0 to 4096 keys, 16 heads 64 and 56 us; 64 of 256, 8 heads 18.0 and 16.4, of 512 to
+// 8192 98 and 100 (on a GPU with slower memory 113 and 109); 4 of 200 to 262 thousand 298 and 289 (343 and 313).  d = 64: 64
+// of 256 17.1 and 12.9, 8 of 32 thousand 71 and 54.  One unit takes longer, though: what does not fill the CTAs, or leaves
+// each a few tiles only, is faster by single heads (one request of 1024 keys 11.6 and 14.9 us with d = 128, 11.3 and 12.2
+// with d = 64; of 32 thousand 20 and 25, 19 and 20; of 131 thousand 50 and 55, 41 and 39).  The lengths are not known here,
+// but how long they can be.  More rows than 16 to a head share their tiles well enough with d = 128.
 Paged8Plan paged8_plan(int B, int max_q_len, int H, int H_kv, int d, int page_size, int max_pages) {
     Paged8Plan pl;
     const long long rows = (long long)max_q_len * (H / H_kv);
     const long long units = (long long)B * H_kv, tiles = units * (((long long)page_size * max_pages + 127) / 128);
-    pl.any = d == 128 && rows <= 8 && H_kv % 2 == 0;
-    if (pl.any) {
-        pl.NH = H_kv % 4 == 0 ? 4 : 2;  // at most
-        pl.R = 8 * pl.NH;
-    } else {
-        const bool large = units > kPaged8Ctas || tiles > kPaged8Ctas * (d == 128 ? 32LL : 8LL);
-        pl.NH = H_kv % 2 == 0 && large && (d == 64 || rows <= 16) ? 2 : 1;
-        pl.R = rows <= 8 ? 8 * pl.NH : rows * pl.NH <= 16 ? 16 : 32;
-    }
+    const bool large = units > kPaged8Ctas || tiles > kPaged8Ctas * (d == 128 ? 32LL : 8LL);
+    pl.NH = H_kv % 2 == 0 && large && (d == 64 || rows <= 16) ? 2 : 1;
+    pl.R = rows <= 8 ? 8 * pl.NH : rows * pl.NH <= 16 ? 16 : 32;
     pl.part_ml = kPaged8Ctas * 2 * sizeof(int4);
     pl.part_o = pl.part_ml + (size_t)2 * kPaged8Ctas * pl.R * 2 * sizeof(float);
     pl.bytes = pl.part_o + (size_t)2 * kPaged8Ctas * pl.R * d * sizeof(float);
@@ -1440,8 +1385,7 @@ Paged8Plan paged8_plan(int B, int max_q_len, int H, int H_kv, int d, int page_si
 
 cudaError_t launch_paged8(int d, const Paged8Params& p, cudaStream_t stream) {
     if (d == 128) {
-        if (p.any) return launch<128, 8, 1, true>(p, stream);
-        if (p.NH == 2) return launch<128, 32, 2>(p, stream);
+        if (p.NH == 2) return p.R == 16 ? launch<128, 16, 2>(p, stream) : launch<128, 32, 2>(p, stream);
         return p.R == 8 ? launch<128, 8, 1>(p, stream) : p.R == 16 ? launch<128, 16, 1>(p, stream) : launch<128, 32, 1>(p, stream);
     }
     if (p.NH == 2) return p.R == 16 ? launch<64, 16, 2>(p, stream) : launch<64, 32, 2>(p, stream);
