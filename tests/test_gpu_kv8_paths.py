@@ -31,6 +31,24 @@ def _long_table(c, H_kv):
     return c
 
 
+def _crowd(lens, q_lens, H_kv):
+    """Requests (these over and over) that make more units than there are CTAs: two KV heads to a unit."""
+    times = -(-(304 // H_kv + 1) // len(lens))
+    return lens * times, None if q_lens is None else q_lens * times
+
+
+def _check_some(c, causal, got, n=30):
+    """_check_fwd for the first, last and longest requests and n others, drawn; the rest have to be finite."""
+    B, T, (o, lse) = len(c["lens"]), c["T"], got
+    cu = c["cu"] or list(range(B + 1))
+    pick = sorted({0, B - 1, c["lens"].index(max(c["lens"]))} | set(random.Random(B).sample(range(B), min(n, B))))
+    rows = torch.cat([torch.arange(cu[r], cu[r + 1]) for r in pick])
+    part = dict(c, table=c["table"][pick], lens=[c["lens"][r] for r in pick], q=c["q"][rows], T=len(rows),
+                cu=None if c["cu"] is None else [0] + torch.tensor([cu[r + 1] - cu[r] for r in pick]).cumsum(0).tolist())
+    _check_fwd(part, causal, (o[rows], lse[rows]))
+    assert torch.isfinite(o[:T].float()).all() and not torch.isnan(lse[:T]).any() and (o[T:] == 9).all() and (lse[T:] == 9).all()
+
+
 def _i32(x):
     return torch.tensor(x, dtype=torch.int32, device=DEV)
 
@@ -518,3 +536,98 @@ def test_tables_filled_to_the_last_page(page):
     for got, name in ((k, "k"), (v, "v")):
         want = torch.cat([ref.values(c[name + "_cache"], c[name + "_scale"], c["table"][r], m) for r, m in enumerate(c["lens"])])
         assert torch.equal(got.cpu().double(), want.float().double())
+
+
+# ---------------------------------------------------------------- many requests: two KV heads to a unit
+
+@pytest.mark.parametrize("H,H_kv", [(2, 2), (16, 2), (6, 6), (16, 4), (64, 8)])
+@pytest.mark.parametrize("page,block", [(16, 1), (8, 8), (128, 32), (1024, 64)])
+def test_two_heads_to_a_unit(H, H_kv, page, block):
+    lens, _ = _crowd([1, 127, 128, 0, 129, 300, 900], None, H_kv)
+    c = _fwd_case(H + block, lens, None, H, H_kv, 128, page, block)
+    _check_some(c, True, _fwd(c, True))
+
+
+@pytest.mark.parametrize("H,H_kv,d", [(4, 2, 128), (8, 4, 128), (8, 8, 64), (48, 8, 128)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_several_tokens_and_heads_to_a_unit(H, H_kv, d, causal):
+    lens, q_lens = _crowd([3, 40, 1, 130, 129, 0, 256, 2], [2, 1, 1, 4, 1, 1, 0, 3], H_kv)
+    c = _fwd_case(H + d, lens, q_lens, H, H_kv, d, 16, 8, pad=2)
+    _check_some(c, causal, _fwd(c, causal))
+
+
+@pytest.mark.parametrize("H_kv", [2, 4])
+def test_a_long_request_among_many(H_kv):
+    """One request in the hands of many CTAs, the others many to a CTA; the same bits each time."""
+    lens, _ = _crowd([60, 300, 0, 90], None, H_kv)
+    lens[len(lens) // 2] = 50000
+    c = _fwd_case(52, lens, None, 2 * H_kv, H_kv, 128, 64, 16)
+    first = _fwd(c, True)
+    _check_some(c, True, first)
+    for _ in range(4):
+        got = _fwd(c, True)
+        assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+
+
+def test_lengths_of_a_captured_call_change():
+    """One graph, its lengths changed between replays, from one tile to hundreds for a unit, in one workspace."""
+    H, H_kv, d, page, B, pages = 8, 4, 128, 64, 40, 360
+    g = torch.Generator().manual_seed(53)
+    cache = [(torch.randn((900, page, H_kv, d), generator=g) * 50).clamp(-448, 448).to(F8).to(DEV) for _ in "kv"] + \
+            [torch.exp2(torch.randint(-6, 3, (900, H_kv, 4), generator=g).float()).to(DEV) / 60 for _ in "kv"]
+    table = torch.randint(0, 900, (B, pages), generator=g).to(torch.int32).to(DEV)
+    q, lens = torch.randn((B, H, d), generator=g).to(BF).to(DEV), torch.zeros(B, dtype=torch.int32, device=DEV)
+    room = torch.empty(attn.attn_paged_fwd_fp8_workspace_size(B, B, 1, H, H_kv, d, page, pages), dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        o, lse = attn.paged_fwd_fp8(q, *cache, table, lens, workspace=room)
+    host = [x.cpu() for x in cache]
+    for n in (50, 15000, 23040, 300, 23040):
+        lens.copy_(torch.full((B,), n, dtype=torch.int32) - torch.arange(B, dtype=torch.int32) % 7 * (n < 23040))
+        graph.replay()
+        got = o.clone(), lse.clone()
+        want = attn.paged_fwd_fp8(q, *cache, table, lens)
+        attn.device_status()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        few = slice(0, 2)
+        wo, wl, bo, bl = ref.attend(q[few].cpu(), *host, table[few].cpu(), lens[few].tolist(), None, d ** -0.5, True)
+        assert ((got[0][few].cpu().double() - wo).abs() <= bo).all() and ((got[1][few].cpu().double() - wl).abs() <= bl).all()
+
+
+def test_not_finite_values_stay_in_their_head():
+    """A NaN among a head's values, scores or queries reaches that head's rows that see it, and no other head of the unit."""
+    lens, q_lens = _crowd([300, 640, 20, 50], [2, 1, 1, 1], 4)
+    c = _fwd_case(50, lens, q_lens, 8, 4, 128, 16, 4)
+    want_o, want_l = _fwd(c, True)
+    at = lambda r, key: (int(c["table"][r, key // 16]), key % 16)
+    p, row = at(0, 299)  # seen by the second token only
+    c["v_cache"].view(torch.uint8)[p, row, 2, 77] = 0xff
+    p, row = at(1, 5)
+    c["k_cache"].view(torch.uint8)[p, row, 3, 127] = 0x7f
+    c["q"][0, 1, 9] = float("nan")
+    o, lse = _fwd(c, True)
+    assert torch.isnan(o[1, 4:6, 77].float()).all() and torch.isnan(o[2, 6:8].float()).all() and torch.isnan(lse[2, 6:8]).all()
+    assert torch.isnan(o[0, 1].float()).all() and torch.isnan(lse[0, 1])
+    same = torch.ones(want_l.shape, dtype=torch.bool)
+    same[1, 4:6] = same[2, 6:8] = same[0, 1] = False
+    assert torch.equal(o[same], want_o[same]) and torch.equal(lse[same], want_l[same])
+    assert torch.equal(lse[1, 4:6], want_l[1, 4:6]) and torch.isfinite(o[1, 4:6, :77].float()).all()
+
+
+def test_recorded_timeout_with_several_heads_to_a_unit():
+    lens, _ = _crowd([700, 40], None, 4)
+    c = _fwd_case(51, lens, None, 16, 4, 128, 16, 16)
+    args = (c["q"].to(DEV), *_gpu_cache(c), c["table"].to(DEV), _i32(c["lens"]))
+    want = attn.paged_fwd_fp8(*args)
+    attn.device_status()
+    o, l = torch.full_like(want[0], 3.0), torch.full_like(want[1], 3.0)
+    assert attn.attn_selftest_wait_timeout(torch.cuda.current_stream().cuda_stream) == attn.ATTN_OK
+    attn.paged_fwd_fp8(*args, out=o, lse=l)
+    with pytest.raises(attn.AttnError) as e:
+        attn.device_status()
+    assert e.value.status == attn.ATTN_ERR_TIMEOUT
+    assert bool((o == 3).all()) and bool((l == 3).all())
+    attn.paged_fwd_fp8(*args, out=o, lse=l)
+    attn.device_status()
+    assert torch.equal(o, want[0]) and torch.equal(l, want[1])
