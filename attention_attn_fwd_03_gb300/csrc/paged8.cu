@@ -13,10 +13,13 @@
 // precision is bought with more rows:
 //   q = 2^x (hi + lo / 16): a bf16 number has 8 significant bits, two e4m3 numbers hold
 //       them; x by the head vector's largest element.
-//   P vs / 2^(running maximum) = hi + mid / 32 + lo / 1024: an fp16 number's 11 bits.
+//   P vs / 2^(running maximum) = hi + mid + (lo + end) / 64: an fp16 number's 11 bits in four e5m2 numbers of 3.
+//       These have the range that small probabilities need: a long tail of them may be all of O, where the large
+//       ones' values are near zero.  (Three e4m3 numbers hold 11 bits down to 2^-13 of the row's largest only, and
+//       nothing below 2^-24; the matrix unit takes e4m3 by e5m2.)
 // Both products are transposed, so that keys (or channels) fill the 128 rows of the
 // matrix instruction and query rows its columns:
-//   S^T [128 keys, 2 R] = Kc [128, d] Q^T,    O^T [d, 3 R] += Vc^T [d, 128 keys] P^T,
+//   S^T [128 keys, 2 R] = Kc [128, d] Q^T,    O^T [d, 2 R or 4 R] += Vc^T [d, 128 keys] P^T,
 // R = 8, 16 or 32 query rows (tokens times the heads of a group; those of two KV heads, if a
 // unit has two: each head's rows meet that head's codes only).  A thread of the softmax
 // then has one key and 8 rows: no thread is idle.  It takes 32 / R tiles of 128 keys (a step) at a time:
@@ -53,11 +56,15 @@ namespace attn {
 
 namespace {
 
-// How far a row's maximum may lag behind, in log2 units, and the scale of P, at most 2^(kTau + kBase) = 256: hi is then
-// off by at most 8, mid = 32 times that by as much again.  What lies 2^-24 below the row's largest is lost.  (kTau 1,
-// kBase 7: a maximum grew in nearly every step of 32 rows.)
+// How far a row's maximum may lag behind, in log2 units, and the scale of P, which is 2^(kTau + kBase) = 2^15 at most: e5m2
+// numbers reach 1.75 2^15, fp16 numbers as far.  hi leaves 2^-3 of a number, mid 2^-3 of that: 64 times what is left then
+// is 2^15 at most again.  The smallest step is 2^-16 / 64: with fp16's own, 2^-24, P is off by less than 2^-33 of the
+// row's largest, and by 2^-11 of itself where that is more.
 constexpr float kTau = 4.f;
-constexpr float kBase = 4.f;
+constexpr float kBase = 11.f;
+// log2 of how much smaller the values' scales may be than 1 before P gets smaller than kBase says: so far P's factor,
+// 2^(kVMin + kBase), and its inverse at the unit's end are normal numbers.
+constexpr float kVMin = 112.f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kThreads8 = 384;
 constexpr float kHuge = 3e38f;
@@ -77,24 +84,30 @@ struct Cfg {
     static constexpr int TPK = NH == 2 && D == 128 ? 2 : 1;  // tiles to 128 keys: one for each head
     static constexpr int W = WIDE ? 128 : D;           // bytes of a tile's row
     static constexpr int PH = TPK == 2 ? RH : R;       // rows of a P operand
-    static constexpr int NPV = PH == 8 ? 32 : 3 * PH;  // columns of O^T: hi, mid, lo (a multiple of 16)
+    // hi and mid may share O's columns, as lo and end may: half as many to rescale, for twice as many instructions.  Drafted
+    // tokens in units of 32 rows take 53.2 us so, 57.0 with columns for each; with 8 rows to an operand one request of 32 thousand keys
+    // takes 22.9 and 22.2, 33 requests with 16 heads 59.3 and 57.8, four long ones 314 and 317.
+    static constexpr bool FOLD = R == 32;
+    static constexpr int NPV = (FOLD ? 2 : 4) * PH;    // columns of O^T
     static constexpr int TILE = 128 * W;               // bytes of a K or V tile
     static constexpr int NST = (SB * NH == 4 ? 5 : 4) * 128 / W;  // ring stages
     static constexpr int QBYTES = 2 * R * D;
-    // A tile of P: keys as its rows and hi, mid, lo of the query rows side by side in each (a thread's eight rows are then
-    // eight bytes: 53.5 us instead of 55.4 for 8 tokens of 16 requests); for 8 rows, whose 24 bytes would take 32, hi, mid and lo as its rows.  The product's last 8 columns come
-    // from what follows then, and are not used.
+    // A tile of P: keys as its rows and hi, lo, mid, end of the query rows side by side in each (a thread's eight rows are then
+    // eight bytes: 53.5 us instead of 55.4 for 1 to 8 tokens of 16 requests); for 8 rows hi, lo, mid and end as its rows.
     static constexpr bool KEYS = PH >= 16;
     static constexpr int WP = PH == 32 ? 128 : PH == 16 ? 64 : 128;  // bytes of a row of P, and its swizzle
-    static constexpr int PTILE = KEYS ? 128 * WP : 3 * PH * 128;
+    static constexpr int PTILE = KEYS ? 128 * WP : 4 * PH * 128;
     static constexpr int PBUF = SB * NH == 4 || TPK == 2 || R == 32 ? 1 : 2;  // steps' P held at once
+    // Steps' scales held at once: they are read at a step's start, and the next ones' come during the rest of it.  Two heads'
+    // tiles of P leave room for one step only.
+    static constexpr int SCB = TPK == 2 && R == 16 ? 1 : 2;
     static constexpr uint32_t TM_O = 128;              // S: two buffers of 64 columns
     static constexpr uint32_t TM_COLS = 256;
     static constexpr int OFF_KV = 0;
     static constexpr int OFF_P = OFF_KV + NST * TILE;
     static constexpr int OFF_Q = OFF_P + PBUF * SB * TPK * PTILE;
-    static constexpr int OFF_SC = OFF_Q + 2 * QBYTES;                 // float2 [2][NH][SB * 128]: ks, vs of 1 .. 16 keys
-    static constexpr int OFF_ROW = OFF_SC + 2 * NH * SB * 128 * 8;    // int4 [2][R]: factor, last visible key, output row
+    static constexpr int OFF_SC = OFF_Q + 2 * QBYTES;                 // float2 [SCB][NH][SB * 128]: ks, vs of 1 .. 16 keys
+    static constexpr int OFF_ROW = OFF_SC + SCB * NH * SB * 128 * 8;    // int4 [2][R]: factor, last visible key, output row
     static constexpr int OFF_STAT = OFF_ROW + 2 * R * 16;             // float2 [R]: running maxima of s and of s + log2 vs
     static constexpr int OFF_PAR = OFF_STAT + R * 8;                  // float2 [R]: the maximum, and P's factor
     static constexpr int OFF_ALPHA = OFF_PAR + R * 8;                 // float2 [R]
@@ -107,6 +120,7 @@ struct Cfg {
     static constexpr int OFF_MISC = OFF_UQ + 4 * kQN * kUnitInts;
     static constexpr int SMEM_BYTES = OFF_MISC + 144 + 1024;
     static_assert(SMEM_BYTES <= 115712, "two CTAs to an SM");
+    static_assert(TPK * NPV <= 128, "columns of O^T");
     static_assert(OFF_P % 1024 == 0 && PTILE % 1024 == 0 && OFF_Q % 1024 == 0 && QBYTES % 1024 == 0, "swizzle atoms");
 };
 
@@ -115,8 +129,8 @@ struct Bars {
     uint64_t* kv_empty;  // [NST]
     uint64_t* q_full;    // [2] query rows prepared
     uint64_t* q_empty;   // [2] the unit's last S product, and the eight softmax warps
-    uint64_t* sc_full;   // [2] scales of a step: 32 lanes' copies
-    uint64_t* sc_empty;  // [2] eight softmax warps
+    uint64_t* sc_full;   // [SCB] scales of a step: 32 lanes' copies
+    uint64_t* sc_empty;  // [SCB] eight softmax warps
     uint64_t* s_full;    // [2]
     uint64_t* p_full;    // [2] 256 arrivals per step
     uint64_t* o_full;    // [2] PV products of a step, and the issuing lane
@@ -261,12 +275,15 @@ __device__ __forceinline__ void copies_arrive(uint64_t* bar) {  // this thread's
 }
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// Two fp16 numbers <-> two e4m3 numbers (nearest, saturating; NaN stays NaN).
-__device__ __forceinline__ uint32_t e4m3_of(uint32_t h2) {
+// Two fp16 numbers -> two e5m2 numbers (nearest, saturating; NaN stays NaN), and back: an e5m2 number is an fp16
+// number's upper byte.
+__device__ __forceinline__ uint32_t e5m2_of(uint32_t h2) {
     uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
     return r;
 }
+__device__ __forceinline__ uint32_t half2_of_e5m2(uint32_t e) { return __byte_perm(e, 0u, 0x1404); }
+// Two e4m3 numbers -> two fp16 numbers.
 __device__ __forceinline__ uint32_t half2_of(uint32_t e) {
     uint32_t r;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)e));
@@ -282,9 +299,9 @@ __device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b) {
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ uint32_t h2_mul32(uint32_t a) {
+__device__ __forceinline__ uint32_t h2_mul64(uint32_t a) {
     uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0x50005000u));  // 32
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0x54005400u));  // 64
     return r;
 }
 
@@ -481,10 +498,15 @@ __device__ __forceinline__ void product_s(uint32_t d, uint64_t k, uint64_t q) {
 // One tile's part of O^T: four blocks of 32 keys.
 template <int D, int R, int NH>
 __device__ __forceinline__ void product_pv(uint32_t o, uint64_t v, uint64_t p, bool accumulate) {
-    constexpr uint32_t ID = idesc_make(Cfg<D, R, NH>::W, Cfg<D, R, NH>::NPV, 0u, true, Cfg<D, R, NH>::KEYS);
+    constexpr uint32_t ID = idesc_make(Cfg<D, R, NH>::W, Cfg<D, R, NH>::NPV, 0u, true, Cfg<D, R, NH>::KEYS) |
+                            1u << 10;  // B's format: e5m2
     constexpr int VS = (32 * Cfg<D, R, NH>::W) >> 4;  // 32 rows of V in descriptor units
     constexpr int PS = Cfg<D, R, NH>::KEYS ? (32 * Cfg<D, R, NH>::WP) >> 4 : 2;
     mma4_ss<VS, 2 * VS, 3 * VS, PS, 2 * PS, 3 * PS, true>(o, v, p, ID, accumulate ? 1u : 0u);
+    if (Cfg<D, R, NH>::FOLD) {  // mid and end behind hi and lo in each row of P
+        static_assert(!Cfg<D, R, NH>::FOLD || Cfg<D, R, NH>::KEYS, "by keys");
+        mma4_ss<VS, 2 * VS, 3 * VS, PS, 2 * PS, 3 * PS, true>(o, v, p + (2 * Cfg<D, R, NH>::PH >> 4), ID, 1u);
+    }
 }
 
 // S^T of step n + 1, then O^T += V^T P^T of step n: the order of the ring.  (Two issuers, one for each product, were
@@ -774,7 +796,7 @@ __device__ void scale_role(const Paged8Params& p, uint8_t* smem, const Bars& b, 
         if (u.r < 0) break;
 #pragma unroll 1
         for (int s = 0; s < u.nt; s += C::SB, ++n) {
-            const uint32_t buf = n & 1u;
+            const uint32_t buf = n % C::SCB;
             const int groups = (min(C::SB, u.nt - s) * 128) >> gshift;
             const long long key0 = (long long)(u.tile0 + s) * 128;
             // pages of the step (64 at most): x in lane x % 32, register x / 32
@@ -786,7 +808,7 @@ __device__ void scale_role(const Paged8Params& p, uint8_t* smem, const Bars& b, 
                 id[i] = -1;
                 if (key < key0 + C::SB * 128 && key < u.kv_len) id[i] = __ldg(p.block_table + (size_t)u.r * p.max_pages + page);
             }
-            if (n >= 2 && !(ok = warp_wait(&b.sc_empty[buf], ((n >> 1) - 1u) & 1u, abort_flag, p.status))) break;
+            if (n >= C::SCB && !(ok = warp_wait(&b.sc_empty[buf], (n / C::SCB - 1u) & 1u, abort_flag, p.status))) break;
 #pragma unroll 1
             for (int x0 = 0; x0 < NH * groups; x0 += 32) {
                 const int x = x0 + lane, head = NH == 2 && x >= groups, g = x - head * groups;
@@ -887,10 +909,10 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
 
         for (int s = 0; s < u.nt; s += SB, ++n) {
             const int nt = min(SB, u.nt - s);
-            const uint32_t buf = n & 1u;
+            const uint32_t buf = n & 1u, sc_buf = n % C::SCB;
             const int key0 = (u.tile0 + s) * 128;  // below kv_len
             const bool diagonal = first_last < u.kv_len - 1 && (long long)key0 + nt * 128 - 1 > first_last;
-            wait(&b.sc_full[buf], (n >> 1) & 1u);
+            wait(&b.sc_full[sc_buf], (n / C::SCB) & 1u);
             wait(&b.s_full[buf], (n >> 1) & 1u);
             tc_fence_after();
             // ---- scores in log2 units, -inf where masked; the rows' maxima over the warp
@@ -907,7 +929,7 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
                     const uint32_t col = buf * 64u + (uint32_t)(t * 2 * R + rb / RH * 2 * RH + rb % RH);
                     tmem_ld8(tS + col, x);
                     tmem_ld8(tS + col + (uint32_t)RH, x + 8);
-                    const float2 sc = s_scale[(buf * NH + rb / RH) * SB * 128 + ((t * 128 + tid) >> gshift)];
+                    const float2 sc = s_scale[(sc_buf * NH + rb / RH) * SB * 128 + ((t * 128 + tid) >> gshift)];
                     // the rows of keys past the request's end are zeros
                     const float mask = (unsigned)key0 + (unsigned)(t * 128 + tid) < (unsigned)u.kv_len ? 0.f : -INFINITY;
                     vk1 = sc.y;
@@ -948,6 +970,8 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
                     }
                 }
             }
+            __syncwarp();
+            if (lane == 0) bar_arrive(&b.sc_empty[sc_buf]);
             if (softmax_any(grew || fail)) {
                 if (softmax_any(fail)) return;
                 if (gtid < R) {
@@ -961,9 +985,9 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
                         now.x = fmaxf(now.x, x.x);
                         now.y = fmaxf(now.y, x.y);
                     }
-                    // (so that P's factor, and its inverse at the unit's end, stay normal numbers: scales of V are 2^-126 at least;
-                    // P of a row whose own are all below 2^-120 is smaller than it might be, by up to 2^6)
-                    now.y = fmaxf(now.y, now.x - 120.f);
+                    // (scales of V are 2^-126 at least: P of a row whose own are all below 2^-kVMin is smaller than it might be, by
+                    // up to 2^14)
+                    now.y = fmaxf(now.y, now.x - kVMin);
                     const float m = now.x == -INFINITY ? 0.f : now.x;
                     s_stat[gtid] = now;
                     s_par[gtid] = make_float2(m, now.y == -INFINITY ? 0.f : ex2(m - now.y + kBase));
@@ -977,10 +1001,10 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
                     if (lane < R) s_sum[warp8 * R + lane] *= s_alpha[lane].x;
                     __syncwarp();
 #pragma unroll 1
-                    for (int c = 8 * grp; c < 3 * R; c += 16) {  // hi, mid, lo
+                    for (int c = 8 * grp; c < R / PH * C::NPV; c += 16) {
                         uint32_t x[8];
-                        const uint32_t col = tO + (uint32_t)(c / (3 * PH) * C::NPV + c % (3 * PH));
-                        const int r = c / (3 * PH) * PH + c % PH;
+                        const uint32_t col = tO + (uint32_t)c;
+                        const int r = c / C::NPV * PH + c % PH;
                         tmem_ld8(col, x);
                         tmem_ld_wait();
                         reg_after_wait<8>(x);
@@ -1001,7 +1025,7 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
             for (int j = 0; j < 2; ++j) {
                 const int t = tile_of(j), rb = row_of(j);
                 if (t < nt && rb % RH < u.nr) {
-                    uint32_t h[4], hi[4], mid[4], lo[4];
+                    uint32_t h[4], hi[4], mid[4], lo[4], end[4];
 #pragma unroll
                     for (int i = 0; i < 8; i += 2) {  // two rows share the conversions
                         const float2 par0 = s_par[rb + i], par1 = s_par[rb + i + 1];
@@ -1011,15 +1035,17 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
                         h[i / 2] = pack_half(p0 * fminf(vk0 * par0.y, kHuge), p1 * fminf(vk0 * par1.y, kHuge));
                     }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) hi[i] = e4m3_of(h[i]);
+                    for (int i = 0; i < 4; ++i) hi[i] = e5m2_of(h[i]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) h[i] = h2_mul32(h2_sub(h[i], half2_of(hi[i])));
+                    for (int i = 0; i < 4; ++i) h[i] = h2_sub(h[i], half2_of_e5m2(hi[i]));
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) mid[i] = e4m3_of(h[i]);
+                    for (int i = 0; i < 4; ++i) mid[i] = e5m2_of(h[i]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) h[i] = h2_mul32(h2_sub(h[i], half2_of(mid[i])));
+                    for (int i = 0; i < 4; ++i) h[i] = h2_mul64(h2_sub(h[i], half2_of_e5m2(mid[i])));
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) lo[i] = e4m3_of(h[i]);
+                    for (int i = 0; i < 4; ++i) lo[i] = e5m2_of(h[i]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) end[i] = e5m2_of(h2_sub(h[i], half2_of_e5m2(lo[i])));
                     const uint32_t tile = p_at + (uint32_t)((((C::PBUF == 2 ? buf : 0u) * SB + t) * C::TPK + rb / PH) * C::PTILE);
                     if (C::KEYS) {
                         const uint32_t turn = (uint32_t)(C::WP == 128 ? tid & 7 : (tid >> 1) & 3) << 4;
@@ -1027,8 +1053,9 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
                             st_v2(tile + ((uint32_t)col ^ turn), x[0] | x[1] << 16, x[2] | x[3] << 16);
                         };
                         put(rb % PH, hi);
-                        put(PH + rb % PH, mid);
-                        put(2 * PH + rb % PH, lo);
+                        put(PH + rb % PH, lo);
+                        put(2 * PH + rb % PH, mid);
+                        put(3 * PH + rb % PH, end);
                     } else {
                         const uint32_t at = tile + (uint32_t)(rb % PH * 128);
 #pragma unroll
@@ -1037,10 +1064,12 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
                             const uint32_t a1 = (at ^ (uint32_t)((2 * i + 1) << 4)) + (uint32_t)((2 * i + 1) * 128);
                             st_u8(a0, hi[i]);
                             st_u8(a1, hi[i] >> 8);
-                            st_u8(a0 + PH * 128, mid[i]);
-                            st_u8(a1 + PH * 128, mid[i] >> 8);
-                            st_u8(a0 + 2 * PH * 128, lo[i]);
-                            st_u8(a1 + 2 * PH * 128, lo[i] >> 8);
+                            st_u8(a0 + PH * 128, lo[i]);
+                            st_u8(a1 + PH * 128, lo[i] >> 8);
+                            st_u8(a0 + 2 * PH * 128, mid[i]);
+                            st_u8(a1 + 2 * PH * 128, mid[i] >> 8);
+                            st_u8(a0 + 3 * PH * 128, end[i]);
+                            st_u8(a1 + 3 * PH * 128, end[i] >> 8);
                         }
                     }
                 }
@@ -1060,8 +1089,6 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
             fence_async_smem();
             tc_fence_before();
             bar_arrive(&b.p_full[buf]);
-            __syncwarp();
-            if (lane == 0) bar_arrive(&b.sc_empty[buf]);
         }
 
         // ---- the unit's end: O by channel, every other row by each group
@@ -1075,11 +1102,14 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
             const int head = C::WIDE ? tid / D : x >= u.nr, y = C::WIDE ? x : x - head * u.nr, r = head * RH + y;
             float v = 0.f, m = 0.f, sum = 0.f;
             if (u.nt > 0) {
-                uint32_t x[3];
+                uint32_t x[4] = {0u, 0u, 0u, 0u};
                 const uint32_t col = tO + (uint32_t)(r / PH * C::NPV + r % PH);
                 tmem_ld1(col, x);
                 tmem_ld1(col + (uint32_t)PH, x + 1);
-                tmem_ld1(col + (uint32_t)(2 * PH), x + 2);
+                if (!C::FOLD) {
+                    tmem_ld1(col + (uint32_t)(2 * PH), x + 2);
+                    tmem_ld1(col + (uint32_t)(3 * PH), x + 3);
+                }
                 const int from = R == 8 ? 0 : (r >> 3 & 1) * 4;
 #pragma unroll
                 for (int w = 0; w < (R == 8 ? 8 : 4); ++w) sum += s_sum[(from + w) * R + r];
@@ -1087,8 +1117,8 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
                 m = st.x == -INFINITY ? 0.f : st.x;
                 const float f = st.y == -INFINITY ? 0.f : ex2(st.y - kBase - m);
                 tmem_ld_wait();
-                reg_after_wait<3>(x);
-                v = fmaf(__uint_as_float(x[2]), 0x1p-10f, fmaf(__uint_as_float(x[1]), 0x1p-5f, __uint_as_float(x[0]))) * f;
+                reg_after_wait<4>(x);
+                v = fmaf(__uint_as_float(x[1]) + __uint_as_float(x[3]), 0x1p-6f, __uint_as_float(x[0]) + __uint_as_float(x[2])) * f;
                 if (y >= s_nan[head * D + chan]) v = __int_as_float(0x7fffffff);
             }
             if (u.slot < 0) {

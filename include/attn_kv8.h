@@ -97,9 +97,9 @@ attn_status_t attn_paged_read_fp8(const void* k_cache, const void* v_cache, cons
  * fp32 sums.  q enters as two e4m3 numbers for each element over a power of two of its
  * head vector: exact where it is above 2^-12 of the vector's largest, off by less than 2^-22
  * of that below.  Probabilities (times their block's scale) enter
- * the second product as three e4m3 numbers each, together good to 2^-11, but
- * for what lies 2^-24 below the row's largest (2^-18, if every scale of V that
- * the row sees is below 2^-120).
+ * the second product as fp16 numbers, in four e5m2 numbers each: off by at most 2^-11 of themselves and
+ * 2^-33 of the row's largest (2^-19 of it, if every scale of V that the row sees is below
+ * 2^-112), so that a long tail of small ones counts in O as it does in the sum.
  * Maxima, sums and exponentials are fp32; O is rounded once.
  * A token that sees no key gets O = 0 and lse = -inf; one with a NaN among its
  * scores NaN in both; rows behind the last request are left as they were.
