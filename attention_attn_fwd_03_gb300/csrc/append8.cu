@@ -446,6 +446,11 @@ struct Read8Params {
 
 constexpr int kReadRows = 8;  // rows of a CTA
 
+// Offsets a, b of a request that are in order, in range, and not of more keys than its table holds.
+__device__ __forceinline__ bool read_ok(const Read8Params& p, int a, int b) {
+    return a >= 0 && b >= a && b <= p.total && (long long)b - a <= ((long long)p.max_pages << p.page_shift);
+}
+
 // Bound by memory: a code is read, two bytes (or four) written.  A CTA takes 8 rows of K and V: their
 // requests and cache rows are looked up once, then each thread moves 16 codes at a time.  Measured: 57 thousand keys of 8
 // heads, d = 128, 57 us, 0.91 of a copy; 777 keys of 2 heads 2.4 us.
@@ -454,6 +459,11 @@ __global__ void __launch_bounds__(kReadThreads) read8_kernel(const __grid_consta
     __shared__ int s_row[kReadRows];  // cache row, -1: left as it is, -2: zeros
     const int tid = threadIdx.x;
     const int t0 = blockIdx.x * kReadRows;
+    // the offsets are looked through by warps that wait for the first one's search: a bad pair need not have a row that finds it
+    constexpr int kLookers = kReadThreads - 32;
+    if (tid >= 32)
+        for (long long r = (long long)blockIdx.x * kLookers + tid - 32; r < p.B; r += (long long)gridDim.x * kLookers)
+            if (!read_ok(p, __ldg(p.cu + r), __ldg(p.cu + r + 1))) atomicOr(p.status, 1u << kStatusDeviceData);
     if (tid < kReadRows) {
         const int t = t0 + tid;
         int row = -1;
@@ -467,9 +477,7 @@ __global__ void __launch_bounds__(kReadThreads) read8_kernel(const __grid_consta
                     hi = mid - 1;
             }
             const int a = __ldg(p.cu + lo), b = __ldg(p.cu + lo + 1);
-            if (a < 0 || b < a || b > p.total || ((long long)p.max_pages << p.page_shift) < (long long)b - a) {
-                atomicOr(p.status, 1u << kStatusDeviceData);
-            } else if (t >= a && t < b) {
+            if (t >= a && t < b && read_ok(p, a, b)) {
                 const int key = t - a;
                 const int id = __ldg(p.table + (long long)lo * p.max_pages + (key >> p.page_shift));
                 if (id >= 0 && id < p.num_pages) {

@@ -78,7 +78,8 @@ attn_status_t attn_paged_append_fp8(const void* q, void* q_out, const void* k, c
  *   B, total_k, H_kv, max_pages >= 1; H_kv at most 65535.
  * On the device, reported as ATTN_ERR_DEVICE_DATA: offsets that are not
  * 0 <= cu[r] <= cu[r + 1] <= total_k, or more keys than the table holds (such
- * a request is skipped); a page id out of range (its rows become 0).
+ * a request is skipped, and where offsets are not in order, rows of others may
+ * be left as they were too); a page id out of range (its rows become 0).
  * Errors: ATTN_ERR_INVALID_ARG / ATTN_ERR_UNSUPPORTED before the launch;
  * ATTN_ERR_CUDA when it fails. */
 attn_status_t attn_paged_read_fp8(const void* k_cache, const void* v_cache, const float* k_scale,
