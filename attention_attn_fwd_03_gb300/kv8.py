@@ -188,7 +188,8 @@ def paged_fwd_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, 
     if cu_seqlens_q is not None:
         cp = _check(cu_seqlens_q, "cu_seqlens_q", i32, dev, (B + 1,))
         if max_q_len is None:
-            max_q_len = int((cu_seqlens_q[1:] - cu_seqlens_q[:-1]).max().item()) if B else 0
+            with _on(stream):  # what writes the offsets may be under way there
+                max_q_len = int((cu_seqlens_q[1:] - cu_seqlens_q[:-1]).max().item()) if B else 0
     elif max_q_len is None:
         max_q_len = 1
     max_q_len = _size(max_q_len, "max_q_len")

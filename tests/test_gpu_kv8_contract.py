@@ -58,3 +58,24 @@ def test_read_many_requests_one_pair_not_in_order():
         with pytest.raises(attn.AttnError) as e:
             attn.device_status()
         assert e.value.status == attn.ATTN_ERR_DEVICE_DATA
+
+
+# ---------------------------------------------------------------- attention's helper
+
+def test_longest_request_is_read_on_the_calls_stream():
+    """cu_seqlens_q is still being written by work on the stream that the call is given."""
+    c, g = _read_case(5, [40, 9], 16, 16, 2, 64)
+    cache, table, lens = _gpu_cache(c), c["table"].to(DEV), _i32(c["lens"])
+    q = torch.randn((7, 4, 64), generator=g).to(BF).to(DEV)
+    ready = _i32([0, 5, 7])
+    want, want_lse = attn.paged_fwd_fp8(q, *cache, table, lens, cu_seqlens_q=ready, max_q_len=5, causal=True)
+    attn.paged_fwd_fp8(q, *cache, table, lens, cu_seqlens_q=ready, causal=True)  # what the helper runs is loaded
+    cu, side = torch.zeros_like(ready), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)  # a tenth of a second
+        cu.copy_(ready)
+    o, lse = attn.paged_fwd_fp8(q, *cache, table, lens, cu_seqlens_q=cu, causal=True, stream=side)
+    torch.cuda.synchronize()
+    attn.device_status()
+    assert torch.equal(o, want) and torch.equal(lse, want_lse)
