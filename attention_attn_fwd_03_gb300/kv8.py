@@ -144,7 +144,7 @@ def paged_read_fp8(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens_k
     dev = _device(k_cache, "k_cache")
     cache, (num_pages, page_size, block, H_kv, d) = _cache(k_cache, v_cache, k_scale, v_scale, dev)
     _dims(block_table, "block_table", 2)
-    B, max_pages = block_table.shape
+    B, max_pages = (_size(n, "a size of block_table") for n in block_table.shape)
     total_k = _size(total_k, "total_k")
     given = k_out if k_out is not None else v_out
     if given is not None:
@@ -182,7 +182,7 @@ def paged_fwd_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, 
     cache, (num_pages, page_size, block, H_kv, cd) = _cache(k_cache, v_cache, k_scale, v_scale, dev)
     if cd != d:
         raise ValueError("q has head dim %d, the cache %d" % (d, cd))
-    B, max_pages = block_table.shape
+    B, max_pages = (_size(n, "a size of block_table") for n in block_table.shape)
     i32 = _i32
     cp = None
     if cu_seqlens_q is not None:

@@ -79,3 +79,21 @@ def test_longest_request_is_read_on_the_calls_stream():
     torch.cuda.synchronize()
     attn.device_status()
     assert torch.equal(o, want) and torch.equal(lse, want_lse)
+
+
+def test_tables_past_32_bits_are_refused():
+    """Sizes that a C int would take the low 32 bits of."""
+    c, g = _read_case(6, [40], 16, 16, 2, 64)
+    cache, lens, q = _gpu_cache(c), _i32(c["lens"]), torch.zeros((1, 4, 64), dtype=BF, device=DEV)
+    wide = torch.empty((1, (1 << 32) + 4), dtype=torch.int32, device=DEV)
+    wide[:, :4] = c["table"][:, :4].to(DEV)
+    with pytest.raises(ValueError, match="32 bits"):
+        attn.paged_fwd_fp8(q, *cache, wide, lens)
+    with pytest.raises(ValueError, match="32 bits"):
+        attn.paged_read_fp8(*cache, wide, _i32([0, 40]), 40)
+    many = wide.view(-1, 1)
+    with pytest.raises(ValueError, match="32 bits"):
+        attn.paged_fwd_fp8(q, *cache, many, lens)
+    with pytest.raises(ValueError, match="32 bits"):
+        attn.paged_read_fp8(*cache, many, _i32([0, 40]), 40)
+    attn.device_status()
