@@ -276,18 +276,18 @@ __global__ void __launch_bounds__(4 * D, 1024 / (4 * D)) append8_kernel(const __
     if (lead == 0ull) return;  // the tokens here belong to a run that began before, or to none
     const int first = t0 + __ffsll((long long)lead) - 1, last_lead = t0 + 63 - __clzll((long long)lead);
 
-    // token t's row of heads h, h + 1, ..
+    // token t's row of heads h, h + 1, .., unless it is skipped
     uint4 x[kHeads], y[kHeads];
-    auto fetch = [&](int t, int h) {
+    auto fetch = [&](int t, int h, bool there) {
         const char* src = p.in[side] + t * p.it[side] + (h0 + h) * p.ih[side];
 #pragma unroll
         for (int i = 0; i < kHeads; ++i)
-            if (h + i < nh && t < p.T) {
+            if (h + i < nh && there) {
                 x[i] = ld16(src + i * p.ih[side] + at.off_a * 2);
                 y[i] = ld16(src + i * p.ih[side] + at.off_b * 2);
             }
     };
-    fetch(first + at.row, 0);
+    fetch(first + at.row, 0, s_slot[first - t0 + at.row] >= 0);  // (its place is below 2 kWindow; past T there is no slot)
     int end = last_lead + 1;
     {  // the end of the last run: its first token that does not follow on
         const int s0 = s_slot[last_lead - t0];
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(4 * D, 1024 / (4 * D)) append8_kernel(const __
         if (in) at.angles(p, s_turn, t, w);
 #pragma unroll 1
         for (int h = 0; h < nh; h += kHeads) {
-            if (pass + h > 0) fetch(t, h);
+            if (pass + h > 0) fetch(t, h, in);
 #pragma unroll
             for (int i = 0; i < kHeads; ++i) {
                 unsigned top = 0u;  // of the bits: as numbers, in the same order
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(4 * D, 1024 / (4 * D)) append8_kernel(const __
         const int s = s_slot[run] + (t - t0 - run);  // a run's slots follow one another
 #pragma unroll 1
         for (int h = (nh - 1) / kHeads * kHeads; h >= 0; h -= kHeads) {
-            if (pass != passes - 1 || h + kHeads < nh) fetch(t, h);
+            if (pass != passes - 1 || h + kHeads < nh) fetch(t, h, true);
 #pragma unroll
             for (int i = 0; i < kHeads; ++i)
                 if (h + i < nh) {
