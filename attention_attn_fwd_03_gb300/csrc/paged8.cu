@@ -40,8 +40,10 @@
 //
 // Measured (inputs from HBM, d = 128, 32 heads over 8 unless said).  4 requests of 200 to 262 thousand keys: 287 to 319 us
 // on different GPUs, 5.9 to 6.6 TB/s (a copy: 6.8); 64 of 512 to 8192: 99 to 108 us, 5.3 to 5.8 TB/s; 33 of 0 to 4096 with
-// 16 heads over 16: 56 us; one of 32 thousand (which stays in L2): 22 us; 8 tokens of 16 requests, d = 64, 16 heads over 2,
-// a scale to every token: 53 us, 0.9 of it in the softmax.  A call of one tile takes 11 us: 4 until the first page is asked
+// 16 heads over 16: 58 us; one of 32 thousand (which stays in L2): 22 us; 1 to 8 tokens of 16 requests, d = 64, 16 heads over 2,
+// a scale to every token: 53 us, 0.9 of it in the softmax.  16 requests of 8192, by query rows (tokens times heads of a
+// group) to each of 8 KV heads: 4 to 8 57 to 60 us, 16 68 to 70, 32 117, 64 210, 128 394, where reading the codes back and attn_varlen_fwd
+// take 244 for 64 and 269 for 128.  A call of one tile takes 11 us: 4 until the first page is asked
 // for, 4 for the tile, 2 to 3 for the merge; a unit's start and end, and the last CTAs' lead over the mean, take most of what
 // is not streaming in the others.
 #include <cuda_fp16.h>
