@@ -934,7 +934,7 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
                     const float2 sc = s_scale[(sc_buf * NH + rb / RH) * SB * 128 + ((t * 128 + tid) >> gshift)];
                     // the rows of keys past the request's end are zeros
                     const float mask = (unsigned)key0 + (unsigned)(t * 128 + tid) < (unsigned)u.kv_len ? 0.f : -INFINITY;
-                    vk1 = sc.y;
+                    vk1 = fminf(sc.y, kHuge);  // (a masked key's may be an infinity or NaN)
                     float f[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) f[i] = __int_as_float(s_row[rb + i].x) * sc.x;
@@ -1034,7 +1034,8 @@ __device__ void softmax_role(const Paged8Params& p, uint8_t* smem, const Bars& b
                         const float p0 = ex2(e0[i] - par0.x), p1 = ex2(e0[i + 1] - par1.x);
                         l[i] += p0;
                         l[i + 1] += p1;
-                        h[i / 2] = pack_half(p0 * fminf(vk0 * par0.y, kHuge), p1 * fminf(vk0 * par1.y, kHuge));
+                        // (the factor first: times the scale it may overflow, where the scales of a row are far apart)
+                        h[i / 2] = pack_half(p0 * par0.y * vk0, p1 * par1.y * vk0);
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) hi[i] = e5m2_of(h[i]);

@@ -100,7 +100,8 @@ attn_status_t attn_paged_read_fp8(const void* k_cache, const void* v_cache, cons
  * of that below.  Probabilities (times their block's scale) enter
  * the second product as fp16 numbers, in four e5m2 numbers each: off by at most 2^-11 of themselves and
  * 2^-33 of the row's largest (2^-19 of it, if every scale of V that the row sees is below
- * 2^-112), so that a long tail of small ones counts in O as it does in the sum.
+ * 2^-112), so that a long tail of small ones counts in O as it does in the sum. Those below
+ * 2^-126 of the largest are zero.  O is summed in fp32 before it is divided by the sum of probabilities.
  * Maxima, sums and exponentials are fp32; O is rounded once.
  * A token that sees no key gets O = 0 and lse = -inf; one with a NaN among its
  * scores NaN in both; rows behind the last request are left as they were.

@@ -96,3 +96,44 @@ def test_long_tail_under_one_large_key(d):
     """262 thousand keys, each 2^-24.1 of one: 1.5% of the sum, and all of O."""
     c = _case(262144, 24.1, 4, 2, d, 1, 320)
     _check(c, _run(c))
+
+
+@pytest.mark.parametrize("H,H_kv,d,q_len", FORMS)
+@pytest.mark.parametrize("bits,up,down", [(60.4, 50, -40), (113.7, 62, -62), (118.3, 62, -62), (124.6, 80, -50), (100.2, 100, 10),
+                                          (20.5, 100, 100), (20.5, -126, -126)])
+def test_small_probabilities_of_large_values(H, H_kv, d, q_len, bits, up, down):
+    """The scales of the tail's values are 2^up, that of the large key's, which is not zero, 2^down: O is a sum of both, of any size.
+    (Not up to 2^120: codes above 255 are no 32-bit numbers there, and O is a sum in 32 bits before it is divided.)"""
+    c = _case(1111, bits, H, H_kv, d, q_len, 640 // H_kv, block=1)
+    c["q"][:, :, 0] = 1.0
+    n, page = 1111, c["page"]
+    c["v"][n // 3] = 300.0
+    c["v"] = c["v"].to(F8).double()
+    i = int(c["table"][0, n // 3 // page])
+    c["v_scale"][:] = 2.0 ** up
+    c["v_scale"][i, :, n // 3 % page] = 2.0 ** down
+    keys = c["k_cache"].float()  # one size of the tail's probabilities
+    keys[:, :, :, 0] = torch.where(keys[:, :, :, 0] < 0, -8.0, keys[:, :, :, 0])
+    c["k_cache"] = keys.to(F8)
+    c["k"] = torch.where(c["k"] < 0, -8.0, c["k"])
+    codes = c["v_cache"].float()
+    codes[i, n // 3 % page] = 300.0
+    c["v_cache"] = codes.to(F8)
+    w = torch.full((n, 1), 2.0 ** up, dtype=torch.float64)
+    w[n // 3] = 2.0 ** down
+    o, lse = _run(c)
+    # as in _check, but that the row's largest is that of probability times scale, and that bf16's steps do not get smaller than
+    # 2^-133; scales below 2^-112 leave 2^-19 of the largest
+    floor = 2.0 ** (-19 if max(up, down) < -112 else -33)
+    G = H // H_kv
+    for t in range(q_len):
+        seen = n - q_len + 1 + t
+        for h in range(H):
+            s = c["k"][:seen, h // G, 0] * c["scale"]
+            p, v = torch.exp(s - s.max())[:, None] * w[:seen], c["v"][:seen, h // G]
+            total = torch.exp(s - s.max()).sum()
+            want = (p * v).sum(0) / total
+            off = 2.0 ** -21 * float(s.abs().max()) + 2.0 ** -18
+            bound = want * (2.0 ** -8 + 2.0 ** -11 + n / 32 * 2.0 ** -23 + 2 * off) * 1.01 + floor * p.max() * v.sum(0) / total + 2.0 ** -134
+            e = (o[:, t, h] - want).abs()
+            assert (e <= bound).all(), (t, h, float((e / want).max()), float((bound / want).max()))
